@@ -63,7 +63,11 @@ typedef enum {
   GMM_ERR_WORKSPACE = 6    /* workspace null, misaligned or smaller than required */
 } gmm_status;
 
-typedef enum { GMM_F32 = 0, GMM_BF16 = 1 } gmm_dtype;
+typedef enum {
+  GMM_F32 = 0,
+  GMM_BF16 = 1,
+  GMM_F16 = 2 /* logits and expert layers only: X of a mixture is fp32 or bf16 */
+} gmm_dtype;
 
 typedef enum {
   GMM_INIT_VAR_ONE = 0, /* every variance starts at 1 */
@@ -80,14 +84,15 @@ typedef struct {
 } gmm_problem;
 
 /* Device status bits recorded in the workspace (see gmm_device_status). */
-#define GMM_DEVFLAG_NONFINITE_X 0x1u     /* a NaN or Inf element in X */
+#define GMM_DEVFLAG_NONFINITE_X 0x1u     /* a NaN or Inf element in X; a NaN or +Inf logit */
 #define GMM_DEVFLAG_BAD_PARAMS 0x2u      /* w < 0, var <= 0 or a non-finite parameter */
 #define GMM_DEVFLAG_WAIT_TIMEOUT 0x4u    /* a bounded spin on a barrier gave up */
 #define GMM_DEVFLAG_X_RANGE 0x8u         /* an element of X lies so far from the mixture mean
                                             (over 240 scale units, about 480 mixture standard
                                             deviations) that the tensor-core path clipped it */
 #define GMM_DEVFLAG_BAD_INDEX 0x10u      /* gmm_ivf_build: a component index outside [0, K)
-                                            or repeated within one point's row */
+                                            or repeated within one point's row; elsewhere
+                                            an index outside [-1, K) */
 
 /* How the library runs a problem on the current device (see gmm_plan). */
 typedef struct {
@@ -352,6 +357,130 @@ gmm_status gmm_ivf_workspace_size(int64_t N, int32_t K, size_t* bytes);
 gmm_status gmm_ivf_build(int64_t N, int32_t K, int32_t m, const int32_t* idx, const float* resp,
                          float tau, int64_t* offsets, int64_t* ids, int64_t ids_capacity,
                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Log probabilities over rows of logits
+ * -------------------------------------
+ * gmm_loglik and gmm_assign_topm answer for the mixture's own log-joints; these
+ * calls answer the same questions for rows that come from elsewhere: a linear
+ * head over a vocabulary, a router over experts, log-joints already in memory.
+ *
+ * A row n of Z holds K logits x, and z_k = scale * x_k in float32 (scale = 1 / T
+ * for a temperature T):
+ *   lse_n = log sum_k e^{z_k},  log p_k = z_k - lse_n,  H_n = -sum_k p_k log p_k.
+ * Sums are formed in float32, in a fixed order: results do not change from run to
+ * run.  (The order may depend on N: few rows are cut into more slices.)
+ *
+ *  - Z is N x K of type dtype, element-aligned, its rows ld >= K elements apart;
+ *    any K up to 2^24 and any ld.  N = 0 is allowed and does nothing.
+ *  - A logit whose z is -inf is a masked class: it has p = 0 and is never an
+ *    alternative.  (A mask by the type's lowest value also gives p = 0 beside an
+ *    ordinary logit, but stays a class.)
+ *  - A row with every class masked has lse = -inf, log p = -inf, H = 0, no
+ *    alternatives and gradient 0.
+ *  - A row with a NaN or a z of +inf gives NaN (and index -1) for all its results,
+ *    a NaN gradient, and raises GMM_DEVFLAG_NONFINITE_X in *dev_flags.
+ *  - dev_flags (device, 1 uint32, may be NULL): bits are OR-ed in, never cleared.
+ * Neither call uses a workspace.
+ */
+typedef struct {
+  int64_t N;     /* rows, >= 0 */
+  int64_t ld;    /* elements from one row to the next, >= K */
+  int32_t K;     /* classes, >= 1 */
+  int32_t dtype; /* gmm_dtype of Z: GMM_F32, GMM_BF16 or GMM_F16 */
+  float scale;   /* > 0, finite */
+} gmm_rows;
+
+/*
+ * Per row: the log probability of a given class, the entropy, the log-sum-exp and
+ * the m most probable classes.
+ *   ids       device, N int32, or NULL: the class whose log p goes to logp[n].
+ *             -1 is no label (logp = 0); any other index outside [0, K) gives NaN
+ *             and raises GMM_DEVFLAG_BAD_INDEX.
+ *   logp      device, N floats; given with ids, NULL without.
+ *   entropy, lse  device, N floats each, or NULL.
+ *   m         0 <= m <= 32.  m > 0: top_idx and top_logp (device, N x m) get the m
+ *             classes of largest z, descending, equal z in ascending index order,
+ *             and their log p; where fewer than m classes are left, -1 and -inf.
+ * GMM_ERR_INVALID_ARG when no output is asked for.
+ */
+gmm_status gmm_logprobs(const gmm_rows* r, const void* Z, const int32_t* ids, int32_t m,
+                        float* logp, float* entropy, float* lse, int32_t* top_idx,
+                        float* top_logp, uint32_t* dev_flags, void* stream);
+
+/*
+ * Gradient of gmm_logprobs with respect to the logits, for upstream gradients
+ * dlogp, dentropy, dlse (device, N floats each, NULL for 0) and dtop (device,
+ * N x m, with m = 0 and NULL for none):
+ *   dx_k = scale * ( dlogp [k = id] + sum_j dtop_j [k = top_idx_j]
+ *          + p_k (dlse - dlogp - sum_j dtop_j - dentropy (log p_k + H)) )
+ * rounded once to dtype.
+ *   ids, lse, entropy, top_idx   as gmm_logprobs took and wrote them (entropy may be
+ *             NULL without dentropy, ids without dlogp).  An index of -1 has no
+ *             gradient; any other outside [0, K) has none either and raises
+ *             GMM_DEVFLAG_BAD_INDEX.  The same class may be named more than once.
+ *   dZ        device, N x K of type dtype, rows ldd >= K apart; entries between rows
+ *             are left as they were.  dZ may be Z itself with ldd = ld (the logits are
+ *             overwritten by their gradient); they must not overlap otherwise.
+ */
+gmm_status gmm_logprobs_backward(const gmm_rows* r, const void* Z, const int32_t* ids,
+                                 const float* lse, const float* entropy, const float* dlogp,
+                                 const float* dentropy, const float* dlse, int32_t m,
+                                 const int32_t* top_idx, const float* dtop, void* dZ, int64_t ldd,
+                                 uint32_t* dev_flags, void* stream);
+
+/*
+ * Routing: the m most probable classes (experts) of each row and their weights,
+ * laid out as gmm_assign_topm's assignment.  1 <= m <= min(K, 8).
+ *   idx, resp  device, N x m; order as gmm_logprobs.  resp is p_k, or with
+ *              renorm != 0 p_k divided by the sum over the row's m chosen classes.
+ *              Where fewer than m classes are left: -1 and 0.
+ */
+gmm_status gmm_route(const gmm_rows* r, const void* Z, int32_t m, int32_t renorm, int32_t* idx,
+                     float* resp, uint32_t* dev_flags, void* stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens:
+ *   Y_t = sum_j resp_tj W_down[e] ( act(W_gate[e] X_t) * (W_lin[e] X_t) ),  e = idx_tj.
+ *   X       device, T x D, rows ldx apart; ldx a multiple of 8, 16-byte aligned.
+ *   idx, resp  device, T x m: the assignment of gmm_route or gmm_assign_topm.  -1 is
+ *           an unused choice; any other index outside [0, E) is left out and raises
+ *           GMM_DEVFLAG_BAD_INDEX in the workspace's status word.  An expert that a token
+ *           names twice counts with the sum of its weights.
+ *   W_up    device, E x 2F x D: for each expert the F rows of W_gate, then the F rows
+ *           of W_lin.  W_down: device, E x D x F.  Both 16-byte aligned.
+ *   Y       device, T x D, rows ldy apart; a token without an expert gets zeros.  Must not
+ *           overlap the inputs.
+ *   ws      device workspace of gmm_moe_workspace_size bytes, 256-byte aligned, its first
+ *           word the status word (zero it once; a call leaves it unchanged unless it
+ *           raises a bit).  Calls that share it must be ordered on one stream.
+ * Everything has type dtype (GMM_BF16 or GMM_F16).  Products are summed in float32 in a
+ * fixed order, the inner activations are kept to twice the type's precision, and Y is
+ * rounded once; an inner activation beyond the type's range is infinite.  The result
+ * for a token does not depend on timing.
+ * T = 0 is allowed and does nothing.  GMM_ERR_UNSUPPORTED: T > 256, E > 1024, D or F not
+ * a multiple of 8, GMM_F32, a misaligned pointer.  m as gmm_route, but may exceed E.
+ */
+typedef enum {
+  GMM_ACT_SILU = 0, /* x / (1 + e^-x) */
+  GMM_ACT_GELU = 1  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+} gmm_act;
+
+typedef struct {
+  int32_t T;     /* tokens, 0 <= T <= 256 */
+  int32_t m;     /* choices per token, 1 <= m <= 8 */
+  int32_t E;     /* experts */
+  int32_t D;     /* width of X and Y */
+  int32_t F;     /* inner width */
+  int32_t dtype; /* GMM_BF16 or GMM_F16 */
+  int32_t act;   /* gmm_act */
+  int64_t ldx, ldy;
+} gmm_moe_problem;
+
+gmm_status gmm_moe_workspace_size(const gmm_moe_problem* p, size_t* bytes);
+gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, const float* resp,
+                   const void* W_up, const void* W_down, void* Y, void* ws, size_t ws_bytes,
+                   void* stream);
 
 /*
  * Waits for stream, then reads the device status word of ws into *flags

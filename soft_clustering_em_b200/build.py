@@ -13,9 +13,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libscem_gmm.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-SOURCES = ["gmm_api.cu"]
+SOURCES = ["gmm_api.cu", "rows_api.cu", "moe_api.cu"]
+OBJ = os.path.join(HERE, "_build")  # one object per source
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-         "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-shared", "--expt-relaxed-constexpr"]
+         "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
 
 
 def _inputs():
@@ -24,17 +25,41 @@ def _inputs():
     return files
 
 
+def _object(src):
+    return os.path.join(OBJ, os.path.splitext(src)[0] + ".o")
+
+
+def _stale(src):
+    """Whether a source's object is missing or older than a file it was made from."""
+    obj, deps = _object(src), _object(src)[:-2] + ".d"
+    if not (os.path.exists(obj) and os.path.exists(deps)):
+        return True
+    with open(deps) as f:
+        names = f.read().replace("\\\n", " ").split(":", 1)[-1].split()
+    made = os.path.getmtime(obj)
+    ours = [n for n in names if os.path.abspath(n).startswith(ROOT + os.sep)]
+    return not ours or any(not os.path.exists(n) or os.path.getmtime(n) > made for n in ours)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the library if it is missing or older than any source."""
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(f) for f in _inputs())
         if os.path.getmtime(LIB) >= newest:
             return LIB
-    cmd = [NVCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp",
-           *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+    os.makedirs(OBJ, exist_ok=True)
+    jobs = []
+    for src in SOURCES:
+        if not force and not _stale(src):
+            continue
+        obj = _object(src)
+        cmd = [NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, "-I", INCLUDE, "-I", CSRC,
+               "-MD", "-MF", obj[:-2] + ".d", "-c", os.path.join(CSRC, src), "-o", obj]
+        jobs.append((cmd, subprocess.Popen(cmd)))
+    failed = [(cmd, job.returncode) for cmd, job in jobs if job.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+    subprocess.check_call([NVCC, *FLAGS, "-shared", "-o", LIB + ".tmp", *map(_object, SOURCES)])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -12,6 +12,7 @@
 #include <unordered_set>
 #include <vector>
 
+#include "api_common.h"
 #include "common.cuh"
 #include "gmm.h"
 #include "ivf.cuh"
@@ -740,6 +741,11 @@ void sample_rows(int64_t N, int K, uint64_t seed, std::vector<int64_t>* rows) {
 }
 
 }  // namespace
+
+namespace scem {
+gmm_status api_launched(int n) { return launched(n); }
+gmm_status api_device_sms(int* sms) { return device_sms(sms); }
+}  // namespace scem
 
 extern "C" {
 

@@ -8,6 +8,7 @@ raises -- there is no fallback implementation.
 """
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -16,7 +17,8 @@ LIB_PATH = os.path.join(_HERE, "libscem_gmm.so")
 
 GMM_OK, GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED, GMM_ERR_CUDA = 0, 1, 2, 3
 GMM_ERR_NUMERIC, GMM_ERR_TIMEOUT, GMM_ERR_WORKSPACE = 4, 5, 6
-GMM_F32, GMM_BF16 = 0, 1
+GMM_F32, GMM_BF16, GMM_F16 = 0, 1, 2
+GMM_ACT_SILU, GMM_ACT_GELU = 0, 1
 GMM_INIT_VAR_ONE, GMM_INIT_VAR_DATA = 0, 1
 GMM_DEVFLAG_NONFINITE_X, GMM_DEVFLAG_BAD_PARAMS, GMM_DEVFLAG_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 GMM_DEVFLAG_X_RANGE, GMM_DEVFLAG_BAD_INDEX = 0x8, 0x10
@@ -25,7 +27,9 @@ EXPORTS = ("gmm_workspace_size", "gmm_plan", "gmm_init", "gmm_init_rows", "gmm_e
            "gmm_em_step_hard", "gmm_em_step_spherical", "gmm_kmeans_step", "gmm_em_step_noalloc",
            "gmm_host_staging_size", "gmm_em_step_host",
            "gmm_estep_stats", "gmm_mstep", "gmm_fit", "gmm_loglik",
-           "gmm_assign_topm", "gmm_ivf_workspace_size", "gmm_ivf_build", "gmm_device_status",
+           "gmm_assign_topm", "gmm_ivf_workspace_size", "gmm_ivf_build", "gmm_logprobs",
+           "gmm_logprobs_backward", "gmm_route", "gmm_moe_workspace_size", "gmm_moe",
+           "gmm_device_status",
            "gmm_trace_fused", "gmm_set_wait_budget", "gmm_launch_count", "gmm_status_string")
 
 
@@ -38,6 +42,17 @@ class gmm_plan_info(ctypes.Structure):
     _fields_ = [("tensor_cores", ctypes.c_int32), ("cluster_ctas", ctypes.c_int32),
                 ("groups", ctypes.c_int32), ("fit_one_launch", ctypes.c_int32),
                 ("chunk_rows", ctypes.c_int64)]
+
+
+class gmm_rows(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("ld", ctypes.c_int64), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class gmm_moe_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("m", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class GmmError(RuntimeError):
@@ -78,6 +93,12 @@ def load_library(path: str = LIB_PATH):
     lib.gmm_assign_topm.argtypes = [PP, P, P, P, P, I32, P, P, P, SZ, P]
     lib.gmm_ivf_workspace_size.argtypes = [I64, I32, ctypes.POINTER(SZ)]
     lib.gmm_ivf_build.argtypes = [I64, I32, I32, P, P, ctypes.c_float, P, P, I64, P, SZ, P]
+    PR, PM = ctypes.POINTER(gmm_rows), ctypes.POINTER(gmm_moe_problem)
+    lib.gmm_logprobs.argtypes = [PR, P, P, I32, P, P, P, P, P, P, P]
+    lib.gmm_logprobs_backward.argtypes = [PR, P, P, P, P, P, P, P, I32, P, P, P, I64, P, P]
+    lib.gmm_route.argtypes = [PR, P, I32, I32, P, P, P, P]
+    lib.gmm_moe_workspace_size.argtypes = [PM, ctypes.POINTER(SZ)]
+    lib.gmm_moe.argtypes = [PM, P, P, P, P, P, P, P, SZ, P]
     lib.gmm_device_status.argtypes = [P, SZ, P, ctypes.POINTER(ctypes.c_uint32), I32]
     lib.gmm_trace_fused.argtypes = [P, P]
     lib.gmm_set_wait_budget.argtypes = [ctypes.c_uint64]
@@ -365,6 +386,190 @@ def gmm_ivf_build(idx, resp, K, tau, ws=None, stream=None):
                                         float(tau), _ptr(offsets), _ptr(ids), N * m, _ptr(ws),
                                         ws.numel(), _stream(stream)), "gmm_ivf_build")
     return offsets, ids
+
+
+_DTYPES = {torch.float32: GMM_F32, torch.bfloat16: GMM_BF16, torch.float16: GMM_F16}
+
+
+def _rows(Z, scale) -> gmm_rows:
+    """The rows of a logits tensor (N x K, any row stride, unit column stride)."""
+    if Z.dtype not in _DTYPES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {Z.dtype}")
+    if Z.dim() != 2 or (Z.shape[1] > 1 and Z.stride(1) != 1):
+        raise ValueError("logits must be N x K with a unit column stride")
+    N, K = Z.shape
+    ld = Z.stride(0) if N > 1 else max(Z.stride(0), K)
+    return gmm_rows(N, ld, K, _DTYPES[Z.dtype], scale)
+
+
+def _same_device(X, *others):
+    """Every tensor of a call is on X's CUDA device."""
+    if not X.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.device != X.device:
+            raise ValueError(f"the tensors are on different devices: {X.device}, {t.device}")
+
+
+def _vector(t, n, dtype, name):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {n}, got {tuple(t.shape)}")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(fn, what, device, stream, *args):
+    """Call fn(*args, stream) with `device` current; stream None: its current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(fn, what, device, stream, *args)
+    s = torch.cuda.current_stream() if stream is None else stream
+    _check(fn(*args, s.cuda_stream), what)
+
+
+class RowLogprobs(NamedTuple):
+    """Results of gmm_logprobs; logp is None without ids, the alternatives with m = 0."""
+
+    logp: Optional[torch.Tensor]      # N
+    entropy: torch.Tensor             # N
+    lse: torch.Tensor                 # N
+    top_idx: Optional[torch.Tensor]   # N x m int32
+    top_logp: Optional[torch.Tensor]  # N x m
+
+
+def gmm_logprobs(Z, ids=None, m=0, scale=1.0, dev_flags=None, stream=None) -> RowLogprobs:
+    """Log probability of the class ids[n] of each row of logits Z, entropy, log-sum-exp, and
+    the m most probable classes with their log probabilities.
+
+    Z: N x K float32, bfloat16 or float16, any row stride; the logits are scale * Z.
+    ids: N int32, -1 for rows without a label (logp 0).  m <= 32.  dev_flags (1 int32
+    device tensor, optional) collects the device status bits.
+    """
+    r = _rows(Z, scale)
+    N, m = Z.shape[0], int(m)
+    _same_device(Z, ids, dev_flags)
+    _vector(ids, (N,), torch.int32, "ids")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    out = torch.empty(3, N, dtype=torch.float32, device=Z.device).unbind(0)
+    logp, entropy, lse = out if ids is not None else (None, *out[1:])
+    top_idx = top_logp = None
+    if m > 0:
+        top_idx = torch.empty(N, m, dtype=torch.int32, device=Z.device)
+        top_logp = torch.empty(N, m, dtype=torch.float32, device=Z.device)
+    _launch(load_library().gmm_logprobs, "gmm_logprobs", Z.device, stream, ctypes.byref(r),
+            Z.data_ptr(), _address(ids), m, _address(logp), entropy.data_ptr(), lse.data_ptr(),
+            _address(top_idx), _address(top_logp), _address(dev_flags))
+    return RowLogprobs(logp, entropy, lse, top_idx, top_logp)
+
+
+def gmm_logprobs_backward(Z, ids, lse, dlogp=None, entropy=None, dentropy=None, dlse=None,
+                          top_idx=None, dtop=None, scale=1.0, out=None, dev_flags=None,
+                          stream=None):
+    """Gradient with respect to Z of gmm_logprobs(Z, ids, m, scale), for the upstream gradients
+    dlogp, dentropy, dlse (N float32 each, None: 0) and dtop (N x m float32, or None).
+
+    lse, entropy and top_idx as gmm_logprobs returned them (entropy only with dentropy, top_idx
+    with dtop).  out: N x K of Z's type to write to, Z itself included; allocated when None.
+    """
+    r = _rows(Z, scale)
+    N, K = Z.shape
+    m = 0 if dtop is None else (dtop.shape[1] if dtop.dim() == 2 else -1)
+    if m < 0 or (dtop is not None and top_idx is None):
+        raise ValueError("dtop must be N x m and needs top_idx")
+    _same_device(Z, ids, lse, dlogp, entropy, dentropy, dlse, top_idx, dtop, out, dev_flags)
+    _vector(ids, (N,), torch.int32, "ids")
+    for t, name in ((lse, "lse"), (dlogp, "dlogp"), (entropy, "entropy"),
+                    (dentropy, "dentropy"), (dlse, "dlse")):
+        _vector(t, (N,), torch.float32, name)
+    if m:
+        _vector(top_idx, (N, m), torch.int32, "top_idx")
+        _vector(dtop, (N, m), torch.float32, "dtop")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    if out is None:
+        out = torch.empty(N, K, dtype=Z.dtype, device=Z.device)
+    o = _rows(out, 1.0)
+    if out.dtype != Z.dtype or out.shape != Z.shape:
+        raise ValueError("out must have the shape and type of Z")
+    _launch(load_library().gmm_logprobs_backward, "gmm_logprobs_backward", Z.device, stream,
+            ctypes.byref(r), Z.data_ptr(), _address(ids), lse.data_ptr(), _address(entropy),
+            _address(dlogp), _address(dentropy), _address(dlse), m,
+            _address(top_idx) if m else None, _address(dtop) if m else None, out.data_ptr(), o.ld,
+            _address(dev_flags))
+    return out
+
+
+def gmm_route(Z, m, renorm=False, scale=1.0, dev_flags=None, stream=None):
+    """(idx N x m int32, resp N x m float32): the m most probable classes of each row of logits
+    and their probabilities, divided by their sum with renorm; -1 and 0 where classes run out.
+    """
+    r = _rows(Z, scale)
+    _same_device(Z, dev_flags)
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    N, m = Z.shape[0], int(m)
+    idx = torch.empty(N, max(m, 0), dtype=torch.int32, device=Z.device)
+    resp = torch.empty(N, max(m, 0), dtype=torch.float32, device=Z.device)
+    _launch(load_library().gmm_route, "gmm_route", Z.device, stream, ctypes.byref(r),
+            Z.data_ptr(), m, int(bool(renorm)), idx.data_ptr(), resp.data_ptr(),
+            _address(dev_flags))
+    return idx, resp
+
+
+def moe_problem(X, idx, W_down, act=GMM_ACT_SILU, out=None) -> gmm_moe_problem:
+    """The problem of a gmm_moe call on these tensors."""
+    if X.dtype not in _DTYPES:
+        raise TypeError(f"X must be bfloat16 or float16, got {X.dtype}")
+    T, D = X.shape
+    E, _, F = W_down.shape
+    ld = [max(t.stride(0), D) if T <= 1 else t.stride(0) for t in (X, X if out is None else out)]
+    return gmm_moe_problem(T, idx.shape[1], E, D, F, _DTYPES[X.dtype], int(act), ld[0],
+                           D if out is None else ld[1])
+
+
+def gmm_moe_workspace_size(p: gmm_moe_problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().gmm_moe_workspace_size(ctypes.byref(p), ctypes.byref(n)),
+           "gmm_moe_workspace_size")
+    return int(n.value)
+
+
+def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, stream=None):
+    """Mixture-of-experts layer for a few tokens: for each token the sum over its choices of
+    resp * W_down[e] (act(W_gate[e] x) * (W_lin[e] x)).
+
+    X: T x D bfloat16 or float16 (T <= 256, any row stride that is a multiple of 8); idx, resp:
+    T x m as gmm_route or gmm_assign_topm return them, -1 for an unused choice; W_up:
+    E x 2F x D, W_gate's F rows over W_lin's; W_down: E x D x F.  Returns T x D of X's type.
+    ws: a uint8 device tensor of gmm_moe_workspace_size bytes (allocated here when None), its
+    first word the device status word: zero it once to read it with gmm_device_status.
+    """
+    if X.dim() != 2 or idx.dim() != 2 or W_up.dim() != 3 or W_down.dim() != 3:
+        raise ValueError("X is T x D, idx T x m, W_up E x 2F x D, W_down E x D x F")
+    (T, D), (E, _, F) = X.shape, W_down.shape
+    _same_device(X, idx, resp, W_up, W_down, out, ws)
+    _vector(idx, (T, idx.shape[1]), torch.int32, "idx")
+    _vector(resp, (T, idx.shape[1]), torch.float32, "resp")
+    _vector(W_up, (E, 2 * F, D), X.dtype, "W_up")
+    _vector(W_down, (E, D, F), X.dtype, "W_down")
+    if out is None:
+        out = torch.empty(T, D, dtype=X.dtype, device=X.device)
+    if out.dtype != X.dtype or out.shape != X.shape:
+        raise ValueError("out must have the shape and type of X")
+    for t in (X, out):
+        if D > 1 and t.stride(1) != 1:
+            raise ValueError("X and out must have a unit column stride")
+    p = moe_problem(X, idx, W_down, act, out)
+    if ws is None:
+        ws = torch.empty(gmm_moe_workspace_size(p), dtype=torch.uint8, device=X.device)
+    _launch(load_library().gmm_moe, "gmm_moe", X.device, stream, ctypes.byref(p), X.data_ptr(),
+            idx.data_ptr(), resp.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), out.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    return out
 
 
 def gmm_device_status(ws, clear=True, stream=None):
