@@ -58,6 +58,40 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two floats in a register pair: one instruction for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // 16 bytes of a row as floats.
 template <typename T>
 struct Vec16;
@@ -72,6 +106,17 @@ struct Vec16<float> {
   }
   static __device__ __forceinline__ uint4 neg_inf() {
     return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
+  // the largest of kN vectors' entries, a NaN if there is one
+  template <int kN>
+  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
+    float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < kN; j++) {
+      m[0] = max3_nan(m[0], __uint_as_float(r[j].x), __uint_as_float(r[j].y));
+      m[1] = max3_nan(m[1], __uint_as_float(r[j].z), __uint_as_float(r[j].w));
+    }
+    return max_nan(m[0], m[1]);
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
@@ -91,6 +136,18 @@ struct Vec16<__nv_bfloat16> {
   }
   static __device__ __forceinline__ uint4 neg_inf() {
     return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
+  template <int kN>
+  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
+    uint32_t m = 0xff80ff80u;
+#pragma unroll
+    for (int j = 0; j < kN; j++) {
+      const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    }
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     uint32_t w[4];
@@ -116,6 +173,19 @@ struct Vec16<__half> {
   }
   static __device__ __forceinline__ uint4 neg_inf() {
     return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+  }
+  template <int kN>
+  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
+    uint32_t m = 0xfc00fc00u;
+#pragma unroll
+    for (int j = 0; j < kN; j++) {
+      const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+    }
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max_nan(f.x, f.y);
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     uint32_t w[4];
@@ -238,13 +308,33 @@ __device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, ui
 
 // ------------------------------------------------------------------ short rows
 // kLanes lanes hold a row of at most kLanes * kEl classes in registers, so a
-// warp holds 32 / kLanes rows.  kVec: rows start on 16 bytes.
+// warp holds 32 / kLanes rows; lane l takes vectors l, l + kLanes, ... of 16
+// bytes.  kVec: rows start on 16 bytes (else the same entries one by one).
+//
+// Alternatives in m rounds.  Only each vector's largest entry stays in registers;
+// a round finds the lowest vector that holds the row's largest, reads it again
+// (it is in L1) and leaves it with its largest entry behind the one just taken.
+template <typename T, bool kVec>
+__device__ __forceinline__ uint4 load_row_vec(const T* row, int k0, int K) {
+  constexpr int V = Vec16<T>::n;
+  if (kVec && k0 + V <= K) return load16(row + k0);
+  union {
+    uint4 r;
+    T x[V];
+  } u;
+  u.r = Vec16<T>::neg_inf();
+#pragma unroll
+  for (int e = 0; e < V; e++)
+    if (k0 + e < K) u.x[e] = row[k0 + e];
+  return u.r;
+}
+
 template <typename T, int kLanes, int kEl, bool kVec>
-__global__ void __launch_bounds__(256) row_short_kernel(RowArgs a) {
+__global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowArgs a) {
   constexpr int kRows = 32 / kLanes;
-  constexpr int V = kVec ? Vec16<T>::n : 1;
+  constexpr int V = Vec16<T>::n;
   constexpr int kChunks = kEl / V;
-  static_assert(kEl % V == 0, "whole vectors");
+  static_assert(kEl % V == 0 && kLanes >= 8, "whole vectors; a lane for each chosen expert");
   const int lane = threadIdx.x & 31, l = lane % kLanes;
   const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * 8 * kRows;
@@ -252,40 +342,44 @@ __global__ void __launch_bounds__(256) row_short_kernel(RowArgs a) {
     const int64_t n = n0 + lane / kLanes;
     const bool live = n < a.N;
     const T* row = (const T*)a.Z + (live ? n : n0) * a.ld;
-    float z[kEl];
+    uint4 r[kChunks];
+    float top[kChunks];  // the largest z of each vector
+#pragma unroll
+    for (int c = 0; c < kChunks; c++)
+      r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
+    float R = -FLT_MAX;
 #pragma unroll
     for (int c = 0; c < kChunks; c++) {
-      const int k0 = (c * kLanes + l) * V;
-      if constexpr (kVec) {
-        float x[V];
-        if (k0 + V <= a.K) {
-          Vec16<T>::unpack(load16(row + k0), x);
-        } else {
+      const uint4 one[1] = {r[c]};
+      top[c] = Vec16<T>::max_of(one) * a.scale;
+      R = max_nan(R, top[c]);
+    }
 #pragma unroll
-          for (int e = 0; e < V; e++) x[e] = k0 + e < a.K ? to_f32(row[k0 + e]) : -INFINITY;
-        }
+    for (int o = kLanes / 2; o > 0; o >>= 1) R = max_nan(R, __shfl_xor_sync(0xffffffffu, R, o));
+    F2 S2 = f2(0.f, 0.f), U2 = S2;
+    const F2 scale2 = f2(a.scale, a.scale), ref2 = f2(-R, -R), log2 = f2(kLog2e, kLog2e);
 #pragma unroll
-        for (int e = 0; e < V; e++) z[c * V + e] = x[e];
-      } else {
-        z[c] = k0 < a.K ? to_f32(row[k0]) : -INFINITY;
+    for (int c = 0; c < kChunks; c++) {
+      float x[V];
+      Vec16<T>::unpack(r[c], x);
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        float d0, d1, t0, t1;
+        f2_get(f2_fma(f2(x[e], x[e + 1]), scale2, ref2), d0, d1);
+        const F2 d = f2(fmaxf(d0, kFloorD), fmaxf(d1, kFloorD));
+        f2_get(f2_mul(d, log2), t0, t1);
+        const F2 y = f2(ex2(t0), ex2(t1));
+        S2 = f2_add(S2, y);
+        U2 = f2_fma(y, d, U2);
       }
     }
-    Part p = part_empty();
-#pragma unroll
-    for (int i = 0; i < kEl; i++) {
-      z[i] *= a.scale;
-      p.R = max_nan(p.R, z[i]);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1)
-      p.R = max_nan(p.R, __shfl_xor_sync(0xffffffffu, p.R, o));
-#pragma unroll
-    for (int i = 0; i < kEl; i++) {
-      const float d = fmaxf(z[i] - p.R, kFloorD);
-      const float e = ex2(d * kLog2e);
-      p.S += e;
-      p.U = fmaf(e, d, p.U);
-    }
+    Part p;
+    float s0, s1;
+    p.R = R;
+    f2_get(S2, s0, s1);
+    p.S = s0 + s1;
+    f2_get(U2, s0, s1);
+    p.U = s0 + s1;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) {
       p.S += __shfl_xor_sync(0xffffffffu, p.S, o);
@@ -294,51 +388,51 @@ __global__ void __launch_bounds__(256) row_short_kernel(RowArgs a) {
     const bool bad = !(p.R < INFINITY);
     const float logS = logf(p.S);
     if (l == 0 && live) write_row<T>(a, n, p, logS, bad);
-    if (a.m > 0) {
-      uint64_t mine = 0;  // lane l holds alternatives l, l + kLanes, ... one at a time
-      float sel = 0.f;
-      // renormalised weights need the chosen sum first: two sweeps over the winners
-      // are avoided by keeping the keys (m <= 8 there, see the host's choice)
-      uint64_t keep[8];
+    float sel = 0.f;
+    float last_z = INFINITY;  // the entry taken last: what follows it in the order is left
+    int last_k = -1;
+    for (int j0 = 0; j0 < a.m; j0 += kLanes) {
+      const int cnt = min(kLanes, a.m - j0);
+      uint64_t mine = 0;  // lane l keeps alternative j0 + l
+      for (int j = 0; j < cnt; j++) {
+        float best = top[0];
 #pragma unroll
-      for (int j = 0; j < 8; j++) keep[j] = 0;
-      for (int j = 0; j < a.m; j++) {
-        float bv = -INFINITY;
-        int bi = -1;
+        for (int c = 1; c < kChunks; c++) best = fmaxf(best, top[c]);
 #pragma unroll
-        for (int i = 0; i < kEl; i++)
-          if (z[i] > bv) {
-            bv = z[i];
-            bi = i;
-          }
-        uint64_t key = 0;
-        if (bi >= 0) key = entry_key(bv, (uint32_t)((bi / V * kLanes + l) * V + bi % V));
-        mine = key;
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        int at = 1 << 30;  // the lowest vector that holds it
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) {
-          const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-          key = other > key ? other : key;
+        for (int c = kChunks - 1; c >= 0; c--)
+          if (top[c] == best) at = c * kLanes + l;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+          at = min(at, __shfl_xor_sync(0xffffffffu, at, o));
+        const bool none = best == -INFINITY || at == 1 << 30;
+        const int k0 = none ? 0 : at * V;
+        float x[V];
+        Vec16<T>::unpack(load_row_vec<T, kVec>(row, k0, a.K), x);
+        int e0 = 0;
+#pragma unroll
+        for (int e = V - 1; e >= 0; e--) {
+          x[e] *= a.scale;
+          if (x[e] == best && (best < last_z || k0 + e > last_k)) e0 = e;
         }
-        if (mine == key) {
+        float next = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kEl; i++)
-            if (i == bi) z[i] = -INFINITY;
-        }
-        if (a.route == 2) {
-          if (key) sel += expf(key_z(key) - p.R);
+        for (int e = 0; e < V; e++)
+          if (x[e] < best || (x[e] == best && e > e0)) next = fmaxf(next, x[e]);
 #pragma unroll
-          for (int t = 0; t < 8; t++)
-            if (t == j) keep[t] = key;
-        } else if (l == 0 && live) {
-          write_alt(a, n, j, key, p, logS, 0.f, bad);
+        for (int c = 0; c < kChunks; c++)
+          if (at == c * kLanes + l) top[c] = next;
+        last_z = best;
+        last_k = k0 + e0;
+        if (!none) {
+          sel += ex2((best - p.R) * kLog2e);
+          if (l == j) mine = entry_key(best, (uint32_t)last_k);
         }
       }
-      if (a.route == 2 && l == 0 && live) {
-        sel = logf(sel);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-          if (j < a.m) write_alt(a, n, j, keep[j], p, logS, sel, bad);
-      }
+      if (l < cnt && live) write_alt(a, n, j0 + l, mine, p, logS, a.route == 2 ? logf(sel) : 0.f, bad);
     }
   }
 }
@@ -470,26 +564,31 @@ __global__ void __launch_bounds__(kRowThreads) row_long_kernel(RowArgs a, int C)
         const int v = base + j * kRowThreads;
         r[j] = v < s.v1 ? load16(s.vec(v)) : Vec16<T>::neg_inf();
       }
-      float x[kRowBatch][V];
-      float mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kRowBatch; j++) {
-        Vec16<T>::unpack(r[j], x[j]);
-#pragma unroll
-        for (int e = 0; e < V; e++) mx = max_nan(mx, x[j][e]);
-      }
-      const float zm = mx * s.scale;
+      const float zm = Vec16<T>::max_of(r) * s.scale;
       if (zm > p.R || (where == -2 && zm == p.R)) where = b;
       part_shift(p, max_nan(p.R, zm));
+      const F2 scale2 = f2(s.scale, s.scale), ref2 = f2(-p.R, -p.R), log2 = f2(kLog2e, kLog2e);
+      F2 S2 = f2(p.S, 0.f), U2 = f2(p.U, 0.f);
 #pragma unroll
-      for (int j = 0; j < kRowBatch; j++)
+      for (int j = 0; j < kRowBatch; j++) {
+        float x[V];
+        Vec16<T>::unpack(r[j], x);
 #pragma unroll
-        for (int e = 0; e < V; e++) {
-          const float d = fmaxf(fmaf(x[j][e], s.scale, -p.R), kFloorD);
-          const float y = ex2(d * kLog2e);
-          p.S += y;
-          p.U = fmaf(y, d, p.U);
+        for (int e = 0; e < V; e += 2) {
+          float d0, d1, t0, t1;
+          f2_get(f2_fma(f2(x[e], x[e + 1]), scale2, ref2), d0, d1);
+          const F2 d = f2(fmaxf(d0, kFloorD), fmaxf(d1, kFloorD));
+          f2_get(f2_mul(d, log2), t0, t1);
+          const F2 y = f2(ex2(t0), ex2(t1));
+          S2 = f2_add(S2, y);
+          U2 = f2_fma(y, d, U2);
         }
+      }
+      float s0, s1;
+      f2_get(S2, s0, s1);
+      p.S = s0 + s1;
+      f2_get(U2, s0, s1);
+      p.U = s0 + s1;
     }
     if (s.last && t < s.tailn) single(s.tail0 + t, nb);
 

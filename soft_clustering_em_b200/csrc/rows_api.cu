@@ -49,12 +49,12 @@ gmm_status rows_launch(const RowArgs& a, cudaStream_t st) {
   if (s != GMM_OK) return s;
   if (a.K <= kShortRow) {
     const bool vec = (uintptr_t)a.Z % 16 == 0 && (a.ld * sizeof(T)) % 16 == 0;
-    if (a.K <= 32)
-      short_launch<T, 4, 8>(a, vec, st);
-    else if (a.K <= 256 && a.N <= 16 * sms)
+    if (a.K <= 256 && a.N <= 16 * sms)
       short_launch<T, 32, 8>(a, vec, st);
+    else if (a.K <= 64)
+      short_launch<T, 8, 8>(a, vec, st);
     else if (a.K <= 128)
-      short_launch<T, 4, 32>(a, vec, st);
+      short_launch<T, 8, 16>(a, vec, st);
     else if (a.K <= 256)
       short_launch<T, 8, 32>(a, vec, st);
     else if (a.K <= 512)

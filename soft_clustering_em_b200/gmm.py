@@ -406,8 +406,9 @@ def _same_device(X, *others):
     """Every tensor of a call is on X's CUDA device."""
     if not X.is_cuda:
         raise ValueError("the tensors must be on a CUDA device")
+    index = X.get_device()
     for t in others:
-        if t is not None and t.device != X.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"the tensors are on different devices: {X.device}, {t.device}")
 
 
@@ -416,7 +417,7 @@ def _vector(t, n, dtype, name):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != n or not t.is_contiguous():
+    if t.shape != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous of shape {n}, got {tuple(t.shape)}")
 
 
@@ -429,8 +430,12 @@ def _launch(fn, what, device, stream, *args):
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch(fn, what, device, stream, *args)
-    s = torch.cuda.current_stream() if stream is None else stream
-    _check(fn(*args, s.cuda_stream), what)
+    # (the raw handle: building a torch.cuda.Stream object costs as much as a launch)
+    s = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+         else stream.cuda_stream)
+    rc = fn(*args, s)
+    if rc != GMM_OK:
+        raise GmmError(rc, what)
 
 
 class RowLogprobs(NamedTuple):
