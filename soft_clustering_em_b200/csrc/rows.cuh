@@ -2,20 +2,17 @@
 // gmm_logprobs_backward and gmm_route.
 //
 // A row holds one logit x_k per class (a mixture component, a vocabulary entry,
-// an expert) and z_k = fl32(scale * x_k).  Per row, with M = max_k z_k:
-//   S = sum_k e^{z_k - M}      lse = M + log S       log p_k = (z_k - M) - log S
-//   U = sum_k e^{z_k - M} (z_k - M)                  H = -sum_k p_k log p_k = log S - U / S
+// an expert) and z_k = fl32(scale * x_k).  With c = scale * log2 e, a reference B
+// near the largest c x_k, and t_k = c x_k - B:
+//   S = sum_k 2^{t_k}            lse = log 2 (B + log2 S)
+//   U = sum_k 2^{t_k} t_k        log p_k = log 2 (t_k - log2 S)
+//                                H = -sum_k p_k log p_k = log 2 (log2 S - U / S)
 // and the m classes of largest z, equal z in ascending index order.
 //
-// S and U come from one pass: a thread (or a lane) keeps a reference R, its
-// running maximum, and S and U relative to it; when R rises by a, S <- S e^{-a}
-// and U <- e^{-a} (U - a S).  Partial results merge by the same rule, in a fixed
-// order.  Everything is held in 32 bits.
-//
-// R starts at the lowest float rather than at -inf, and z - R is clamped from
-// below at kFloorD, where e^{z-R} is exactly 0: classes masked by -inf, or by
-// the type's lowest value, add 0 to both sums without a 0 * inf.  A row with no
-// class left ends with S = 0.
+// S and U come from one pass.  Any B does as long as no 2^t overflows; partial
+// results with other references merge by S <- S 2^a, U <- 2^a (U + a S) for a
+// difference a of theirs, in a fixed order.  t is one fused multiply-add, so a
+// rounded B takes nothing from log p and H.  Everything is held in 32 bits.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,8 +24,10 @@
 namespace scem {
 
 constexpr int kMaxAlt = 32;          // most alternatives per row
-constexpr float kFloorD = -150.f;    // e^-150 < 2^-149: 0 in float32
+constexpr float kFloorT = -200.f;    // 2^-200 is 0 in float32
+constexpr float kFloorD = -150.f;    // and so is e^-150
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct RowArgs {
   const void* Z;
@@ -209,27 +208,29 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
 }
 
-// Reference, sum and first moment of a part of a row.
+// Reference, S and U of a part of a row.
 struct Part {
-  float R, S, U;
+  float B, S, U;
 };
 
-__device__ __forceinline__ Part part_empty() { return {-FLT_MAX, 0.f, 0.f}; }
+constexpr float kFar = 1e30f;  // rows with a |c x| beyond kNear take a path of their own
+constexpr float kNear = 1e29f;
 
-// Move p's reference to R >= p.R.
-__device__ __forceinline__ void part_shift(Part& p, float R) {
-  const float a = fmaxf(p.R - R, kFloorD);
-  const float f = ex2(a * kLog2e);
-  p.U = f * fmaf(a, p.S, p.U);
-  p.S *= f;
-  p.R = R;
+__device__ __forceinline__ Part part_empty() { return {-kFar, 0.f, 0.f}; }
+
+// S and U to a reference a powers of two lower (a <= 0: higher).
+__device__ __forceinline__ void sums_shift(float& S, float& U, float a) {
+  a = fmaxf(a, kFloorT);
+  const float f = ex2(a);
+  U = f * fmaf(a, S, U);
+  S *= f;
 }
 
 __device__ __forceinline__ Part part_merge(Part p, Part q) {
-  const float R = max_nan(p.R, q.R);
-  part_shift(p, R);
-  part_shift(q, R);
-  return {R, p.S + q.S, p.U + q.U};
+  const float B = max_nan(p.B, q.B);
+  sums_shift(p.S, p.U, p.B - B);
+  sums_shift(q.S, q.U, q.B - B);
+  return {B, p.S + q.S, p.U + q.U};
 }
 
 template <int kLanes>
@@ -237,7 +238,7 @@ __device__ __forceinline__ Part part_reduce(Part p) {
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) {
     Part q;
-    q.R = __shfl_xor_sync(0xffffffffu, p.R, o);
+    q.B = __shfl_xor_sync(0xffffffffu, p.B, o);
     q.S = __shfl_xor_sync(0xffffffffu, p.S, o);
     q.U = __shfl_xor_sync(0xffffffffu, p.U, o);
     p = part_merge(p, q);
@@ -266,15 +267,37 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-// What a row's sums say, written by one thread.  bad: a NaN or +inf in the row.
+// What a row's sums say.
+struct RowSums {
+  float B, L, H;     // lse = log 2 B + L, or B + L where B is a logit
+  bool bad, empty;   // a NaN or +inf in the row; nothing but masked classes
+  bool logit;
+  // relative to B = about the largest c x
+  static __device__ __forceinline__ RowSums near(const Part& p) {
+    const float l = log2f(p.S);
+    return {p.B, l, fmaxf(kLn2 * (l - p.U / p.S), 0.f), false, false, false};
+  }
+  // relative to the largest logit x itself, t = c (x_k - x)
+  static __device__ __forceinline__ RowSums at(float x, float scale, float S, float U) {
+    const float Z = x * scale, l = logf(S);
+    return {Z, l, fmaxf(fmaf(-kLn2, U / S, l), 0.f), !(Z < INFINITY), Z == -INFINITY, true};
+  }
+  __device__ __forceinline__ float lse() const {
+    return logit ? B + L : kLn2 * (B + L);
+  }
+  __device__ __forceinline__ float log_p(float z) const {
+    if (logit) return (z - B) - L;
+    return fabsf(z) < kNear ? kLn2 * (fmaf(z, kLog2e, -B) - L) : z - lse();
+  }
+};
+
+// By one thread: lse, entropy and the label's log p of row n.
 template <typename T>
-__device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const Part& p, float logS,
-                                          bool bad) {
+__device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const RowSums& s) {
   const float nan = __int_as_float(0x7fffffff);
-  const bool empty = p.S == 0.f;
-  if (bad && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
-  if (a.lse) a.lse[n] = bad ? nan : empty ? -INFINITY : p.R + logS;
-  if (a.entropy) a.entropy[n] = bad ? nan : empty ? 0.f : fmaxf(logS - p.U / p.S, 0.f);
+  if (s.bad && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
+  if (a.lse) a.lse[n] = s.bad ? nan : s.empty ? -INFINITY : s.lse();
+  if (a.entropy) a.entropy[n] = s.bad ? nan : s.empty ? 0.f : s.H;
   if (a.ids) {
     const int id = a.ids[n];
     float lp;
@@ -285,24 +308,24 @@ __device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const Par
       if (a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
     } else {
       const float z = to_f32(((const T*)a.Z)[n * a.ld + id]) * a.scale;
-      lp = bad ? nan : empty || z == -INFINITY ? -INFINITY : (z - p.R) - logS;
+      lp = s.bad ? nan : z == -INFINITY ? -INFINITY : s.log_p(z);
     }
     a.logp[n] = lp;
   }
 }
 
-// Alternative j of row n (key 0: none); sel: log-sum of the m chosen relative to p.R.
+// Alternative j of row n (key 0: none); sel: log of the m chosen classes' probability.
 __device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, uint64_t key,
-                                          const Part& p, float logS, float sel, bool bad) {
+                                          const RowSums& s, float sel) {
   const float nan = __int_as_float(0x7fffffff);
-  const bool none = bad || key == 0;
+  const bool none = s.bad || key == 0;
   a.top_idx[n * a.m + j] = none ? -1 : (int32_t)key_idx(key);
-  const float d = key_z(key) - p.R;
+  const float lp = s.log_p(key_z(key));
   float v;
   if (a.route == 0)
-    v = bad ? nan : none ? -INFINITY : d - logS;
+    v = s.bad ? nan : none ? -INFINITY : lp;
   else
-    v = bad ? nan : none ? 0.f : expf(d - (a.route == 2 ? sel : logS));
+    v = s.bad ? nan : none ? 0.f : expf(a.route == 2 ? lp - sel : lp);
   a.top_val[n * a.m + j] = v;
 }
 
@@ -347,47 +370,55 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowAr
 #pragma unroll
     for (int c = 0; c < kChunks; c++)
       r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
-    float R = -FLT_MAX;
+    float xm = -INFINITY, S, U;
 #pragma unroll
     for (int c = 0; c < kChunks; c++) {
       const uint4 one[1] = {r[c]};
-      top[c] = Vec16<T>::max_of(one) * a.scale;
-      R = max_nan(R, top[c]);
+      const float x = Vec16<T>::max_of(one);
+      top[c] = x * a.scale;
+      xm = max_nan(xm, x);
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) R = max_nan(R, __shfl_xor_sync(0xffffffffu, R, o));
-    F2 S2 = f2(0.f, 0.f), U2 = S2;
-    const F2 scale2 = f2(a.scale, a.scale), ref2 = f2(-R, -R), log2 = f2(kLog2e, kLog2e);
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+      xm = max_nan(xm, __shfl_xor_sync(0xffffffffu, xm, o));
+    const float ref = fmaxf(xm, -FLT_MAX);
+    const F2 c2 = f2(a.scale * kLog2e, a.scale * kLog2e), ref2 = f2(-ref, -ref);
+    auto sums = [&](bool clamp) {
+      F2 S2 = f2(0.f, 0.f), U2 = S2;
 #pragma unroll
-    for (int c = 0; c < kChunks; c++) {
-      float x[V];
-      Vec16<T>::unpack(r[c], x);
+      for (int c = 0; c < kChunks; c++) {
+        float x[V];
+        Vec16<T>::unpack(r[c], x);
 #pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        float d0, d1, t0, t1;
-        f2_get(f2_fma(f2(x[e], x[e + 1]), scale2, ref2), d0, d1);
-        const F2 d = f2(fmaxf(d0, kFloorD), fmaxf(d1, kFloorD));
-        f2_get(f2_mul(d, log2), t0, t1);
-        const F2 y = f2(ex2(t0), ex2(t1));
-        S2 = f2_add(S2, y);
-        U2 = f2_fma(y, d, U2);
+        for (int e = 0; e < V; e += 2) {
+          float t0, t1;
+          f2_get(f2_mul(f2_add(f2(x[e], x[e + 1]), ref2), c2), t0, t1);
+          if (clamp) t0 = fmaxf(t0, kFloorT), t1 = fmaxf(t1, kFloorT);
+          const F2 y = f2(ex2(t0), ex2(t1));
+          S2 = f2_add(S2, y);
+          U2 = f2_fma(y, f2(t0, t1), U2);
+        }
       }
+      float s0, s1;
+      f2_get(S2, s0, s1);
+      S = s0 + s1;
+      f2_get(U2, s0, s1);
+      U = s0 + s1;
+    };
+    // a masked class gives 0 * -inf: only then the exponents are clamped
+    if (a.K < kLanes * kEl) {
+      sums(true);
+    } else {
+      sums(false);
+      if (__any_sync(0xffffffffu, !(U == U))) sums(true);
     }
-    Part p;
-    float s0, s1;
-    p.R = R;
-    f2_get(S2, s0, s1);
-    p.S = s0 + s1;
-    f2_get(U2, s0, s1);
-    p.U = s0 + s1;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) {
-      p.S += __shfl_xor_sync(0xffffffffu, p.S, o);
-      p.U += __shfl_xor_sync(0xffffffffu, p.U, o);
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      U += __shfl_xor_sync(0xffffffffu, U, o);
     }
-    const bool bad = !(p.R < INFINITY);
-    const float logS = logf(p.S);
-    if (l == 0 && live) write_row<T>(a, n, p, logS, bad);
+    const RowSums row_sums = RowSums::at(xm, a.scale, S, U);
+    if (l == 0 && live) write_row<T>(a, n, row_sums);
     float sel = 0.f;
     float last_z = INFINITY;  // the entry taken last: what follows it in the order is left
     int last_k = -1;
@@ -428,28 +459,49 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowAr
         last_z = best;
         last_k = k0 + e0;
         if (!none) {
-          sel += ex2((best - p.R) * kLog2e);
+          sel += ex2(row_sums.log_p(best) * kLog2e);
           if (l == j) mine = entry_key(best, (uint32_t)last_k);
         }
       }
-      if (l < cnt && live) write_alt(a, n, j0 + l, mine, p, logS, a.route == 2 ? logf(sel) : 0.f, bad);
+      if (l < cnt && live)
+        write_alt(a, n, j0 + l, mine, row_sums, a.route == 2 ? logf(sel) : 0.f);
     }
   }
 }
 
 // ------------------------------------------------------------------ long rows
-// One cluster of gridDim-wide C CTAs per row, each CTA a contiguous slice of
-// its 16-byte vectors; the row's unaligned ends go to the first and last CTA.
+// One cluster of C CTAs per row, each CTA a contiguous slice of its 16-byte
+// vectors, each warp a contiguous slice of that; the row's unaligned ends go to
+// the first and the last warp.  A warp walks its slice in batches of kRowBatch
+// vectors per lane.  Each lane copies its own vectors into its own places of a ring
+// in shared memory, kRowStages batches ahead, and reads them back itself: the loads
+// in flight cost no registers and nobody waits for anybody.
 //
-// Alternatives without a second pass over the row: let a thread's key be the
-// best entry it saw.  An entry among the CTA's m best lies with one of the m
-// threads of largest key (otherwise m threads hold a better entry each), so only
-// those threads' entries are read again, by a warp each, and only entries not
-// below the m-th of those keys are taken from them.  The lists are sorted, and
-// merge by m rounds of a warp-wide maximum.
+// Alternatives without a second pass over the row.  The m-th largest of the lanes'
+// maxima bounds the m-th largest entry from below, and each warp keeps the largest
+// entry of up to 32 units of consecutive batches.  Only units that reach the bound are
+// read again, and only entries that reach it are candidates: about m of them, chosen
+// from by one warp.  Where ties or masks leave more candidates than the buffer holds,
+// the m units of largest entry (which hold the m best, or m units would hold a better
+// one each) give a sorted list of their best each, and those merge.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowBatch = 4;  // 16-byte vectors in flight per thread
+constexpr int kRowBatch = 4;
+constexpr int kRowStages = 3;
+constexpr int kRowStep = 32 * kRowBatch;  // vectors of a warp's batch
+constexpr int kRowCand = 512;
+constexpr float kLargeSum = 1048576.f;  // of a lane: its reference is raised beyond
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 
 template <typename T>
 struct RowSlice {
@@ -458,6 +510,7 @@ struct RowSlice {
   float scale;
   int head, tail0, tailn;  // entries before the first vector; first entry after the last; count
   int v0, v1;              // this CTA's vectors
+  int per_unit;            // batches per unit
   bool first, last;
 
   __device__ __forceinline__ RowSlice(const RowArgs& a, int64_t n, int rank, int C) {
@@ -470,56 +523,53 @@ struct RowSlice {
     tailn = a.K - tail0;
     v0 = (int)((int64_t)nv * rank / C);
     v1 = (int)((int64_t)nv * (rank + 1) / C);
+    const int most = (v1 - v0 + kRowWarps - 1) / kRowWarps;  // vectors of a warp
+    per_unit = max(1, (most + 32 * kRowStep - 1) / (32 * kRowStep));
     first = rank == 0;
     last = rank == C - 1;
   }
+  // first vector of warp w's slice
+  __device__ __forceinline__ int begin(int w) const {
+    return v0 + (int)((int64_t)(v1 - v0) * w / kRowWarps);
+  }
+  __device__ __forceinline__ int batches(int w) const {
+    return (begin(w + 1) - begin(w) + kRowStep - 1) / kRowStep;
+  }
+  // the last unit of the last warp, which has the row's tail
+  __device__ __forceinline__ int tail_unit() const {
+    return max(0, batches(kRowWarps - 1) - 1) / per_unit;
+  }
   __device__ __forceinline__ const T* vec(int v) const { return row + head + (int64_t)v * V; }
-  __device__ __forceinline__ float z(int k) const { return to_f32(row[k]) * scale; }
-  // best key of vector v below `below`
-  __device__ __forceinline__ uint64_t best_of(int v, uint64_t below) const {
-    float x[V];
-    Vec16<T>::unpack(load16(vec(v)), x);
-    uint64_t b = 0;
+  __device__ __forceinline__ float x(int k) const { return to_f32(row[k]); }
+
+  // f(z, k) for the entries of unit u of warp w, shared out over the lanes
+  template <typename Fn>
+  __device__ __forceinline__ void each(int w, int u, int lane, Fn f) const {
+    const int end = min(begin(w) + (u + 1) * per_unit * kRowStep, begin(w + 1));
+    for (int v = begin(w) + u * per_unit * kRowStep + lane; v < end; v += 32) {
+      float e[V];
+      Vec16<T>::unpack(load16(vec(v)), e);
 #pragma unroll
-    for (int e = 0; e < V; e++) {
-      const uint64_t k = entry_key(x[e] * scale, (uint32_t)(head + v * V + e));
-      if (k < below && k > b) b = k;
+      for (int i = 0; i < V; i++) f(e[i] * scale, head + v * V + i);
     }
-    return b;
-  }
-  // best key of thread t's entries below `below`, shared out over the warp's lanes
-  __device__ __forceinline__ uint64_t best_of_thread(int t, int lane, uint64_t below) const {
-    uint64_t b = 0;
-    for (int v = v0 + t + lane * kRowThreads; v < v1; v += 32 * kRowThreads) {
-      const uint64_t k = best_of(v, below);
-      if (k > b) b = k;
-    }
-    if (lane == 0 && first && t < head) {
-      const uint64_t k = entry_key(z(t), (uint32_t)t);
-      if (k < below && k > b) b = k;
-    }
-    if (lane == 0 && last && t < tailn) {
-      const uint64_t k = entry_key(z(tail0 + t), (uint32_t)(tail0 + t));
-      if (k < below && k > b) b = k;
-    }
-    return warp_max_key(b);
-  }
-  // the thread that owns entry k of this slice
-  __device__ __forceinline__ int owner(int k) const {
-    if (k < head) return k;
-    if (k >= tail0) return k - tail0;
-    return ((k - head) / V - v0) % kRowThreads;
+    if (first && w == 0 && u == 0 && lane < head) f(x(lane) * scale, lane);
+    if (last && w == kRowWarps - 1 && u == tail_unit() && lane < tailn)
+      f(x(tail0 + lane) * scale, tail0 + lane);
   }
 };
 
 struct RowShared {
   Part part[kRowWarps];
   Part total;
+  int count;
   uint64_t list[kRowWarps][kMaxAlt];
   uint64_t win[kMaxAlt];
-  uint64_t cand[kMaxAlt][kMaxAlt];
   uint64_t out[kMaxAlt];
+  // the candidates, or a list of them per winning unit (list j from j * (2 m - j + 1) / 2:
+  // unit j, j better units before it, gives at most m - j)
+  uint64_t cand[kMaxAlt * (kMaxAlt + 1) / 2];
 };
+static_assert(kRowCand <= kMaxAlt * (kMaxAlt + 1) / 2, "candidate buffer");
 
 // Merge: lane's list is get(0), get(1), ... (descending, 0 when it ends); the m
 // best of all lists, in order, are given to put(j, key) on every lane.
@@ -534,137 +584,300 @@ __device__ __forceinline__ void merge_lists(int m, Get get, Put put) {
   }
 }
 
+// Sum over the CTA, and largest value of it, in every thread.
+__device__ __forceinline__ float cta_sum(RowShared& sh, float v) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5].S = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < kRowWarps; i++) v += sh.part[i].S;
+  return v;
+}
+__device__ __forceinline__ float cta_max(RowShared& sh, float v) {
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5].S = v;
+  __syncthreads();
+  v = -INFINITY;
+  for (int i = 0; i < kRowWarps; i++) v = max_nan(v, sh.part[i].S);
+  return v;
+}
+
+// The slice once more, from memory, with its largest logit X as the reference and
+// t = c (x - X): for what the pass above does not cover: no class left, a NaN or an
+// infinity, or logits so far from 0 that c x overflows (all at the type's lowest value,
+// say).
+struct FarSums {
+  float X, S, U;
+};
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) row_long_kernel(RowArgs a, int C) {
+__device__ __noinline__ FarSums far_sums(RowArgs a, int64_t n, int rank, int C, RowShared& sh) {
+  const RowSlice<T> s(a, n, rank, C);
+  const int t = threadIdx.x;
+  const float c = a.scale * kLog2e;
+  float X = -INFINITY, S = 0.f, U = 0.f;
+  auto each = [&](auto f) {
+    if (s.first && t < s.head) f(s.x(t));
+    for (int v = s.v0 + t; v < s.v1; v += kRowThreads) {
+      float x[Vec16<T>::n];
+      Vec16<T>::unpack(load16(s.vec(v)), x);
+#pragma unroll
+      for (int e = 0; e < Vec16<T>::n; e++) f(x[e]);
+    }
+    if (s.last && t < s.tailn) f(s.x(s.tail0 + t));
+  };
+  each([&](float x) { X = max_nan(X, x); });
+  X = cta_max(sh, X);
+  const float ref = fmaxf(X, -FLT_MAX);
+  each([&](float x) {
+    const float e = fmaxf((x - ref) * c, kFloorT), y = ex2(e);
+    S += y;
+    U = fmaf(y, e, U);
+  });
+  return {X, cta_sum(sh, S), cta_sum(sh, U)};
+}
+
+// The m largest of the lanes' keys, over the whole CTA and in order, into sh.win.
+__device__ __forceinline__ void cta_top(RowShared& sh, int m, uint64_t key) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int j = 0; j < m; j++) {
+    const uint64_t best = warp_max_key(key);
+    if (lane == 0) sh.list[w][j] = best;
+    if (key == best) key = 0;
+  }
+  __syncthreads();
+  if (w == 0) {
+    if (lane == 0) sh.count = 0;
+    merge_lists(
+        m, [&](int i) { return lane < kRowWarps && i < m ? sh.list[lane][i] : 0ull; },
+        [&](int j, uint64_t k) {
+          if (lane == 0) sh.win[j] = k;
+        });
+  }
+  __syncthreads();
+}
+
+// The m best of the slice into sh.out, given each lane's largest z and that of the
+// warp's unit `lane`.
+template <typename T>
+__device__ __forceinline__ void row_alternatives(const RowSlice<T>& s, RowShared& sh, int m,
+                                                 float lane_z, float unit_z) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  cta_top(sh, m, entry_key(lane_z, (uint32_t)threadIdx.x));
+  const float least = sh.win[m - 1] ? key_z(sh.win[m - 1]) : -FLT_MAX;
+  for (uint32_t units = __ballot_sync(0xffffffffu, unit_z >= least); units; units &= units - 1)
+    s.each(w, __ffs(units) - 1, lane, [&](float z, int k) {
+      if (z >= least) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kRowCand) sh.cand[at] = entry_key(z, (uint32_t)k);
+      }
+    });
+  __syncthreads();
+  const int count = sh.count;
+  if (count <= kRowCand) {
+    if (w == 0) {
+      uint64_t last = ~0ull;
+      for (int j = 0; j < m; j++) {
+        uint64_t best = 0;
+        for (int i = lane; i < count; i += 32) {
+          const uint64_t k = sh.cand[i];
+          if (k < last && k > best) best = k;
+        }
+        last = warp_max_key(best);
+        if (lane == 0) sh.out[j] = last;
+        if (last == 0) last = 1;  // none left: nothing is below
+      }
+    }
+    return;
+  }
+  __syncthreads();  // everyone has read sh.count; the buffer is free
+  cta_top(sh, m, entry_key(unit_z, (uint32_t)threadIdx.x));
+  for (int j = w; j < m; j += kRowWarps) {
+    const int unit = (int)key_idx(sh.win[j]);
+    uint64_t* mine = sh.cand + j * (2 * m - j + 1) / 2;
+    uint64_t last = ~0ull;
+    for (int i = 0; i < m - j; i++) {
+      uint64_t best = 0;
+      if (last != 0 && sh.win[j] != 0)
+        s.each(unit >> 5, unit & 31, lane, [&](float z, int k) {
+          const uint64_t q = entry_key(z, (uint32_t)k);
+          if (q < last && q > best) best = q;
+        });
+      last = warp_max_key(best);
+      if (lane == 0) mine[i] = last;
+    }
+  }
+  __syncthreads();
+  if (w == 0)
+    merge_lists(
+        m,
+        [&](int i) {
+          return lane < m && i < m - lane ? sh.cand[lane * (2 * m - lane + 1) / 2 + i] : 0ull;
+        },
+        [&](int j, uint64_t k) {
+          if (lane == 0) sh.out[j] = k;
+        });
+}
+
+// kAlt: with alternatives.
+template <typename T, bool kAlt>
+__global__ void __launch_bounds__(kRowThreads, 4) row_long_kernel(RowArgs a, int C) {
   constexpr int V = Vec16<T>::n;
+  extern __shared__ uint4 ring[];  // [warp][stage][batch vector][lane]
   __shared__ RowShared sh;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int rank = C > 1 ? (int)sm100::cluster_ctarank() : 0;
   const int64_t clusters = gridDim.x / C;
+  const float c = a.scale * kLog2e;
+  uint4* own = ring + w * kRowStages * kRowStep + lane;
   for (int64_t n = blockIdx.x / C; n < a.N; n += clusters) {
     const RowSlice<T> s(a, n, rank, C);
-    Part p = part_empty();
-    int where = -2;  // batch of the thread's first maximum: -1 head, nb tail
-    const int nb = (s.v1 - s.v0 + kRowThreads * kRowBatch - 1) / (kRowThreads * kRowBatch);
-    auto single = [&](int k, int b) {
-      const float z = s.z(k);
-      if (z > p.R || (where == -2 && z == p.R)) where = b;
-      part_shift(p, max_nan(p.R, z));
-      const float d = fmaxf(z - p.R, kFloorD);
-      const float e = ex2(d * kLog2e);
-      p.S += e;
-      p.U = fmaf(e, d, p.U);
+    float B = -kFar, S = 0.f, U = 0.f;
+    float xm = -INFINITY;      // kAlt: the lane's largest x
+    float unit_z = -INFINITY;  // kAlt: the largest z of the warp's unit `lane`
+    bool masked = false;
+    auto raise = [&](float x) {
+      const float to = fmaxf(x * c, B);
+      sums_shift(S, U, B - to);
+      B = to;
     };
-    if (s.first && t < s.head) single(t, -1);
-    for (int b = 0; b < nb; b++) {
-      uint4 r[kRowBatch];
-      const int base = s.v0 + b * kRowThreads * kRowBatch + t;
-#pragma unroll
-      for (int j = 0; j < kRowBatch; j++) {
-        const int v = base + j * kRowThreads;
-        r[j] = v < s.v1 ? load16(s.vec(v)) : Vec16<T>::neg_inf();
+    auto unit_max = [&](float x, int u) {
+      const uint32_t b = __float_as_uint(x);
+      const uint32_t o = __reduce_max_sync(
+          0xffffffffu, b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u));
+      const float z = __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o) * a.scale;
+      xm = fmaxf(xm, x);
+      if (lane == u) unit_z = fmaxf(unit_z, z);
+    };
+    auto single = [&](bool mine, int k, int u) {
+      const float x = mine ? s.x(k) : -INFINITY;
+      if (mine) {
+        raise(x);
+        const float e = max_nan(fmaf(x, c, -B), kFloorT);
+        const float y = ex2(e);
+        S += y;
+        U = fmaf(y, e, U);
       }
-      const float zm = Vec16<T>::max_of(r) * s.scale;
-      if (zm > p.R || (where == -2 && zm == p.R)) where = b;
-      part_shift(p, max_nan(p.R, zm));
-      const F2 scale2 = f2(s.scale, s.scale), ref2 = f2(-p.R, -p.R), log2 = f2(kLog2e, kLog2e);
-      F2 S2 = f2(p.S, 0.f), U2 = f2(p.U, 0.f);
+      if (kAlt) unit_max(x, u);
+    };
+    if (s.first && w == 0 && s.head > 0) single(lane < s.head, lane, 0);
+
+    const int from = s.begin(w), to = s.begin(w + 1);
+    const int nb = (to - from + kRowStep - 1) / kRowStep;
+    const T* src = s.vec(from + lane);
+    auto fetch = [&](int b, int stage) {
+      const int left = to - from - b * kRowStep - lane;  // vector j is there if left > 32 j
+      uint4* dst = own + stage * kRowStep;
+      const T* p = src + (int64_t)b * kRowStep * V;
+#pragma unroll
+      for (int j = 0; j < kRowBatch; j++)
+        if (left > 32 * j) copy_async16(dst + 32 * j, p + j * 32 * V);
+      copy_async_commit();
+    };
+    // Adds a batch, `left` vectors of it from this lane on.  Returns its largest x.
+    auto add = [&](const uint4* batch, bool clamp, int left) {
+      const F2 c2 = f2(c, c), B2 = f2(-B, -B);
+      F2 S2 = f2(S, 0.f), U2 = f2(U, 0.f);
+      float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kRowBatch; j++) {
+        uint4 r[1] = {batch[32 * j]};
+        if (clamp && left <= 32 * j) r[0] = Vec16<T>::neg_inf();
+        if (kAlt) top = max_nan(top, Vec16<T>::max_of(r));
         float x[V];
-        Vec16<T>::unpack(r[j], x);
+        Vec16<T>::unpack(r[0], x);
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-          float d0, d1, t0, t1;
-          f2_get(f2_fma(f2(x[e], x[e + 1]), scale2, ref2), d0, d1);
-          const F2 d = f2(fmaxf(d0, kFloorD), fmaxf(d1, kFloorD));
-          f2_get(f2_mul(d, log2), t0, t1);
+          F2 tt = f2_fma(f2(x[e], x[e + 1]), c2, B2);
+          float t0, t1;
+          f2_get(tt, t0, t1);
+          if (clamp) {
+            t0 = max_nan(t0, kFloorT), t1 = max_nan(t1, kFloorT);
+            tt = f2(t0, t1);
+          }
           const F2 y = f2(ex2(t0), ex2(t1));
           S2 = f2_add(S2, y);
-          U2 = f2_fma(y, d, U2);
+          U2 = f2_fma(y, tt, U2);
         }
       }
       float s0, s1;
       f2_get(S2, s0, s1);
-      p.S = s0 + s1;
+      S = s0 + s1;
       f2_get(U2, s0, s1);
-      p.U = s0 + s1;
-    }
-    if (s.last && t < s.tailn) single(s.tail0 + t, nb);
-
-    const Part wp = part_reduce<32>(p);
-    if (lane == 0) sh.part[w] = wp;
-    if (a.m > 0) {
-      // the thread's key: its first entry equal to its maximum
-      uint64_t key = 0;
-      if (where == -1) {
-        key = entry_key(s.z(t), (uint32_t)t);
-      } else if (where == nb) {
-        key = entry_key(s.z(s.tail0 + t), (uint32_t)(s.tail0 + t));
-      } else if (where >= 0) {
-        const int base = s.v0 + where * kRowThreads * kRowBatch + t;
+      U = s0 + s1;
+      return top;
+    };
 #pragma unroll
-        for (int j = 0; j < kRowBatch; j++) {
-          const int v = base + j * kRowThreads;
-          if (v < s.v1) {
-            const uint64_t k = s.best_of(v, ~0ull);
-            if (k > key) key = k;
-          }
+    for (int b = 0; b < kRowStages; b++) fetch(b, b);
+    int stage = 0, unit = 0, in_unit = 0;
+    for (int b = 0; b < nb; b++) {
+      copy_async_wait<kRowStages - 1>();
+      const uint4* batch = own + stage * kRowStep;
+      const int left = to - from - b * kRowStep - lane;
+      const bool whole = from + (b + 1) * kRowStep <= to;
+      const float S0 = S, U0 = U;
+      float top = -INFINITY;
+      bool done = false;
+      if (b > 0 && !masked && whole) {
+        // The reference stays while the sums stay small: no maximum is needed.  A masked
+        // class gives 0 * -inf, a logit far above the others a large or infinite sum.
+        top = add(batch, false, left);
+        done = !__any_sync(0xffffffffu, !(U == U) || !(S < kLargeSum));
+        if (!done) {
+          masked = __any_sync(0xffffffffu, !(U == U) && S < kLargeSum);
+          S = S0;
+          U = U0;
         }
       }
-      for (int j = 0; j < a.m; j++) {
-        const uint64_t best = warp_max_key(key);
-        if (lane == 0) sh.list[w][j] = best;
-        if (key == best) key = 0;
+      if (!done) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kRowBatch; j++) {
+          const uint4 r[1] = {batch[32 * j]};
+          if (left > 32 * j) x = max_nan(x, Vec16<T>::max_of(r));
+        }
+        raise(x);
+        top = add(batch, true, left);
       }
+      if (kAlt) {
+        unit_max(top, unit);
+        if (++in_unit == s.per_unit) in_unit = 0, unit++;
+      }
+      fetch(b + kRowStages, stage);
+      stage = stage + 1 == kRowStages ? 0 : stage + 1;
     }
+    copy_async_wait<0>();
+    if (s.last && w == kRowWarps - 1 && s.tailn > 0)
+      single(lane < s.tailn, s.tail0 + lane, s.tail_unit());
+
+    const Part p = part_reduce<32>({B, S, U});
+    if (lane == 0) sh.part[w] = p;
     __syncthreads();
     if (w == 0) {
       Part q = lane < kRowWarps ? sh.part[lane] : part_empty();
       q = part_reduce<32>(q);
       if (lane == 0) sh.total = q;
-      if (a.m > 0)
-        merge_lists(
-            a.m,
-            [&](int i) { return lane < kRowWarps && i < a.m ? sh.list[lane][i] : 0ull; },
-            [&](int j, uint64_t k) {
-              if (lane == 0) sh.win[j] = k;
-            });
     }
     __syncthreads();
-    if (a.m > 0) {
-      const uint64_t least = sh.win[a.m - 1];
-      for (int j = w; j < a.m; j += kRowWarps) {
-        uint64_t k = sh.win[j];
-        const int owner = k ? s.owner((int)key_idx(k)) : 0;
-        int c = 0;
-        for (; c < a.m - j && k != 0 && k >= least; c++) {
-          if (lane == 0) sh.cand[j][c] = k;
-          k = s.best_of_thread(owner, lane, k);
-        }
-        if (lane == 0 && c < a.m) sh.cand[j][c] = 0;
-      }
-      __syncthreads();
-      if (w == 0)
-        merge_lists(
-            a.m, [&](int i) { return lane < a.m && i < a.m - lane ? sh.cand[lane][i] : 0ull; },
-            [&](int j, uint64_t k) {
-              if (lane == 0) sh.out[j] = k;
-            });
-    }
+    if (kAlt) row_alternatives(s, sh, a.m, xm * a.scale, unit_z);
+    const Part q = sh.total;
+    const bool near = q.S > 0.f && q.S < INFINITY && fabsf(q.B) < kNear;
+    FarSums f = {0.f, 0.f, 0.f};
+    if (!near) f = far_sums<T>(a, n, rank, C, sh);
     if (w == 0) {
       __syncwarp();
-      const Part q = sh.total;
-      const bool bad = !(q.R < INFINITY);
-      const float logS = logf(q.S);
-      if (lane == 0) write_row<T>(a, n, q, logS, bad);
-      float sel = 0.f;
-      if (a.route == 2) {
-        for (int j = 0; j < a.m; j++)
-          if (sh.out[j]) sel += expf(key_z(sh.out[j]) - q.R);
-        sel = logf(sel);
+      const RowSums sums = near ? RowSums::near(q) : RowSums::at(f.X, a.scale, f.S, f.U);
+      if (lane == 0) write_row<T>(a, n, sums);
+      if (kAlt) {
+        float sel = 0.f;
+        if (a.route == 2) {
+          for (int j = 0; j < a.m; j++)
+            if (sh.out[j]) sel += expf(sums.log_p(key_z(sh.out[j])));
+          sel = logf(sel);
+        }
+        if (lane < a.m) write_alt(a, n, lane, sh.out[lane], sums, sel);
       }
-      if (lane < a.m) write_alt(a, n, lane, sh.out[lane], q, logS, sel, bad);
     }
     __syncthreads();
   }

@@ -64,7 +64,12 @@ gmm_status rows_launch(const RowArgs& a, cudaStream_t st) {
     return api_launched(1);
   }
   const unsigned grid = (unsigned)std::min<int64_t>(a.N, 1 << 24);
-  row_long_kernel<T><<<grid, kRowThreads, 0, st>>>(a, 1);
+  constexpr int smem = kRowWarps * kRowStages * kRowStep * 16;
+  auto kern = a.m > 0 ? row_long_kernel<T, true> : row_long_kernel<T, false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return api_launched(0), GMM_ERR_CUDA;
+  kern<<<grid, kRowThreads, smem, st>>>(a, 1);
   return api_launched(1);
 }
 
