@@ -24,8 +24,8 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
-#include "rows.cuh"
 #include "sm100_prims.cuh"
+#include "vec16.cuh"
 
 namespace scem {
 

@@ -14,12 +14,11 @@
 // difference a of theirs, in a fixed order.  t is one fused multiply-add, so a
 // rounded B takes nothing from log p and H.  Everything is held in 32 bits.
 #pragma once
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <float.h>
 
 #include "common.cuh"
 #include "sm100_prims.cuh"
+#include "vec16.cuh"
 
 namespace scem {
 
@@ -45,169 +44,6 @@ struct RowArgs {
   uint32_t* flags;      // may be null
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-// Two floats in a register pair: one instruction for both.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_get(F2 p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
-}
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-// 16 bytes of a row as floats.
-template <typename T>
-struct Vec16;
-template <>
-struct Vec16<float> {
-  static constexpr int n = 4;
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&x)[4]) {
-    x[0] = __uint_as_float(r.x);
-    x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z);
-    x[3] = __uint_as_float(r.w);
-  }
-  static __device__ __forceinline__ uint4 neg_inf() {
-    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-  }
-  // the largest of kN vectors' entries, a NaN if there is one
-  template <int kN>
-  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
-    float m[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < kN; j++) {
-      m[0] = max3_nan(m[0], __uint_as_float(r[j].x), __uint_as_float(r[j].y));
-      m[1] = max3_nan(m[1], __uint_as_float(r[j].z), __uint_as_float(r[j].w));
-    }
-    return max_nan(m[0], m[1]);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-  }
-};
-template <>
-struct Vec16<__nv_bfloat16> {
-  static constexpr int n = 8;
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&x)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 neg_inf() {
-    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-  }
-  template <int kN>
-  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
-    uint32_t m = 0xff80ff80u;
-#pragma unroll
-    for (int j = 0; j < kN; j++) {
-      const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-    }
-    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec16<__half> {
-  static constexpr int n = 8;
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&x)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 neg_inf() {
-    return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
-  }
-  template <int kN>
-  static __device__ __forceinline__ float max_of(const uint4 (&r)[kN]) {
-    uint32_t m = 0xfc00fc00u;
-#pragma unroll
-    for (int j = 0; j < kN; j++) {
-      const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-    }
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
-    return max_nan(f.x, f.y);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f32(__half* p, float x) { *p = __float2half_rn(x); }
-
-__device__ __forceinline__ uint4 load16(const void* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-
 // Reference, S and U of a part of a row.
 struct Part {
   float B, S, U;
@@ -226,39 +62,38 @@ __device__ __forceinline__ void sums_shift(float& S, float& U, float a) {
   S *= f;
 }
 
-__device__ __forceinline__ Part part_merge(Part p, Part q) {
-  const float B = max_nan(p.B, q.B);
-  sums_shift(p.S, p.U, p.B - B);
-  sums_shift(q.S, q.U, q.B - B);
-  return {B, p.S + q.S, p.U + q.U};
-}
-
+// Over groups of kLanes lanes, in a fixed order.
 template <int kLanes>
 __device__ __forceinline__ Part part_reduce(Part p) {
+  float B = p.B;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) B = max_nan(B, __shfl_xor_sync(0xffffffffu, B, o));
+  sums_shift(p.S, p.U, p.B - B);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) {
-    Part q;
-    q.B = __shfl_xor_sync(0xffffffffu, p.B, o);
-    q.S = __shfl_xor_sync(0xffffffffu, p.S, o);
-    q.U = __shfl_xor_sync(0xffffffffu, p.U, o);
-    p = part_merge(p, q);
+    p.S += __shfl_xor_sync(0xffffffffu, p.S, o);
+    p.U += __shfl_xor_sync(0xffffffffu, p.U, o);
   }
-  return p;
+  return {B, p.S, p.U};
+}
+
+// Floats as unsigned integers of the same order; 0 for -inf (masked).
+__device__ __forceinline__ uint32_t float_order(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);  // -0 and +0 are equal
+  return z == -INFINITY ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_float(uint32_t o) {
+  return o == 0u ? -INFINITY : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
 // Key of an entry: larger keys are better, 0 is none.  Larger z first, then the
 // lower index; z = -inf (masked) is none.
 __device__ __forceinline__ uint64_t entry_key(float z, uint32_t idx) {
-  if (z == -INFINITY) return 0;
-  const uint32_t b = __float_as_uint(z + 0.f);  // -0 and +0 are equal
-  const uint32_t o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return ((uint64_t)o << 32) | (0xffffffffu - idx);
+  const uint32_t o = float_order(z);
+  return o == 0u ? 0ull : ((uint64_t)o << 32) | (0xffffffffu - idx);
 }
 __device__ __forceinline__ uint32_t key_idx(uint64_t k) { return 0xffffffffu - (uint32_t)k; }
-__device__ __forceinline__ float key_z(uint64_t k) {
-  const uint32_t o = (uint32_t)(k >> 32);
-  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
+__device__ __forceinline__ float key_z(uint64_t k) { return order_float((uint32_t)(k >> 32)); }
 
 __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
@@ -269,7 +104,7 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 
 // What a row's sums say.
 struct RowSums {
-  float B, L, H;     // lse = log 2 B + L, or B + L where B is a logit
+  float B, L, H;     // lse = log 2 (B + L), or B + L where B is a logit
   bool bad, empty;   // a NaN or +inf in the row; nothing but masked classes
   bool logit;
   // relative to B = about the largest c x
@@ -291,26 +126,20 @@ struct RowSums {
   }
 };
 
-// By one thread: lse, entropy and the label's log p of row n.
-template <typename T>
-__device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const RowSums& s) {
+// By one thread: lse, entropy and the log p of row n's label id, whose logit is z.
+__device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const RowSums& s, int id,
+                                          float z) {
   const float nan = __int_as_float(0x7fffffff);
   if (s.bad && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
   if (a.lse) a.lse[n] = s.bad ? nan : s.empty ? -INFINITY : s.lse();
   if (a.entropy) a.entropy[n] = s.bad ? nan : s.empty ? 0.f : s.H;
   if (a.ids) {
-    const int id = a.ids[n];
-    float lp;
-    if (id == -1) {
-      lp = 0.f;  // no label
-    } else if (id < 0 || id >= a.K) {
-      lp = nan;
-      if (a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    } else {
-      const float z = to_f32(((const T*)a.Z)[n * a.ld + id]) * a.scale;
-      lp = s.bad ? nan : z == -INFINITY ? -INFINITY : s.log_p(z);
-    }
-    a.logp[n] = lp;
+    const bool legal = id >= 0 && id < a.K;
+    if (id != -1 && !legal && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+    a.logp[n] = id == -1               ? 0.f  // no label
+                : s.bad || !legal      ? nan
+                : z == -INFINITY       ? -INFINITY
+                                       : s.log_p(z);
   }
 }
 
@@ -418,7 +247,11 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowAr
       U += __shfl_xor_sync(0xffffffffu, U, o);
     }
     const RowSums row_sums = RowSums::at(xm, a.scale, S, U);
-    if (l == 0 && live) write_row<T>(a, n, row_sums);
+    if (l == 0 && live) {
+      const int id = a.ids ? a.ids[n] : -1;
+      const bool legal = id >= 0 && id < a.K;
+      write_row(a, n, row_sums, id, legal ? to_f32(row[id]) * a.scale : 0.f);
+    }
     float sel = 0.f;
     float last_z = INFINITY;  // the entry taken last: what follows it in the order is left
     int last_k = -1;
@@ -477,19 +310,23 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowAr
 // in shared memory, kRowStages batches ahead, and reads them back itself: the loads
 // in flight cost no registers and nobody waits for anybody.
 //
-// Alternatives without a second pass over the row.  The m-th largest of the lanes'
-// maxima bounds the m-th largest entry from below, and each warp keeps the largest
-// entry of up to 32 units of consecutive batches.  Only units that reach the bound are
-// read again, and only entries that reach it are candidates: about m of them, chosen
-// from by one warp.  Where ties or masks leave more candidates than the buffer holds,
-// the m units of largest entry (which hold the m best, or m units would hold a better
+// Alternatives without a second pass over the row.  Each warp finds the Q largest of its
+// lanes' maxima (Q a little over m / 8); the m-th largest of the 8 Q is a lower bound of the
+// CTA's m-th largest entry.  Each warp also keeps the largest entry of each of its units (up to
+// kRowUnits runs of consecutive batches).  Only units that reach the bound are read again,
+// and only entries that reach it are candidates: about m of them, put in order by counting,
+// for each, how many are better.  Where ties or masks leave more candidates than the buffer
+// holds, the m units of largest entry (which hold the m best, or m units would hold a better
 // one each) give a sorted list of their best each, and those merge.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowBatch = 4;
+constexpr int kRowCtas = 4;  // resident per SM
 constexpr int kRowStages = 3;
 constexpr int kRowStep = 32 * kRowBatch;  // vectors of a warp's batch
+constexpr int kRowUnits = 32;  // per warp, at most (a lane each)
 constexpr int kRowCand = 512;
+constexpr int kRowLists = kMaxAlt / kRowWarps + 3;  // most lane maxima kept per warp
 constexpr float kLargeSum = 1048576.f;  // of a lane: its reference is raised beyond
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src)
@@ -521,16 +358,16 @@ struct RowSlice {
     const int nv = (a.K - head) / V;
     tail0 = head + nv * V;
     tailn = a.K - tail0;
-    v0 = (int)((int64_t)nv * rank / C);
-    v1 = (int)((int64_t)nv * (rank + 1) / C);
+    v0 = nv * rank / C;  // (K is at most 2^24 and C at most 8)
+    v1 = nv * (rank + 1) / C;
     const int most = (v1 - v0 + kRowWarps - 1) / kRowWarps;  // vectors of a warp
-    per_unit = max(1, (most + 32 * kRowStep - 1) / (32 * kRowStep));
+    per_unit = max(1, (most + kRowUnits * kRowStep - 1) / (kRowUnits * kRowStep));
     first = rank == 0;
     last = rank == C - 1;
   }
   // first vector of warp w's slice
   __device__ __forceinline__ int begin(int w) const {
-    return v0 + (int)((int64_t)(v1 - v0) * w / kRowWarps);
+    return v0 + (v1 - v0) * w / kRowWarps;
   }
   __device__ __forceinline__ int batches(int w) const {
     return (begin(w + 1) - begin(w) + kRowStep - 1) / kRowStep;
@@ -542,26 +379,61 @@ struct RowSlice {
   __device__ __forceinline__ const T* vec(int v) const { return row + head + (int64_t)v * V; }
   __device__ __forceinline__ float x(int k) const { return to_f32(row[k]); }
 
-  // f(z, k) for the entries of unit u of warp w, shared out over the lanes
+  // f(z, k) for the entries with z >= least of unit u of warp w, shared out over the lanes
+  // (most vectors have none)
   template <typename Fn>
-  __device__ __forceinline__ void each(int w, int u, int lane, Fn f) const {
+  __device__ __forceinline__ void each(int w, int u, int lane, float least, Fn f) const {
     const int end = min(begin(w) + (u + 1) * per_unit * kRowStep, begin(w + 1));
-    for (int v = begin(w) + u * per_unit * kRowStep + lane; v < end; v += 32) {
-      float e[V];
-      Vec16<T>::unpack(load16(vec(v)), e);
+#pragma unroll 1
+    for (int v = begin(w) + u * per_unit * kRowStep + lane; v < end; v += kRowStep) {
+      uint4 r[kRowBatch];  // all on their way before the first is looked at
 #pragma unroll
-      for (int i = 0; i < V; i++) f(e[i] * scale, head + v * V + i);
+      for (int j = 0; j < kRowBatch; j++)
+        r[j] = v + 32 * j < end ? load16(vec(v + 32 * j)) : Vec16<T>::neg_inf();
+      uint32_t hit = 0;
+#pragma unroll
+      for (int j = 0; j < kRowBatch; j++) {
+        const uint4 one[1] = {r[j]};
+        if (Vec16<T>::max_of(one) * scale >= least) hit |= 1u << j;
+      }
+#pragma unroll 1
+      for (; hit; hit &= hit - 1) {
+        const int j = __ffs(hit) - 1;
+        uint4 q = r[0];
+#pragma unroll
+        for (int i = 1; i < kRowBatch; i++)
+          if (j == i) q = r[i];
+        float e[V];
+        Vec16<T>::unpack(q, e);
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (e[i] * scale >= least) f(e[i] * scale, head + (v + 32 * j) * V + i);
+      }
     }
-    if (first && w == 0 && u == 0 && lane < head) f(x(lane) * scale, lane);
-    if (last && w == kRowWarps - 1 && u == tail_unit() && lane < tailn)
-      f(x(tail0 + lane) * scale, tail0 + lane);
+    auto single = [&](int k) {
+      const float z = x(k) * scale;
+      if (z >= least) f(z, k);
+    };
+    if (first && w == 0 && u == 0 && lane < head) single(lane);
+    if (last && w == kRowWarps - 1 && u == tail_unit() && lane < tailn) single(tail0 + lane);
   }
+};
+
+// S and U with the largest logit X as the reference: t = c (x - X).
+struct FarSums {
+  float X, S, U;
 };
 
 struct RowShared {
   Part part[kRowWarps];
   Part total;
+  FarSums far;  // with near == 0
+  int near;     // total is good
+  int id;       // the row's label and its logit
+  float id_z;
   int count;
+  float least;  // lower bound of the m-th largest z
+  uint32_t lane_top[kRowWarps * kRowLists];
   uint64_t list[kRowWarps][kMaxAlt];
   uint64_t win[kMaxAlt];
   uint64_t out[kMaxAlt];
@@ -605,12 +477,8 @@ __device__ __forceinline__ float cta_max(RowShared& sh, float v) {
 }
 
 // The slice once more, from memory, with its largest logit X as the reference and
-// t = c (x - X): for what the pass above does not cover: no class left, a NaN or an
-// infinity, or logits so far from 0 that c x overflows (all at the type's lowest value,
-// say).
-struct FarSums {
-  float X, S, U;
-};
+// t = c (x - X): for what the pass above does not cover, a NaN or an infinity, or logits so
+// far from 0 that c x overflows (all at the type's lowest value, say).
 template <typename T>
 __device__ __noinline__ FarSums far_sums(RowArgs a, int64_t n, int rank, int C, RowShared& sh) {
   const RowSlice<T> s(a, n, rank, C);
@@ -619,11 +487,19 @@ __device__ __noinline__ FarSums far_sums(RowArgs a, int64_t n, int rank, int C, 
   float X = -INFINITY, S = 0.f, U = 0.f;
   auto each = [&](auto f) {
     if (s.first && t < s.head) f(s.x(t));
-    for (int v = s.v0 + t; v < s.v1; v += kRowThreads) {
-      float x[Vec16<T>::n];
-      Vec16<T>::unpack(load16(s.vec(v)), x);
+    for (int v = s.v0 + t; v < s.v1; v += kRowBatch * kRowThreads) {
+      uint4 r[kRowBatch];
 #pragma unroll
-      for (int e = 0; e < Vec16<T>::n; e++) f(x[e]);
+      for (int j = 0; j < kRowBatch; j++)
+        r[j] = v + j * kRowThreads < s.v1 ? load16(s.vec(v + j * kRowThreads))
+                                          : Vec16<T>::neg_inf();
+#pragma unroll
+      for (int j = 0; j < kRowBatch; j++) {
+        float x[Vec16<T>::n];
+        Vec16<T>::unpack(r[j], x);
+#pragma unroll
+        for (int e = 0; e < Vec16<T>::n; e++) f(x[e]);
+      }
     }
     if (s.last && t < s.tailn) f(s.x(s.tail0 + t));
   };
@@ -638,74 +514,116 @@ __device__ __noinline__ FarSums far_sums(RowArgs a, int64_t n, int rank, int C, 
   return {X, cta_sum(sh, S), cta_sum(sh, U)};
 }
 
-// The m largest of the lanes' keys, over the whole CTA and in order, into sh.win.
-__device__ __forceinline__ void cta_top(RowShared& sh, int m, uint64_t key) {
+// The q largest of the warp's lane keys, in order, into the warp's list.
+__device__ __forceinline__ void warp_top(RowShared& sh, int q, uint64_t key) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int j = 0; j < m; j++) {
+#pragma unroll 1
+  for (int j = 0; j < q; j++) {
     const uint64_t best = warp_max_key(key);
     if (lane == 0) sh.list[w][j] = best;
     if (key == best) key = 0;
   }
+}
+
+// The m best of keys[0 .. n), different where not 0, in order into out (0 where they run out),
+// by the whole CTA: a key's place is the number of better ones.
+__device__ __forceinline__ void cta_rank(const uint64_t* keys, int n, int m, uint64_t* out) {
+  if (threadIdx.x < m) out[threadIdx.x] = 0;
   __syncthreads();
-  if (w == 0) {
-    if (lane == 0) sh.count = 0;
+  for (int i = threadIdx.x; i < n; i += kRowThreads) {
+    const uint64_t k = keys[i];
+    if (k == 0) continue;
+    int place = 0;
+#pragma unroll 2
+    for (int q = 0; q < n; q++) place += keys[q] > k;
+    if (place < m) out[place] = k;
+  }
+}
+
+// Lane maxima that a warp keeps.
+__device__ __forceinline__ int row_lists(int m) {
+  return min(m, (m + kRowWarps - 1) / kRowWarps + 3);
+}
+
+// The warp's largest lane maxima (z), any order among equal ones.
+__device__ __forceinline__ void lane_tops(RowShared& sh, int q, float z) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  uint32_t o = float_order(z);
+#pragma unroll 1
+  for (int j = 0; j < q; j++) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, o);
+    if (lane == 0) sh.lane_top[w * q + j] = best;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, o == best)) - 1) o = 0;
+  }
+}
+
+// By one warp: the m-th largest of the warps' lane maxima into sh.least.
+__device__ __forceinline__ void lane_bound(RowShared& sh, int m) {
+  const int lane = threadIdx.x & 31, n = kRowWarps * row_lists(m);
+  static_assert(kRowWarps * kRowLists <= 64, "two per lane");
+  uint32_t mine[2];
+  int above[2] = {0, 0}, equal[2] = {0, 0};
+#pragma unroll
+  for (int h = 0; h < 2; h++) mine[h] = lane + 32 * h < n ? sh.lane_top[lane + 32 * h] : 0;
+#pragma unroll 2
+  for (int i = 0; i < n; i++) {
+    const uint32_t o = sh.lane_top[i];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      above[h] += o > mine[h];
+      equal[h] += o == mine[h];
+    }
+  }
+  uint32_t found = 0;
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+    if (mine[h] != 0 && above[h] < m && m <= above[h] + equal[h]) found = mine[h];
+  found = __reduce_max_sync(0xffffffffu, found);
+  if (lane == 0) sh.least = found ? order_float(found) : -FLT_MAX;
+}
+
+// The m best of the slice into sh.out, given the bound sh.least and each lane's unit_z, the
+// largest z of the warp's unit `lane`.  Ends with a barrier.
+template <typename T>
+__device__ __forceinline__ void row_alternatives(const RowSlice<T>& s, RowShared& sh, int m,
+                                                 float unit_z) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const float least = sh.least;
+  for (uint32_t units = __ballot_sync(0xffffffffu, unit_z >= least); units; units &= units - 1)
+    s.each(w, __ffs(units) - 1, lane, least, [&](float z, int k) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kRowCand) sh.cand[at] = entry_key(z, (uint32_t)k);
+    });
+  __syncthreads();
+  const int count = sh.count;
+  if (count <= kRowCand) {
+    cta_rank(sh.cand, count, m, sh.out);
+    __syncthreads();
+    return;
+  }
+  __syncthreads();  // everyone has read the lists and the count; the buffer is free
+  warp_top(sh, m, entry_key(unit_z, (uint32_t)threadIdx.x));
+  __syncthreads();
+  if (w == 0)
     merge_lists(
         m, [&](int i) { return lane < kRowWarps && i < m ? sh.list[lane][i] : 0ull; },
         [&](int j, uint64_t k) {
           if (lane == 0) sh.win[j] = k;
         });
-  }
   __syncthreads();
-}
-
-// The m best of the slice into sh.out, given each lane's largest z and that of the
-// warp's unit `lane`.
-template <typename T>
-__device__ __forceinline__ void row_alternatives(const RowSlice<T>& s, RowShared& sh, int m,
-                                                 float lane_z, float unit_z) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  cta_top(sh, m, entry_key(lane_z, (uint32_t)threadIdx.x));
-  const float least = sh.win[m - 1] ? key_z(sh.win[m - 1]) : -FLT_MAX;
-  for (uint32_t units = __ballot_sync(0xffffffffu, unit_z >= least); units; units &= units - 1)
-    s.each(w, __ffs(units) - 1, lane, [&](float z, int k) {
-      if (z >= least) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kRowCand) sh.cand[at] = entry_key(z, (uint32_t)k);
-      }
-    });
-  __syncthreads();
-  const int count = sh.count;
-  if (count <= kRowCand) {
-    if (w == 0) {
-      uint64_t last = ~0ull;
-      for (int j = 0; j < m; j++) {
-        uint64_t best = 0;
-        for (int i = lane; i < count; i += 32) {
-          const uint64_t k = sh.cand[i];
-          if (k < last && k > best) best = k;
-        }
-        last = warp_max_key(best);
-        if (lane == 0) sh.out[j] = last;
-        if (last == 0) last = 1;  // none left: nothing is below
-      }
-    }
-    return;
-  }
-  __syncthreads();  // everyone has read sh.count; the buffer is free
-  cta_top(sh, m, entry_key(unit_z, (uint32_t)threadIdx.x));
   for (int j = w; j < m; j += kRowWarps) {
     const int unit = (int)key_idx(sh.win[j]);
-    uint64_t* mine = sh.cand + j * (2 * m - j + 1) / 2;
+    uint64_t* list = sh.cand + j * (2 * m - j + 1) / 2;
     uint64_t last = ~0ull;
     for (int i = 0; i < m - j; i++) {
       uint64_t best = 0;
       if (last != 0 && sh.win[j] != 0)
-        s.each(unit >> 5, unit & 31, lane, [&](float z, int k) {
-          const uint64_t q = entry_key(z, (uint32_t)k);
-          if (q < last && q > best) best = q;
+        s.each(unit >> 5, unit & 31, lane, -FLT_MAX, [&](float z, int k) {
+          const uint64_t key = entry_key(z, (uint32_t)k);
+          if (key < last && key > best) best = key;
         });
       last = warp_max_key(best);
-      if (lane == 0) mine[i] = last;
+      if (lane == 0) list[i] = last;
     }
   }
   __syncthreads();
@@ -718,11 +636,59 @@ __device__ __forceinline__ void row_alternatives(const RowSlice<T>& s, RowShared
         [&](int j, uint64_t k) {
           if (lane == 0) sh.out[j] = k;
         });
+  __syncthreads();
+}
+
+// What the C CTAs of a row found, joined by one warp of the first: lane r reads CTA r's
+// sums.  Parts of the same kind merge; a NaN or infinity decides the row, then logits far
+// above 0, ordinary ones, logits far below, and nothing.
+__device__ __forceinline__ uint32_t ld_cta(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
+               : "r"(sm100::map_to_rank(sm100::smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cta64(const uint64_t* p, int rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];"
+               : "=l"(v)
+               : "r"(sm100::map_to_rank(sm100::smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ RowSums join_sums(const RowShared& sh, int C, float scale) {
+  const int lane = threadIdx.x & 31;
+  const float c = scale * kLog2e;
+  Part p = part_empty();
+  FarSums f = {-INFINITY, 0.f, 0.f};
+  int kind = -1;
+  if (lane < C) {
+    if (ld_cta(&sh.near, lane)) {
+      kind = 1;
+      p = {__uint_as_float(ld_cta(&sh.total.B, lane)), __uint_as_float(ld_cta(&sh.total.S, lane)),
+           __uint_as_float(ld_cta(&sh.total.U, lane))};
+    } else {
+      f = {__uint_as_float(ld_cta(&sh.far.X, lane)), __uint_as_float(ld_cta(&sh.far.S, lane)),
+           __uint_as_float(ld_cta(&sh.far.U, lane))};
+      const float Z = f.X * scale;
+      kind = !(Z < INFINITY) ? 3 : Z == -INFINITY ? -1 : f.X > 0.f ? 2 : 0;
+    }
+  }
+  const int best = __reduce_max_sync(0xffffffffu, kind);
+  if (best == 1) return RowSums::near(part_reduce<32>(kind == 1 ? p : part_empty()));
+  if (kind != best) f = {-INFINITY, 0.f, 0.f};
+  float X = f.X;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) X = max_nan(X, __shfl_xor_sync(0xffffffffu, X, o));
+  sums_shift(f.S, f.U, (f.X - X) * c);
+  return RowSums::at(X, scale, warp_sum(f.S), warp_sum(f.U));
 }
 
 // kAlt: with alternatives.
 template <typename T, bool kAlt>
-__global__ void __launch_bounds__(kRowThreads, 4) row_long_kernel(RowArgs a, int C) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs a, int C) {
   constexpr int V = Vec16<T>::n;
   extern __shared__ uint4 ring[];  // [warp][stage][batch vector][lane]
   __shared__ RowShared sh;
@@ -731,50 +697,67 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_long_kernel(RowArgs a, int
   const int64_t clusters = gridDim.x / C;
   const float c = a.scale * kLog2e;
   uint4* own = ring + w * kRowStages * kRowStep + lane;
+  const T* from;  // the lane's first vector of the batch to copy next
+  int left;       // vectors of the warp's slice from there on
+  auto fetch_from = [&](const RowSlice<T>& s) {
+    from = s.vec(s.begin(w) + lane);
+    left = s.begin(w + 1) - s.begin(w) - lane;
+  };
+  auto fetch = [&](uint4* dst) {
+    if (left >= kRowStep) {
+#pragma unroll
+      for (int j = 0; j < kRowBatch; j++) copy_async16(dst + 32 * j, from + j * 32 * V);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRowBatch; j++)
+        if (left > 32 * j) copy_async16(dst + 32 * j, from + j * 32 * V);
+    }
+    copy_async_commit();
+    from += kRowStep * V;
+    left -= kRowStep;
+  };
+  fetch_from(RowSlice<T>(a, blockIdx.x / C, rank, C));
+#pragma unroll
+  for (int b = 0; b < kRowStages; b++) fetch(own + b * kRowStep);
   for (int64_t n = blockIdx.x / C; n < a.N; n += clusters) {
     const RowSlice<T> s(a, n, rank, C);
     float B = -kFar, S = 0.f, U = 0.f;
-    float xm = -INFINITY;      // kAlt: the lane's largest x
+    float xm = -INFINITY;      // the lane's largest x: with kAlt, or while S is 0
     float unit_z = -INFINITY;  // kAlt: the largest z of the warp's unit `lane`
     bool masked = false;
+    if (rank == 0 && t == kRowThreads - 1 && a.ids) {  // read while the row streams
+      const int id = a.ids[n];
+      sh.id = id;
+      sh.id_z = id >= 0 && id < a.K ? s.x(id) * a.scale : 0.f;
+    }
+    if (kAlt && t == 0) sh.count = 0;
     auto raise = [&](float x) {
       const float to = fmaxf(x * c, B);
       sums_shift(S, U, B - to);
       B = to;
     };
-    auto unit_max = [&](float x, int u) {
-      const uint32_t b = __float_as_uint(x);
-      const uint32_t o = __reduce_max_sync(
-          0xffffffffu, b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u));
-      const float z = __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o) * a.scale;
-      xm = fmaxf(xm, x);
+    // um: the lane's largest x in the warp's unit u, which ends here
+    auto unit_end = [&](float um, int u) {
+      const float z = order_float(__reduce_max_sync(0xffffffffu, float_order(um))) * a.scale;
+      xm = fmaxf(xm, um);
       if (lane == u) unit_z = fmaxf(unit_z, z);
     };
     auto single = [&](bool mine, int k, int u) {
       const float x = mine ? s.x(k) : -INFINITY;
       if (mine) {
         raise(x);
+        xm = fmaxf(xm, x);
         const float e = max_nan(fmaf(x, c, -B), kFloorT);
         const float y = ex2(e);
         S += y;
         U = fmaf(y, e, U);
       }
-      if (kAlt) unit_max(x, u);
+      if (kAlt) unit_end(x, u);
     };
     if (s.first && w == 0 && s.head > 0) single(lane < s.head, lane, 0);
 
-    const int from = s.begin(w), to = s.begin(w + 1);
-    const int nb = (to - from + kRowStep - 1) / kRowStep;
-    const T* src = s.vec(from + lane);
-    auto fetch = [&](int b, int stage) {
-      const int left = to - from - b * kRowStep - lane;  // vector j is there if left > 32 j
-      uint4* dst = own + stage * kRowStep;
-      const T* p = src + (int64_t)b * kRowStep * V;
-#pragma unroll
-      for (int j = 0; j < kRowBatch; j++)
-        if (left > 32 * j) copy_async16(dst + 32 * j, p + j * 32 * V);
-      copy_async_commit();
-    };
+    const int nb = s.batches(w);
+    int here = s.begin(w + 1) - s.begin(w) - lane;  // vectors from this lane's first on
     // Adds a batch, `left` vectors of it from this lane on.  Returns its largest x.
     auto add = [&](const uint4* batch, bool clamp, int left) {
       const F2 c2 = f2(c, c), B2 = f2(-B, -B);
@@ -808,78 +791,118 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_long_kernel(RowArgs a, int
       U = s0 + s1;
       return top;
     };
-#pragma unroll
-    for (int b = 0; b < kRowStages; b++) fetch(b, b);
-    int stage = 0, unit = 0, in_unit = 0;
+    int unit = 0, in_unit = s.per_unit;
+    float um = -INFINITY;
+    uint4* batch = own;
     for (int b = 0; b < nb; b++) {
       copy_async_wait<kRowStages - 1>();
-      const uint4* batch = own + stage * kRowStep;
-      const int left = to - from - b * kRowStep - lane;
-      const bool whole = from + (b + 1) * kRowStep <= to;
+      const bool whole = here + lane >= kRowStep;
       const float S0 = S, U0 = U;
       float top = -INFINITY;
       bool done = false;
-      if (b > 0 && !masked && whole) {
+      if (b > 0) {
         // The reference stays while the sums stay small: no maximum is needed.  A masked
-        // class gives 0 * -inf, a logit far above the others a large or infinite sum.
-        top = add(batch, false, left);
+        // class gives 0 * -inf (then the exponents are clamped from there on), a logit far
+        // above the others a large or infinite sum.
+        top = masked || !whole ? add(batch, true, here) : add(batch, false, here);
         done = !__any_sync(0xffffffffu, !(U == U) || !(S < kLargeSum));
         if (!done) {
-          masked = __any_sync(0xffffffffu, !(U == U) && S < kLargeSum);
+          masked |= __any_sync(0xffffffffu, !(U == U) && S < kLargeSum);
           S = S0;
           U = U0;
         }
       }
-      if (!done) {
+      if (!done || (!kAlt && S == 0.f)) {
         float x = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kRowBatch; j++) {
           const uint4 r[1] = {batch[32 * j]};
-          if (left > 32 * j) x = max_nan(x, Vec16<T>::max_of(r));
+          if (here > 32 * j) x = max_nan(x, Vec16<T>::max_of(r));
         }
-        raise(x);
-        top = add(batch, true, left);
+        xm = fmaxf(xm, x);
+        if (!done) {
+          raise(x);
+          top = add(batch, true, here);
+        }
       }
       if (kAlt) {
-        unit_max(top, unit);
-        if (++in_unit == s.per_unit) in_unit = 0, unit++;
+        um = fmaxf(um, top);
+        if (--in_unit == 0 || b == nb - 1) {
+          unit_end(um, unit++);
+          in_unit = s.per_unit;
+          um = -INFINITY;
+        }
       }
-      fetch(b + kRowStages, stage);
-      stage = stage + 1 == kRowStages ? 0 : stage + 1;
+      fetch(batch);
+      here -= kRowStep;
+      batch = batch == own + (kRowStages - 1) * kRowStep ? own : batch + kRowStep;
     }
     copy_async_wait<0>();
+    if (n + clusters < a.N) {  // the next row is on its way while this one is finished
+      fetch_from(RowSlice<T>(a, n + clusters, rank, C));
+#pragma unroll
+      for (int b = 0; b < kRowStages; b++) fetch(own + b * kRowStep);
+    }
     if (s.last && w == kRowWarps - 1 && s.tailn > 0)
       single(lane < s.tailn, s.tail0 + lane, s.tail_unit());
 
     const Part p = part_reduce<32>({B, S, U});
     if (lane == 0) sh.part[w] = p;
-    __syncthreads();
+    if (kAlt) lane_tops(sh, row_lists(a.m), xm * a.scale);
+    const bool some = __syncthreads_or(xm > -INFINITY || !(S == 0.f));
     if (w == 0) {
-      Part q = lane < kRowWarps ? sh.part[lane] : part_empty();
-      q = part_reduce<32>(q);
-      if (lane == 0) sh.total = q;
+      const Part q = part_reduce<8>(sh.part[lane % 8]);
+      if (lane == 0) {
+        sh.total = q;
+        sh.near = q.S > 0.f && q.S < INFINITY && fabsf(q.B) < kNear;
+        sh.far = {-INFINITY, 0.f, 0.f};  // every class masked
+      }
+    } else if (kAlt && w == 1) {
+      lane_bound(sh, a.m);
     }
     __syncthreads();
-    if (kAlt) row_alternatives(s, sh, a.m, xm * a.scale, unit_z);
-    const Part q = sh.total;
-    const bool near = q.S > 0.f && q.S < INFINITY && fabsf(q.B) < kNear;
-    FarSums f = {0.f, 0.f, 0.f};
-    if (!near) f = far_sums<T>(a, n, rank, C, sh);
-    if (w == 0) {
-      __syncwarp();
-      const RowSums sums = near ? RowSums::near(q) : RowSums::at(f.X, a.scale, f.S, f.U);
-      if (lane == 0) write_row<T>(a, n, sums);
-      if (kAlt) {
-        float sel = 0.f;
-        if (a.route == 2) {
-          for (int j = 0; j < a.m; j++)
-            if (sh.out[j]) sel += expf(sums.log_p(key_z(sh.out[j])));
-          sel = logf(sel);
+    if (kAlt) row_alternatives(s, sh, a.m, unit_z);
+    if (!sh.near && some) {
+      const FarSums far = far_sums<T>(a, n, rank, C, sh);
+      if (t == 0) sh.far = far;
+    }
+    const uint64_t* alt = sh.out;
+    RowSums sums;
+    if (C == 1) {
+      // (thread 0 wrote these; only its warp uses them)
+      if (w == 0) {
+        __syncwarp();
+        sums = sh.near ? RowSums::near(sh.total)
+                       : RowSums::at(sh.far.X, a.scale, sh.far.S, sh.far.U);
+      }
+    } else {
+      sm100::cluster_sync();
+      if (rank == 0) {
+        if (w == 0) sums = join_sums(sh, C, a.scale);
+        if (kAlt) {
+          for (int i = t; i < C * a.m; i += kRowThreads)
+            sh.cand[i] = ld_cta64(&sh.out[i % a.m], i / a.m);
+          __syncthreads();
+          cta_rank(sh.cand, C * a.m, a.m, sh.win);
+          __syncthreads();
+          alt = sh.win;
         }
-        if (lane < a.m) write_alt(a, n, lane, sh.out[lane], sums, sel);
       }
     }
-    __syncthreads();
+    if (rank == 0 && w == 0) {
+      if (lane == 0) write_row(a, n, sums, a.ids ? sh.id : -1, sh.id_z);
+      if (kAlt) {
+        float sel = 0.f;
+        if (a.route == 2)
+          for (int j = 0; j < a.m; j++)
+            if (alt[j]) sel += expf(sums.log_p(key_z(alt[j])));
+        if (lane < a.m) write_alt(a, n, lane, alt[lane], sums, logf(sel));
+      }
+    }
+    if (C > 1)
+      sm100::cluster_sync();  // the others' shared memory has been read
+    else
+      __syncthreads();
   }
 }
 

@@ -42,6 +42,32 @@ void short_launch(const RowArgs& a, bool vec, cudaStream_t st) {
     row_short_kernel<T, kLanes, kEl, false><<<grid, 256, 0, st>>>(a);
 }
 
+// CTAs per long row, 1, 2, 4 or 8: the fewest microseconds by a model of what was measured.  A
+// call takes `rounds` turns of the resident CTAs.  A turn is a slice at 27 or 40 GB/s a CTA, or at
+// its share of the memory bandwidth, and a fixed part: the joining of sums and alternatives,
+// dearer across a cluster, and dearer the fuller the SMs are.  (64 rows of 131,072 bf16 with
+// 20 alternatives: 20.4 us on one CTA each, 17.0 on four; 592 rows of 4,096: 10.5 on one, 77
+// on four.)
+int row_cluster(int64_t N, double row_bytes, int m, int slots) {
+#ifdef RC
+  return RC;
+#endif
+  int best = 1;
+  double best_us = 1e30;
+  for (int C = 1; C <= 8; C *= 2) {
+    if (C > 1 && row_bytes / C < 4096) break;
+    const int64_t rounds = (N * C + slots - 1) / slots;
+    const double active = (double)std::min<int64_t>(N * C, slots);
+    const double full = active / slots;
+    const double rate = std::min(m > 0 ? 27e3 : 40e3, 6.5e6 / active);  // bytes per us
+    const double join = C == 1 ? (m > 0 ? 6.0 + 0.18 * m : 3.0) * (0.7 + 0.3 * full)
+                               : (m > 0 ? 11.0 + 0.2 * m : 7.0) * (0.4 + 0.6 * full);
+    const double us = rounds * (row_bytes / C / rate + join);
+    if (us < best_us) best = C, best_us = us;
+  }
+  return best;
+}
+
 template <typename T>
 gmm_status rows_launch(const RowArgs& a, cudaStream_t st) {
   int sms = 0;
@@ -63,13 +89,24 @@ gmm_status rows_launch(const RowArgs& a, cudaStream_t st) {
       short_launch<T, 32, 32>(a, vec, st);
     return api_launched(1);
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(a.N, 1 << 24);
   constexpr int smem = kRowWarps * kRowStages * kRowStep * 16;
   auto kern = a.m > 0 ? row_long_kernel<T, true> : row_long_kernel<T, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return api_launched(0), GMM_ERR_CUDA;
-  kern<<<grid, kRowThreads, smem, st>>>(a, 1);
+  int C = row_cluster(a.N, (double)a.K * sizeof(T), a.m, kRowCtas * sms);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.N * C, kRowCtas * sms / C * C));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, a, C) != cudaSuccess) return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
 
