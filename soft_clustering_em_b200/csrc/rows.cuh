@@ -143,13 +143,14 @@ __device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const Row
   }
 }
 
-// Alternative j of row n (key 0: none); sel: log of the m chosen classes' probability.
-__device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, uint64_t key,
+// Alternative j of row n: class k (-1: none) at z; sel: log of the m chosen classes'
+// probability.
+__device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, int k, float z,
                                           const RowSums& s, float sel) {
   const float nan = __int_as_float(0x7fffffff);
-  const bool none = s.bad || key == 0;
-  a.top_idx[n * a.m + j] = none ? -1 : (int32_t)key_idx(key);
-  const float lp = s.log_p(key_z(key));
+  const bool none = s.bad || k < 0;
+  a.top_idx[n * a.m + j] = none ? -1 : k;
+  const float lp = s.log_p(z);
   float v;
   if (a.route == 0)
     v = s.bad ? nan : none ? -INFINITY : lp;
@@ -165,7 +166,8 @@ __device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, ui
 //
 // Alternatives in m rounds.  Only each vector's largest entry stays in registers;
 // a round finds the lowest vector that holds the row's largest, reads it again
-// (it is in L1) and leaves it with its largest entry behind the one just taken.
+// (it is in L1), an entry per lane, and leaves it with its largest entry behind the
+// one just taken.
 template <typename T, bool kVec>
 __device__ __forceinline__ uint4 load_row_vec(const T* row, int k0, int K) {
   constexpr int V = Vec16<T>::n;
@@ -181,8 +183,34 @@ __device__ __forceinline__ uint4 load_row_vec(const T* row, int k0, int K) {
   return u.r;
 }
 
+// Over groups of kLanes lanes.
+template <int kLanes>
+__device__ __forceinline__ float group_max(float v) {
+  if constexpr (kLanes == 32) {
+    return order_float(__reduce_max_sync(0xffffffffu, float_order(v)));
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int kLanes>
+__device__ __forceinline__ int group_min(int v) {
+  if constexpr (kLanes == 32) {
+    return __reduce_min_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int kLanes>
+__device__ __forceinline__ uint32_t group_mask() {
+  return kLanes == 32 ? 0xffffffffu : (1u << (kLanes & 31)) - 1u;
+}
+
 template <typename T, int kLanes, int kEl, bool kVec>
-__global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowArgs a) {
+__global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 5) row_short_kernel(RowArgs a) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
   constexpr int kChunks = kEl / V;
@@ -257,47 +285,45 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 4) row_short_kernel(RowAr
     int last_k = -1;
     for (int j0 = 0; j0 < a.m; j0 += kLanes) {
       const int cnt = min(kLanes, a.m - j0);
-      uint64_t mine = 0;  // lane l keeps alternative j0 + l
+      float mine_z = -INFINITY;  // lane l keeps alternative j0 + l
+      int mine_k = -1;
+#pragma unroll 1
       for (int j = 0; j < cnt; j++) {
         float best = top[0];
 #pragma unroll
         for (int c = 1; c < kChunks; c++) best = fmaxf(best, top[c]);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        best = group_max<kLanes>(best);
         int at = 1 << 30;  // the lowest vector that holds it
 #pragma unroll
         for (int c = kChunks - 1; c >= 0; c--)
           if (top[c] == best) at = c * kLanes + l;
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-          at = min(at, __shfl_xor_sync(0xffffffffu, at, o));
+        at = group_min<kLanes>(at);
         const bool none = best == -INFINITY || at == 1 << 30;
-        const int k0 = none ? 0 : at * V;
-        float x[V];
-        Vec16<T>::unpack(load_row_vec<T, kVec>(row, k0, a.K), x);
-        int e0 = 0;
-#pragma unroll
-        for (int e = V - 1; e >= 0; e--) {
-          x[e] *= a.scale;
-          if (x[e] == best && (best < last_z || k0 + e > last_k)) e0 = e;
-        }
-        float next = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < V; e++)
-          if (x[e] < best || (x[e] == best && e > e0)) next = fmaxf(next, x[e]);
+        // lane e looks at entry e of it
+        const int k = none ? 0 : at * V + l;
+        const float z = l < V && !none && k < a.K ? to_f32(row[k]) * a.scale : -INFINITY;
+        const uint32_t equal = __ballot_sync(
+            0xffffffffu, z == best && (best < last_z || k > last_k) && !none);
+        const int first = __ffs((equal >> (lane - l)) & group_mask<kLanes>()) - 1;
+        const float next =
+            group_max<(V < kLanes ? V : kLanes)>(z < best || (z == best && l > first)
+                                                     ? z
+                                                     : -INFINITY);
+        // (lanes V and up reduced among themselves: the vector's owner asks lane 0 of the group)
+        const float left = __shfl_sync(0xffffffffu, next, lane - l);
 #pragma unroll
         for (int c = 0; c < kChunks; c++)
-          if (at == c * kLanes + l) top[c] = next;
+          if (at == c * kLanes + l) top[c] = left;
         last_z = best;
-        last_k = k0 + e0;
-        if (!none) {
-          sel += ex2(row_sums.log_p(best) * kLog2e);
-          if (l == j) mine = entry_key(best, (uint32_t)last_k);
+        last_k = none ? last_k : at * V + first;
+        if (l == j && !none) {
+          mine_z = best;
+          mine_k = last_k;
         }
+        if (a.route == 2 && !none) sel += ex2(row_sums.log_p(best) * kLog2e);
       }
       if (l < cnt && live)
-        write_alt(a, n, j0 + l, mine, row_sums, a.route == 2 ? logf(sel) : 0.f);
+        write_alt(a, n, j0 + l, mine_k, mine_z, row_sums, a.route == 2 ? logf(sel) : 0.f);
     }
   }
 }
@@ -896,7 +922,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
         if (a.route == 2)
           for (int j = 0; j < a.m; j++)
             if (alt[j]) sel += expf(sums.log_p(key_z(alt[j])));
-        if (lane < a.m) write_alt(a, n, lane, alt[lane], sums, logf(sel));
+        if (lane < a.m)
+          write_alt(a, n, lane, alt[lane] ? (int)key_idx(alt[lane]) : -1, key_z(alt[lane]), sums,
+                    logf(sel));
       }
     }
     if (C > 1)
