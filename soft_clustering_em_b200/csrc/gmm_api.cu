@@ -745,6 +745,7 @@ void sample_rows(int64_t N, int K, uint64_t seed, std::vector<int64_t>* rows) {
 namespace scem {
 gmm_status api_launched(int n) { return launched(n); }
 gmm_status api_device_sms(int* sms) { return device_sms(sms); }
+uint64_t api_wait_budget() { return g_wait_budget_ns.load(); }
 }  // namespace scem
 
 extern "C" {

@@ -6,19 +6,27 @@
 // where W_up[e] (2F x D) stacks W_gate over W_lin and W_down[e] is D x F.
 //
 // With few tokens the layer is bound by reading the chosen experts' weights
-// (3 D F elements each) once: an expert's tokens, 8 at a time, are the columns of
-// one warp-level matrix product, so every weight read is used for all of them.
-// The weights go straight from global memory to the fragments of the
-// m16n8k16 product: a contraction may run over its index in any order, so a
-// thread takes 8 consecutive elements of a row (16 bytes) as its share of two
-// k-steps, and the same 8 of its token.  There is nothing for shared memory to
-// rearrange, and tensor memory with its 128-row tiles would only add latency to
-// a kernel whose products take a few percent of its time.
+// (3 D F elements each) once.  Both kernels are a stream of jobs on one CTA per SM: 128
+// weight rows of one expert against up to kN of its tokens, on the tensor cores.  The
+// weights are the M operand (rows of the tile), the tokens the N operand, accumulators
+// in tensor memory, two of them in turn.  The warps have a part each:
+//   - four copy weight tiles and, four rows at a time (gather4), the tokens' elements by TMA
+//     into a ring of stages of 64 along K (mostly eight, 16 KB of weights each: about 130 KB
+//     per SM on their way at any time, on across the jobs);
+//   - four issue the products, each into an accumulator of its own;
+//   - four take finished accumulators out of tensor memory and add them up.
+// One thread alone takes about 600 cycles to issue a stage's copies and as many for its
+// products, twice what the memory needs to deliver it, so warps take the stages in turn.
+// (Gathering the tokens with loads instead costs a proxy fence per stage, which waits for
+// every copy of the thread: a microsecond.)
+// A 128-row tile may be partly filled, and columns may be empty: what stands there from
+// before only reaches results that nobody takes.
 //
-// Kernel 1 (up) writes h for every (token, choice) into the workspace; kernel 2
-// (down) forms y.  Both sort the T * m choices by expert in shared memory first.
-// h is kept as two halves of the weights' type, hi + lo, so that rounding it
-// adds nothing visible to y.
+// Kernel 1 (up) holds 64 rows of W_gate over the same 64 rows of W_lin in a tile and
+// writes h for every (token, choice) into the workspace; kernel 2 (down) forms y, summing
+// a token's experts in shared memory, in ascending order.  h is kept as two halves of
+// the weights' type, hi + lo, so that rounding it adds nothing visible to y: its products
+// are two passes over the same weight stage.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,121 +40,145 @@ namespace scem {
 constexpr int kMoeMaxT = 256;
 constexpr int kMoeMaxE = 1024;
 constexpr int kMoeMaxSlots = kMoeMaxT * kMaxTopM;
-constexpr int kMoeThreads = 256;
-constexpr int kMoeWarps = kMoeThreads / 32;
-constexpr int kMoeRows = 16;  // weight rows per tile
+constexpr int kMoeCopyWarps = 4, kMoeMmaWarps = 4;
+constexpr int kMoeThreads = (4 + kMoeCopyWarps + kMoeMmaWarps) * 32;
+constexpr int kMoeTile = 128;     // weight rows of a job
+constexpr int kMoeK = 64;         // elements along K of a stage
+constexpr int kMoeAccCols = 64;   // of an accumulator, at most
+constexpr int kMoeTmemCols = 2 * kMoeMmaWarps * kMoeAccCols;
+constexpr uint64_t kMoeDrainNs = 1000000000ull;
 
 struct MoeArgs {
-  const void *X, *W_up, *W_down;
   void* Y;
   const int32_t* idx;
   const float* resp;
   void *h_hi, *h_lo;  // T * m x F
   int T, m, E, D, F;
-  int64_t ldx, ldy;
+  int64_t ldy;
   int act;
-  int row_blocks;  // down: blocks of rows of y
+  int ring_bytes;  // shared memory of the stages
+  uint64_t wait_ns;
   unsigned int* status;
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1, __nv_bfloat16) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1, __half) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Both k-steps of 8 elements per thread: rows g (lo) and g + 8 (hi) of the
-// weights against column g of the tokens.
-template <typename T>
-__device__ __forceinline__ void mma_k32(float (&c)[4], const uint4& lo, const uint4& hi,
-                                        const uint4& b) {
-  mma_16816(c, lo.x, hi.x, lo.y, hi.y, b.x, b.y, T());
-  mma_16816(c, lo.z, hi.z, lo.w, hi.w, b.z, b.w, T());
-}
-
-__device__ __forceinline__ uint4 zero16() { return make_uint4(0, 0, 0, 0); }
-
 // The T * m choices sorted by expert: active experts a = 0..n-1 in ascending
-// order, act[a] the expert, its choices slot[off[a] .. off[a+1]).  A choice that
-// repeats an expert within its token is left out; its weight counts with the
-// first one.  The order inside an expert is free: it only decides the column of
-// a product.
+// order, act[a] the expert, its choices slot[off[a] .. off[a+1]) with their weights.  A
+// choice that repeats an expert within its token is left out; its weight counts with the
+// first one.  The order inside an expert is free: it only decides the column of a product.
 struct MoeLists {
-  int cnt[kMoeMaxE];
-  uint16_t act[kMoeMaxE];
-  uint16_t off[kMoeMaxE + 1];
-  uint16_t slot[kMoeMaxSlots];
-  int warp_n[kMoeWarps], warp_a[kMoeWarps];
-  int n;
+  uint16_t *act, *off, *slot;
+  float* gate;
+  int warp_n[8], warp_a[8], warp_most[8];
+  int n;     // active experts
+  int most;  // choices of the busiest
+  uint32_t inv_m;
+  // slot / m: exact for slots below 2^11 and m up to 8 with inv_m = ceil(2^16 / m)
+  __device__ __forceinline__ int token(int slot) const { return (int)(slot * inv_m >> 16); }
 };
 
-// The expert of choice i, or -1: unused, out of range, or repeated.
-__device__ __forceinline__ int moe_expert(const MoeArgs& a, int i) {
-  const int e = a.idx[i];
-  if (e < 0 || e >= a.E) return -1;
-  for (int q = i - i % a.m; q < i; q++)
-    if (a.idx[q] == e) return -1;
-  return e;
+// Bytes of the lists behind the struct, and their places.
+__host__ __device__ constexpr int moe_list_bytes(int E, int slots) {
+  return (E * 2 + (E + 2) * 2 + slots * 2 + slots * 4 + 3 * 16 + 255) / 256 * 256;
+}
+__device__ __forceinline__ void moe_place_lists(MoeLists& L, char* at, int E, int slots) {
+  L.gate = (float*)at;
+  at += (slots * 4 + 15) / 16 * 16;
+  L.act = (uint16_t*)at;
+  at += (E * 2 + 15) / 16 * 16;
+  L.off = (uint16_t*)at;
+  L.slot = L.off + E + 2;
 }
 
-__device__ __forceinline__ void moe_sort(const MoeArgs& a, MoeLists& L) {
-  constexpr int kPer = kMoeMaxE / kMoeThreads;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = a.T * a.m;
-  for (int e = tid; e < kMoeMaxE; e += kMoeThreads) L.cnt[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += kMoeThreads) {
-    const int e = moe_expert(a, i);
-    if (e >= 0) atomicAdd(&L.cnt[e], 1);
+// By the first 256 threads, a token each; the whole CTA calls it.  cnt: kMoeMaxE ints of shared
+// memory.
+__device__ __forceinline__ void moe_sort(const MoeArgs& a, MoeLists& L, int* cnt) {
+  constexpr int kThreads = 256, kPer = kMoeMaxE / kThreads;
+  static_assert(kMoeMaxT <= kThreads, "a token per thread");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  int e[kMaxTopM];
+  float gate[kMaxTopM];
+#pragma unroll
+  for (int q = 0; q < kMaxTopM; q++) {  // all on their way at once
+    const bool mine = tid < a.T && q < a.m;
+    e[q] = mine ? __ldcg(a.idx + tid * a.m + q) : -1;
+    gate[q] = mine ? __ldcg(a.resp + tid * a.m + q) : 0.f;
+  }
+  for (int i = tid; i < kMoeMaxE; i += kMoeThreads) cnt[i] = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxTopM; q++) {
+    if (e[q] >= a.E) e[q] = -1;
+#pragma unroll
+    for (int r = 0; r < q; r++)
+      if (e[q] >= 0 && e[r] == e[q]) {
+        gate[r] += gate[q];
+        e[q] = -1;
+      }
   }
   __syncthreads();
-  int c[kPer], sum = 0, act = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    c[i] = L.cnt[tid * kPer + i];
-    sum += c[i];
-    act += c[i] > 0;
-  }
-  int xs = sum, xa = act;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int ys = __shfl_up_sync(0xffffffffu, xs, o), ya = __shfl_up_sync(0xffffffffu, xa, o);
-    if (lane >= o) xs += ys, xa += ya;
-  }
-  if (lane == 31) L.warp_n[w] = xs, L.warp_a[w] = xa;
+  for (int q = 0; q < kMaxTopM; q++)
+    if (e[q] >= 0) atomicAdd(&cnt[e[q]], 1);
   __syncthreads();
-  xs -= sum;
-  xa -= act;
-  for (int q = 0; q < w; q++) xs += L.warp_n[q], xa += L.warp_a[q];
+  int c[kPer], sum = 0, act = 0, most = 0, xs = 0, xa = 0;
+  if (tid < kThreads) {
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    L.cnt[tid * kPer + i] = xs;
-    if (c[i]) {
-      L.act[xa] = (uint16_t)(tid * kPer + i);
-      L.off[xa++] = (uint16_t)xs;
+    for (int i = 0; i < kPer; i++) {
+      c[i] = cnt[tid * kPer + i];
+      sum += c[i];
+      act += c[i] > 0;
+      most = max(most, c[i]);
     }
-    xs += c[i];
-  }
-  if (tid == kMoeThreads - 1) {
-    L.n = xa;
-    L.off[xa] = (uint16_t)xs;
+    xs = sum;
+    xa = act;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ys = __shfl_up_sync(0xffffffffu, xs, o), ya = __shfl_up_sync(0xffffffffu, xa, o);
+      if (lane >= o) xs += ys, xa += ya;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) L.warp_n[w] = xs, L.warp_a[w] = xa, L.warp_most[w] = most;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kMoeThreads) {
-    const int e = moe_expert(a, i);
-    if (e >= 0) L.slot[atomicAdd(&L.cnt[e], 1)] = (uint16_t)i;
+  if (tid < kThreads) {
+    xs -= sum;
+    xa -= act;
+#pragma unroll
+    for (int q = 0; q < kThreads / 32; q++)
+      if (q < w) xs += L.warp_n[q], xa += L.warp_a[q];
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      cnt[tid * kPer + i] = xs;
+      if (c[i]) {
+        L.act[xa] = (uint16_t)(tid * kPer + i);
+        L.off[xa++] = (uint16_t)xs;
+      }
+      xs += c[i];
+    }
+    if (tid == kThreads - 1) {
+      L.n = xa;
+      L.inv_m = (65536u + a.m - 1) / a.m;
+      L.off[xa] = (uint16_t)xs;
+      for (int q = 0; q < kThreads / 32; q++) most = max(most, L.warp_most[q]);
+      L.most = most;
+    }
   }
   __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kMaxTopM; q++)
+    if (e[q] >= 0) {
+      const int at = atomicAdd(&cnt[e[q]], 1);
+      L.slot[at] = (uint16_t)(tid * a.m + q);
+      L.gate[at] = gate[q];
+    }
+  __syncthreads();
+}
+
+// Instruction descriptor of a 128 x n product, both operands K-major.
+__device__ __forceinline__ uint32_t moe_idesc(__nv_bfloat16, int n) {
+  return sm100::idesc_bf16_f32(128, n, false, false);
+}
+__device__ __forceinline__ uint32_t moe_idesc(__half, int n) {
+  return sm100::idesc_f16_f32(128, n, false, false);
 }
 
 __device__ __forceinline__ float moe_act(float x, int act) {
@@ -158,240 +190,489 @@ __device__ __forceinline__ float moe_act(float x, int act) {
   return x / (1.f + expf(-x));
 }
 
-// ------------------------------------------------------------------ up
-// The active experts' F rows are laid end to end and cut evenly over the CTAs,
-// to the row; a CTA takes its range in tiles of up to 16 rows of one expert.  The
-// warps split D, so a CTA reads 512 bytes in a row of each weight row at a time.
-template <typename T, int kNT, int kU>
-__device__ __forceinline__ void up_product(const MoeArgs& a, const T* gate, const T* lin, int rows,
-                                           const int64_t (&xoff)[kNT], float (&acc)[2][kNT][4]) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const T* X = (const T*)a.X;
-  const int64_t r0 = (int64_t)g * a.D, r1 = (int64_t)(g + 8) * a.D;
-  const bool ok0 = g < rows, ok1 = g + 8 < rows;
-  for (int k0 = w * 32 + t * 8; k0 < a.D + t * 8; k0 += kMoeWarps * 32 * kU) {
-    uint4 A[kU][4], B[kU][kNT];
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      const int k = k0 + u * kMoeWarps * 32;
-      const bool in = k < a.D;
-      A[u][0] = in && ok0 ? __ldg((const uint4*)(gate + r0 + k)) : zero16();
-      A[u][1] = in && ok1 ? __ldg((const uint4*)(gate + r1 + k)) : zero16();
-      A[u][2] = in && ok0 ? __ldg((const uint4*)(lin + r0 + k)) : zero16();
-      A[u][3] = in && ok1 ? __ldg((const uint4*)(lin + r1 + k)) : zero16();
-#pragma unroll
-      for (int q = 0; q < kNT; q++)
-        B[u][q] = in && xoff[q] >= 0 ? load16(X + xoff[q] + k) : zero16();
-    }
-#pragma unroll
-    for (int u = 0; u < kU; u++)
-#pragma unroll
-      for (int q = 0; q < kNT; q++) {
-        mma_k32<T>(acc[0][q], A[u][0], A[u][1], B[u][q]);
-        mma_k32<T>(acc[1][q], A[u][2], A[u][3], B[u][q]);
-      }
+// One job.  Up: rows f0 .. f0 + rows of the expert's F, of which every active expert has `per`
+// units of `size` rows; the units are shared out evenly, and up to 64 rows of consecutive ones
+// make a job.  Down: the CTA's block of rows of y,
+// one active expert after the other (every stride-th).
+template <bool kDown, int kN>
+struct MoeJob {
+  int act, f0, rows, s0, ntok;
+  int unit, end, per, size;  // up
+  int stride;          // down: CTAs of the cluster
+
+  __device__ __forceinline__ bool more(const MoeLists& L) const {
+    if constexpr (kDown) return act < L.n;
+    return unit < end;
   }
+  __device__ __forceinline__ void tokens(const MoeLists& L) {
+    ntok = min(kN, L.off[act + 1] - s0);
+  }
+  __device__ __forceinline__ void fit(const MoeArgs& a, const MoeLists& L) {
+    if constexpr (!kDown) {
+      act = unit / per;
+      f0 = (unit - act * per) * size;
+      rows = min(min(64, a.F - f0), (end - unit) * size);
+    }
+    s0 = L.off[act];
+    tokens(L);
+  }
+  __device__ __forceinline__ void next(const MoeArgs& a, const MoeLists& L) {
+    s0 += kN;
+    if (s0 < L.off[act + 1]) return tokens(L);
+    if constexpr (kDown)
+      act += stride;
+    else
+      unit += (rows + size - 1) / size;
+    if (more(L)) fit(a, L);
+  }
+};
+
+struct MoeBarriers {
+  uint64_t full[16], empty[16];  // per stage
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drained;
+  unsigned int abort;  // a wait of this CTA gave up
+  uint32_t tmem;
+};
+
+// Shared memory: the two structs, the lists; up: 2 x 128 x 33 floats, down: T x 128
+// floats; the
+// stages on a 1024-byte boundary.
+constexpr int kMoeStructs =
+    (int)((sizeof(MoeLists) + 255) / 256 * 256 + (sizeof(MoeBarriers) + 255) / 256 * 256);
+__host__ __device__ constexpr int moe_fixed(int E, int slots) {
+  return kMoeStructs + moe_list_bytes(E, slots);
+}
+constexpr int kMoeSwap = 2 * kMoeTile * 33 * 4;
+__host__ __device__ constexpr int moe_stage_bytes(bool down, int kN) {
+  return kMoeTile * 128 + (down ? 2 : 1) * kN * 128;
 }
 
-template <typename T, int kNT, int kU>
-__device__ __forceinline__ void up_tile(const MoeArgs& a, int e, int f0, int rows,
-                                        const uint16_t* slot, int ntok, float* red) {
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2;
-  const T* gate = (const T*)a.W_up + ((int64_t)e * 2 * a.F + f0) * a.D;
-  const T* lin = gate + (int64_t)a.F * a.D;
-  int64_t xoff[kNT];
-#pragma unroll
-  for (int q = 0; q < kNT; q++) {
-    const int col = q * 8 + g;
-    xoff[q] = col < ntok ? (int64_t)(slot[col] / a.m) * a.ldx : -1;
-  }
-  float acc[2][kNT][4];
-#pragma unroll
-  for (int q = 0; q < kNT; q++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) acc[0][q][i] = acc[1][q][i] = 0.f;
-  up_product<T, kNT, kU>(a, gate, lin, rows, xoff, acc);
-  // sum over the warps' shares of D, in warp order
-  constexpr int kHalf = kNT * 128;
-#pragma unroll
-  for (int s = 0; s < 2; s++)
-#pragma unroll
-    for (int q = 0; q < kNT; q++)
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        red[(w * 2 + s) * kHalf + (q * 4 + i) * 32 + lane] = acc[s][q][i];
-  __syncthreads();
-  for (int o = tid; o < kHalf; o += kMoeThreads) {
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int v = 0; v < kMoeWarps; v++) {
-      x += red[(v * 2) * kHalf + o];
-      y += red[(v * 2 + 1) * kHalf + o];
+// Bounded wait on a phase, as mbar_wait_bounded, for waits on the path of every stage: the
+// clock is read only after some tries (reading it takes longer than most waits).  kSleep:
+// nanoseconds between tries, for waits whose polling would slow down the others'.
+template <int kSleep = 0>
+__device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity,
+                                         volatile unsigned int* abort, uint64_t budget_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; i++) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if ((i & 31) == 31) {
+      if (*abort & GMM_DEVFLAG_WAIT_TIMEOUT) return false;
+      const uint64_t now = sm100::globaltimer_ns();
+      if (i == 31) {
+        t0 = now;
+      } else if (now - t0 > budget_ns) {
+        atomicOr(const_cast<unsigned int*>(abort), GMM_DEVFLAG_WAIT_TIMEOUT);
+        return false;
+      }
     }
-    const int ol = o & 31, i = (o >> 5) & 3, q = o >> 7;
-    const int row = (ol >> 2) + (i >> 1) * 8, col = q * 8 + (ol & 3) * 2 + (i & 1);
-    if (row < rows && col < ntok) {
-      const float h = moe_act(x, a.act) * y;
-      const int64_t at = (int64_t)slot[col] * a.F + f0 + row;
-      T hi, lo;
-      from_f32(&hi, h);
-      const float left = h - to_f32(hi);
-      from_f32(&lo, isfinite(left) ? left : 0.f);  // h beyond the type's range stays infinite
-      ((T*)a.h_hi)[at] = hi;
-      ((T*)a.h_lo)[at] = lo;
-    }
-  }
-  __syncthreads();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_up_kernel(MoeArgs a) {
-  __shared__ MoeLists L;
-  __shared__ float red[kMoeWarps * 2 * 4 * 128];
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.T * a.m; i += kMoeThreads)
-      if (a.idx[i] < -1 || a.idx[i] >= a.E) atomicOr(a.status, GMM_DEVFLAG_BAD_INDEX);
-  moe_sort(a, L);
-  const int64_t all = (int64_t)L.n * a.F;
-  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
-  int64_t r = all * blockIdx.x / gridDim.x;
-  while (r < end) {
-    const int act = (int)(r / a.F), f0 = (int)(r - (int64_t)act * a.F);
-    const int rows = (int)min((int64_t)min(kMoeRows, a.F - f0), end - r);
-    const int e = L.act[act];
-    for (int s0 = L.off[act]; s0 < L.off[act + 1];) {
-      const int left = L.off[act + 1] - s0;
-      const uint16_t* slot = L.slot + s0;
-      if (left <= 8)
-        up_tile<T, 1, 4>(a, e, f0, rows, slot, left, red);
-      else if (left <= 16)
-        up_tile<T, 2, 2>(a, e, f0, rows, slot, left, red);
-      else
-        up_tile<T, 4, 2>(a, e, f0, rows, slot, min(left, 32), red);
-      s0 += left <= 8 ? 8 : left <= 16 ? 16 : 32;
-    }
-    r += rows;
+    if (kSleep) __nanosleep(kSleep);
   }
 }
+// The same by a warp's first lane for the warp.
+template <int kSleep = 0>
+__device__ __forceinline__ bool moe_warp_wait(uint64_t* bar, uint32_t parity,
+                                              volatile unsigned int* abort, uint64_t budget_ns) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = moe_wait<kSleep>(bar, parity, abort, budget_ns);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // every lane sees the phase itself, for the order of what it reads next
+  return ok && (sm100::mbar_try_wait(bar, parity) || moe_wait(bar, parity, abort, budget_ns));
+}
 
-// ------------------------------------------------------------------ down
-// A cluster owns a block of up to 16 rows of y for every token.  Its warps share
-// out (expert, slice of F) units; a warp adds each unit's weighted product to
-// its own copy of the block, and the copies are summed in warp and CTA order, so
-// no addition depends on timing.
-template <typename T, int kNT, int kU>
-__device__ __forceinline__ void down_unit(const MoeArgs& a, int e, int d0, int rows, int c0, int c1,
-                                          const uint16_t* slot, int ntok, float* y) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const T* W = (const T*)a.W_down + ((int64_t)e * a.D + d0) * a.F;
-  const int64_t r0 = (int64_t)g * a.F, r1 = (int64_t)(g + 8) * a.F;
-  const bool ok0 = g < rows, ok1 = g + 8 < rows;
-  int64_t hoff[kNT];
+__host__ __device__ constexpr int moe_stages(int ring_bytes, bool down, int kN) {
+  const int s = ring_bytes / moe_stage_bytes(down, kN) / kMoeCopyWarps * kMoeCopyWarps;
+  return s < 16 ? s : 16;
+}
+static_assert(kMoeCopyWarps % kMoeMmaWarps == 0, "a stage has one warp of each kind");
+
+// Four rows of a matrix (a tensor map with a box of one row) at column k, one below the other.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int k, int4 rows,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(sm100::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+// Rows [row, row + rows) of a weight matrix at column k: boxes of 64 and of 16 rows.
+__device__ __forceinline__ void moe_load_rows(char* dst, const CUtensorMap* tm64,
+                                              const CUtensorMap* tm16, int k, int row, int rows,
+                                              uint64_t* bar) {
+  int r = 0;
+  for (; r + 64 <= rows; r += 64) sm100::tma_load_2d(dst + r * 128, tm64, k, row + r, bar);
+  for (; r < rows; r += 16) sm100::tma_load_2d(dst + r * 128, tm16, k, row + r, bar);
+}
+__device__ __forceinline__ int moe_box_rows(int rows) { return (rows + 15) / 16 * 16; }
+
+template <typename T, bool kDown, int kN>
+__device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, MoeBarriers& bar,
+                                           MoeJob<kDown, kN> job, char* ring, float* side,
+                                           const CUtensorMap* tm64, const CUtensorMap* tm16,
+                                           const CUtensorMap* tok0, const CUtensorMap* tok1) {
+  using namespace sm100;
+  constexpr int kH = kDown ? 2 : 1;  // halves of a token: x, or h hi and lo
+  constexpr int kStage = moe_stage_bytes(kDown, kN);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int K = kDown ? a.F : a.D, steps = (K + kMoeK - 1) / kMoeK;
+  // Stages: a multiple of the warps that take them in turn, so that a stage always belongs to
+  // the same copying and the same multiplying warp.  (A wait on a phase by its parity means that
+  // phase only while the phase before is known to be over.)
+  const int S = moe_stages(a.ring_bytes, kDown, kN);
+  volatile unsigned int* abort = &bar.abort;
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return moe_wait(b, parity, abort, a.wait_ns);
+  };
+  // Step s of the stream uses stage s % S for the (s / S)-th time.  A warp takes every kTurns-th
+  // step; `at` is its next one.
+  int at = 0, stage = 0;
+  uint32_t parity = 0;
+  auto advance = [&](int turns) {
+    at += turns;
+    for (stage += turns; stage >= S; stage -= S) parity ^= 1u;
+  };
+
+  if (w >= 4 && w < 4 + kMoeCopyWarps) {
+    // ---- copies: lane 0 the weights, lane l token rows 4 l .. (down: the hi, then the lo rows)
+    static_assert(kH * kN / 4 <= 32, "a lane for four token rows");
+    bool ok = true;
+    int4 from;  // lane l's rows 4 l .. of the stage, of them kN / 4 lanes for each half
+    bool mine4 = false;
+    auto aim = [&](const MoeJob<kDown, kN>& j) {
+      const int col = lane * 4 % kN;
+      mine4 = lane * 4 < kH * kN && col < j.ntok;
+      int r[4];
 #pragma unroll
-  for (int q = 0; q < kNT; q++) hoff[q] = q * 8 + g < ntok ? (int64_t)slot[q * 8 + g] * a.F : -1;
-  float acc[kNT][4];
-#pragma unroll
-  for (int q = 0; q < kNT; q++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) acc[q][i] = 0.f;
-  for (int c = c0; c < c1; c += kU) {
-    uint4 A[kU][2], B[kU][kNT][2];
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      const int k = (c + u) * 32 + t * 8;
-      const bool in = c + u < c1 && k < a.F;
-      A[u][0] = in && ok0 ? __ldg((const uint4*)(W + r0 + k)) : zero16();
-      A[u][1] = in && ok1 ? __ldg((const uint4*)(W + r1 + k)) : zero16();
-#pragma unroll
-      for (int q = 0; q < kNT; q++) {
-        B[u][q][0] = in && hoff[q] >= 0 ? load16((const T*)a.h_hi + hoff[q] + k) : zero16();
-        B[u][q][1] = in && hoff[q] >= 0 ? load16((const T*)a.h_lo + hoff[q] + k) : zero16();
+      for (int i = 0; i < 4; i++) {  // (past the last token: the last again)
+        const int slot = L.slot[j.s0 + min(col + i, j.ntok - 1)];
+        r[i] = kDown ? slot : L.token(slot);
+      }
+      from = make_int4(r[0], r[1], r[2], r[3]);
+    };
+    auto weights = [&](const MoeJob<kDown, kN>& j, int c) {  // by lane 0
+      const uint32_t bytes = (uint32_t)(moe_box_rows(j.rows) * (kDown ? 1 : 2) +
+                                        (j.ntok + 3) / 4 * 4 * kH) * 128u;
+      const int e = L.act[j.act];
+      const int row = kDown ? e * a.D + j.f0 : e * 2 * a.F + j.f0;
+      char* dst = ring + stage * kStage;
+      mbar_arrive_expect_tx(&bar.full[stage], bytes);
+      moe_load_rows(dst, tm64, tm16, c * kMoeK, row, j.rows, &bar.full[stage]);
+      if (!kDown)
+        moe_load_rows(dst + 64 * 128, tm64, tm16, c * kMoeK, row + a.F, j.rows, &bar.full[stage]);
+    };
+    auto tokens = [&](int c) {
+      if (mine4)
+        tma_gather4(ring + stage * kStage + kMoeTile * 128 + lane * 512,
+                    lane * 4 < kN ? tok0 : tok1, c * kMoeK, from, &bar.full[stage]);
+    };
+    // Down: the weights of the first steps do not depend on the kernel before, h does.
+    int early = 0;
+    if (kDown) {
+      MoeJob<kDown, kN> j = job;
+      int base = 0;
+      advance(w - 4);
+      for (; at < S && j.more(L); j.next(a, L), base += steps)
+        for (; at < S && at < base + steps; advance(kMoeCopyWarps))
+          if (lane == 0) weights(j, at - base);
+      early = at;
+      at = stage = 0;
+      parity = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    int base = 0, mine = 0;  // first step of the job; steps of this warp so far
+    advance(w - 4);
+    for (; ok && job.more(L); job.next(a, L), base += steps) {
+      aim(job);
+      for (; at < base + steps; advance(kMoeCopyWarps)) {
+        ok = __all_sync(0xffffffffu,
+                        moe_warp_wait(&bar.empty[stage], parity ^ 1u, abort, a.wait_ns));
+        if (!ok) break;
+        if (lane == 0 && at >= early) weights(job, at - base);
+        __syncwarp();
+        tokens(at - base);
+        mine++;
       }
     }
-#pragma unroll
-    for (int u = 0; u < kU; u++)
-#pragma unroll
-      for (int q = 0; q < kNT; q++) {
-        mma_k32<T>(acc[q], A[u][0], A[u][1], B[u][q][0]);
-        mma_k32<T>(acc[q], A[u][0], A[u][1], B[u][q][1]);
+    if (!ok && lane == 0) {
+      // What is on its way has to land before the CTA ends: this warp's last steps.  (A wait
+      // that gave up is for a step beyond the first S, and so beyond the early ones.)
+      for (int left = min(mine, S); left > 0; left--) {
+        at -= kMoeCopyWarps;
+        mbar_wait_bounded(&bar.full[at % S], (uint32_t)(at / S) & 1u, abort, 0u, kMoeDrainNs);
       }
+    }
+  } else if (w >= 4 + kMoeCopyWarps) {
+    // ---- products
+    if (lane == 0) {
+      const int turn = w - 4 - kMoeCopyWarps;
+      bool ok = true;
+      uint32_t n = 0;  // jobs so far
+      int base = 0;
+      const uint32_t idesc = moe_idesc(T(), kN);
+      const uint64_t a0 = sw128_desc(smem_u32(ring), 16, 1024);
+      const uint64_t b0 = sw128_desc(smem_u32(ring) + kMoeTile * 128, 16, 1024);
+      advance(turn);
+      for (; ok && job.more(L); job.next(a, L), base += steps, n++) {
+        const uint32_t buf = n & 1u, acc = bar.tmem + (buf * kMoeMmaWarps + turn) * kMoeAccCols;
+        if (!(ok = wait(&bar.acc_empty[buf], ((n >> 1) & 1u) ^ 1u))) break;
+        tc_fence_after_sync();
+        bool more = false;  // the accumulator holds something
+        for (; at < base + steps; advance(kMoeMmaWarps)) {
+          if (!(ok = wait(&bar.full[stage], parity))) break;
+          tc_fence_after_sync();
+          const uint64_t off = (uint64_t)((uint32_t)(stage * kStage) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kMoeK / 16; ks++)
+#pragma unroll
+            for (int h = 0; h < kH; h++) {
+              mma_bf16(acc, a0 + off + 2 * ks, b0 + off + (h * kN * 128 >> 4) + 2 * ks, idesc,
+                       more);
+              more = true;
+            }
+          mma_commit(&bar.empty[stage]);
+        }
+        if (ok) mma_commit(&bar.acc_full[buf]);
+      }
+      // tensor memory is given back when every product is done
+      mma_commit(&bar.drained);
+      mbar_wait_bounded(&bar.drained, 0, abort, 0u, kMoeDrainNs);
+    }
+  } else if (w < 4) {
+    // ---- out of tensor memory: thread t has weight row t of the tile
+    uint32_t n = 0;
+    int swap = 0;
+    bool ok = true;
+    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+    for (; job.more(L); job.next(a, L), n++) {  // to the end even when a wait gave up: the
+      const uint32_t buf = n & 1u;              // warps meet at barriers
+      ok = ok && moe_warp_wait<100>(&bar.acc_full[buf], (n >> 1) & 1u, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after_sync();
+      const uint32_t first = n * (uint32_t)steps;  // the job's first step
+      for (int j0 = 0; j0 < job.ntok; j0 += 32) {
+        const int cnt = min(32, job.ntok - j0);
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) v[j] = 0.f;
+        if (ok) {
+          // the warps' shares of K (a job of few steps has not all of them), in a fixed order
+#pragma unroll 1
+          for (int i = 0; i < min(steps, kMoeMmaWarps); i++) {
+            const uint32_t turn = steps >= kMoeMmaWarps ? (uint32_t)i
+                                                        : (first + i) % kMoeMmaWarps;
+            float u[32];
+            tmem_ld32(bar.tmem + lanes + (uint32_t)j0 +
+                          (buf * kMoeMmaWarps + turn) * kMoeAccCols,
+                      u);
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] += u[j];
+          }
+        }
+        if constexpr (kDown) {
+          if (tid < job.rows) {
+#pragma unroll
+            for (int j = 0; j < (kN < 32 ? kN : 32); j++)
+              if (j < cnt) {
+                const int s = job.s0 + j0 + j;
+                float* at = side + L.token(L.slot[s]) * kMoeTile + tid;
+                *at = fmaf(L.gate[s], v[j], *at);
+              }
+          }
+        } else {
+          // Rows 64.. are the linear half of rows 0..  Two threads share a row's columns, in a
+          // loop (unrolled over the columns the code is so long that fetching it costs 8 us).
+          float* x = side + swap * kMoeTile * 33 + tid * 33;
+#pragma unroll
+          for (int j = 0; j < 32; j++) x[j] = v[j];
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          const int row = tid & 63;
+          const float* gate = side + swap * kMoeTile * 33 + row * 33;
+          swap ^= 1;
+          if (row < job.rows) {
+#pragma unroll 1
+            for (int j = tid >> 6; j < cnt; j += 2) {
+              const float h = moe_act(gate[j], a.act) * gate[64 * 33 + j];
+              const int64_t at = (int64_t)L.slot[job.s0 + j0 + j] * a.F + job.f0 + row;
+              T hi, lo;
+              from_f32(&hi, h);
+              const float left = h - to_f32(hi);
+              from_f32(&lo, isfinite(left) ? left : 0.f);  // h beyond the type's range stays so
+              ((T*)a.h_hi)[at] = hi;
+              ((T*)a.h_lo)[at] = lo;
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&bar.acc_empty[buf]);
+    }
   }
-#pragma unroll
-  for (int q = 0; q < kNT; q++)
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int col = q * 8 + t * 2 + i;
-      if (col < ntok) {
-        const int s = slot[col], tok = s / a.m;
-        float gate = 0.f;
-        for (int j = s; j < (tok + 1) * a.m; j++) gate += a.idx[j] == e ? a.resp[j] : 0.f;
-        y[tok * kMoeRows + g] = fmaf(gate, acc[q][i], y[tok * kMoeRows + g]);
-        y[tok * kMoeRows + g + 8] = fmaf(gate, acc[q][i + 2], y[tok * kMoeRows + g + 8]);
-      }
-    }
   __syncwarp();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(MoeArgs a, int C) {
-  __shared__ MoeLists L;
-  extern __shared__ float yw[];  // [warp][token][kMoeRows]
-  const int tid = threadIdx.x, w = tid >> 5;
-  const int rank = C > 1 ? (int)sm100::cluster_ctarank() : 0;
-  const int blk = blockIdx.x / C;
-  const int d0 = (int)((int64_t)a.D * blk / a.row_blocks);
-  const int rows = (int)((int64_t)a.D * (blk + 1) / a.row_blocks) - d0;
-  const int per = a.T * kMoeRows;
-  for (int i = tid; i < per * kMoeWarps; i += kMoeThreads) yw[i] = 0.f;
-  moe_sort(a, L);
-  const int chunks = (a.F + 31) / 32, W = kMoeWarps * C;
-  const int S = max(1, min((4 * W + L.n - 1) / max(L.n, 1), chunks / 4));
-  float* y = yw + w * per;
-  for (int u = rank * kMoeWarps + w; u < L.n * S; u += W) {
-    const int act = u / S, s = u - act * S, e = L.act[act];
-    const int c0 = chunks * s / S, c1 = chunks * (s + 1) / S;
-    for (int s0 = L.off[act]; s0 < L.off[act + 1];) {
-      const int left = L.off[act + 1] - s0;
-      const uint16_t* slot = L.slot + s0;
-      if (left <= 8)
-        down_unit<T, 1, 4>(a, e, d0, rows, c0, c1, slot, left, y);
-      else if (left <= 16)
-        down_unit<T, 2, 2>(a, e, d0, rows, c0, c1, slot, left, y);
-      else
-        down_unit<T, 4, 2>(a, e, d0, rows, c0, c1, slot, min(left, 32), y);
-      s0 += left <= 8 ? 8 : left <= 16 ? 16 : 32;
+// Start of both kernels: barriers, tensor memory.
+__device__ __forceinline__ void moe_begin(MoeBarriers& bar) {
+  using namespace sm100;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 16; i++) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&bar.acc_full[i], kMoeMmaWarps);
+      mbar_init(&bar.acc_empty[i], 128);
+    }
+    mbar_init(&bar.drained, kMoeMmaWarps);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 32) {
+    tmem_alloc(&bar.tmem, kMoeTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+}
+// And their end.
+__device__ __forceinline__ void moe_end(const MoeArgs& a, MoeBarriers& bar) {
+  sm100::tc_fence_before_sync();
+  __syncthreads();
+  sm100::tc_fence_after_sync();
+  if (threadIdx.x < 32) sm100::tmem_dealloc(bar.tmem, kMoeTmemCols);
+  if (threadIdx.x == 0 && bar.abort) atomicOr(a.status, GMM_DEVFLAG_WAIT_TIMEOUT);
+}
+
+__device__ __forceinline__ char* align1024(char* p) {
+  return (char*)(((uintptr_t)p + 1023) & ~(uintptr_t)1023);
+}
+
+template <typename T, int kN>
+__device__ __forceinline__ void moe_up_run(const MoeArgs& a, MoeLists& L, MoeBarriers& bar,
+                                           char* ring, float* side, const CUtensorMap* tm64,
+                                           const CUtensorMap* tm16, const CUtensorMap* tok) {
+  MoeJob<false, kN> job;
+  // Units of 64 rows, or of 32 or 16 where they share out so much better that it makes up for
+  // their steps, which take 0.6 and 0.45 of a full one's time.
+  int64_t all = 0;
+  float best = 0.f;
+  for (int size = 64; size >= 16; size /= 2) {
+    const int per = (a.F + size - 1) / size;
+    const int64_t units = (int64_t)L.n * per;
+    const float cost = (float)((units + gridDim.x - 1) / gridDim.x) *
+                       (size == 64 ? 1.f : size == 32 ? 0.6f : 0.45f);
+    if (size == 64 || cost < best) {
+      best = cost;
+      all = units;
+      job.size = size;
+      job.per = per;
     }
   }
-  __syncthreads();
-  for (int i = tid; i < per; i += kMoeThreads) {
-    float v = yw[i];
-#pragma unroll
-    for (int q = 1; q < kMoeWarps; q++) v += yw[q * per + i];
-    yw[i] = v;
-  }
-  if (C > 1)
-    sm100::cluster_sync();
+  job.unit = (int)(all * blockIdx.x / gridDim.x);
+  job.end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+  if (job.more(L)) job.fit(a, L);
+  moe_stream<T, false, kN>(a, L, bar, job, ring, side, tm64, tm16, tok, tok);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_up_kernel(MoeArgs a, const __grid_constant__ CUtensorMap tm64,
+                  const __grid_constant__ CUtensorMap tm16,
+                  const __grid_constant__ CUtensorMap tok) {
+  extern __shared__ __align__(256) char smem[];
+  MoeLists& L = *(MoeLists*)smem;
+  MoeBarriers& bar = *(MoeBarriers*)(smem + (sizeof(MoeLists) + 255) / 256 * 256);
+  const int fixed = moe_fixed(a.E, a.T * a.m);
+  float* side = (float*)(smem + fixed);
+  char* ring = align1024(smem + fixed + kMoeSwap);
+  if (threadIdx.x == 0) moe_place_lists(L, smem + kMoeStructs, a.E, a.T * a.m);
+  moe_begin(bar);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.T * a.m; i += kMoeThreads) {
+      const int e = __ldcg(a.idx + i);
+      if (e < -1 || e >= a.E) atomicOr(a.status, GMM_DEVFLAG_BAD_INDEX);
+    }
+  moe_sort(a, L, (int*)side);
+  if (L.most <= 16)
+    moe_up_run<T, 16>(a, L, bar, ring, side, &tm64, &tm16, &tok);
+  else if (L.most <= 32)
+    moe_up_run<T, 32>(a, L, bar, ring, side, &tm64, &tm16, &tok);
   else
-    __syncthreads();
+    moe_up_run<T, 64>(a, L, bar, ring, side, &tm64, &tm16, &tok);
+  moe_end(a, bar);
+}
+
+template <typename T, int kN>
+__device__ __forceinline__ void moe_down_run(const MoeArgs& a, MoeLists& L, MoeBarriers& bar,
+                                             char* ring, float* y, int d0, int rows, int rank,
+                                             int C, const CUtensorMap* tm64,
+                                             const CUtensorMap* tm16, const CUtensorMap* hi,
+                                             const CUtensorMap* lo) {
+  MoeJob<true, kN> job;
+  job.f0 = d0;
+  job.rows = rows;
+  job.act = rank;
+  job.stride = C;
+  if (job.more(L)) job.fit(a, L);
+  moe_stream<T, true, kN>(a, L, bar, job, ring, y, tm64, tm16, hi, lo);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_down_kernel(MoeArgs a, int C, const __grid_constant__ CUtensorMap tm64,
+                    const __grid_constant__ CUtensorMap tm16,
+                    const __grid_constant__ CUtensorMap hi,
+                    const __grid_constant__ CUtensorMap lo) {
+  extern __shared__ __align__(256) char smem[];
+  MoeLists& L = *(MoeLists*)smem;
+  MoeBarriers& bar = *(MoeBarriers*)(smem + (sizeof(MoeLists) + 255) / 256 * 256);
+  const int tid = threadIdx.x, per = a.T * kMoeTile;
+  const int fixed = moe_fixed(a.E, a.T * a.m);
+  float* y = (float*)(smem + fixed);  // [token][row of the block]
+  char* ring = align1024(smem + fixed + per * 4);
+  const int rank = C > 1 ? (int)sm100::cluster_ctarank() : 0;
+  const int d0 = (int)(blockIdx.x / C) * kMoeTile, rows = min(kMoeTile, a.D - d0);
+  if (tid == 0) moe_place_lists(L, smem + kMoeStructs, a.E, a.T * a.m);
+  moe_begin(bar);
+  // (idx and resp were complete before the up kernel let this one start)
+  moe_sort(a, L, (int*)ring);
+  for (int i = tid; i < per; i += kMoeThreads) y[i] = 0.f;
+  sm100::fence_proxy_async_smem();  // the sort's counters lay where TMA writes
+  __syncthreads();
+  if (L.most <= 16 || moe_stages(a.ring_bytes, true, 32) == 0)
+    moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+  else if (L.most <= 32 || moe_stages(a.ring_bytes, true, 64) == 0)
+    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+  else
+    moe_down_run<T, 64>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // before Y is written
+  moe_end(a, bar);
+  if (C > 1) sm100::cluster_sync();
   T* Y = (T*)a.Y;
   for (int i = tid; i < per; i += kMoeThreads) {
-    const int tok = i / kMoeRows, row = i % kMoeRows;
+    const int tok = i / kMoeTile, row = i % kMoeTile;
     if (tok % C != rank || row >= rows) continue;
-    float v = yw[i];
-    if (C > 1) {
+    float v = y[i];
+    if (C > 1) {  // the cluster's copies, in CTA order
       v = 0.f;
-      const uint32_t at = sm100::smem_u32(yw + i);
+      const uint32_t at = sm100::smem_u32(y + i);
       for (int q = 0; q < C; q++) {
         float x;
         asm volatile("ld.shared::cluster.f32 %0, [%1];"
                      : "=f"(x)
-                     : "r"(sm100::map_to_rank(at, q)));
+                     : "r"(sm100::map_to_rank(at, q))
+                     : "memory");
         v += x;
       }
     }
     from_f32(Y + (int64_t)tok * a.ldy + d0 + row, v);
   }
-  if (C > 1) sm100::cluster_sync();
+  if (C > 1) sm100::cluster_sync();  // the others' shared memory has been read
 }
 
 }  // namespace scem

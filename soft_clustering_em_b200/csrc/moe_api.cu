@@ -3,6 +3,7 @@
 
 #include "api_common.h"
 #include "moe.cuh"
+#include "tma_host.h"
 
 using namespace scem;
 
@@ -22,6 +23,8 @@ gmm_status check_moe(const gmm_moe_problem* p) {
   if (p->D > (1 << 20) || p->F > (1 << 20) || p->ldx > ((int64_t)1 << 40) ||
       p->ldy > ((int64_t)1 << 40))
     return GMM_ERR_UNSUPPORTED;
+  if ((int64_t)p->E * 2 * p->F >= ((int64_t)1 << 31) || (int64_t)p->E * p->D >= ((int64_t)1 << 31))
+    return GMM_ERR_UNSUPPORTED;
   return GMM_OK;
 }
 
@@ -39,20 +42,74 @@ MoeLayout moe_layout(const gmm_moe_problem* p) {
   return L;
 }
 
+// A launch that may start while the kernel before it in the stream ends: both kernels wait
+// (griddepcontrol) before they touch what it wrote.
+template <typename Kern, typename... Args>
+bool launch(Kern kern, unsigned grid, int cluster, int smem, cudaStream_t st, Args... args) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return false;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kMoeThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
+constexpr int kMoeSmem = 227 * 1024;
+
+// Shared memory for the stages behind the fixed parts.
+int ring_bytes(int fixed) { return kMoeSmem - fixed - 1024; }
+
+constexpr int kMostFixed = moe_fixed(kMoeMaxE, kMoeMaxSlots);
+static_assert(moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeMaxT * kMoeTile * 4, true, 16) > 0 &&
+                  moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeSwap, false, 64) > 0,
+              "a ring at the most tokens");
+
 template <typename T>
-gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, cudaStream_t st) {
+gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const void* W_up,
+                      const void* W_down, cudaStream_t st) {
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
-  moe_up_kernel<T><<<2 * sms, kMoeThreads, 0, st>>>(a);
-  if ((s = api_launched(1)) != GMM_OK) return s;
-  a.row_blocks = (p->D + kMoeRows - 1) / kMoeRows;
-  const size_t smem = (size_t)p->T * kMoeRows * kMoeWarps * 4;
-  auto kern = moe_down_kernel<T>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
+  CUtensorMap up64, up16, down64, down16, x1, hi1, lo1;
+  const uint64_t D = p->D, F = p->F, E = p->E, slots = (uint64_t)p->T * p->m;
+  if (!make_tmap_16b_sw128(&up64, W_up, D, E * 2 * F, D * 2, 64) ||
+      !make_tmap_16b_sw128(&up16, W_up, D, E * 2 * F, D * 2, 16) ||
+      !make_tmap_16b_sw128(&down64, W_down, F, E * D, F * 2, 64) ||
+      !make_tmap_16b_sw128(&down16, W_down, F, E * D, F * 2, 16) ||
+      !make_tmap_16b_sw128(&x1, X, D, p->T, (uint64_t)p->ldx * 2, 1) ||
+      !make_tmap_16b_sw128(&hi1, a.h_hi, F, slots, F * 2, 1) ||
+      !make_tmap_16b_sw128(&lo1, a.h_lo, F, slots, F * 2, 1))
+    return GMM_ERR_CUDA;
+  a.wait_ns = api_wait_budget();
+  const int fixed = moe_fixed(p->E, p->T * p->m), up_fixed = fixed + kMoeSwap;
+  a.ring_bytes = ring_bytes(up_fixed);
+  if (!launch(moe_up_kernel<T>, sms, 1, up_fixed + 1024 + a.ring_bytes, st, a, up64, up16,
+              x1))
     return api_launched(0), GMM_ERR_CUDA;
-  kern<<<a.row_blocks, kMoeThreads, smem, st>>>(a, 1);
+  if ((s = api_launched(1)) != GMM_OK) return s;
+  // Blocks of 128 rows of y, and as many CTAs per block (sharing out its experts) as fit the
+  // SMs at once: clusters of 4 and 8 do not pack the GPCs (35 of 37 and 16 of 18 fit, and one
+  // more would take a second turn).
+  const int blocks = (p->D + kMoeTile - 1) / kMoeTile;
+  const int fit[4] = {sms, sms / 2, sms / 4 - sms / 74, sms / 8 - sms / 74};
+  int c = 0;
+  while (c < 3 && blocks <= fit[c + 1] && (2 << c) <= p->T * p->m) c++;
+  const int down_fixed = fixed + p->T * kMoeTile * 4;
+  a.ring_bytes = ring_bytes(down_fixed);
+  if (!launch(moe_down_kernel<T>, blocks << c, 1 << c, down_fixed + 1024 + a.ring_bytes, st, a,
+              1 << c, down64, down16, hi1, lo1))
+    return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
 
@@ -81,11 +138,11 @@ gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, 
   const MoeLayout L = moe_layout(p);
   if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
   char* b = (char*)ws;
-  MoeArgs a = {X,      W_up, W_down, Y,    idx,    resp,   b + L.hi, b + L.lo, p->T,
-               p->m,   p->E, p->D,   p->F, p->ldx, p->ldy, p->act,   0,        (unsigned int*)ws};
+  MoeArgs a = {Y,    idx,    resp,   b + L.hi, b + L.lo, p->T, p->m, p->E,
+               p->D, p->F,   p->ldy, p->act,   0,        0,    (unsigned int*)ws};
   cudaStream_t st = (cudaStream_t)stream;
-  if (p->dtype == GMM_BF16) return moe_launch<__nv_bfloat16>(p, a, st);
-  return moe_launch<__half>(p, a, st);
+  if (p->dtype == GMM_BF16) return moe_launch<__nv_bfloat16>(p, a, X, W_up, W_down, st);
+  return moe_launch<__half>(p, a, X, W_up, W_down, st);
 }
 
 }  // extern "C"
