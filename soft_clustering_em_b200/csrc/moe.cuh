@@ -25,8 +25,8 @@
 // Kernel 1 (up) holds 64 rows of W_gate over the same 64 rows of W_lin in a tile and
 // writes h for every (token, choice) into the workspace; kernel 2 (down) forms y, summing
 // a token's experts in shared memory, in ascending order.  h is kept as two halves of
-// the weights' type, hi + lo, so that rounding it adds nothing visible to y: its products
-// are two passes over the same weight stage.
+// the weights' type, hi + lo, so that rounding it adds nothing visible to y: columns of
+// their own of the same product, added when they leave tensor memory.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,6 +56,7 @@ struct MoeArgs {
   int T, m, E, D, F;
   int64_t ldy;
   int act;
+  int block_rows;  // down: rows of y per cluster
   int ring_bytes;  // shared memory of the stages
   uint64_t wait_ns;
   unsigned int* status;
@@ -255,12 +256,13 @@ template <int kSleep = 0>
 __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity,
                                          volatile unsigned int* abort, uint64_t budget_ns) {
   uint64_t t0 = 0;
+  const uint32_t tries = budget_ns < 100000 ? 0 : 31;  // between looks at the clock
   for (uint32_t i = 0;; i++) {
     if (sm100::mbar_try_wait(bar, parity)) return true;
-    if ((i & 31) == 31) {
+    if ((i & tries) == tries) {
       if (*abort & GMM_DEVFLAG_WAIT_TIMEOUT) return false;
       const uint64_t now = sm100::globaltimer_ns();
-      if (i == 31) {
+      if (t0 == 0) {
         t0 = now;
       } else if (now - t0 > budget_ns) {
         atomicOr(const_cast<unsigned int*>(abort), GMM_DEVFLAG_WAIT_TIMEOUT);
@@ -286,6 +288,14 @@ __host__ __device__ constexpr int moe_stages(int ring_bytes, bool down, int kN) 
   return s < 16 ? s : 16;
 }
 static_assert(kMoeCopyWarps % kMoeMmaWarps == 0, "a stage has one warp of each kind");
+// Columns of a job's product: more where an expert has more tokens, unless that costs stages.
+__device__ __forceinline__ int moe_columns(int ring_bytes, bool down, int most) {
+  int n = 16;
+  for (int wide = 32; wide <= (down ? 32 : 64); wide *= 2)
+    if (most > wide / 2 && moe_stages(ring_bytes, down, wide) >= moe_stages(ring_bytes, down, n))
+      n = wide;
+  return n;
+}
 
 // Four rows of a matrix (a tensor map with a box of one row) at column k, one below the other.
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int k, int4 rows,
@@ -411,12 +421,16 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
       bool ok = true;
       uint32_t n = 0;  // jobs so far
       int base = 0;
-      const uint32_t idesc = moe_idesc(T(), kN);
+      const uint32_t idesc = moe_idesc(T(), kH * kN);
+      static_assert(kH * kN <= kMoeAccCols, "accumulator columns");
       const uint64_t a0 = sw128_desc(smem_u32(ring), 16, 1024);
       const uint64_t b0 = sw128_desc(smem_u32(ring) + kMoeTile * 128, 16, 1024);
       advance(turn);
       for (; ok && job.more(L); job.next(a, L), base += steps, n++) {
-        const uint32_t buf = n & 1u, acc = bar.tmem + (buf * kMoeMmaWarps + turn) * kMoeAccCols;
+        // the accumulator goes by the step within the job, so that a sum's parts do not depend
+        // on the jobs before
+        const uint32_t buf = n & 1u, part = (uint32_t)(turn - base) % kMoeMmaWarps;
+        const uint32_t acc = bar.tmem + (buf * kMoeMmaWarps + part) * kMoeAccCols;
         if (!(ok = wait(&bar.acc_empty[buf], ((n >> 1) & 1u) ^ 1u))) break;
         tc_fence_after_sync();
         bool more = false;  // the accumulator holds something
@@ -426,12 +440,8 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
           const uint64_t off = (uint64_t)((uint32_t)(stage * kStage) >> 4);
 #pragma unroll
           for (int ks = 0; ks < kMoeK / 16; ks++)
-#pragma unroll
-            for (int h = 0; h < kH; h++) {
-              mma_bf16(acc, a0 + off + 2 * ks, b0 + off + (h * kN * 128 >> 4) + 2 * ks, idesc,
-                       more);
-              more = true;
-            }
+            mma_bf16(acc, a0 + off + 2 * ks, b0 + off + 2 * ks, idesc, more || ks > 0);
+          more = true;
           mma_commit(&bar.empty[stage]);
         }
         if (ok) mma_commit(&bar.acc_full[buf]);
@@ -451,24 +461,28 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
       ok = ok && moe_warp_wait<100>(&bar.acc_full[buf], (n >> 1) & 1u, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after_sync();
-      const uint32_t first = n * (uint32_t)steps;  // the job's first step
       for (int j0 = 0; j0 < job.ntok; j0 += 32) {
         const int cnt = min(32, job.ntok - j0);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; j++) v[j] = 0.f;
         if (ok) {
-          // the warps' shares of K (a job of few steps has not all of them), in a fixed order
+          // the warps' shares of K (a job of few steps has not all of them), in order
 #pragma unroll 1
           for (int i = 0; i < min(steps, kMoeMmaWarps); i++) {
-            const uint32_t turn = steps >= kMoeMmaWarps ? (uint32_t)i
-                                                        : (first + i) % kMoeMmaWarps;
+            const uint32_t at = bar.tmem + lanes + (buf * kMoeMmaWarps + i) * kMoeAccCols;
             float u[32];
-            tmem_ld32(bar.tmem + lanes + (uint32_t)j0 +
-                          (buf * kMoeMmaWarps + turn) * kMoeAccCols,
-                      u);
+            tmem_ld32(at + (uint32_t)j0, u);
 #pragma unroll
             for (int j = 0; j < 32; j++) v[j] += u[j];
+            if constexpr (kDown && kN == 16) {  // lo beside hi
+#pragma unroll
+              for (int j = 0; j < 16; j++) v[j] += u[j + 16];
+            } else if constexpr (kDown) {
+              tmem_ld32(at + (uint32_t)kN, u);
+#pragma unroll
+              for (int j = 0; j < 32; j++) v[j] += u[j];
+            }
           }
         }
         if constexpr (kDown) {
@@ -598,9 +612,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (e < -1 || e >= a.E) atomicOr(a.status, GMM_DEVFLAG_BAD_INDEX);
     }
   moe_sort(a, L, (int*)side);
-  if (L.most <= 16)
+  const int columns = moe_columns(a.ring_bytes, false, L.most);
+  if (columns == 16)
     moe_up_run<T, 16>(a, L, bar, ring, side, &tm64, &tm16, &tok);
-  else if (L.most <= 32)
+  else if (columns == 32)
     moe_up_run<T, 32>(a, L, bar, ring, side, &tm64, &tm16, &tok);
   else
     moe_up_run<T, 64>(a, L, bar, ring, side, &tm64, &tm16, &tok);
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   float* y = (float*)(smem + fixed);  // [token][row of the block]
   char* ring = align1024(smem + fixed + per * 4);
   const int rank = C > 1 ? (int)sm100::cluster_ctarank() : 0;
-  const int d0 = (int)(blockIdx.x / C) * kMoeTile, rows = min(kMoeTile, a.D - d0);
+  const int d0 = (int)(blockIdx.x / C) * a.block_rows, rows = min(a.block_rows, a.D - d0);
   if (tid == 0) moe_place_lists(L, smem + kMoeStructs, a.E, a.T * a.m);
   moe_begin(bar);
   // (idx and resp were complete before the up kernel let this one start)
@@ -644,12 +659,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   for (int i = tid; i < per; i += kMoeThreads) y[i] = 0.f;
   sm100::fence_proxy_async_smem();  // the sort's counters lay where TMA writes
   __syncthreads();
-  if (L.most <= 16 || moe_stages(a.ring_bytes, true, 32) == 0)
+  if (moe_columns(a.ring_bytes, true, L.most) == 16)
     moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
-  else if (L.most <= 32 || moe_stages(a.ring_bytes, true, 64) == 0)
-    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
   else
-    moe_down_run<T, 64>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // before Y is written
   moe_end(a, bar);
   if (C > 1) sm100::cluster_sync();

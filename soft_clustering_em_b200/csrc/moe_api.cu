@@ -1,5 +1,6 @@
 // moe_api.cu -- host side of gmm_moe: argument checks, workspace layout and launches.
 #include <algorithm>
+#include <atomic>
 
 #include "api_common.h"
 #include "moe.cuh"
@@ -75,6 +76,58 @@ static_assert(moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeMaxT * kMoeTile * 4,
                   moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeSwap, false, 64) > 0,
               "a ring at the most tokens");
 
+// How many clusters of C of the down kernel's CTAs (one per SM) are resident at once: they do not
+// pack the GPCs (148, 74, 45, 33, 26, 22, 15, 15 for C = 1..8 on 148 SMs).  Asked once per device.
+template <typename T>
+int down_clusters(int device, int C) {
+  static std::atomic<int> known[64][9];
+  const bool keep = device >= 0 && device < 64;
+  if (keep)
+    if (int n = known[device][C].load()) return n;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(kMoeThreads);
+  cfg.dynamicSmemBytes = kMoeSmem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(moe_down_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kMoeSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, moe_down_kernel<T>, &cfg) != cudaSuccess || n < 1)
+    return 0;
+  if (keep) known[device][C] = n;
+  return n;
+}
+
+// Rows of y per cluster (a multiple of 16 up to 128) and CTAs per cluster (which share out the
+// experts): the least time of a CTA, whose step costs by its rows but not below those of about
+// 56, and by its tokens, among the shapes whose clusters are all resident at once (one more
+// would take a second turn: 58 us instead of 42 for 32 tokens).
+template <typename T>
+bool down_shape(const gmm_moe_problem* p, int sms, int* C, int* rows) {
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return false;
+  const int experts = std::min(p->E, p->T * p->m);
+  *C = 1;
+  *rows = kMoeTile;
+  double best = 1e30;
+  const double tokens = std::min(32.0, (double)p->T * p->m / experts);
+  for (int c = 1; c <= 8 && c <= experts; c++) {
+    const int fit = c == 1 ? sms : down_clusters<T>(device, c);
+    if (fit < 1) return false;
+    for (int r = 16; r <= kMoeTile; r += 16) {
+      if ((p->D + r - 1) / r > fit) continue;
+      const double cost = ((experts + c - 1) / c) * (std::max(r, 56) + 8 + 2 * tokens) + 0.01 * c;
+      if (cost < best) best = cost, *C = c, *rows = r;
+    }
+  }
+  return true;
+}
+
 template <typename T>
 gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const void* W_up,
                       const void* W_down, cudaStream_t st) {
@@ -98,17 +151,13 @@ gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const 
               x1))
     return api_launched(0), GMM_ERR_CUDA;
   if ((s = api_launched(1)) != GMM_OK) return s;
-  // Blocks of 128 rows of y, and as many CTAs per block (sharing out its experts) as fit the
-  // SMs at once: clusters of 4 and 8 do not pack the GPCs (35 of 37 and 16 of 18 fit, and one
-  // more would take a second turn).
-  const int blocks = (p->D + kMoeTile - 1) / kMoeTile;
-  const int fit[4] = {sms, sms / 2, sms / 4 - sms / 74, sms / 8 - sms / 74};
-  int c = 0;
-  while (c < 3 && blocks <= fit[c + 1] && (2 << c) <= p->T * p->m) c++;
+  int C = 1;
+  if (!down_shape<T>(p, sms, &C, &a.block_rows)) return api_launched(0), GMM_ERR_CUDA;
+  const int blocks = (p->D + a.block_rows - 1) / a.block_rows;
   const int down_fixed = fixed + p->T * kMoeTile * 4;
   a.ring_bytes = ring_bytes(down_fixed);
-  if (!launch(moe_down_kernel<T>, blocks << c, 1 << c, down_fixed + 1024 + a.ring_bytes, st, a,
-              1 << c, down64, down16, hi1, lo1))
+  if (!launch(moe_down_kernel<T>, blocks * C, C, down_fixed + 1024 + a.ring_bytes, st, a, C, down64,
+              down16, hi1, lo1))
     return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
@@ -139,7 +188,7 @@ gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, 
   if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
   char* b = (char*)ws;
   MoeArgs a = {Y,    idx,    resp,   b + L.hi, b + L.lo, p->T, p->m, p->E,
-               p->D, p->F,   p->ldy, p->act,   0,        0,    (unsigned int*)ws};
+               p->D, p->F,   p->ldy, p->act,   0,        0,    0,    (unsigned int*)ws};
   cudaStream_t st = (cudaStream_t)stream;
   if (p->dtype == GMM_BF16) return moe_launch<__nv_bfloat16>(p, a, X, W_up, W_down, st);
   return moe_launch<__half>(p, a, X, W_up, W_down, st);

@@ -202,6 +202,59 @@ def test_two_streams_and_a_captured_graph(G):
         assert torch.equal(gy, G.gmm_moe(X, i, r, *W))
 
 
+def test_a_short_budget_times_out_and_the_next_call_is_exact(G):
+    import torch
+
+    rng = np.random.default_rng(12)
+    T, E, D, F, m = 20, 12, 512, 256, 3
+    X, W = _tokens(rng, T, D, "bf16"), _weights(rng, E, D, F, "bf16")
+    idx, resp = G.gmm_route(torch.randn(T, E, device="cuda"), m)
+    ws = torch.zeros(G.gmm_moe_workspace_size(G.moe_problem(X, idx, W[1])), dtype=torch.uint8,
+                     device="cuda")
+    try:
+        G.gmm_set_wait_budget(1)  # 1 ns: a wait that is not over at the second look gives up
+        G.gmm_moe(X, idx, resp, *W, ws=ws)
+        rc, flags = G.gmm_device_status(ws)
+    finally:
+        G.gmm_set_wait_budget(0)
+    assert rc == G.GMM_ERR_TIMEOUT and flags == G.GMM_DEVFLAG_WAIT_TIMEOUT
+    _, rc, flags = _check(G, X, idx, resp, *W)
+    assert rc == 0 and flags == 0
+
+
+@pytest.mark.parametrize("T,E,D,F,m", [(256, 2, 1024, 512, 2), (70, 3, 264, 712, 2),
+                                       (200, 16, 2048, 64, 4), (31, 160, 136, 72, 8)])
+def test_longer_streams(G, T, E, D, F, m):
+    """Many jobs per CTA, rings that wrap, experts of several column groups, unequal tails."""
+    import torch
+
+    rng = np.random.default_rng(T)
+    X, W = _tokens(rng, T, D, "bf16"), _weights(rng, E, D, F, "bf16")
+    idx, resp = G.gmm_route(torch.randn(T, E, device="cuda"), m)
+    Y, rc, flags = _check(G, X, idx, resp, *W)
+    assert rc == 0 and flags == 0
+    for _ in range(5):
+        assert torch.equal(Y, G.gmm_moe(X, idx, resp, *W))
+
+
+def test_weights_of_other_experts_do_not_reach_a_token(G):
+    """NaN and infinities in the weights of an expert reach the tokens that chose it alone."""
+    import torch
+
+    rng = np.random.default_rng(13)
+    T, E, D, F, m = 18, 5, 128, 96, 2
+    X, W = _tokens(rng, T, D, "bf16"), _weights(rng, E, D, F, "bf16")
+    idx, resp = G.gmm_route(torch.randn(T, E, device="cuda"), m)
+    clean = G.gmm_moe(X, idx, resp, *W)
+    W[0][3, 5, 7] = float("nan")
+    W[1][3, 64:, :] = float("inf")
+    got = G.gmm_moe(X, idx, resp, *W)
+    chose = (idx == 3).any(1)
+    assert chose.any() and not chose.all()
+    assert torch.equal(got[~chose], clean[~chose])
+    assert torch.isnan(got[chose]).any(1).all()
+
+
 def test_no_tokens(G):
     import torch
 
