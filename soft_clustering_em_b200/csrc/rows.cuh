@@ -305,15 +305,18 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 5) row_short_kernel(RowAr
         const uint32_t equal = __ballot_sync(
             0xffffffffu, z == best && (best < last_z || k > last_k) && !none);
         const int first = __ffs((equal >> (lane - l)) & group_mask<kLanes>()) - 1;
-        const float next =
-            group_max<(V < kLanes ? V : kLanes)>(z < best || (z == best && l > first)
-                                                     ? z
-                                                     : -INFINITY);
-        // (lanes V and up reduced among themselves: the vector's owner asks lane 0 of the group)
-        const float left = __shfl_sync(0xffffffffu, next, lane - l);
+        if (j0 + j + 1 < a.m) {
+          // what follows in that vector is left (lanes V and up reduce among themselves: the
+          // vector's owner asks lane 0 of the group)
+          const float next =
+              group_max<(V < kLanes ? V : kLanes)>(z < best || (z == best && l > first)
+                                                       ? z
+                                                       : -INFINITY);
+          const float left = __shfl_sync(0xffffffffu, next, lane - l);
 #pragma unroll
-        for (int c = 0; c < kChunks; c++)
-          if (at == c * kLanes + l) top[c] = left;
+          for (int c = 0; c < kChunks; c++)
+            if (at == c * kLanes + l) top[c] = left;
+        }
         last_z = best;
         last_k = none ? last_k : at * V + first;
         if (l == j && !none) {
@@ -966,9 +969,10 @@ __device__ __forceinline__ void group_sync() {
 }
 
 template <typename T, int kGroup>
-__global__ void __launch_bounds__(256) row_grad_kernel(RowGradArgs a) {
+__global__ void __launch_bounds__(256, kGroup == 32 ? 4 : 5) row_grad_kernel(RowGradArgs a) {
   constexpr int V = Vec16<T>::n;
   constexpr int kGroups = 256 / kGroup;
+  constexpr int kBatch = 4;  // 16-byte vectors in flight per thread
   constexpr int kOwn = (kMaxAlt + 1 + kGroup - 1) / kGroup;
   __shared__ int s_idx[kGroups][kMaxAlt + 1];
   __shared__ float s_coef[kGroups][kMaxAlt + 1];
@@ -991,35 +995,52 @@ __global__ void __launch_bounds__(256) row_grad_kernel(RowGradArgs a) {
     const int v1 = (int)((int64_t)nv * (rank + 1) / a.slices);
     const bool last = rank == a.slices - 1;
 
+    // The first vectors are on their way while the row's scalars are read.  (Nobody else
+    // writes this slice, so what is loaded early is what stands there.)
+    const T* vin = row + head;
+    T* vout = out + head;
+    uint4 r[kBatch];
+    auto load = [&](int v) {
+#pragma unroll
+      for (int j = 0; j < kBatch; j++)
+        if (v + j * kGroup < v1) r[j] = load16(vin + (int64_t)(v + j * kGroup) * V);
+    };
+    load(v0 + t);
+
+    // So are the scalars, all at once, and then the named entries: alternatives 0..m-1, the label.
     const float lse_in = a.lse[n];
-    const bool empty = lse_in == -INFINITY;
-    const float lse = empty ? INFINITY : lse_in;
     const int id = a.ids ? a.ids[n] : -1;
-    const bool has_id = id >= 0 && id < a.K && !empty;
-    const float la = has_id && a.dlogp ? a.dlogp[n] : 0.f;
-    // the named entries: alternatives 0..m-1, then the label
-    for (int j = t; j <= a.m; j += kGroup) {
-      int k = -1;
-      float c = 0.f;
-      if (j == a.m) {
-        if (has_id && a.dlogp) k = id, c = la;
-        if (rank == 0 && a.flags && (id < -1 || id >= a.K))
-          atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-      } else {
-        const int v = a.top_idx[n * a.m + j];
-        if (v >= 0 && v < a.K && !empty)
-          k = v, c = a.dtop[n * a.m + j];
-        else if (rank == 0 && a.flags && (v < -1 || v >= a.K))
-          atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-      }
-      s_idx[g][j] = k;
-      s_coef[g][j] = c;
-    }
-    group_sync<kGroup>();
     float slope = a.dlse ? a.dlse[n] : 0.f;
-    for (int j = 0; j <= a.m; j++) slope -= s_coef[g][j];
     const float h = a.dentropy ? a.dentropy[n] : 0.f;
     const float H = a.dentropy ? a.entropy[n] : 0.f;
+    int named_k[kOwn];
+    float named_c[kOwn], named_x[kOwn];
+    bool here[kOwn];  // the entry exists and lies in this slice
+#pragma unroll
+    for (int i = 0; i < kOwn; i++) {
+      const int j = t + i * kGroup;
+      named_k[i] = j < a.m ? a.top_idx[n * a.m + j] : j == a.m ? id : -1;
+      named_c[i] = j < a.m ? a.dtop[n * a.m + j] : j == a.m && a.dlogp ? a.dlogp[n] : 0.f;
+    }
+    const bool empty = lse_in == -INFINITY;
+    const float lse = empty ? INFINITY : lse_in;
+#pragma unroll
+    for (int i = 0; i < kOwn; i++) {
+      const int j = t + i * kGroup, k = named_k[i];
+      const bool legal = k >= 0 && k < a.K;
+      if (!legal && k != -1 && rank == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+      const bool used = legal && !empty && (j < a.m || a.dlogp);
+      here[i] = used && (k < head    ? k >= h0 && k < h1
+                         : k < tail0 ? (k - head) / V >= v0 && (k - head) / V < v1
+                                     : last);
+      named_x[i] = here[i] ? to_f32(row[k]) : 0.f;
+      if (j <= a.m) {
+        s_idx[g][j] = used ? k : -1;
+        s_coef[g][j] = used ? named_c[i] : 0.f;
+      }
+    }
+    group_sync<kGroup>();
+    for (int j = 0; j <= a.m; j++) slope -= s_coef[g][j];
     // dx = p (A + B log p) away from the named entries
     const bool bad = !(lse_in < INFINITY);
     const float A = empty ? 0.f
@@ -1031,30 +1052,18 @@ __global__ void __launch_bounds__(256) row_grad_kernel(RowGradArgs a) {
       return ex2(lp * kLog2e) * fmaf(B, lp, A);
     };
     float named[kOwn];
-    bool here[kOwn];  // the named entry lies in this slice
 #pragma unroll
     for (int i = 0; i < kOwn; i++) {
-      const int j = t + i * kGroup;
-      const int k = j <= a.m ? s_idx[g][j] : -1;
-      here[i] = k >= 0 && (k < head    ? k >= h0 && k < h1
-                           : k < tail0 ? (k - head) / V >= v0 && (k - head) / V < v1
-                                       : last);
+      named[i] = 0.f;
       if (here[i]) {
         float c = 0.f;  // an entry may be named more than once
-        for (int q = 0; q <= a.m; q++) c += s_idx[g][q] == k ? s_coef[g][q] : 0.f;
-        named[i] = fmaf(a.scale, c, grad(to_f32(row[k])));
+        for (int q = 0; q <= a.m; q++) c += s_idx[g][q] == named_k[i] ? s_coef[g][q] : 0.f;
+        named[i] = fmaf(a.scale, c, grad(named_x[i]));
       }
     }
     group_sync<kGroup>();
     for (int k = h0 + t; k < h1; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
-    const T* vin = row + head;
-    T* vout = out + head;
-    constexpr int kBatch = 4;
-    for (int v = v0 + t; v < v1; v += kBatch * kGroup) {
-      uint4 r[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; j++)
-        if (v + j * kGroup < v1) r[j] = load16(vin + (int64_t)(v + j * kGroup) * V);
+    for (int v = v0 + t; v < v1;) {
 #pragma unroll
       for (int j = 0; j < kBatch; j++)
         if (v + j * kGroup < v1) {
@@ -1064,15 +1073,15 @@ __global__ void __launch_bounds__(256) row_grad_kernel(RowGradArgs a) {
           for (int e = 0; e < V; e++) x[e] = grad(x[e]);
           *reinterpret_cast<uint4*>(vout + (int64_t)(v + j * kGroup) * V) = Vec16<T>::pack(x);
         }
+      v += kBatch * kGroup;
+      load(v);
     }
     if (last)
       for (int k = tail0 + t; k < a.K; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
     group_sync<kGroup>();
 #pragma unroll
-    for (int i = 0; i < kOwn; i++) {
-      const int j = t + i * kGroup;
-      if (here[i]) from_f32(out + s_idx[g][j], named[i]);
-    }
+    for (int i = 0; i < kOwn; i++)
+      if (here[i]) from_f32(out + named_k[i], named[i]);
     group_sync<kGroup>();
   }
 }
