@@ -190,6 +190,41 @@ def test_alternatives_where_one_thread_holds_them_all(G, K, m):
         _check(G, Z, v, None, m, 1.0)
 
 
+def test_the_most_classes(G):
+    """2^24 classes, with ties at the top and masked stretches."""
+    K = 1 << 24
+    rng = np.random.default_rng(8)
+    x = rng.integers(-40, 9, size=(2, K)).astype(np.float32)
+    x[0, 1000:9000] = -np.inf
+    x[1, K - 3], x[1, 77] = 12.0, 12.0
+    Z, v = _place(x, "bf16", 3, 1)
+    _check(G, Z, v, np.array([5, K - 1], np.int32), 7, 1.0)
+    Zg = Z[:, :1 << 20]
+    _grad_check(G, Zg, v[:, :1 << 20], np.array([5, 77], np.int32), 3, 1.0)
+
+
+def test_rows_that_only_a_stretch_is_left_of(G):
+    """A mask that leaves one stretch of classes: whole warps and CTAs see nothing."""
+    K = 50_000
+    for lo, hi in ((0, 40), (25_000, 25_300), (K - 9, K), (49_000, 49_001)):
+        x = np.full((3, K), -np.inf, np.float32)
+        x[:, lo:hi] = np.random.default_rng(lo).normal(size=(3, hi - lo)) * 30 - 500
+        for dtype in ("f32", "bf16"):
+            Z, v = _place(x, dtype, 1)
+            _check(G, Z, v, np.array([lo, hi - 1, 0], np.int32), 32, 1.0)
+
+
+def test_rising_and_falling_logits(G):
+    """The reference has to follow: rows that rise by hundreds of powers of two, and fall."""
+    K = 40_000
+    ramp = np.linspace(-30_000, 30_000, K).astype(np.float32)
+    x = np.stack([ramp, -ramp, np.abs(ramp), -np.abs(ramp), np.roll(ramp, K // 3)])
+    for dtype in TYPES:
+        Z, v = _place(x, dtype)
+        _check(G, Z, v, np.array([K - 1, 0, 3, K // 2, 9], np.int32), 6, 1.0)
+        _check(G, Z, v, np.array([K - 1, 0, 3, K // 2, 9], np.int32), 0, 0.5)
+
+
 def _grad_case(rng, K, N, m, dtype, pad, shift, masked):
     x = _logits(rng, N, K)
     if masked:
