@@ -16,7 +16,8 @@
 //   - four issue the products, each into an accumulator of its own;
 //   - four take finished accumulators out of tensor memory and add them up.
 // One thread alone takes about 600 cycles to issue a stage's copies and as many for its
-// products, twice what the memory needs to deliver it, so warps take the stages in turn.
+// products, twice what the memory needs to deliver it, so warps take the stages in turn (two
+// instead of four of each: 280 us instead of 222 for 32 tokens of 128 experts).
 // (Gathering the tokens with loads instead costs a proxy fence per stage, which waits for
 // every copy of the thread: a microsecond.)
 // A 128-row tile may be partly filled, and columns may be empty: what stands there from
@@ -27,6 +28,12 @@
 // a token's experts in shared memory, in ascending order.  h is kept as two halves of
 // the weights' type, hi + lo, so that rounding it adds nothing visible to y: columns of
 // their own of the same product, added when they leave tensor memory.
+//
+// Measured: 32 tokens with 8 of 128 experts, 2048 x 768 bf16 (about 1.05 GB of weights):
+// 187 us, 5.6 TB/s; kernel 1 alone reads 5.9 TB/s, kernel 2 4.7.  100 tokens, 4 of 32 experts,
+// 4096 x 1432 fp16: 228 us, 4.9 TB/s.  One token, 8 of 64 experts, 2048 x 1024: 31 us for
+// 100 MB, of which 15 are the reading and 8 the two kernels' starts (the sort 2.4 each).  The
+// tensor pipe is 5 to 11 % busy.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
