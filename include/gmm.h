@@ -457,9 +457,13 @@ gmm_status gmm_route(const gmm_rows* r, const void* Z, int32_t m, int32_t renorm
  * Everything has type dtype (GMM_BF16 or GMM_F16).  Products are summed in float32 in a
  * fixed order, the inner activations are kept to twice the type's precision, and Y is
  * rounded once; an inner activation beyond the type's range is infinite.  The result
- * for a token does not depend on timing.
+ * for a token does not depend on timing.  A NaN or infinity in a token's row of X, in its
+ * weights resp or in an expert's weights reaches only the tokens concerned.
+ * Device-side waits are bounded as gmm_set_wait_budget says; one that gives up raises
+ * GMM_DEVFLAG_WAIT_TIMEOUT, and Y is then not meaningful.
  * T = 0 is allowed and does nothing.  GMM_ERR_UNSUPPORTED: T > 256, E > 1024, D or F not
- * a multiple of 8, GMM_F32, a misaligned pointer.  m as gmm_route, but may exceed E.
+ * a multiple of 8 or above 2^20, 2 E F or E D of 2^31 or more, GMM_F32, a misaligned pointer.
+ * m as gmm_route, but may exceed E.
  */
 typedef enum {
   GMM_ACT_SILU = 0, /* x / (1 + e^-x) */
@@ -505,7 +509,7 @@ gmm_status gmm_trace_fused(void* start_event, void* stop_event);
 
 /*
  * Longest time, in nanoseconds, that any device-side wait of the tensor-core
- * pass spins on a barrier for another warp or CTA before it gives up
+ * pass (or of gmm_moe) spins on a barrier for another warp or CTA before it gives up
  * (default 1e9, one second; 0 restores the default).  A wait that gives up
  * sets GMM_DEVFLAG_WAIT_TIMEOUT in the workspace status word; every other wait
  * of the launch then gives up too, the kernel still waits (up to one second)
