@@ -59,7 +59,7 @@ struct MoeArgs {
   void* Y;
   const int32_t* idx;
   const float* resp;
-  void *h_hi, *h_lo;  // T * m x F
+  void *h_hi, *h_lo;  // T * m x F each, lo directly behind hi
   int T, m, E, D, F;
   int64_t ldy;
   int act;
@@ -329,7 +329,7 @@ template <typename T, bool kDown, int kN>
 __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, MoeBarriers& bar,
                                            MoeJob<kDown, kN> job, char* ring, float* side,
                                            const CUtensorMap* tm64, const CUtensorMap* tm16,
-                                           const CUtensorMap* tok0, const CUtensorMap* tok1) {
+                                           const CUtensorMap* tok) {
   using namespace sm100;
   constexpr int kH = kDown ? 2 : 1;  // halves of a token: x, or h hi and lo
   constexpr int kStage = moe_stage_bytes(kDown, kN);
@@ -365,7 +365,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
 #pragma unroll
       for (int i = 0; i < 4; i++) {  // (past the last token: the last again)
         const int slot = L.slot[j.s0 + min(col + i, j.ntok - 1)];
-        r[i] = kDown ? slot : L.token(slot);
+        r[i] = kDown ? slot + (lane * 4 < kN ? 0 : a.T * a.m) : L.token(slot);  // lo behind hi
       }
       from = make_int4(r[0], r[1], r[2], r[3]);
     };
@@ -382,8 +382,8 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
     };
     auto tokens = [&](int c) {
       if (mine4)
-        tma_gather4(ring + stage * kStage + kMoeTile * 128 + lane * 512,
-                    lane * 4 < kN ? tok0 : tok1, c * kMoeK, from, &bar.full[stage]);
+        tma_gather4(ring + stage * kStage + kMoeTile * 128 + lane * 512, tok, c * kMoeK, from,
+                    &bar.full[stage]);
     };
     // Down: the weights of the first steps do not depend on the kernel before, h does.
     int early = 0;
@@ -595,7 +595,7 @@ __device__ __forceinline__ void moe_up_run(const MoeArgs& a, MoeLists& L, MoeBar
   job.unit = (int)(all * blockIdx.x / gridDim.x);
   job.end = (int)(all * (blockIdx.x + 1) / gridDim.x);
   if (job.more(L)) job.fit(a, L);
-  moe_stream<T, false, kN>(a, L, bar, job, ring, side, tm64, tm16, tok, tok);
+  moe_stream<T, false, kN>(a, L, bar, job, ring, side, tm64, tm16, tok);
 }
 
 template <typename T>
@@ -633,23 +633,21 @@ template <typename T, int kN>
 __device__ __forceinline__ void moe_down_run(const MoeArgs& a, MoeLists& L, MoeBarriers& bar,
                                              char* ring, float* y, int d0, int rows, int rank,
                                              int C, const CUtensorMap* tm64,
-                                             const CUtensorMap* tm16, const CUtensorMap* hi,
-                                             const CUtensorMap* lo) {
+                                             const CUtensorMap* tm16, const CUtensorMap* h) {
   MoeJob<true, kN> job;
   job.f0 = d0;
   job.rows = rows;
   job.act = rank;
   job.stride = C;
   if (job.more(L)) job.fit(a, L);
-  moe_stream<T, true, kN>(a, L, bar, job, ring, y, tm64, tm16, hi, lo);
+  moe_stream<T, true, kN>(a, L, bar, job, ring, y, tm64, tm16, h);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_down_kernel(MoeArgs a, int C, const __grid_constant__ CUtensorMap tm64,
                     const __grid_constant__ CUtensorMap tm16,
-                    const __grid_constant__ CUtensorMap hi,
-                    const __grid_constant__ CUtensorMap lo) {
+                    const __grid_constant__ CUtensorMap h) {
   extern __shared__ __align__(256) char smem[];
   MoeLists& L = *(MoeLists*)smem;
   MoeBarriers& bar = *(MoeBarriers*)(smem + (sizeof(MoeLists) + 255) / 256 * 256);
@@ -667,9 +665,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   sm100::fence_proxy_async_smem();  // the sort's counters lay where TMA writes
   __syncthreads();
   if (moe_columns(a.ring_bytes, true, L.most) == 16)
-    moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+    moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &h);
   else
-    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &hi, &lo);
+    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &h);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // before Y is written
   moe_end(a, bar);
   if (C > 1) sm100::cluster_sync();

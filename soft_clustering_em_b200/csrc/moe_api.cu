@@ -29,18 +29,11 @@ gmm_status check_moe(const gmm_moe_problem* p) {
   return GMM_OK;
 }
 
-// Workspace: status word, then h as hi and lo halves, T * m rows of F each.
-struct MoeLayout {
-  size_t hi, lo, total;
-};
+// Workspace: status word, then h: T * m rows of F hi halves, and as many of lo halves.
+constexpr size_t kMoeH = 256;
 
-MoeLayout moe_layout(const gmm_moe_problem* p) {
-  MoeLayout L;
-  const size_t h = align_up((size_t)p->T * p->m * p->F * 2, 256);
-  L.hi = 256;
-  L.lo = L.hi + h;
-  L.total = L.lo + h;
-  return L;
+size_t moe_bytes(const gmm_moe_problem* p) {
+  return kMoeH + 2 * align_up((size_t)p->T * p->m * p->F * 2, 256);
 }
 
 // A launch that may start while the kernel before it in the stream ends: both kernels wait
@@ -134,15 +127,16 @@ gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const 
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
-  CUtensorMap up64, up16, down64, down16, x1, hi1, lo1;
+  int C = 1;
+  if (!down_shape<T>(p, sms, &C, &a.block_rows)) return api_launched(0), GMM_ERR_CUDA;
+  CUtensorMap up64, up16, down64, down16, x1, h1;
   const uint64_t D = p->D, F = p->F, E = p->E, slots = (uint64_t)p->T * p->m;
   if (!make_tmap_16b_sw128(&up64, W_up, D, E * 2 * F, D * 2, 64) ||
       !make_tmap_16b_sw128(&up16, W_up, D, E * 2 * F, D * 2, 16) ||
       !make_tmap_16b_sw128(&down64, W_down, F, E * D, F * 2, 64) ||
       !make_tmap_16b_sw128(&down16, W_down, F, E * D, F * 2, 16) ||
       !make_tmap_16b_sw128(&x1, X, D, p->T, (uint64_t)p->ldx * 2, 1) ||
-      !make_tmap_16b_sw128(&hi1, a.h_hi, F, slots, F * 2, 1) ||
-      !make_tmap_16b_sw128(&lo1, a.h_lo, F, slots, F * 2, 1))
+      !make_tmap_16b_sw128(&h1, a.h_hi, F, 2 * slots, F * 2, 1))
     return GMM_ERR_CUDA;
   a.wait_ns = api_wait_budget();
   const int fixed = moe_fixed(p->E, p->T * p->m), up_fixed = fixed + kMoeSwap;
@@ -151,13 +145,11 @@ gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const 
               x1))
     return api_launched(0), GMM_ERR_CUDA;
   if ((s = api_launched(1)) != GMM_OK) return s;
-  int C = 1;
-  if (!down_shape<T>(p, sms, &C, &a.block_rows)) return api_launched(0), GMM_ERR_CUDA;
   const int blocks = (p->D + a.block_rows - 1) / a.block_rows;
   const int down_fixed = fixed + p->T * kMoeTile * 4;
   a.ring_bytes = ring_bytes(down_fixed);
   if (!launch(moe_down_kernel<T>, blocks * C, C, down_fixed + 1024 + a.ring_bytes, st, a, C, down64,
-              down16, hi1, lo1))
+              down16, h1))
     return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
@@ -170,7 +162,7 @@ gmm_status gmm_moe_workspace_size(const gmm_moe_problem* p, size_t* bytes) {
   gmm_status s = check_moe(p);
   if (s != GMM_OK) return s;
   if (!bytes) return GMM_ERR_INVALID_ARG;
-  *bytes = moe_layout(p).total;
+  *bytes = moe_bytes(p);
   return GMM_OK;
 }
 
@@ -184,11 +176,11 @@ gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, 
   if ((uintptr_t)X % 16 != 0 || (uintptr_t)W_up % 16 != 0 || (uintptr_t)W_down % 16 != 0 ||
       (uintptr_t)Y % 2 != 0)
     return GMM_ERR_UNSUPPORTED;
-  const MoeLayout L = moe_layout(p);
-  if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
-  char* b = (char*)ws;
-  MoeArgs a = {Y,    idx,    resp,   b + L.hi, b + L.lo, p->T, p->m, p->E,
-               p->D, p->F,   p->ldy, p->act,   0,        0,    0,    (unsigned int*)ws};
+  if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < moe_bytes(p)) return GMM_ERR_WORKSPACE;
+  char* hi = (char*)ws + kMoeH;
+  char* lo = hi + (size_t)p->T * p->m * p->F * 2;
+  MoeArgs a = {Y,    idx,  resp,   hi,     lo, p->T, p->m, p->E,
+               p->D, p->F, p->ldy, p->act, 0,  0,    0,    (unsigned int*)ws};
   cudaStream_t st = (cudaStream_t)stream;
   if (p->dtype == GMM_BF16) return moe_launch<__nv_bfloat16>(p, a, X, W_up, W_down, st);
   return moe_launch<__half>(p, a, X, W_up, W_down, st);

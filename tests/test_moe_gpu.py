@@ -202,6 +202,78 @@ def test_two_streams_and_a_captured_graph(G):
         assert torch.equal(gy, G.gmm_moe(X, i, r, *W))
 
 
+def test_four_threads_at_once(G):
+    """Host threads with a stream and a workspace each."""
+    import threading
+
+    import torch
+
+    rng = np.random.default_rng(14)
+    T, E, D, F, m = 8, 16, 512, 128, 4
+    X, W = _tokens(rng, T, D, "bf16"), _weights(rng, E, D, F, "bf16")
+    idx, resp = G.gmm_route(torch.randn(T, E, device="cuda"), m)
+    want = G.gmm_moe(X, idx, resp, *W)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got = G.gmm_moe(X, idx, resp, *W)
+                s.synchronize()
+                if not torch.equal(got, want):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_the_first_call_of_a_process_may_be_captured(G):
+    """Routing, experts, log probabilities and gradient into a graph before any eager call."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from soft_clustering_em_b200 import gmm as G
+T, E, D, F, m, K = 6, 8, 512, 64, 2, 70_001
+X = torch.randn(T, D, device="cuda").bfloat16()
+U = torch.randn(E, 2 * F, D, device="cuda").mul_(D ** -0.5).bfloat16()
+W = torch.randn(E, D, F, device="cuda").mul_(F ** -0.5).bfloat16()
+Z, L = torch.randn(T, E, device="cuda"), torch.randn(3, K, device="cuda")
+w = torch.ones(3, device="cuda")
+ids = torch.zeros(3, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    i, r = G.gmm_route(Z, m)
+    y = G.gmm_moe(X, i, r, U, W)
+    q = G.gmm_logprobs(L, ids, m=3)
+    d = G.gmm_logprobs_backward(L, ids, q.lse, dlogp=w)
+for _ in range(2):
+    Z.normal_()
+    L.normal_()
+    g.replay()
+    j, s = G.gmm_route(Z, m)
+    p = G.gmm_logprobs(L, ids, m=3)
+    assert torch.equal(i, j) and torch.equal(y, G.gmm_moe(X, j, s, U, W))
+    assert torch.equal(q.top_idx, p.top_idx) and torch.equal(q.lse, p.lse)
+    assert torch.equal(d, G.gmm_logprobs_backward(L, ids, p.lse, dlogp=w))
+print("same")
+"""
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=240)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
+
+
 def test_a_short_budget_times_out_and_the_next_call_is_exact(G):
     import torch
 
