@@ -49,9 +49,6 @@ void short_launch(const RowArgs& a, bool vec, cudaStream_t st) {
 // 20 alternatives: 20.4 us on one CTA each, 17.0 on four; 592 rows of 4,096: 10.5 on one, 77
 // on four.)
 int row_cluster(int64_t N, double row_bytes, int m, int slots) {
-#ifdef RC
-  return RC;
-#endif
   int best = 1;
   double best_us = 1e30;
   for (int C = 1; C <= 8; C *= 2) {
