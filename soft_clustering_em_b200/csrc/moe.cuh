@@ -252,13 +252,13 @@ __device__ __forceinline__ float moe_act(float x, int act) {
 
 // One job.  Up: rows f0 .. f0 + rows of the expert's F, of which every active expert has `per`
 // units of `size` rows; the units are shared out evenly, and up to 64 rows of consecutive ones
-// make a job.  Down: the CTA's block of rows of y,
-// one active expert after the other (every stride-th).
+// make a job.  Down: the CTA's block of rows of y, one active expert after the other (every
+// stride-th).
 template <bool kDown, int kN>
 struct MoeJob {
   int act, f0, rows, s0, ntok;
   int unit, end, per, size;  // up
-  int stride;          // down: CTAs of the cluster
+  int stride;                // down: CTAs of the cluster
 
   __device__ __forceinline__ bool more(const MoeLists& L) const {
     if constexpr (kDown) return act < L.n;
@@ -295,8 +295,7 @@ struct MoeBarriers {
   uint32_t tmem;
 };
 
-// Shared memory: the two structs, the lists; up: 2 x 128 x 33 floats, down: T x 128
-// floats; the
+// Shared memory: the two structs, the lists; up: 2 x 128 x 33 floats, down: T x 128 floats; the
 // stages on a 1024-byte boundary.
 constexpr int kMoeStructs =
     (int)((sizeof(MoeLists) + 255) / 256 * 256 + (sizeof(MoeBarriers) + 255) / 256 * 256);
@@ -465,14 +464,14 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
         mine++;
       }
     }
-    if (!ok && lane == 0) {
-      // What is on its way has to land before the CTA ends: this warp's last steps.  (A wait
-      // that gave up is for a step beyond the first S, and so beyond the early ones.)
-      for (int left = min(mine, S); left > 0; left--) {
+    // What is on its way has to land before the CTA ends, also when it was another warp whose wait
+    // gave up: the last step of each of this warp's stages.  (A wait of its own that gave up is
+    // for a step beyond the first S, and so beyond the early ones.)
+    if (lane == 0)
+      for (int left = min(mine, S / kMoeCopyWarps); left > 0; left--) {
         at -= kMoeCopyWarps;
         mbar_wait_bounded(&bar.full[at % S], (uint32_t)(at / S) & 1u, abort, 0u, kMoeDrainNs);
       }
-    }
   } else if (w >= 4 + kMoeCopyWarps) {
     // ---- products
     if (lane == 0) {

@@ -21,8 +21,8 @@ gmm_status check_moe(const gmm_moe_problem* p) {
   if (p->dtype == GMM_F32) return GMM_ERR_UNSUPPORTED;
   if (p->T > kMoeMaxT || p->E > kMoeMaxE) return GMM_ERR_UNSUPPORTED;
   if (p->D % 8 != 0 || p->F % 8 != 0 || p->ldx % 8 != 0) return GMM_ERR_UNSUPPORTED;
-  if (p->D > (1 << 20) || p->F > (1 << 20) || p->ldx > ((int64_t)1 << 40) ||
-      p->ldy > ((int64_t)1 << 40))
+  if (p->D > (1 << 20) || p->F > (1 << 20) || p->ldx >= ((int64_t)1 << 39) ||  // (a tensor map's row
+      p->ldy > ((int64_t)1 << 40))                                              // stride: 2^40 bytes)
     return GMM_ERR_UNSUPPORTED;
   if ((int64_t)p->E * 2 * p->F >= ((int64_t)1 << 31) || (int64_t)p->E * p->D >= ((int64_t)1 << 31))
     return GMM_ERR_UNSUPPORTED;

@@ -294,6 +294,30 @@ def test_a_short_budget_times_out_and_the_next_call_is_exact(G):
     assert rc == 0 and flags == 0
 
 
+@pytest.mark.parametrize("D,F", [(64, 64), (256, 128), (512, 512)])
+def test_a_short_budget_with_every_copy_on_its_way(G, D, F):
+    """Streams no longer than the ring: no copy waits for a stage, the products give up.  The CTAs
+    end after their copies have landed, so the calls right behind them are exact."""
+    import torch
+
+    rng = np.random.default_rng(D)
+    X, W = _tokens(rng, 5, D, "f16"), _weights(rng, 3, D, F, "f16")
+    idx, resp = G.gmm_route(torch.randn(5, 3, device="cuda"), 2)
+    want = G.gmm_moe(X, idx, resp, *W)
+    p = G.moe_problem(X, idx, W[1])
+    for _ in range(20):
+        ws = torch.zeros(G.gmm_moe_workspace_size(p), dtype=torch.uint8, device="cuda")
+        ws2 = torch.zeros_like(ws)
+        try:
+            G.gmm_set_wait_budget(1)
+            G.gmm_moe(X, idx, resp, *W, ws=ws)
+        finally:
+            G.gmm_set_wait_budget(0)
+        got = G.gmm_moe(X, idx, resp, *W, ws=ws2)
+        assert G.gmm_device_status(ws2) == (0, 0)
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("T,E,D,F,m", [(256, 2, 1024, 512, 2), (70, 3, 264, 712, 2),
                                        (200, 16, 2048, 64, 4), (31, 160, 136, 72, 8)])
 def test_longer_streams(G, T, E, D, F, m):

@@ -108,6 +108,7 @@ def moe_p(T=4, m=2, E=4, D=16, F=8, dtype=G.GMM_BF16, act=0, ldx=16, ldy=16):
     (dict(F=0), BAD), (dict(dtype=5), BAD), (dict(act=2), BAD), (dict(act=-1), BAD),
     (dict(ldx=8), BAD), (dict(ldy=15), BAD), (dict(dtype=G.GMM_F32), UNSUP), (dict(T=257), UNSUP),
     (dict(E=1025), UNSUP), (dict(D=12), UNSUP), (dict(F=12), UNSUP), (dict(ldx=20), UNSUP),
+    (dict(ldx=1 << 39), UNSUP),
     (dict(F=(1 << 20) + 8), UNSUP), (dict(ldy=(1 << 40) + 1), UNSUP),
 ])
 def test_moe_problems(lib, kw, code):
