@@ -425,15 +425,20 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(fn, what, device, stream, *args):
-    """Call fn(*args, stream) with `device` current; stream None: its current stream."""
+def _on(stream, X):
+    """The context of a call on `stream`: what the call allocates belongs to that stream."""
+    if stream.device != X.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {X.device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(fn, what, device, *args):
+    """Call fn(*args, stream) with `device` current, on its current stream."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _launch(fn, what, device, stream, *args)
+            return _launch(fn, what, device, *args)
     # (the raw handle: building a torch.cuda.Stream object costs as much as a launch)
-    s = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-         else stream.cuda_stream)
-    rc = fn(*args, s)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != GMM_OK:
         raise GmmError(rc, what)
 
@@ -454,8 +459,12 @@ def gmm_logprobs(Z, ids=None, m=0, scale=1.0, dev_flags=None, stream=None) -> Ro
 
     Z: N x K float32, bfloat16 or float16, any row stride; the logits are scale * Z.
     ids: N int32, -1 for rows without a label (logp 0).  m <= 32.  dev_flags (1 int32
-    device tensor, optional) collects the device status bits.
+    device tensor, optional) collects the device status bits.  stream (None: the current one)
+    runs the call and owns the results.
     """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_logprobs(Z, ids, m, scale, dev_flags)
     r = _rows(Z, scale)
     N, m = Z.shape[0], int(m)
     _same_device(Z, ids, dev_flags)
@@ -467,7 +476,7 @@ def gmm_logprobs(Z, ids=None, m=0, scale=1.0, dev_flags=None, stream=None) -> Ro
     if m > 0:
         top_idx = torch.empty(N, m, dtype=torch.int32, device=Z.device)
         top_logp = torch.empty(N, m, dtype=torch.float32, device=Z.device)
-    _launch(load_library().gmm_logprobs, "gmm_logprobs", Z.device, stream, ctypes.byref(r),
+    _launch(load_library().gmm_logprobs, "gmm_logprobs", Z.device, ctypes.byref(r),
             Z.data_ptr(), _address(ids), m, _address(logp), entropy.data_ptr(), lse.data_ptr(),
             _address(top_idx), _address(top_logp), _address(dev_flags))
     return RowLogprobs(logp, entropy, lse, top_idx, top_logp)
@@ -482,6 +491,10 @@ def gmm_logprobs_backward(Z, ids, lse, dlogp=None, entropy=None, dentropy=None, 
     lse, entropy and top_idx as gmm_logprobs returned them (entropy only with dentropy, top_idx
     with dtop).  out: N x K of Z's type to write to, Z itself included; allocated when None.
     """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_logprobs_backward(Z, ids, lse, dlogp, entropy, dentropy, dlse, top_idx,
+                                         dtop, scale, out, dev_flags)
     r = _rows(Z, scale)
     N, K = Z.shape
     m = 0 if dtop is None else (dtop.shape[1] if dtop.dim() == 2 else -1)
@@ -501,7 +514,7 @@ def gmm_logprobs_backward(Z, ids, lse, dlogp=None, entropy=None, dentropy=None, 
     o = _rows(out, 1.0)
     if out.dtype != Z.dtype or out.shape != Z.shape:
         raise ValueError("out must have the shape and type of Z")
-    _launch(load_library().gmm_logprobs_backward, "gmm_logprobs_backward", Z.device, stream,
+    _launch(load_library().gmm_logprobs_backward, "gmm_logprobs_backward", Z.device,
             ctypes.byref(r), Z.data_ptr(), _address(ids), lse.data_ptr(), _address(entropy),
             _address(dlogp), _address(dentropy), _address(dlse), m,
             _address(top_idx) if m else None, _address(dtop) if m else None, out.data_ptr(), o.ld,
@@ -513,13 +526,16 @@ def gmm_route(Z, m, renorm=False, scale=1.0, dev_flags=None, stream=None):
     """(idx N x m int32, resp N x m float32): the m most probable classes of each row of logits
     and their probabilities, divided by their sum with renorm; -1 and 0 where classes run out.
     """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_route(Z, m, renorm, scale, dev_flags)
     r = _rows(Z, scale)
     _same_device(Z, dev_flags)
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
     N, m = Z.shape[0], int(m)
     idx = torch.empty(N, max(m, 0), dtype=torch.int32, device=Z.device)
     resp = torch.empty(N, max(m, 0), dtype=torch.float32, device=Z.device)
-    _launch(load_library().gmm_route, "gmm_route", Z.device, stream, ctypes.byref(r),
+    _launch(load_library().gmm_route, "gmm_route", Z.device, ctypes.byref(r),
             Z.data_ptr(), m, int(bool(renorm)), idx.data_ptr(), resp.data_ptr(),
             _address(dev_flags))
     return idx, resp
@@ -531,9 +547,8 @@ def moe_problem(X, idx, W_down, act=GMM_ACT_SILU, out=None) -> gmm_moe_problem:
         raise TypeError(f"X must be bfloat16 or float16, got {X.dtype}")
     T, D = X.shape
     E, _, F = W_down.shape
-    ld = [max(t.stride(0), D) if T <= 1 else t.stride(0) for t in (X, X if out is None else out)]
-    return gmm_moe_problem(T, idx.shape[1], E, D, F, _DTYPES[X.dtype], int(act), ld[0],
-                           D if out is None else ld[1])
+    ldx, ldy = [D if T <= 1 or t is None else t.stride(0) for t in (X, out)]
+    return gmm_moe_problem(T, idx.shape[1], E, D, F, _DTYPES[X.dtype], int(act), ldx, ldy)
 
 
 def gmm_moe_workspace_size(p: gmm_moe_problem) -> int:
@@ -552,7 +567,11 @@ def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, str
     E x 2F x D, W_gate's F rows over W_lin's; W_down: E x D x F.  Returns T x D of X's type.
     ws: a uint8 device tensor of gmm_moe_workspace_size bytes (allocated here when None), its
     first word the device status word: zero it once to read it with gmm_device_status.
+    stream (None: the current one) runs the call and owns what is allocated here.
     """
+    if stream is not None:
+        with _on(stream, X):
+            return gmm_moe(X, idx, resp, W_up, W_down, act, out, ws)
     if X.dim() != 2 or idx.dim() != 2 or W_up.dim() != 3 or W_down.dim() != 3:
         raise ValueError("X is T x D, idx T x m, W_up E x 2F x D, W_down E x D x F")
     (T, D), (E, _, F) = X.shape, W_down.shape
@@ -571,7 +590,7 @@ def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, str
     p = moe_problem(X, idx, W_down, act, out)
     if ws is None:
         ws = torch.empty(gmm_moe_workspace_size(p), dtype=torch.uint8, device=X.device)
-    _launch(load_library().gmm_moe, "gmm_moe", X.device, stream, ctypes.byref(p), X.data_ptr(),
+    _launch(load_library().gmm_moe, "gmm_moe", X.device, ctypes.byref(p), X.data_ptr(),
             idx.data_ptr(), resp.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), out.data_ptr(),
             ws.data_ptr(), ws.numel())
     return out

@@ -274,6 +274,44 @@ print("same")
     assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
 
 
+def test_a_call_on_a_given_stream_owns_its_workspace(G):
+    """The workspace made for a call on another stream is not handed out again before it ran."""
+    import torch
+
+    rng = np.random.default_rng(14)
+    T, E, D, F, m = 7, 9, 256, 128, 2
+    X, W = _tokens(rng, T, D, "bf16"), _weights(rng, E, D, F, "bf16")
+    Z = torch.randn(T, E, device="cuda")
+    idx, resp = G.gmm_route(Z, m)
+    want = G.gmm_moe(X, idx, resp, *W)
+    size = G.gmm_moe_workspace_size(G.moe_problem(X, idx, W[1]))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    out = torch.empty_like(X)
+    G.gmm_moe(X, idx, resp, *W, out=out, stream=side)
+    route = G.gmm_route(Z, m, stream=side)
+    others = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((o == 255).all()) for o in others)
+    assert torch.equal(out, want) and torch.equal(route[0], idx) and torch.equal(route[1], resp)
+
+
+def test_one_token_of_any_stride(G):
+    import torch
+
+    rng = np.random.default_rng(15)
+    W = _weights(rng, 3, 64, 32, "bf16")
+    big = torch.zeros(2, 1001, dtype=torch.bfloat16, device="cuda")
+    big[:, :64] = _tokens(rng, 2, 64, "bf16")
+    idx, resp = G.gmm_route(torch.randn(1, 3, device="cuda"), 2)
+    X, out = big[:1, :64], torch.empty(2, 77, dtype=torch.bfloat16, device="cuda")[:1, :64]
+    assert torch.equal(G.gmm_moe(X, idx, resp, *W, out=out),
+                       G.gmm_moe(X.contiguous(), idx, resp, *W))
+
+
 def test_a_short_budget_times_out_and_the_next_call_is_exact(G):
     import torch
 
