@@ -295,16 +295,17 @@ struct MoeBarriers {
   uint32_t tmem;
 };
 
-// Shared memory: the two structs, the lists; up: 2 x 128 x 33 floats, down: T x 128 floats; the
-// stages on a 1024-byte boundary.
+// Shared memory: the two structs, the lists; up: 2 x 128 x 33 floats, down: T x block_rows floats;
+// the stages on a 1024-byte boundary.
 constexpr int kMoeStructs =
     (int)((sizeof(MoeLists) + 255) / 256 * 256 + (sizeof(MoeBarriers) + 255) / 256 * 256);
 __host__ __device__ constexpr int moe_fixed(int E, int slots) {
   return kMoeStructs + moe_list_bytes(E, slots);
 }
 constexpr int kMoeSwap = 2 * kMoeTile * 33 * 4;
-__host__ __device__ constexpr int moe_stage_bytes(bool down, int kN) {
-  return kMoeTile * 128 + (down ? 2 : 1) * kN * 128;
+// Of a stage: `rows` weight rows and the tokens.
+__host__ __device__ constexpr int moe_stage_bytes(bool down, int kN, int rows) {
+  return rows * 128 + (down ? 2 : 1) * kN * 128;
 }
 
 // Bounded wait on a phase, as mbar_wait_bounded, for waits on the path of every stage: the
@@ -341,16 +342,19 @@ __device__ __forceinline__ bool moe_warp_wait(uint64_t* bar, uint32_t parity,
   return ok && (sm100::mbar_try_wait(bar, parity) || moe_wait(bar, parity, abort, budget_ns));
 }
 
-__host__ __device__ constexpr int moe_stages(int ring_bytes, bool down, int kN) {
-  const int s = ring_bytes / moe_stage_bytes(down, kN) / kMoeCopyWarps * kMoeCopyWarps;
+// (A product reads a whole tile from a stage's start on, of a small last stage past its end.)
+__host__ __device__ constexpr int moe_stages(int ring_bytes, bool down, int kN, int rows) {
+  const int bytes = moe_stage_bytes(down, kN, rows), past = kMoeTile * 128 - bytes;
+  const int s = (ring_bytes - (past > 0 ? past : 0)) / bytes / kMoeCopyWarps * kMoeCopyWarps;
   return s < 16 ? s : 16;
 }
 static_assert(kMoeCopyWarps % kMoeMmaWarps == 0, "a stage has one warp of each kind");
 // Columns of a job's product: more where an expert has more tokens, unless that costs stages.
-__device__ __forceinline__ int moe_columns(int ring_bytes, bool down, int most) {
+__device__ __forceinline__ int moe_columns(int ring_bytes, bool down, int rows, int most) {
   int n = 16;
   for (int wide = 32; wide <= (down ? 32 : 64); wide *= 2)
-    if (most > wide / 2 && moe_stages(ring_bytes, down, wide) >= moe_stages(ring_bytes, down, n))
+    if (most > wide / 2 &&
+        moe_stages(ring_bytes, down, wide, rows) >= moe_stages(ring_bytes, down, n, rows))
       n = wide;
   return n;
 }
@@ -383,13 +387,14 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
                                            const CUtensorMap* tok) {
   using namespace sm100;
   constexpr int kH = kDown ? 2 : 1;  // halves of a token: x, or h hi and lo
-  constexpr int kStage = moe_stage_bytes(kDown, kN);
+  const int tile = kDown ? a.block_rows : kMoeTile;  // weight rows that a stage has room for
+  const int stage_bytes = moe_stage_bytes(kDown, kN, tile);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int K = kDown ? a.F : a.D, steps = (K + kMoeK - 1) / kMoeK;
   // Stages: a multiple of the warps that take them in turn, so that a stage always belongs to
   // the same copying and the same multiplying warp.  (A wait on a phase by its parity means that
   // phase only while the phase before is known to be over.)
-  const int S = moe_stages(a.ring_bytes, kDown, kN);
+  const int S = moe_stages(a.ring_bytes, kDown, kN, tile);
   volatile unsigned int* abort = &bar.abort;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     return moe_wait(b, parity, abort, a.wait_ns);
@@ -421,19 +426,22 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
       from = make_int4(r[0], r[1], r[2], r[3]);
     };
     auto weights = [&](const MoeJob<kDown, kN>& j, int c) {  // by lane 0
-      const uint32_t bytes = (uint32_t)(moe_box_rows(j.rows) * (kDown ? 1 : 2) +
+      const uint32_t bytes = (uint32_t)((kDown ? tile : 2 * moe_box_rows(j.rows)) +
                                         (j.ntok + 3) / 4 * 4 * kH) * 128u;
       const int e = L.act[j.act];
       const int row = kDown ? e * a.D + j.f0 : e * 2 * a.F + j.f0;
-      char* dst = ring + stage * kStage;
+      char* dst = ring + stage * stage_bytes;
       mbar_arrive_expect_tx(&bar.full[stage], bytes);
-      moe_load_rows(dst, tm64, tm16, c * kMoeK, row, j.rows, &bar.full[stage]);
-      if (!kDown)
+      if (kDown) {  // (the box is the block; of the last one it may reach past the expert)
+        tma_load_2d(dst, tm64, c * kMoeK, row, &bar.full[stage]);
+      } else {
+        moe_load_rows(dst, tm64, tm16, c * kMoeK, row, j.rows, &bar.full[stage]);
         moe_load_rows(dst + 64 * 128, tm64, tm16, c * kMoeK, row + a.F, j.rows, &bar.full[stage]);
+      }
     };
     auto tokens = [&](int c) {
       if (mine4)
-        tma_gather4(ring + stage * kStage + kMoeTile * 128 + lane * 512, tok, c * kMoeK, from,
+        tma_gather4(ring + stage * stage_bytes + tile * 128 + lane * 512, tok, c * kMoeK, from,
                     &bar.full[stage]);
     };
     // Down: the weights of the first steps do not depend on the kernel before, h does.
@@ -482,7 +490,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
       const uint32_t idesc = moe_idesc(T(), kH * kN);
       static_assert(kH * kN <= kMoeAccCols, "accumulator columns");
       const uint64_t a0 = sw128_desc(smem_u32(ring), 16, 1024);
-      const uint64_t b0 = sw128_desc(smem_u32(ring) + kMoeTile * 128, 16, 1024);
+      const uint64_t b0 = sw128_desc(smem_u32(ring) + tile * 128, 16, 1024);
       advance(turn);
       for (; ok && job.more(L); job.next(a, L), base += steps, n++) {
         // the accumulator goes by the step within the job, so that a sum's parts do not depend
@@ -495,7 +503,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
         for (; at < base + steps; advance(kMoeMmaWarps)) {
           if (!(ok = wait(&bar.full[stage], parity))) break;
           tc_fence_after_sync();
-          const uint64_t off = (uint64_t)((uint32_t)(stage * kStage) >> 4);
+          const uint64_t off = (uint64_t)((uint32_t)(stage * stage_bytes) >> 4);
 #pragma unroll
           for (int ks = 0; ks < kMoeK / 16; ks++)
             mma_bf16(acc, a0 + off + 2 * ks, b0 + off + 2 * ks, idesc, more || ks > 0);
@@ -549,7 +557,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
             for (int j = 0; j < (kN < 32 ? kN : 32); j++)
               if (j < cnt) {
                 const int s = job.s0 + j0 + j;
-                float* at = side + L.token(L.slot[s]) * kMoeTile + tid;
+                float* at = side + L.token(L.slot[s]) * tile + tid;
                 *at = fmaf(L.gate[s], v[j], *at);
               }
           }
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       if (e < -1 || e >= a.E) atomicOr(a.status, GMM_DEVFLAG_BAD_INDEX);
     }
   moe_sort(a, L, (int*)side);
-  const int columns = moe_columns(a.ring_bytes, false, L.most);
+  const int columns = moe_columns(a.ring_bytes, false, kMoeTile, L.most);
   if (columns == 16)
     moe_up_run<T, 16>(a, L, bar, ring, side, &tm64, &tm16, &tok);
   else if (columns == 32)
@@ -683,26 +691,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 template <typename T, int kN>
 __device__ __forceinline__ void moe_down_run(const MoeArgs& a, MoeLists& L, MoeBarriers& bar,
                                              char* ring, float* y, int d0, int rows, int rank,
-                                             int C, const CUtensorMap* tm64,
-                                             const CUtensorMap* tm16, const CUtensorMap* h) {
+                                             int C, const CUtensorMap* weights,
+                                             const CUtensorMap* h) {
   MoeJob<true, kN> job;
   job.f0 = d0;
   job.rows = rows;
   job.act = rank;
   job.stride = C;
   if (job.more(L)) job.fit(a, L);
-  moe_stream<T, true, kN>(a, L, bar, job, ring, y, tm64, tm16, h);
+  moe_stream<T, true, kN>(a, L, bar, job, ring, y, weights, weights, h);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kMoeThreads, 1)
-    moe_down_kernel(MoeArgs a, int C, const __grid_constant__ CUtensorMap tm64,
-                    const __grid_constant__ CUtensorMap tm16,
+    moe_down_kernel(MoeArgs a, int C, const __grid_constant__ CUtensorMap weights,
                     const __grid_constant__ CUtensorMap h) {
   extern __shared__ __align__(256) char smem[];
   MoeLists& L = *(MoeLists*)smem;
   MoeBarriers& bar = *(MoeBarriers*)(smem + (sizeof(MoeLists) + 255) / 256 * 256);
-  const int tid = threadIdx.x, per = a.T * kMoeTile;
+  const int tid = threadIdx.x, per = a.T * a.block_rows;
   const int fixed = moe_fixed(a.E, a.T * a.m);
   float* y = (float*)(smem + fixed);  // [token][row of the block]
   char* ring = align1024(smem + fixed + per * 4);
@@ -715,16 +722,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   for (int i = tid; i < per; i += kMoeThreads) y[i] = 0.f;
   sm100::fence_proxy_async_smem();  // the sort's counters lay where TMA writes
   __syncthreads();
-  if (moe_columns(a.ring_bytes, true, L.most) == 16)
-    moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &h);
+  if (moe_columns(a.ring_bytes, true, a.block_rows, L.most) == 16)
+    moe_down_run<T, 16>(a, L, bar, ring, y, d0, rows, rank, C, &weights, &h);
   else
-    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &tm64, &tm16, &h);
+    moe_down_run<T, 32>(a, L, bar, ring, y, d0, rows, rank, C, &weights, &h);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // before Y is written
   moe_end(a, bar);
   if (C > 1) sm100::cluster_sync();
   T* Y = (T*)a.Y;
   for (int i = tid; i < per; i += kMoeThreads) {
-    const int tok = i / kMoeTile, row = i % kMoeTile;
+    const int tok = i / a.block_rows, row = i - tok * a.block_rows;
     if (tok % C != rank || row >= rows) continue;
     float v = y[i];
     if (C > 1) {  // the cluster's copies, in CTA order

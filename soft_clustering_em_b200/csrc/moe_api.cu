@@ -65,8 +65,9 @@ constexpr int kMoeSmem = 227 * 1024;
 int ring_bytes(int fixed) { return kMoeSmem - fixed - 1024; }
 
 constexpr int kMostFixed = moe_fixed(kMoeMaxE, kMoeMaxSlots);
-static_assert(moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeMaxT * kMoeTile * 4, true, 16) > 0 &&
-                  moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeSwap, false, 64) > 0,
+static_assert(moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeMaxT * kMoeTile * 4, true, 16,
+                         kMoeTile) > 0 &&
+                  moe_stages(kMoeSmem - 1024 - kMostFixed - kMoeSwap, false, 64, kMoeTile) > 0,
               "a ring at the most tokens");
 
 // How many clusters of C of the down kernel's CTAs (one per SM) are resident at once: they do not
@@ -96,25 +97,31 @@ int down_clusters(int device, int C) {
   return n;
 }
 
-// Rows of y per cluster (a multiple of 16 up to 128) and CTAs per cluster (which share out the
+// Rows of y per cluster (a multiple of 8 up to 128) and CTAs per cluster (which share out the
 // experts): the least time of a CTA, whose step costs by its rows but not below those of about
-// 56, and by its tokens, among the shapes whose clusters are all resident at once (one more
-// would take a second turn: 58 us instead of 42 for 32 tokens).
+// 56, by its tokens, and by how much less than 56 KB of weights its ring holds, among the shapes
+// whose clusters are all resident at once (one more would take a second turn: 58 us instead of 42
+// for 32 tokens).  No odd clusters: 43 of the 45 resident clusters of 3 take 228 us where 37 take
+// 183 and 22 of 6 take 172 (32 tokens, 8 of 128 experts of 2048 x 768).
 template <typename T>
 bool down_shape(const gmm_moe_problem* p, int sms, int* C, int* rows) {
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return false;
-  const int experts = std::min(p->E, p->T * p->m);
+  const int experts = std::min(p->E, p->T * p->m), fixed = moe_fixed(p->E, p->T * p->m);
   *C = 1;
   *rows = kMoeTile;
   double best = 1e30;
   const double tokens = std::min(32.0, (double)p->T * p->m / experts);
-  for (int c = 1; c <= 8 && c <= experts; c++) {
+  for (int c = 1; c <= 8 && c <= experts; c += c == 1 ? 1 : 2) {
     const int fit = c == 1 ? sms : down_clusters<T>(device, c);
     if (fit < 1) return false;
-    for (int r = 16; r <= kMoeTile; r += 16) {
+    for (int r = 8; r <= kMoeTile; r += 8) {
       if ((p->D + r - 1) / r > fit) continue;
-      const double cost = ((experts + c - 1) / c) * (std::max(r, 56) + 8 + 2 * tokens) + 0.01 * c;
+      const int stages =
+          moe_stages(ring_bytes(fixed + p->T * r * 4), true, tokens > 16 ? 32 : 16, r);
+      const double cost = ((experts + c - 1) / c) * (std::max(r, 56) + 8 + 2 * tokens) *
+                              std::max(1.0, 56.0 * 1024 / (128 * r * std::max(stages, 1))) +
+                          0.01 * c;
       if (cost < best) best = cost, *C = c, *rows = r;
     }
   }
@@ -129,12 +136,11 @@ gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const 
   if (s != GMM_OK) return s;
   int C = 1;
   if (!down_shape<T>(p, sms, &C, &a.block_rows)) return api_launched(0), GMM_ERR_CUDA;
-  CUtensorMap up64, up16, down64, down16, x1, h1;
+  CUtensorMap up64, up16, down, x1, h1;
   const uint64_t D = p->D, F = p->F, E = p->E, slots = (uint64_t)p->T * p->m;
   if (!make_tmap_16b_sw128(&up64, W_up, D, E * 2 * F, D * 2, 64) ||
       !make_tmap_16b_sw128(&up16, W_up, D, E * 2 * F, D * 2, 16) ||
-      !make_tmap_16b_sw128(&down64, W_down, F, E * D, F * 2, 64) ||
-      !make_tmap_16b_sw128(&down16, W_down, F, E * D, F * 2, 16) ||
+      !make_tmap_16b_sw128(&down, W_down, F, E * D, F * 2, a.block_rows) ||
       !make_tmap_16b_sw128(&x1, X, D, p->T, (uint64_t)p->ldx * 2, 1) ||
       !make_tmap_16b_sw128(&h1, a.h_hi, F, 2 * slots, F * 2, 1))
     return GMM_ERR_CUDA;
@@ -146,10 +152,10 @@ gmm_status moe_launch(const gmm_moe_problem* p, MoeArgs a, const void* X, const 
     return api_launched(0), GMM_ERR_CUDA;
   if ((s = api_launched(1)) != GMM_OK) return s;
   const int blocks = (p->D + a.block_rows - 1) / a.block_rows;
-  const int down_fixed = fixed + p->T * kMoeTile * 4;
+  const int down_fixed = fixed + p->T * a.block_rows * 4;
   a.ring_bytes = ring_bytes(down_fixed);
-  if (!launch(moe_down_kernel<T>, blocks * C, C, down_fixed + 1024 + a.ring_bytes, st, a, C, down64,
-              down16, h1))
+  if (!launch(moe_down_kernel<T>, blocks * C, C, down_fixed + 1024 + a.ring_bytes, st, a, C, down,
+              h1))
     return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
