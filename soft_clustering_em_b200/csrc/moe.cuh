@@ -11,8 +11,8 @@
 // weights are the M operand (rows of the tile), the tokens the N operand, accumulators
 // in tensor memory, two of them in turn.  The warps have a part each:
 //   - four copy weight tiles and, four rows at a time (gather4), the tokens' elements by TMA
-//     into a ring of stages of 64 along K (mostly eight, 16 KB of weights each: about 130 KB
-//     per SM on their way at any time, on across the jobs);
+//     into a ring of stages of 64 along K (8 to 16 of them, some 130 KB of weights per SM on
+//     their way at any time, on across the jobs);
 //   - four issue the products, each into an accumulator of its own;
 //   - four take finished accumulators out of tensor memory and add them up.
 // One thread alone takes about 600 cycles to issue a stage's copies and as many for its
@@ -30,10 +30,10 @@
 // their own of the same product, added when they leave tensor memory.
 //
 // Measured: 32 tokens with 8 of 128 experts, 2048 x 768 bf16 (about 1.05 GB of weights):
-// 187 us, 5.6 TB/s; kernel 1 alone reads 5.9 TB/s, kernel 2 4.7.  100 tokens, 4 of 32 experts,
-// 4096 x 1432 fp16: 228 us, 4.9 TB/s.  One token, 8 of 64 experts, 2048 x 1024: 31 us for
-// 100 MB, of which 15 are the reading and 8 the two kernels' starts (the sort 2.4 each).  The
-// tensor pipe is 5 to 11 % busy.
+// 179 to 189 us, 5.6 to 5.9 TB/s; kernel 1 alone reads 6.0 TB/s, kernel 2 5.2.  100 tokens, 4 of 32
+// experts, 4096 x 1432 fp16: 228 us, 4.9 TB/s (kernel 2 on 128 SMs, 4.3).  One token, 8 of 64
+// experts, 2048 x 1024: 27 us for 100 MB, of which 15 are the reading and 6 the two kernels'
+// starts.  The tensor pipe is 5 to 13 % busy.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
