@@ -389,6 +389,25 @@ def test_weights_of_other_experts_do_not_reach_a_token(G):
     assert torch.isnan(got[chose]).any(1).all()
 
 
+def test_weights_of_more_than_32_bits(G):
+    """Experts 2^31 elements and 2^32 bytes into the weights, against the same ones by themselves
+    (one choice per token: no sum whose order could differ)."""
+    import torch
+
+    rng = np.random.default_rng(16)
+    E, D, F = 300, 2048, 2048
+    some = [0, 131, 262, 299]
+    X, (U, V) = _tokens(rng, 6, D, "bf16"), _weights(rng, len(some), D, F, "bf16")
+    big_u = torch.zeros(E, 2 * F, D, dtype=U.dtype, device="cuda")
+    big_v = torch.zeros(E, D, F, dtype=U.dtype, device="cuda")
+    big_u[some], big_v[some] = U, V
+    few = torch.tensor([[0], [1], [2], [3], [3], [2]], dtype=torch.int32, device="cuda")
+    many = torch.tensor(some, dtype=torch.int32, device="cuda")[few.long()]
+    resp = torch.rand(6, 1, device="cuda")
+    got = G.gmm_moe(X, many, resp, big_u, big_v)
+    assert torch.equal(got, G.gmm_moe(X, few, resp, U, V)) and bool((got != 0).any(1).all())
+
+
 def test_no_tokens(G):
     import torch
 
