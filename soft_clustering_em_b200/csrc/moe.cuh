@@ -11,7 +11,7 @@
 // weights are the M operand (rows of the tile), the tokens the N operand, accumulators
 // in tensor memory, two of them in turn.  The warps have a part each:
 //   - four copy weight tiles and, four rows at a time (gather4), the tokens' elements by TMA
-//     into a ring of stages of 64 along K (8 to 16 of them, some 130 KB of weights per SM on
+//     into a ring of stages of 64 along K (mostly 8 to 16, some 130 KB of weights per SM on
 //     their way at any time, on across the jobs);
 //   - four issue the products, each into an accumulator of its own;
 //   - four take finished accumulators out of tensor memory and add them up.
