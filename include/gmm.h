@@ -455,8 +455,9 @@ gmm_status gmm_route(const gmm_rows* r, const void* Z, int32_t m, int32_t renorm
  *           word the status word (zero it once; a call leaves it unchanged unless it
  *           raises a bit).  Calls that share it must be ordered on one stream.
  * Everything has type dtype (GMM_BF16 or GMM_F16).  Products are summed in float32 in a
- * fixed order, the inner activations are kept to twice the type's precision, and Y is
- * rounded once; an inner activation beyond the type's range is infinite.  The result
+ * fixed order.  The inner activations are kept as two values of the type: to 2^-17 in relation
+ * (GMM_BF16), or to 2^-22 or, below 2^-14, 2^-36 absolutely (GMM_F16); one beyond the type's
+ * range is infinite.  Y is rounded once.  The result
  * for a token does not depend on timing.  A NaN or infinity in a token's row of X, in its
  * weights resp or in an expert's weights reaches only the tokens concerned.
  * Device-side waits are bounded as gmm_set_wait_budget says; one that gives up raises

@@ -132,3 +132,43 @@ def moe(X, idx, resp, W_up, W_down, act=0):
             h = np.abs(a) * size[F:] + 1.13 * size[:F] * np.abs(up[F:])
             bound[t] += abs(resp[t, j]) * (np.abs(W_down[e]) @ h)
     return Y, bound
+
+
+def to_type(v, dtype):
+    """v (float64) rounded once to bf16 or f16, as float64."""
+    import torch
+
+    t = torch.from_numpy(np.ascontiguousarray(v, np.float64))
+    return t.to({"bf16": torch.bfloat16, "f16": torch.float16}[dtype]).double().numpy()
+
+
+def moe_limit(X, idx, resp, W_up, W_down, act, dtype):
+    """(Y, limit): Y, and for each token the largest 2-norm that Y's error may have.
+
+    A product of the tensor cores over n elements is off by at most (n / 16 + 32) 2^-23 of its
+    magnitudes (16 elements at a time, a step rounded or cut at 2^-23), an activation by 2^-21 in
+    relation, the inner activation h kept in two halves by 2^-17 (bf16) or 2^-22 and 2^-36 (f16).
+    An error d of h reaches y as W_down d, whose norm is at most the spectral norm times d's.
+    With e for all of this in y, the rounded y is off by at most |round(y) - y| + 2 |e|: the
+    distance to the nearest value of the type changes by |e| at most.
+    """
+    X, resp = np.asarray(X, np.float64), np.asarray(resp, np.float64)
+    E, D, F = W_down.shape
+    rel, low = (2.0 ** -17, 0.0) if dtype == "bf16" else (2.0 ** -22, 2.0 ** -36)
+    up_c, down_c = (D / 16 + 32) * 2.0 ** -23, (F / 16 + 32) * 2.0 ** -23
+    Y, _ = moe(X, idx, resp, W_up, W_down, act)
+    limit = np.linalg.norm(to_type(Y, dtype) - Y, axis=1)
+    for t in range(len(X)):
+        for j in range(idx.shape[1]):
+            e = idx[t, j]
+            if not 0 <= e < E:
+                continue
+            up, off = W_up[e] @ X[t], up_c * (np.abs(W_up[e]) @ np.abs(X[t]))
+            a = activation(up[:F], act)
+            h = a * up[F:]
+            dh = (1.13 * off[:F] + 2.0 ** -21 * np.abs(a)) * np.abs(up[F:]) + np.abs(a) * off[F:]
+            dh = dh + rel * np.abs(h) + low
+            dy = np.linalg.norm(W_down[e], 2) * np.linalg.norm(dh)
+            dy += down_c * np.linalg.norm(np.abs(W_down[e]) @ np.abs(h))
+            limit[t] += 2 * abs(resp[t, j]) * dy
+    return Y, limit

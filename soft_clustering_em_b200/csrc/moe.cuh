@@ -26,8 +26,11 @@
 // Kernel 1 (up) holds 64 rows of W_gate over the same 64 rows of W_lin in a tile and
 // writes h for every (token, choice) into the workspace; kernel 2 (down) forms y, summing
 // a token's experts in shared memory, in ascending order.  h is kept as two halves of
-// the weights' type, hi + lo, so that rounding it adds nothing visible to y: columns of
-// their own of the same product, added when they leave tensor memory.
+// the weights' type, hi + lo: columns of their own of the same product, added when they leave
+// tensor memory.  bf16 has float32's range, and the pair 2^-17 of h at worst (2.5e-6 on average,
+// which turns about 0.3 % of y's own roundings; a third half would take as many columns again).
+// fp16 would lose lo below its smallest number, so lo is kept 2^11 times as large, never above hi:
+// the pair then has 2^-22 of h, or 2^-36 where hi itself is below 2^-14.
 //
 // Measured: 32 tokens with 8 of 128 experts, 2048 x 768 bf16 (about 1.05 GB of weights):
 // 179 to 189 us, 5.6 to 5.9 TB/s; kernel 1 alone reads 6.0 TB/s, kernel 2 5.2.  100 tokens, 4 of 32
@@ -54,6 +57,12 @@ constexpr int kMoeK = 64;         // elements along K of a stage
 constexpr int kMoeAccCols = 64;   // of an accumulator, at most
 constexpr int kMoeTmemCols = 2 * kMoeMmaWarps * kMoeAccCols;
 constexpr uint64_t kMoeDrainNs = 1000000000ull;
+
+// What lo is kept multiplied by.
+template <typename T>
+constexpr float kMoeLo = 1.f;
+template <>
+constexpr float kMoeLo<__half> = 2048.f;
 
 struct MoeArgs {
   void* Y;
@@ -543,11 +552,11 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
             for (int j = 0; j < 32; j++) v[j] += u[j];
             if constexpr (kDown && kN == 16) {  // lo beside hi
 #pragma unroll
-              for (int j = 0; j < 16; j++) v[j] += u[j + 16];
+              for (int j = 0; j < 16; j++) v[j] = fmaf(u[j + 16], 1.f / kMoeLo<T>, v[j]);
             } else if constexpr (kDown) {
               tmem_ld32(at + (uint32_t)kN, u);
 #pragma unroll
-              for (int j = 0; j < 32; j++) v[j] += u[j];
+              for (int j = 0; j < 32; j++) v[j] = fmaf(u[j], 1.f / kMoeLo<T>, v[j]);
             }
           }
         }
@@ -578,7 +587,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
               const int64_t at = (int64_t)L.slot[job.s0 + j0 + j] * a.F + job.f0 + row;
               T hi, lo;
               from_f32(&hi, h);
-              const float left = h - to_f32(hi);
+              const float left = (h - to_f32(hi)) * kMoeLo<T>;
               from_f32(&lo, isfinite(left) ? left : 0.f);  // h beyond the type's range stays so
               ((T*)a.h_hi)[at] = hi;
               ((T*)a.h_lo)[at] = lo;
