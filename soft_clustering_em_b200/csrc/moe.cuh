@@ -252,9 +252,10 @@ __device__ __forceinline__ uint32_t moe_idesc(__half, int n) {
 
 __device__ __forceinline__ float moe_act(float x, int act) {
   if (act == GMM_ACT_GELU) {
-    // x Phi(x) with the tanh form of Phi
+    // x Phi(x) with the tanh form of Phi: (1 + tanh u) / 2 = 1 / (1 + e^-2u), which keeps its
+    // digits where tanh u is near -1
     const float u = 0.7978845608028654f * fmaf(0.044715f * x * x, x, x);
-    return 0.5f * x * (1.f + tanhf(u));
+    return x / (1.f + expf(-2.f * u));
   }
   return x / (1.f + expf(-x));
 }

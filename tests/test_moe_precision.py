@@ -125,3 +125,30 @@ def test_what_is_left_where_the_high_halves_cancel(G, dtype, size):
     c, want, tol = _cancelling(dtype, size)
     Y = G.gmm_moe(*_gpu(dtype, *c)).double().cpu().numpy()
     assert (np.abs(Y - want) <= tol).all(), (Y, want, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_activations_far_below_zero(G, dtype, act):
+    """An activation's own error, by itself: one gate value per expert, 2^10 beside and behind it.
+    The exponent, at most 40, is off by 2^-21 in relation, so its power by 2^-15; h by 2^-17 or, in
+    fp16 below 2^-14, by 2^-36."""
+    t = {"bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    v = np.arange(-7.0, 7.25, 0.25)  # (each of the type)
+    n = len(v)
+    W_up = torch.zeros(n, 16, 8, dtype=t, device="cuda")
+    W_up[:, :8, 0] = torch.from_numpy(v).to(t).cuda()[:, None]
+    W_up[:, 8:, 0] = 1024.0
+    W_down = torch.zeros(n, 8, 8, dtype=t, device="cuda")
+    W_down[:, 0, 0] = 8.0
+    X = torch.zeros(n, 8, dtype=t, device="cuda")
+    X[:, 0] = 1.0
+    idx = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+    resp = torch.ones(n, 1, device="cuda")
+    Y = G.gmm_moe(X, idx, resp, W_up, W_down, act=act)[:, 0].double().cpu().numpy()
+    want = P.activation(v, act) * 8192
+    f = torch.finfo(t)
+    tol = np.abs(want) * (f.eps / 2 + 2.0 ** -15 + 2.0 ** -17) + 8 * 2.0 ** -36
+    tol = tol + f.smallest_normal * f.eps / 2
+    assert (np.abs(Y - want) <= tol).all(), (v[np.abs(Y - want) > tol], np.max(np.abs(Y - want) / tol))
