@@ -368,6 +368,8 @@ gmm_status gmm_ivf_build(int64_t N, int32_t K, int32_t m, const int32_t* idx, co
  * A row n of Z holds K logits x, and z_k = scale * x_k in float32 (scale = 1 / T
  * for a temperature T):
  *   lse_n = log sum_k e^{z_k},  log p_k = z_k - lse_n,  H_n = -sum_k p_k log p_k.
+ * (z as rounded decides the order of classes and what is masked; exponents are formed from
+ * scale * x_k before that rounding, the same for the sums and for log p, which is at most 0.)
  * Sums are formed in float32, in a fixed order: results do not change from run to
  * run.  (The order may depend on N: few rows are cut into more slices.)
  *

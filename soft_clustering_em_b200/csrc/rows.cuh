@@ -104,31 +104,38 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
 
 // What a row's sums say.
 struct RowSums {
-  float B, L, H;     // lse = log 2 (B + L), or B + L where B is a logit
+  float B, L, H;     // lse = log 2 (B + L), or scale B + L where B is an x
+  float scale;
   bool bad, empty;   // a NaN or +inf in the row; nothing but masked classes
   bool logit;
   // relative to B = about the largest c x
-  static __device__ __forceinline__ RowSums near(const Part& p) {
+  static __device__ __forceinline__ RowSums near(const Part& p, float scale) {
     const float l = log2f(p.S);
-    return {p.B, l, fmaxf(kLn2 * (l - p.U / p.S), 0.f), false, false, false};
+    return {p.B, l, fmaxf(kLn2 * (l - p.U / p.S), 0.f), scale, false, false, false};
   }
-  // relative to the largest logit x itself, t = c (x_k - x)
+  // relative to the largest x, t = c (x_k - x)
   static __device__ __forceinline__ RowSums at(float x, float scale, float S, float U) {
     const float Z = x * scale, l = logf(S);
-    return {Z, l, fmaxf(fmaf(-kLn2, U / S, l), 0.f), !(Z < INFINITY), Z == -INFINITY, true};
+    return {x, l, fmaxf(fmaf(-kLn2, U / S, l), 0.f), scale, !(Z < INFINITY), Z == -INFINITY, true};
   }
   __device__ __forceinline__ float lse() const {
-    return logit ? B + L : kLn2 * (B + L);
+    return logit ? fmaf(B, scale, L) : kLn2 * (B + L);
   }
-  __device__ __forceinline__ float log_p(float z) const {
-    if (logit) return (z - B) - L;
-    return fabsf(z) < kNear ? kLn2 * (fmaf(z, kLog2e, -B) - L) : z - lse();
+  // Of a class at x: from the exponent that the sums had for it.  (From z, a product rounded
+  // otherwise, log p is off by up to |z| 2^-23, and above 0 for a class that has the row to
+  // itself: 3e-4 at a scale of 100 and an x of 60.)
+  __device__ __forceinline__ float log_p(float x) const {
+    const float z = x * scale;
+    const float d = logit             ? fmaf(x - B, scale, -L)
+                    : fabsf(z) < kNear ? kLn2 * (fmaf(x, scale * kLog2e, -B) - L)
+                                       : z - lse();
+    return fminf(d, 0.f);
   }
 };
 
-// By one thread: lse, entropy and the log p of row n's label id, whose logit is z.
+// By one thread: lse, entropy and the log p of row n's label id, which stands at x.
 __device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const RowSums& s, int id,
-                                          float z) {
+                                          float x) {
   const float nan = __int_as_float(0x7fffffff);
   if (s.bad && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
   if (a.lse) a.lse[n] = s.bad ? nan : s.empty ? -INFINITY : s.lse();
@@ -136,21 +143,20 @@ __device__ __forceinline__ void write_row(const RowArgs& a, int64_t n, const Row
   if (a.ids) {
     const bool legal = id >= 0 && id < a.K;
     if (id != -1 && !legal && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    a.logp[n] = id == -1               ? 0.f  // no label
-                : s.bad || !legal      ? nan
-                : z == -INFINITY       ? -INFINITY
-                                       : s.log_p(z);
+    a.logp[n] = id == -1                   ? 0.f  // no label
+                : s.bad || !legal          ? nan
+                : x * a.scale == -INFINITY ? -INFINITY
+                                           : s.log_p(x);
   }
 }
 
-// Alternative j of row n: class k (-1: none) at z; sel: log of the m chosen classes'
+// Alternative j of row n: class k (-1: none) of this log p; sel: log of the m chosen classes'
 // probability.
-__device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, int k, float z,
+__device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, int k, float lp,
                                           const RowSums& s, float sel) {
   const float nan = __int_as_float(0x7fffffff);
   const bool none = s.bad || k < 0;
   a.top_idx[n * a.m + j] = none ? -1 : k;
-  const float lp = s.log_p(z);
   float v;
   if (a.route == 0)
     v = s.bad ? nan : none ? -INFINITY : lp;
@@ -285,9 +291,8 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 5) row_short_kernel(RowAr
     if (l == 0 && live) {
       const int id = a.ids ? a.ids[n] : -1;
       const bool legal = id >= 0 && id < a.K;
-      write_row(a, n, row_sums, id, legal ? to_f32(row[id]) * a.scale : 0.f);
+      write_row(a, n, row_sums, id, legal ? to_f32(row[id]) : 0.f);
     }
-    float sel = 0.f;
     float last_z = INFINITY;  // the entry taken last: what follows it in the order is left
     int last_k = -1;
     for (int j0 = 0; j0 < a.m; j0 += kLanes) {
@@ -330,10 +335,17 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 5) row_short_kernel(RowAr
           mine_z = best;
           mine_k = last_k;
         }
-        if (a.route == 2 && !none) sel += ex2(row_sums.log_p(best) * kLog2e);
       }
-      if (l < cnt && live)
-        write_alt(a, n, j0 + l, mine_k, mine_z, row_sums, a.route == 2 ? logf(sel) : 0.f);
+      // (at a scale of 1 z is x, else x is still in L1)
+      const float lp = row_sums.log_p(a.scale == 1.f || mine_k < 0 ? mine_z : to_f32(row[mine_k]));
+      float sel = 0.f;
+      if (a.route == 2) {  // (m is at most 8: all of them in this one round)
+        sel = mine_k < 0 ? 0.f : expf(lp);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sel += __shfl_xor_sync(0xffffffffu, sel, o);
+        sel = logf(sel);
+      }
+      if (l < cnt && live) write_alt(a, n, j0 + l, mine_k, lp, row_sums, sel);
     }
   }
 }
@@ -473,8 +485,8 @@ struct RowShared {
   Part total;
   FarSums far;  // with near == 0
   int near;     // total is good
-  int id;       // the row's label and its logit
-  float id_z;
+  int id;       // the row's label and its x
+  float id_x;
   int count;
   float least;  // lower bound of the m-th largest z
   uint32_t lane_top[kRowWarps * kRowLists];
@@ -721,7 +733,7 @@ __device__ __forceinline__ RowSums join_sums(const RowShared& sh, int C, float s
     }
   }
   const int best = __reduce_max_sync(0xffffffffu, kind);
-  if (best == 1) return RowSums::near(part_reduce<32>(kind == 1 ? p : part_empty()));
+  if (best == 1) return RowSums::near(part_reduce<32>(kind == 1 ? p : part_empty()), scale);
   if (kind != best) f = {-INFINITY, 0.f, 0.f};
   float X = f.X;
 #pragma unroll
@@ -772,7 +784,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
     if (rank == 0 && t == kRowThreads - 1 && a.ids) {  // read while the row streams
       const int id = a.ids[n];
       sh.id = id;
-      sh.id_z = id >= 0 && id < a.K ? s.x(id) * a.scale : 0.f;
+      sh.id_x = id >= 0 && id < a.K ? s.x(id) : 0.f;
     }
     if (kAlt && t == 0) sh.count = 0;
     auto raise = [&](float x) {
@@ -916,7 +928,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
       // (thread 0 wrote these; only its warp uses them)
       if (w == 0) {
         __syncwarp();
-        sums = sh.near ? RowSums::near(sh.total)
+        sums = sh.near ? RowSums::near(sh.total, a.scale)
                        : RowSums::at(sh.far.X, a.scale, sh.far.S, sh.far.U);
       }
     } else {
@@ -934,15 +946,14 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
       }
     }
     if (rank == 0 && w == 0) {
-      if (lane == 0) write_row(a, n, sums, a.ids ? sh.id : -1, sh.id_z);
+      if (lane == 0) write_row(a, n, sums, a.ids ? sh.id : -1, sh.id_x);
       if (kAlt) {
-        float sel = 0.f;
-        if (a.route == 2)
-          for (int j = 0; j < a.m; j++)
-            if (alt[j]) sel += expf(sums.log_p(key_z(alt[j])));
-        if (lane < a.m)
-          write_alt(a, n, lane, alt[lane] ? (int)key_idx(alt[lane]) : -1, key_z(alt[lane]), sums,
-                    logf(sel));
+        // (at a scale of 1 z is x, else x is read once more)
+        const uint64_t key = lane < a.m ? alt[lane] : 0;
+        const int k = key ? (int)key_idx(key) : -1;
+        const float lp = sums.log_p(a.scale == 1.f || k < 0 ? key_z(key) : s.x(k));
+        const float sel = a.route == 2 ? logf(warp_sum(k < 0 ? 0.f : expf(lp))) : 0.f;
+        if (lane < a.m) write_alt(a, n, lane, k, lp, sums, sel);
       }
     }
     if (C > 1)
