@@ -416,7 +416,9 @@ gmm_status gmm_logprobs(const gmm_rows* r, const void* Z, const int32_t* ids, in
  * N x m, with m = 0 and NULL for none):
  *   dx_k = scale * ( dlogp [k = id] + sum_j dtop_j [k = top_idx_j]
  *          + p_k (dlse - dlogp - sum_j dtop_j - dentropy (log p_k + H)) )
- * rounded once to dtype.
+ * rounded once to dtype.  p_k comes from lse, whose rounding costs it 3 |lse| 2^-24 in
+ * relation; a row with an |lse| of 1024 or more is summed once more instead (its time
+ * about doubles).
  *   ids, lse, entropy, top_idx   as gmm_logprobs took and wrote them (entropy may be
  *             NULL without dentropy, ids without dlogp).  An index of -1 has no
  *             gradient; any other outside [0, K) has none either and raises

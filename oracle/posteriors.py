@@ -12,14 +12,21 @@ def logits(x, scale=1.0):
         return (np.asarray(x, np.float32) * np.float32(scale)).astype(np.float64)
 
 
-def _rowwise(z):
+def _sums(z):
+    """(bad, empty, base, log sum of e^{z - base}) per row, base the largest z (or 0).  The two
+    are kept apart: beside a base of -3e38 the logarithm would be lost."""
     bad = np.isnan(z).any(1) | (z == np.inf).any(1)
     M = np.where(bad, 0.0, z.max(1))
     empty = M == -np.inf
     base = np.where(empty, 0.0, M)
     with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
-        lse = base + np.log(np.exp(z - base[:, None]).sum(1))
-    return bad, empty, np.where(bad, np.nan, lse)
+        log_sum = np.log(np.exp(z - base[:, None]).sum(1))
+    return bad, empty, base, np.where(bad, np.nan, log_sum)
+
+
+def _rowwise(z):
+    bad, empty, base, log_sum = _sums(z)
+    return bad, empty, base + log_sum
 
 
 def order(z, m):
@@ -36,10 +43,12 @@ def order(z, m):
 def logprobs(x, ids, m, scale=1.0):
     """(logp, entropy, lse, top_idx, top_logp)."""
     z = logits(x, scale)
-    bad, empty, lse = _rowwise(z)
+    bad, empty, base, log_sum = _sums(z)
+    lse = base + log_sum
     rows = np.arange(len(z))
     with np.errstate(invalid="ignore"):
-        lp = np.where((z == -np.inf) | empty[:, None], -np.inf, z - lse[:, None])
+        lp = np.where((z == -np.inf) | empty[:, None], -np.inf,
+                      (z - base[:, None]) - log_sum[:, None])
         p = np.exp(lp)
         H = -np.where(p > 0, p * np.where(p > 0, lp, 0.0), 0.0).sum(1)
     H = np.where(bad, np.nan, H)
@@ -59,7 +68,11 @@ def logprobs(x, ids, m, scale=1.0):
 
 def gradient(x, ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop, scale=1.0):
     """Gradient with respect to x; lse and entropy are taken as given."""
-    z = logits(x, scale)
+    return _gradient(logits(x, scale), ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop,
+                     scale)
+
+
+def _gradient(z, ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop, scale):
     N, K = z.shape
     lse = np.asarray(lse, np.float64)
     empty = lse == -np.inf
@@ -93,17 +106,70 @@ def gradient(x, ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop, scale=1
     return np.float64(np.float32(scale)) * g
 
 
+FAR_LSE = 1024.0  # rows with an |lse| from here on are summed once more by the gradient
+
+
+def gradient_limit(x, ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop, scale, eps,
+                   smallest):
+    """(gradient, tolerance per entry) for a gradient that is rounded to a type of this eps and
+    smallest normal number.  u = 2^-24:
+      log p  from the given lse: off by u (|z| + |lse| + |log p|).  In rows with |lse| >= FAR_LSE
+             from the row's own sum: by u (4 |z - max| + K / 32 + 64), and lse is exact here;
+             p in relation by that, 3 u |log p| and 2^-21 (the hardware exponential), and whole
+             below 2^-126;
+      sums   of the m + 4 terms in brackets: (8 + m) u of their magnitudes;
+      named  entries alone (a label's, an alternative's): (m + 4) u of the magnitudes given to
+             them;
+    and half a step of the type.
+    """
+    u = 2.0 ** -24
+    z = logits(x, scale)
+    N, K = z.shape
+    lse = np.asarray(lse, np.float64)
+    far = np.isfinite(lse) & (np.abs(lse) >= FAR_LSE)
+    _, _, base, log_sum = _sums(z)
+    z = np.where(far[:, None], z - base[:, None], z)  # the same row, its largest z at 0
+    lse = np.where(far, log_sum, lse)
+    want = _gradient(z, ids, lse, entropy, dlogp, dentropy, dlse, top_idx, dtop, scale)
+    live = np.isfinite(z) & np.isfinite(lse)[:, None]
+    zz, ll = np.where(live, z, 0.0), np.where(np.isfinite(lse), lse, 0.0)[:, None]
+    lp = np.where(live, zz - ll, -200.0)
+    p = np.where(live, np.exp(np.minimum(lp, 0.0)), 0.0)
+    zero = np.zeros(N)
+    h = zero if dentropy is None else np.abs(np.asarray(dentropy, np.float64))
+    H = zero if entropy is None else np.abs(np.nan_to_num(np.asarray(entropy, np.float64)))
+    mag = zero + sum(np.abs(d) for d in (dlogp, dlse) if d is not None)
+    m = 0 if dtop is None else dtop.shape[1]
+    named = np.zeros((N, K))
+    pairs = [] if dlogp is None else [(ids, dlogp)]
+    pairs += [(top_idx[:, j], dtop[:, j]) for j in range(m)]
+    for i, d in pairs:
+        use = (i >= 0) & (i < K)
+        np.add.at(named, (np.arange(N), np.where(use, i, 0)), np.where(use, np.abs(d), 0.0))
+    if m:
+        mag = mag + np.abs(dtop).sum(1)
+    terms = mag[:, None] + h[:, None] * (np.abs(lp) + H[:, None])
+    off_lp = np.where(far[:, None], u * (4 * np.abs(zz) + K / 32 + 64),
+                      u * (np.abs(zz) + np.abs(ll) + np.abs(lp)))
+    off_lp = np.where(live, off_lp, 0.0)
+    rel_p = off_lp + 3 * u * np.abs(lp) + 2.0 ** -21
+    tol = p * (terms * (rel_p + (8 + m) * u) + h[:, None] * off_lp) + live * terms * 2.0 ** -126
+    tol = scale * (tol + (m + 4) * u * named)
+    return want, tol * 1.01 + np.abs(want) * (eps / 2 + 2 * u) + smallest * eps
+
+
 def route(x, m, renorm, scale=1.0):
     """(idx, resp)."""
     z = logits(x, scale)
-    bad, empty, lse = _rowwise(z)
+    bad, empty, base, log_sum = _sums(z)
     idx = order(np.where(np.isnan(z), -np.inf, z), m)
     idx[bad] = -1
     zj = np.where(idx >= 0, np.take_along_axis(z, np.maximum(idx, 0), 1), -np.inf)
     if renorm:
-        lse = _rowwise(zj)[2]
+        _, _, base, log_sum = _sums(zj)
+    log_sum = np.where(np.isinf(log_sum), 0.0, log_sum)
     with np.errstate(invalid="ignore"):
-        resp = np.where(idx >= 0, np.exp(zj - np.where(np.isinf(lse), 0.0, lse)[:, None]), 0.0)
+        resp = np.where(idx >= 0, np.exp((zj - base[:, None]) - log_sum[:, None]), 0.0)
     resp[bad] = np.nan
     return idx, resp
 

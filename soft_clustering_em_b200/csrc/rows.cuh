@@ -972,6 +972,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
 // Entries that a label or an alternative names are evaluated once more by the
 // thread that holds the index, before the row is overwritten (dZ may be Z).
 //
+// What lse's rounding costs p is 3 |lse| 2^-24 in relation.  Rows with an |lse| from kFarLse on
+// (2^-12) are therefore summed once more, by one group for the whole row: at the type's lowest value,
+// say, lse has no digit of log K left.
+//
 // HBM bounds it: 4096 rows of 131,072 bf16 take 327 us (6.6 TB/s read and written).  Short
 // rows wait for their scalars first, so those and the first vectors are loaded together:
 // 60,001 rows of 1,024 fp32 with four alternatives 92 us (5.4 TB/s), 112 one after another.
@@ -981,6 +985,7 @@ struct RowGradArgs {
   int64_t N, ld, ldd;
   int K;
   int slices;  // per row
+  unsigned blocks;  // of the grid, for the slices
   float scale;
   const int32_t* ids;
   const float *lse, *entropy, *dlogp, *dentropy, *dlse;
@@ -990,6 +995,8 @@ struct RowGradArgs {
   uint32_t* flags;
 };
 
+constexpr float kFarLse = 1024.f;
+
 template <int kGroup>
 __device__ __forceinline__ void group_sync() {
   if constexpr (kGroup == 32)
@@ -998,121 +1005,200 @@ __device__ __forceinline__ void group_sync() {
     __syncthreads();
 }
 
+// The row's largest x and log sum_k e^{scale (x_k - x)}, by a group; part: a float per warp.
 template <typename T, int kGroup>
-__global__ void __launch_bounds__(256, kGroup == 32 ? 4 : 5) row_grad_kernel(RowGradArgs a) {
+__device__ __noinline__ float2 grad_row_sums(const T* row, int K, float scale, float* part) {
+  const int t = threadIdx.x % kGroup, w = t >> 5;
+  constexpr int kAhead = 8;
+  auto each = [&](auto f) {
+    for (int k = t; k < K; k += kAhead * kGroup) {
+      float x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; j++)
+        x[j] = k + j * kGroup < K ? to_f32(row[k + j * kGroup]) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kAhead; j++) f(x[j]);
+    }
+  };
+  auto join = [&](float v, auto f) {  // in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (kGroup > 32) {
+      __syncthreads();
+      if ((t & 31) == 0) part[w] = v;
+      __syncthreads();
+      v = part[0];
+      for (int i = 1; i < kGroup / 32; i++) v = f(v, part[i]);
+    }
+    return v;
+  };
+  float X = -FLT_MAX, S = 0.f;
+  each([&](float x) { X = fmaxf(X, x); });
+  X = join(X, [](float a, float b) { return fmaxf(a, b); });
+  const float c = scale * kLog2e;
+  each([&](float x) { S += ex2(fmaxf((x - X) * c, kFloorT)); });
+  return make_float2(X, logf(join(S, [](float a, float b) { return a + b; })));
+}
+
+struct GradShared {  // of a group
+  int idx[kMaxAlt + 1];
+  float coef[kMaxAlt + 1];
+  float part[8];  // a float per warp
+};
+
+__device__ __forceinline__ bool grad_is_far(float lse) {
+  return fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY;
+}
+
+// Slice `rank` of `slices` of row n; of a row far from 0 the first slice is all of it (without kFar
+// it is left as it is).
+template <typename T, int kGroup, bool kFar>
+__device__ __forceinline__ void grad_row(const RowGradArgs& a, int64_t n, int rank, int slices,
+                                         GradShared& sh) {
   constexpr int V = Vec16<T>::n;
-  constexpr int kGroups = 256 / kGroup;
   constexpr int kBatch = 4;  // 16-byte vectors in flight per thread
   constexpr int kOwn = (kMaxAlt + 1 + kGroup - 1) / kGroup;
-  __shared__ int s_idx[kGroups][kMaxAlt + 1];
-  __shared__ float s_coef[kGroups][kMaxAlt + 1];
-  const int g = threadIdx.x / kGroup, t = threadIdx.x % kGroup;
+  const int t = threadIdx.x % kGroup;
+  const T* row = (const T*)a.Z + n * a.ld;
+  T* out = (T*)a.dZ + n * a.ldd;
+  const uint32_t off = (uint32_t)((uintptr_t)row & 15u);
+  const bool together = off == (uint32_t)((uintptr_t)out & 15u);  // else entry by entry
+  const int head = together ? min(a.K, (int)(((16u - off) & 15u) / sizeof(T))) : a.K;
+  const int nv = (a.K - head) / V;
+  const int tail0 = head + nv * V;
+  int h0 = (int)((int64_t)head * rank / slices);
+  int h1 = (int)((int64_t)head * (rank + 1) / slices);
+  int v0 = (int)((int64_t)nv * rank / slices);
+  int v1 = (int)((int64_t)nv * (rank + 1) / slices);
+  bool last = rank == slices - 1;
+
+  // The first vectors are on their way while the row's scalars are read.  (Nobody else
+  // writes this slice, so what is loaded early is what stands there.)
+  const T* vin = row + head;
+  T* vout = out + head;
+  uint4 r[kBatch];
+  auto load = [&](int v) {
+#pragma unroll
+    for (int j = 0; j < kBatch; j++)
+      if (v + j * kGroup < v1) r[j] = load16(vin + (int64_t)(v + j * kGroup) * V);
+  };
+  load(v0 + t);
+
+  // So are the scalars, all at once, and then the named entries: alternatives 0..m-1, the label.
+  const float lse_in = a.lse[n];
+  const int id = a.ids ? a.ids[n] : -1;
+  float slope = a.dlse ? a.dlse[n] : 0.f;
+  const float h = a.dentropy ? a.dentropy[n] : 0.f;
+  const float H = a.dentropy ? a.entropy[n] : 0.f;
+  int named_k[kOwn];
+  float named_c[kOwn], named_x[kOwn];
+  bool here[kOwn];  // the entry exists and lies in this slice
+#pragma unroll
+  for (int i = 0; i < kOwn; i++) {
+    const int j = t + i * kGroup;
+    named_k[i] = j < a.m ? a.top_idx[n * a.m + j] : j == a.m ? id : -1;
+    named_c[i] = j < a.m ? a.dtop[n * a.m + j] : j == a.m && a.dlogp ? a.dlogp[n] : 0.f;
+  }
+  const bool empty = lse_in == -INFINITY;
+  float X = 0.f, lse = empty ? INFINITY : lse_in;  // log p = scale (x - X) - lse
+  if (grad_is_far(lse_in)) {
+    if (!kFar || rank > 0) return;
+    const float2 sums = grad_row_sums<T, kGroup>(row, a.K, a.scale, sh.part);
+    X = sums.x;
+    lse = sums.y;
+    h0 = v0 = 0;
+    h1 = head;
+    v1 = nv;
+    last = true;
+    load(t);
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; i++) {
+    const int j = t + i * kGroup, k = named_k[i];
+    const bool legal = k >= 0 && k < a.K;
+    if (!legal && k != -1 && rank == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+    const bool used = legal && !empty && (j < a.m || a.dlogp);
+    here[i] = used && (k < head    ? k >= h0 && k < h1
+                       : k < tail0 ? (k - head) / V >= v0 && (k - head) / V < v1
+                                   : last);
+    named_x[i] = here[i] ? to_f32(row[k]) : 0.f;
+    if (j <= a.m) {
+      sh.idx[j] = used ? k : -1;
+      sh.coef[j] = used ? named_c[i] : 0.f;
+    }
+  }
+  group_sync<kGroup>();
+  for (int j = 0; j <= a.m; j++) slope -= sh.coef[j];
+  // dx = p (A + B log p) away from the named entries
+  const bool bad = !(lse_in < INFINITY);
+  const float A = empty ? 0.f
+                  : bad ? __int_as_float(0x7fffffff)
+                        : a.scale * (slope - h * H);
+  const float B = empty || bad ? 0.f : -a.scale * h;
+  auto grad = [&](float x) {
+    const float lp = fmaxf(fmaf(kFar ? x - X : x, a.scale, -lse), kFloorD);
+    return ex2(lp * kLog2e) * fmaf(B, lp, A);
+  };
+  float named[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; i++) {
+    named[i] = 0.f;
+    if (here[i]) {
+      float c = 0.f;  // an entry may be named more than once
+      for (int q = 0; q <= a.m; q++) c += sh.idx[q] == named_k[i] ? sh.coef[q] : 0.f;
+      named[i] = fmaf(a.scale, c, grad(named_x[i]));
+    }
+  }
+  group_sync<kGroup>();
+  for (int k = h0 + t; k < h1; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
+  for (int v = v0 + t; v < v1;) {
+#pragma unroll
+    for (int j = 0; j < kBatch; j++)
+      if (v + j * kGroup < v1) {
+        float x[V];
+        Vec16<T>::unpack(r[j], x);
+#pragma unroll
+        for (int e = 0; e < V; e++) x[e] = grad(x[e]);
+        *reinterpret_cast<uint4*>(vout + (int64_t)(v + j * kGroup) * V) = Vec16<T>::pack(x);
+      }
+    v += kBatch * kGroup;
+    load(v);
+  }
+  if (last)
+    for (int k = tail0 + t; k < a.K; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
+  group_sync<kGroup>();
+#pragma unroll
+  for (int i = 0; i < kOwn; i++)
+    if (here[i]) from_f32(out + named_k[i], named[i]);
+  group_sync<kGroup>();
+}
+
+// Rows of a warp each: those far from 0 go to blocks of their own behind the others (in the others'
+// loop they cost every row: 60,001 x 1,024 fp32 took 103 us, so it takes 95, without them 91).
+template <typename T>
+__device__ __forceinline__ void grad_far_rows(const RowGradArgs& a, GradShared& sh) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = (int64_t)(gridDim.x - a.blocks) * 8;
+  for (int64_t n0 = (int64_t)(blockIdx.x - a.blocks) * 8 + (threadIdx.x >> 5); n0 < a.N;
+       n0 += 32 * step) {
+    const int64_t n = n0 + lane * step;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, n < a.N && grad_is_far(a.lse[n])); todo;
+         todo &= todo - 1)
+      grad_row<T, 32, true>(a, n0 + (__ffs(todo) - 1) * step, 0, 1, sh);
+  }
+}
+
+template <typename T, int kGroup>
+__global__ void __launch_bounds__(256, kGroup == 32 ? 4 : 5) row_grad_kernel(RowGradArgs a) {
+  constexpr int kGroups = 256 / kGroup;
+  __shared__ GradShared sh[kGroups];
+  const int g = threadIdx.x / kGroup;
+  if constexpr (kGroup == 32)
+    if (blockIdx.x >= a.blocks) return grad_far_rows<T>(a, sh[g]);
   const int64_t items = a.N * a.slices;
-  for (int64_t it = (int64_t)blockIdx.x * kGroups + g; it < items;
-       it += (int64_t)gridDim.x * kGroups) {
+  for (int64_t it = (int64_t)blockIdx.x * kGroups + g; it < items; it += (int64_t)a.blocks * kGroups) {
     const int64_t n = it / a.slices;
-    const int rank = (int)(it - n * a.slices);
-    const T* row = (const T*)a.Z + n * a.ld;
-    T* out = (T*)a.dZ + n * a.ldd;
-    const uint32_t off = (uint32_t)((uintptr_t)row & 15u);
-    const bool together = off == (uint32_t)((uintptr_t)out & 15u);  // else entry by entry
-    const int head = together ? min(a.K, (int)(((16u - off) & 15u) / sizeof(T))) : a.K;
-    const int nv = (a.K - head) / V;
-    const int tail0 = head + nv * V;
-    const int h0 = (int)((int64_t)head * rank / a.slices);
-    const int h1 = (int)((int64_t)head * (rank + 1) / a.slices);
-    const int v0 = (int)((int64_t)nv * rank / a.slices);
-    const int v1 = (int)((int64_t)nv * (rank + 1) / a.slices);
-    const bool last = rank == a.slices - 1;
-
-    // The first vectors are on their way while the row's scalars are read.  (Nobody else
-    // writes this slice, so what is loaded early is what stands there.)
-    const T* vin = row + head;
-    T* vout = out + head;
-    uint4 r[kBatch];
-    auto load = [&](int v) {
-#pragma unroll
-      for (int j = 0; j < kBatch; j++)
-        if (v + j * kGroup < v1) r[j] = load16(vin + (int64_t)(v + j * kGroup) * V);
-    };
-    load(v0 + t);
-
-    // So are the scalars, all at once, and then the named entries: alternatives 0..m-1, the label.
-    const float lse_in = a.lse[n];
-    const int id = a.ids ? a.ids[n] : -1;
-    float slope = a.dlse ? a.dlse[n] : 0.f;
-    const float h = a.dentropy ? a.dentropy[n] : 0.f;
-    const float H = a.dentropy ? a.entropy[n] : 0.f;
-    int named_k[kOwn];
-    float named_c[kOwn], named_x[kOwn];
-    bool here[kOwn];  // the entry exists and lies in this slice
-#pragma unroll
-    for (int i = 0; i < kOwn; i++) {
-      const int j = t + i * kGroup;
-      named_k[i] = j < a.m ? a.top_idx[n * a.m + j] : j == a.m ? id : -1;
-      named_c[i] = j < a.m ? a.dtop[n * a.m + j] : j == a.m && a.dlogp ? a.dlogp[n] : 0.f;
-    }
-    const bool empty = lse_in == -INFINITY;
-    const float lse = empty ? INFINITY : lse_in;
-#pragma unroll
-    for (int i = 0; i < kOwn; i++) {
-      const int j = t + i * kGroup, k = named_k[i];
-      const bool legal = k >= 0 && k < a.K;
-      if (!legal && k != -1 && rank == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-      const bool used = legal && !empty && (j < a.m || a.dlogp);
-      here[i] = used && (k < head    ? k >= h0 && k < h1
-                         : k < tail0 ? (k - head) / V >= v0 && (k - head) / V < v1
-                                     : last);
-      named_x[i] = here[i] ? to_f32(row[k]) : 0.f;
-      if (j <= a.m) {
-        s_idx[g][j] = used ? k : -1;
-        s_coef[g][j] = used ? named_c[i] : 0.f;
-      }
-    }
-    group_sync<kGroup>();
-    for (int j = 0; j <= a.m; j++) slope -= s_coef[g][j];
-    // dx = p (A + B log p) away from the named entries
-    const bool bad = !(lse_in < INFINITY);
-    const float A = empty ? 0.f
-                    : bad ? __int_as_float(0x7fffffff)
-                          : a.scale * (slope - h * H);
-    const float B = empty || bad ? 0.f : -a.scale * h;
-    auto grad = [&](float x) {
-      const float lp = fmaxf(fmaf(x, a.scale, -lse), kFloorD);
-      return ex2(lp * kLog2e) * fmaf(B, lp, A);
-    };
-    float named[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; i++) {
-      named[i] = 0.f;
-      if (here[i]) {
-        float c = 0.f;  // an entry may be named more than once
-        for (int q = 0; q <= a.m; q++) c += s_idx[g][q] == named_k[i] ? s_coef[g][q] : 0.f;
-        named[i] = fmaf(a.scale, c, grad(named_x[i]));
-      }
-    }
-    group_sync<kGroup>();
-    for (int k = h0 + t; k < h1; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
-    for (int v = v0 + t; v < v1;) {
-#pragma unroll
-      for (int j = 0; j < kBatch; j++)
-        if (v + j * kGroup < v1) {
-          float x[V];
-          Vec16<T>::unpack(r[j], x);
-#pragma unroll
-          for (int e = 0; e < V; e++) x[e] = grad(x[e]);
-          *reinterpret_cast<uint4*>(vout + (int64_t)(v + j * kGroup) * V) = Vec16<T>::pack(x);
-        }
-      v += kBatch * kGroup;
-      load(v);
-    }
-    if (last)
-      for (int k = tail0 + t; k < a.K; k += kGroup) from_f32(out + k, grad(to_f32(row[k])));
-    group_sync<kGroup>();
-#pragma unroll
-    for (int i = 0; i < kOwn; i++)
-      if (here[i]) from_f32(out + named_k[i], named[i]);
-    group_sync<kGroup>();
+    grad_row<T, kGroup, kGroup != 32>(a, n, (int)(it - n * a.slices), a.slices, sh[g]);
   }
 }
 

@@ -117,14 +117,17 @@ gmm_status rows_dispatch(const gmm_rows* r, const RowArgs& a, void* stream) {
 template <typename T>
 gmm_status grad_launch(RowGradArgs a, cudaStream_t st) {
   if (a.K <= 2048) {
+    int sms = 0;
+    gmm_status s = api_device_sms(&sms);
+    if (s != GMM_OK) return s;
     a.slices = 1;
-    const unsigned grid = (unsigned)std::min<int64_t>((a.N + 7) / 8, 1 << 24);
-    row_grad_kernel<T, 32><<<grid, 256, 0, st>>>(a);
+    a.blocks = (unsigned)std::min<int64_t>((a.N + 7) / 8, 1 << 24);
+    row_grad_kernel<T, 32><<<a.blocks + std::min(a.blocks, 4u * sms), 256, 0, st>>>(a);
   } else {
     const int per = 4 * 4 * 256 * Vec16<T>::n;  // four batches of a CTA
     a.slices = (a.K + per - 1) / per;
-    const unsigned grid = (unsigned)std::min<int64_t>(a.N * a.slices, 1 << 24);
-    row_grad_kernel<T, 256><<<grid, 256, 0, st>>>(a);
+    a.blocks = (unsigned)std::min<int64_t>(a.N * a.slices, 1 << 24);
+    row_grad_kernel<T, 256><<<a.blocks, 256, 0, st>>>(a);
   }
   return api_launched(1);
 }
@@ -177,7 +180,7 @@ gmm_status gmm_logprobs_backward(const gmm_rows* r, const void* Z, const int32_t
   if (!dlogp && !dentropy && !dlse && m == 0) return GMM_ERR_INVALID_ARG;
   if (dZ == Z && ldd != r->ld) return GMM_ERR_INVALID_ARG;
   if ((uintptr_t)dZ % row_elem(r->dtype) != 0) return GMM_ERR_UNSUPPORTED;
-  RowGradArgs a = {Z,   dZ,      r->N,  r->ld,    ldd,  r->K, 1,       r->scale,
+  RowGradArgs a = {Z,   dZ,      r->N,  r->ld,    ldd,  r->K, 1,  0, r->scale,
                    ids, lse,     entropy, dlogp, dentropy, dlse, m,    top_idx, dtop, dev_flags};
   cudaStream_t st = (cudaStream_t)stream;
   if (r->dtype == GMM_F32) return grad_launch<float>(a, st);

@@ -1,8 +1,11 @@
-"""The row operators where a loose tolerance would hide a mistake: low temperatures."""
+"""The row operators where a loose tolerance would hide a mistake: low temperatures, rows far from
+0, and every entry of the gradient by itself.  Against oracle/posteriors.py, which also says how
+the limits come about."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import posteriors as P
 
 U = 2.0 ** -24
 DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -87,3 +90,69 @@ def test_probabilities_sum_to_one_at_a_low_temperature(G, K, scale):
             lp = r.top_logp[:, :8].double()
             want = (lp.softmax(1) if renorm else lp.exp()).cpu().numpy()
             assert (np.abs(w.double().cpu().numpy() - want) <= want * 2 * _lp_tol(K)).all()
+
+
+# ------------------------------------------------------------------ the gradient
+def _upstream(rng, N, m):
+    up = {k: rng.normal(size=N).astype(np.float32) for k in ("dlogp", "dentropy", "dlse")}
+    up["dtop"] = rng.normal(size=(N, m)).astype(np.float32) if m else None
+    return up
+
+
+def _limit(x, ids, lse, H, up, idx, scale, dtype):
+    f = torch.finfo(DTYPES[dtype])
+    return P.gradient_limit(x, ids, lse, H, up["dlogp"], up["dentropy"], up["dlse"], idx,
+                            up["dtop"], scale, f.eps, f.smallest_normal)
+
+
+def _check(G, Z, x, ids, m, scale, dtype, out=None, seed=0):
+    up = _upstream(np.random.default_rng(seed), len(x), m)
+    ids_d = torch.from_numpy(ids).cuda()
+    r = G.gmm_logprobs(Z, ids_d, m=m, scale=scale)
+    idx = r.top_idx.cpu().numpy() if m else None
+    want, tol = _limit(x, ids, r.lse.cpu().numpy(), r.entropy.cpu().numpy(), up, idx, scale, dtype)
+    d = {k: None if v is None else torch.from_numpy(v).cuda() for k, v in up.items()}
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = G.gmm_logprobs_backward(Z, ids_d, r.lse, entropy=r.entropy, top_idx=r.top_idx,
+                                  scale=scale, out=out, dev_flags=flags, **d)
+    g = got.double().cpu().numpy()
+    bad = ~(np.abs(g - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], g[bad][:4], want[bad][:4],
+                           tol[bad][:4])
+    assert flags.item() == 0
+    return got
+
+
+def _logits(rng, N, K):
+    x = rng.normal(size=(N, K)).astype(np.float32) * 3
+    x[np.arange(N), rng.integers(0, K, N)] += 8
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("K", [1, 7, 300, 2048, 2049, 9000, 40_003])
+def test_gradient_of_rows_far_from_zero(G, K, dtype):
+    """Rows whose log-sum-exp rounds away what p needs: the type's lowest value as a mask that
+    leaves nothing else, log-joints in the thousands, and rows of ordinary size among them."""
+    t = DTYPES[dtype]
+    rng = np.random.default_rng(K)
+    low = float(torch.finfo(t).min)
+    bases = [low, -60_000.0, 30_000.0, -1500.0, 1100.0, 0.0, -5.0, low, -2000.0]
+    if dtype != "f16":
+        bases += [-1e30, 1e30, 3e38, -1e20]
+    x = np.array(bases, np.float32)[:, None] + _logits(rng, len(bases), K)
+    x[0] = low
+    x[4, rng.random(K) < 0.5] = -np.inf
+    x[7, rng.random(K) < 0.5] = -np.inf  # some masked either way
+    x[8, K // 2:] = low
+    x[4, K // 2] = 1100.0
+    x[7, K // 2] = low
+    Z, v = _place(np.maximum(x, low, where=x > -np.inf, out=x), dtype, 3, 1)
+    ids = rng.integers(0, K, len(bases)).astype(np.int32)
+    ids[3] = -1
+    for m, scale in ((0, 1.0), (min(5, K), 0.5), (3, 2.0 if dtype == "f16" else 1.0)):
+        got = _check(G, Z, v, ids, m, scale, dtype, seed=m).clone()
+        W, w = _place(v, dtype, 3, 1)
+        same = _check(G, W, w, ids, m, scale, dtype, out=W, seed=m)  # in place
+        assert torch.equal(got, same)
