@@ -129,6 +129,47 @@ def _logits(rng, N, K):
     return x
 
 
+@pytest.mark.parametrize("m", [0, 5, 32])
+@pytest.mark.parametrize("K", [40, 1001, 2049, 8192, 33_000, 131_072])
+def test_lost_and_turned_entries_of_the_gradient_are_seen(K, m):
+    """Of the entries that no label and no alternative names, a limit lets hardly one pass as 0 or
+    with its sign turned (those whose terms happen to cancel)."""
+    rng = np.random.default_rng(K)
+    x = _logits(rng, 3, K)
+    ids = rng.integers(0, K, 3).astype(np.int32)
+    _, H, lse, idx, _ = P.logprobs(x, ids, m)
+    up = _upstream(rng, 3, m)
+    for dtype in DTYPES:
+        want, tol = _limit(x, ids, lse, H, up, idx if m else None, 1.0, dtype)
+        free = np.ones(x.shape, bool)
+        free[np.arange(3), ids] = False
+        if m:
+            np.put_along_axis(free, idx.astype(np.int64), False, 1)
+        # (fp16: what is below its smallest numbers is 0)
+        free &= np.abs(want) > 2 * torch.finfo(DTYPES[dtype]).smallest_normal
+        assert free.sum() > 0
+        for wrong in (np.zeros_like(want), -want):
+            assert (np.abs(wrong - want) > tol)[free].mean() > 0.99
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("K", [1, 3, 8, 33, 256, 1001, 2048, 2049, 8192, 33_000, 131_072])
+def test_every_entry_of_the_gradient(G, K, dtype):
+    rng = np.random.default_rng(K)
+    N = 23 if K < 20_000 else 3
+    for pad, shift, m, scale, masked in ((0, 0, 0, 1.0, False), (3, 1, 5, 0.75, True),
+                                         (8, 0, 32, 1.25, False)):
+        x = _logits(rng, N, K)
+        if masked:
+            x[rng.random((N, K)) < 0.4] = -np.inf
+            x[2] = -np.inf
+        Z, v = _place(x, dtype, pad, shift)
+        ids = rng.integers(0, K, N).astype(np.int32)
+        ids[1::4] = -1
+        _check(G, Z, v, ids, m, scale, dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("K", [1, 7, 300, 2048, 2049, 9000, 40_003])
