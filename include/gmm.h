@@ -390,7 +390,7 @@ typedef struct {
   int64_t ld;    /* elements from one row to the next, >= K */
   int32_t K;     /* classes, >= 1 */
   int32_t dtype; /* gmm_dtype of Z: GMM_F32, GMM_BF16 or GMM_F16 */
-  float scale;   /* > 0, finite */
+  float scale;   /* > 0, finite; GMM_ERR_UNSUPPORTED above 2.35e38 */
 } gmm_rows;
 
 /*

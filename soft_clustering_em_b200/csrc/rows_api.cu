@@ -22,6 +22,7 @@ gmm_status check_rows(const gmm_rows* r, const void* Z) {
   if (r->dtype != GMM_F32 && r->dtype != GMM_BF16 && r->dtype != GMM_F16)
     return GMM_ERR_INVALID_ARG;
   if (!(r->scale > 0.f) || !isfinite(r->scale)) return GMM_ERR_INVALID_ARG;
+  if (!isfinite(r->scale * kLog2e)) return GMM_ERR_UNSUPPORTED;
   if (r->K > kMaxRowClasses) return GMM_ERR_UNSUPPORTED;
   if (r->N > ((int64_t)1 << 40) || r->ld > ((int64_t)1 << 40) ||
       (double)r->N * (double)r->ld > 1e18)

@@ -155,3 +155,11 @@ def test_binding_refuses_what_it_cannot_pass(lib):
         G.gmm_logprobs_backward(Z, None, torch.zeros(4), dtop=torch.zeros(4, 2))
     with pytest.raises(ValueError):
         G.gmm_moe(Z, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), Z, Z)
+
+
+def test_a_scale_beyond_its_range_is_refused(lib):
+    """scale * log2 e has to be finite: the exponents are formed with it."""
+    r = rows(scale=2.5e38)
+    assert logprobs(lib, r) == UNSUP
+    assert backward(lib, r) == UNSUP
+    assert route(lib, r) == UNSUP
