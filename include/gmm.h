@@ -465,7 +465,7 @@ gmm_status gmm_route(const gmm_rows* r, const void* Z, int32_t m, int32_t renorm
  * for a token does not depend on timing.  A NaN or infinity in a token's row of X, in its
  * weights resp or in an expert's weights reaches only the tokens concerned.
  * Device-side waits are bounded as gmm_set_wait_budget says; one that gives up raises
- * GMM_DEVFLAG_WAIT_TIMEOUT, and Y is then not meaningful.
+ * GMM_DEVFLAG_WAIT_TIMEOUT, and what it would have given is NaN in Y.
  * T = 0 is allowed and does nothing.  GMM_ERR_UNSUPPORTED: T > 256, E > 1024, D or F not
  * a multiple of 8 or above 2^20, 2 E F or E D of 2^31 or more, ldx of 2^39 or more, ldy above
  * 2^40, GMM_F32, a misaligned pointer.

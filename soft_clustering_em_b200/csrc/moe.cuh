@@ -532,8 +532,8 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
     int swap = 0;
     bool ok = true;
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
-    for (; job.more(L); job.next(a, L), n++) {  // to the end even when a wait gave up: the
-      const uint32_t buf = n & 1u;              // warps meet at barriers
+    for (; job.more(L); job.next(a, L), n++) {  // to the end even when a wait gave up (what it
+      const uint32_t buf = n & 1u;              // was for is NaN then): the warps meet at barriers
       ok = ok && moe_warp_wait<100>(&bar.acc_full[buf], (n >> 1) & 1u, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after_sync();
@@ -541,7 +541,7 @@ __device__ __forceinline__ void moe_stream(const MoeArgs& a, const MoeLists& L, 
         const int cnt = min(32, job.ntok - j0);
         float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; j++) v[j] = 0.f;
+        for (int j = 0; j < 32; j++) v[j] = ok ? 0.f : __int_as_float(0x7fffffff);
         if (ok) {
           // the warps' shares of K (a job of few steps has not all of them), in order
 #pragma unroll 1
