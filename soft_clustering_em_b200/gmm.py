@@ -558,7 +558,8 @@ def gmm_moe_workspace_size(p: gmm_moe_problem) -> int:
     return int(n.value)
 
 
-def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, stream=None):
+def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, stream=None,
+            dev_flags=None):
     """Mixture-of-experts layer for a few tokens: for each token the sum over its choices of
     resp * W_down[e] (act(W_gate[e] x) * (W_lin[e] x)).
 
@@ -567,19 +568,22 @@ def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, str
     E x 2F x D, W_gate's F rows over W_lin's; W_down: E x D x F.  Returns T x D of X's type.
     ws: a uint8 device tensor of gmm_moe_workspace_size bytes (allocated here when None), its
     first word the device status word: zero it once to read it with gmm_device_status.
-    stream (None: the current one) runs the call and owns what is allocated here.
+    dev_flags (1 int32 device tensor, optional) collects the device status bits, with or without
+    a ws (with one: all that its status word holds).  stream (None: the current one) runs the call
+    and owns what is allocated here.
     """
     if stream is not None:
         with _on(stream, X):
-            return gmm_moe(X, idx, resp, W_up, W_down, act, out, ws)
+            return gmm_moe(X, idx, resp, W_up, W_down, act, out, ws, None, dev_flags)
     if X.dim() != 2 or idx.dim() != 2 or W_up.dim() != 3 or W_down.dim() != 3:
         raise ValueError("X is T x D, idx T x m, W_up E x 2F x D, W_down E x D x F")
     (T, D), (E, _, F) = X.shape, W_down.shape
-    _same_device(X, idx, resp, W_up, W_down, out, ws)
+    _same_device(X, idx, resp, W_up, W_down, out, ws, dev_flags)
     _vector(idx, (T, idx.shape[1]), torch.int32, "idx")
     _vector(resp, (T, idx.shape[1]), torch.float32, "resp")
     _vector(W_up, (E, 2 * F, D), X.dtype, "W_up")
     _vector(W_down, (E, D, F), X.dtype, "W_down")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
     if out is None:
         out = torch.empty(T, D, dtype=X.dtype, device=X.device)
     if out.dtype != X.dtype or out.shape != X.shape:
@@ -590,9 +594,13 @@ def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, str
     p = moe_problem(X, idx, W_down, act, out)
     if ws is None:
         ws = torch.empty(gmm_moe_workspace_size(p), dtype=torch.uint8, device=X.device)
+        if dev_flags is not None:
+            ws[:4].zero_()
     _launch(load_library().gmm_moe, "gmm_moe", X.device, ctypes.byref(p), X.data_ptr(),
             idx.data_ptr(), resp.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), out.data_ptr(),
             ws.data_ptr(), ws.numel())
+    if dev_flags is not None:
+        dev_flags |= ws[:4].view(torch.int32)
     return out
 
 
