@@ -41,16 +41,47 @@ def _stale(src):
     return not ours or any(not os.path.exists(n) or os.path.getmtime(n) > made for n in ours)
 
 
+def _command():
+    """What the objects come from besides their sources: compiler, version, flags."""
+    try:
+        version = subprocess.run([NVCC, "--version"], capture_output=True, text=True).stdout
+    except OSError:  # (no compiler here: a built library can still be used)
+        return None
+    return "\n".join([NVCC, version, *FLAGS, *SOURCES])
+
+
+def _record():
+    return os.path.join(OBJ, "command")
+
+
+def _recorded():
+    if not os.path.exists(_record()):
+        return None
+    with open(_record()) as f:
+        return f.read()
+
+
+def _write_record(text):
+    with open(_record(), "w") as f:
+        f.write(text)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if it is missing or older than any source."""
-    if not force and os.path.exists(LIB):
+    """Compile the library if it is missing, older than any source, or made by another command.
+
+    (A library that came without the record of its command is taken as it is.)
+    """
+    now, made_by = _command(), _recorded()
+    if not force and os.path.exists(LIB) and (now is None or made_by in (None, now)):
         newest = max(os.path.getmtime(f) for f in _inputs())
         if os.path.getmtime(LIB) >= newest:
             return LIB
     os.makedirs(OBJ, exist_ok=True)
+    every = force or made_by != now
+    _write_record("unfinished")
     jobs = []
     for src in SOURCES:
-        if not force and not _stale(src):
+        if not every and not _stale(src):
             continue
         obj = _object(src)
         cmd = [NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, "-I", INCLUDE, "-I", CSRC,
@@ -61,6 +92,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
     subprocess.check_call([NVCC, *FLAGS, "-shared", "-o", LIB + ".tmp", *map(_object, SOURCES)])
     os.replace(LIB + ".tmp", LIB)
+    _write_record(now)
     return LIB
 
 
