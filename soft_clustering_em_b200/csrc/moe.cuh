@@ -6,7 +6,9 @@
 // where W_up[e] (2F x D) stacks W_gate over W_lin and W_down[e] is D x F.
 //
 // With few tokens the layer is bound by reading the chosen experts' weights
-// (3 D F elements each) once.  Both kernels are a stream of jobs on one CTA per SM: 128
+// (3 D F elements each) once.  Experts with more tokens than a job has columns (16, or 32 and in
+// the up kernel 64 where that costs no stage) have them streamed again for each further group,
+// mostly from L2.  Both kernels are a stream of jobs on one CTA per SM: 128
 // weight rows of one expert against up to kN of its tokens, on the tensor cores.  The
 // weights are the M operand (rows of the tile), the tokens the N operand, accumulators
 // in tensor memory, two of them in turn.  The warps have a part each:
@@ -34,9 +36,11 @@
 //
 // Measured: 32 tokens with 8 of 128 experts, 2048 x 768 bf16 (about 1.05 GB of weights):
 // 179 to 189 us, 5.6 to 5.9 TB/s; kernel 1 alone reads 6.0 TB/s, kernel 2 5.2.  100 tokens, 4 of 32
-// experts, 4096 x 1432 fp16: 228 us, 4.9 TB/s (kernel 2 on 128 SMs, 4.3).  One token, 8 of 64
+// experts, 4096 x 1432 fp16: 224 to 229 us, 4.9 TB/s (kernel 2 on 128 SMs, 4.3).  One token, 8 of 64
 // experts, 2048 x 1024: 27 us for 100 MB, of which 15 are the reading and 6 the two kernels'
-// starts.  The tensor pipe is 5 to 13 % busy.
+// starts.  The tensor pipe is 5 to 13 % busy.  Many tokens per expert, with the routing: 64 tokens,
+// 2 of 8 experts of 4096 x 1024, 71 us (31 at the copy rate); 256 tokens, 4 of 16 of 2048 x 704, 134
+// (21); 256 tokens, 8 of 128 of 2048 x 768, 276 (185).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

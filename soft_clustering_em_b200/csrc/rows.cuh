@@ -179,8 +179,12 @@ __device__ __forceinline__ void write_alt(const RowArgs& a, int64_t n, int j, in
 // with 8 lanes of 32, 297 with 16 of 16 and 464 with 32 of 8 (shuffles and the rounds'
 // fixed part are shared by 32 / kLanes rows).  A few hundred rows take 32 lanes of 8
 // (2.2 against 2.4 us).  Without alternatives the rows above take 165 us (6.2 TB/s); each
-// alternative adds about 30 us, and issue slots bound it (73 % busy).  Back to back the
-// GPU is at its power limit and clocks down to 1.67 GHz: 252 us.
+// alternative adds about 30 us, and issue slots bound it (73 % busy).  Those are short runs; back
+// to back the GPU is at its power limit and clocks down to 1.67 GHz: 246 to 252 us.
+// The fp32 instances with 32 entries per lane spill 48 to 180 bytes per thread at the 48 registers
+// that 5 CTAs per SM leave.  A row narrower than its places pays for all of them, and has its
+// exponents clamped: 2e8 fp32 logits in rows of 300 (512 places) take 202 us where rows of 512
+// take 150, in rows of 600 (1,024) 187; in rows of 1,024, 179.
 template <typename T, bool kVec>
 __device__ __forceinline__ uint4 load_row_vec(const T* row, int k0, int K) {
   constexpr int V = Vec16<T>::n;
@@ -367,13 +371,17 @@ __global__ void __launch_bounds__(256, kEl <= 16 ? 6 : 5) row_short_kernel(RowAr
 // holds, the m units of largest entry (which hold the m best, or m units would hold a better
 // one each) give a sorted list of their best each, and those merge.
 //
-// Measured: 4096 rows of 131,072 bf16 without alternatives 175 to 190 us in short runs (5.7 to
-// 6.1 TB/s; 164 us at the copy rate).  There the exponentials bind (the pipe that makes
-// them is 74 % busy, 16 per clock and SM) with the issue slots (57 %).  Back to back the
-// 1000 W limit holds the clock at 1.54 GHz: 210 us.  Exponentials by polynomial on the
+// Measured: 4096 rows of 131,072 bf16 without alternatives 203 to 214 us back to back (5.0 to
+// 5.3 TB/s; 164 us at the copy rate), at the 1000 W limit, which holds the clock at 1.54 GHz; 175 to
+// 190 us in short runs.  The exponentials bind (the pipe that makes them is 70 % busy, 16 per
+// clock and SM) with the issue slots (55 %).  Exponentials by polynomial on the
 // multiply-add pipe (1 or 2 in 16), batches of 8 vectors, and 3 to 8 CTAs per SM of other
 // sizes gave nothing or lost.  1023 rows of 100,003 fp32, partly masked, with five
-// alternatives: 82 us (5.0 TB/s).  One row: 4.9 us, 10.5 with eight alternatives.
+// alternatives: 82 to 86 us (4.8 to 5.0 TB/s).  One row: 4.9 us, 10.5 with eight alternatives.
+// Many rows of little more than 1,024 classes are far from the copy rate: a CTA's fixed part for
+// a row, 3 us and twice that with alternatives, is then most of its time.  2e8 bf16 logits (61 us
+// at the copy rate) in rows of 1,100 take 1,243 us, of 2,048 635, of 5,000 265, of 8,192 169; with
+// eight alternatives twice as much.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowBatch = 4;
@@ -976,9 +984,13 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) row_long_kernel(RowArgs
 // (2^-12) are therefore summed once more, by one group for the whole row: at the type's lowest value,
 // say, lse has no digit of log K left.
 //
-// HBM bounds it: 4096 rows of 131,072 bf16 take 327 us (6.6 TB/s read and written).  Short
+// HBM bounds it: 4096 rows of 131,072 bf16 take 326 us (6.6 TB/s read and written).  Short
 // rows wait for their scalars first, so those and the first vectors are loaded together:
-// 60,001 rows of 1,024 fp32 with four alternatives 92 us (5.4 TB/s), 112 one after another.
+// 60,001 rows of 1,024 fp32 with four alternatives 95 us (5.2 TB/s; 112 one after another, before
+// rows far from 0 had blocks of their own).  Rows of 256 fp32 leave half a warp's vectors
+// empty: 1e6 of them take 781 us where the copy rate would take 317.
+// Where a row of Z and its row of dZ start in different places of 16 bytes, it is read and written
+// entry by entry: 2,000 rows of 50,000 bf16 take 279 us from a pitch of 50,003, and 71 from 50,000.
 struct RowGradArgs {
   const void* Z;
   void* dZ;
