@@ -493,6 +493,157 @@ gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, 
                    void* stream);
 
 /*
+ * Training a router
+ * -----------------
+ * How the assignment idx of gmm_route loads the experts, and two losses on it, for each of S
+ * segments of rows (packed sequences, each balanced by itself; or one: the whole batch).  With
+ * p = softmax(scale * Z_n) over the K experts, over the L rows of a segment that count:
+ *   load_k    = 1/L sum_n p_nk
+ *   counts_k  = how often idx names expert k
+ *   balance   = K sum_k counts_k / (m L) load_k     (1 for an even load)
+ *   z         = 1/L sum_n lse_n^2
+ * A row counts unless mask is 0 for it or all its classes are masked.  A segment without such
+ * rows has L = 0 and zeros throughout.
+ *   idx       device, N x m; -1 is an unused choice, any other outside [0, K) is left out and
+ *             raises GMM_DEVFLAG_BAD_INDEX.  1 <= m <= 8 (m may exceed K).
+ *   mask      device, N bytes, or NULL: 0 is a row that does not count.
+ *   offsets   device, S + 1 int32, ascending in [0, N], or NULL with S = 1 for all rows: segment
+ *             s is rows offsets[s] .. offsets[s+1] - 1.  Rows in none count nowhere.  Offsets that
+ *             do not ascend raise GMM_DEVFLAG_BAD_INDEX; the results are then not meaningful.
+ *   balance, z  device, S floats each;  load  S x K floats;  counts  S x K int32;  rows  S int32
+ *             (L); each may be NULL, but not all.
+ *   ws        device workspace of gmm_route_loss_workspace_size bytes, 256-byte aligned, any
+ *             content.  Calls that share it must be ordered on one stream.
+ * A NaN or a z of +inf in a row that counts makes its segment's balance, z and load NaN and
+ * raises GMM_DEVFLAG_NONFINITE_X.  Results do not change from run to run.
+ * GMM_ERR_UNSUPPORTED: K > 1024, S > 2^20, N * m >= 2^31.
+ */
+gmm_status gmm_route_loss_workspace_size(const gmm_rows* r, int32_t S, size_t* bytes);
+gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, int32_t m,
+                          const uint8_t* mask, const int32_t* offsets, int32_t S, float* balance,
+                          float* z, float* load, int32_t* counts, int32_t* rows,
+                          uint32_t* dev_flags, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient with respect to the logits of gmm_route's weights resp, for dresp (device, N x m, or
+ * NULL), and of gmm_route_loss's balance and z, for dbalance and dz (device, S floats each, or
+ * NULL); counts and the assignment have none.  With g_k = dbalance K counts_k / (m L^2),
+ *   dx_k = scale * [ p_k (g_k - sum_i p_i g_i + 2 dz lse / L) + r_k ]
+ *   r_k  = sum_j [k = idx_j] a_j - p_k sum_j a_j,  a_j = p_{idx_j} dresp_j            (renorm = 0)
+ *   r_k  = sum_j [k = idx_j] q_j (dresp_j - sum_i q_i dresp_i),  q = resp             (renorm != 0)
+ * rounded once to dtype; the terms of a loss only in the rows that counted in it.
+ *   idx, mask, offsets, m, scale, renorm   as gmm_route and gmm_route_loss took or wrote them
+ *             (idx may be NULL without dresp).
+ *   counts, rows  as gmm_route_loss wrote them (counts only with dbalance), or summed over
+ *             several GPUs' shards of a batch: the gradient is then that of the whole batch's loss.
+ *   dZ        device, N x K of type dtype, rows ldd >= K apart; Z itself with ldd = ld is allowed.
+ *             A row that counts in no loss and has no choice with a dresp gets zeros, and so does
+ *             one with every class masked.  A NaN or a z of +inf makes any other row NaN and raises
+ *             GMM_DEVFLAG_NONFINITE_X.
+ * No workspace.
+ */
+gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* idx, int32_t m,
+                              const float* dresp, int32_t renorm, const int32_t* counts,
+                              const int32_t* rows, const float* dbalance, const float* dz,
+                              const uint8_t* mask, const int32_t* offsets, int32_t S, void* dZ,
+                              int64_t ldd, uint32_t* dev_flags, void* stream);
+
+/*
+ * Rows of a table chosen by an assignment: the embedding of tokens (m = 1), or points put together
+ * from a codebook's or mixture's entries and their responsibilities.
+ *   Y_n = scale * sum_j resp_nj W[idx_nj]          (resp NULL: weights of 1)
+ *   W       device, K x D of type dtype, rows ldw apart; Y device, N x D, rows ldy apart.
+ *   idx     device, N x m; -1 is an unused choice, any other index outside [0, K) is left out and
+ *           raises GMM_DEVFLAG_BAD_INDEX.  A row without choices is zeros.
+ *   resp    device, N x m floats, or NULL.
+ * Sums are formed in float32 and rounded once.  Rows may start anywhere (element-aligned); 16-byte
+ * aligned ones are faster.  N = 0 does nothing.  GMM_ERR_UNSUPPORTED: K > 2^24, D > 2^20,
+ * N * m >= 2^31, N * D > 10^12.
+ */
+typedef struct {
+  int64_t N;          /* rows of idx and Y, >= 0 */
+  int32_t m;          /* choices per row, 1 <= m <= 8 */
+  int32_t K, D;       /* the table's rows and their width */
+  int32_t dtype;      /* gmm_dtype of W and Y */
+  float scale;        /* finite */
+  int64_t ldw, ldy;   /* elements from one row to the next, >= D */
+} gmm_embed_problem;
+
+gmm_status gmm_embed(const gmm_embed_problem* p, const void* W, const int32_t* idx,
+                     const float* resp, void* Y, uint32_t* dev_flags, void* stream);
+
+/*
+ * Gradients of gmm_embed for an upstream gradient dY (device, N x D, rows ldy apart):
+ *   dW_k = scale * sum over (n, j) with idx_nj = k of resp_nj dY_n
+ *   dresp_nj = scale * <dY_n, W[idx_nj]>           (0 for a choice that is left out)
+ * Choices are sorted by class and summed in that order, in float32, without atomics: the result
+ * does not change from run to run, and is rounded once.
+ *   dW        device, K x D of dw_dtype (GMM_F32 or dtype), rows ldd apart, or NULL.  Every row is
+ *             written, zeros where nothing names it; with accumulate != 0 the gradient is added to
+ *             what is there, and rows that nothing names are not touched.
+ *   dresp     device, N x m floats, or NULL; needs W (else unused).
+ *   ws        device workspace of gmm_embed_workspace_size bytes, 256-byte aligned, any content
+ *             (only for dW).  Calls that share it must be ordered on one stream.
+ * N = 0 writes dW's zeros.
+ */
+gmm_status gmm_embed_workspace_size(const gmm_embed_problem* p, size_t* bytes);
+gmm_status gmm_embed_backward(const gmm_embed_problem* p, const void* dY, const int32_t* idx,
+                              const float* resp, const void* W, void* dW, int32_t dw_dtype,
+                              int64_t ldd, int32_t accumulate, float* dresp, uint32_t* dev_flags,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One step of beam search.  The N rows of logits are B groups of w beams (row b w + i); a beam
+ * has the score scores[b, i], the sum of its log probabilities so far.  Candidates of a group are
+ * (i, k) with score scores[b, i] + log p_k of row i, for each class k that is not masked; a beam
+ * that has ended has the one candidate (i, end_id) of score scores[b, i] instead.
+ *   scores   device, B x w floats; -inf is no beam (its row of logits is not looked at).
+ *   ended    device, B x w bytes, or NULL: != 0 is a beam that has ended (nor is its row).
+ *   out_scores, parent, token   device, B x m: the m best candidates, descending, and their i and
+ *            k.  Equal scores go to the lower i, then to the larger logit, then to the lower k.
+ *            Where candidates run out: -inf, -1, -1.
+ *   1 <= w <= 32, 1 <= m <= 32 (m = w for a plain step, 2 w where some may end).
+ *   ws       device workspace of gmm_beam_workspace_size bytes, 256-byte aligned, any content.
+ *            Calls that share it must be ordered on one stream.
+ * Scores are compared before they are rounded to float32 (to about 2e-7; rows of equal logits and
+ * scores are equal where they start alike in 16 bytes).  A NaN or +inf among the scores, or in the
+ * logits of a beam that is alive, gives NaN, -1, -1 for the group and raises
+ * GMM_DEVFLAG_NONFINITE_X.
+ */
+gmm_status gmm_beam_workspace_size(const gmm_rows* r, int32_t w, int32_t m, size_t* bytes);
+gmm_status gmm_beam_select(const gmm_rows* r, const void* Z, int32_t w, const float* scores,
+                           const uint8_t* ended, int32_t end_id, int32_t m, float* out_scores,
+                           int32_t* parent, int32_t* token, uint32_t* dev_flags, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * The beams' states after their parents, in place: state[b, i] <- state[b, parent[b, i]] for
+ * every state and group, as if all were read before any is written.
+ *   parent   device, B x w: a beam of the same group; -1 leaves the beam as it is, and so does any
+ *            other index outside [0, w), which raises GMM_DEVFLAG_BAD_INDEX.
+ *   lens     device, B int32, or NULL: used positions of the group's beams, for states with by_len;
+ *            positions behind them are left as they are.  One outside [0, count] counts as the
+ *            nearer end and raises GMM_DEVFLAG_BAD_INDEX.
+ *   states   host array of n.  The row of beam (b, i) is base + (b w + i) row_stride; it has `outer`
+ *            pieces outer_stride bytes apart (the heads of a cache), each of `count` positions of
+ *            pos_bytes bytes.  Rows and pieces must not overlap.
+ * 1 <= w <= 32.  Nothing is read or written of groups whose beams all stay.  No workspace.
+ * GMM_ERR_UNSUPPORTED: a row of 2^32 or more columns of 16 bytes (4 or 1 where an address, stride or
+ * position is not a multiple of 16 bytes).
+ */
+typedef struct {
+  void* base;
+  int64_t row_stride;
+  int64_t outer, outer_stride;
+  int64_t count, pos_bytes;
+  int32_t by_len; /* != 0: only lens[b] positions are used */
+} gmm_beam_state;
+
+gmm_status gmm_beam_reorder(int64_t B, int32_t w, const int32_t* parent, const int32_t* lens,
+                            int32_t n, const gmm_beam_state* states, uint32_t* dev_flags,
+                            void* stream);
+
+/*
  * Waits for stream, then reads the device status word of ws into *flags
  * (GMM_DEVFLAG_* bits; may be NULL) and, if clear != 0, resets it to 0.
  * Returns GMM_OK when no bit is set, GMM_ERR_TIMEOUT for the wait bit,

@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libscem_gmm.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-SOURCES = ["gmm_api.cu", "rows_api.cu", "moe_api.cu"]
+SOURCES = ["gmm_api.cu", "rows_api.cu", "moe_api.cu", "embed_api.cu", "route_api.cu", "beam_api.cu"]
 OBJ = os.path.join(HERE, "_build")  # one object per source
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]

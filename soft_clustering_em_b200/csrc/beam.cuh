@@ -1,0 +1,229 @@
+// beam.cuh -- kernels of gmm_beam_select and gmm_beam_reorder.
+//
+// A group of w beams, rows b w .. b w + w - 1 of the logits, has the candidates (i, k) of score
+//   scores_i + log p_i(k),
+// and its m best are among the m best classes of each row, which row_short_kernel or
+// row_long_kernel finds while the logits go through once.  What is left is a merge of w sorted
+// lists.
+#pragma once
+
+#include "rows.cuh"
+
+namespace scem {
+
+constexpr int kMostBeams = 32;  // a lane for each
+
+struct BeamArgs {
+  const void* Z;
+  int64_t ld;
+  float scale;
+  int64_t B;
+  int w, m;
+  const float* scores;     // B x w
+  const uint8_t* ended;    // B x w, may be null
+  int end_id;
+  const int32_t* top_idx;  // B w x m: each row's best classes, and their log p
+  const float* top_logp;
+  float* out;              // B x m
+  int32_t *parent, *token;
+  uint32_t* flags;
+};
+
+// Doubles as unsigned integers of the same order; 0 for -inf.
+__device__ __forceinline__ uint64_t double_order(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return v == -INFINITY ? 0ull
+                        : b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double order_double(uint64_t o) {
+  return o == 0 ? -INFINITY
+                : __longlong_as_double((long long)(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
+}
+
+// A warp per group, a lane per beam.  Scores are 64 bits wide: those of different rows lie close
+// together, and in 32 bits a log p of -15 is rounded by 5e-7.  A row's first log p is the
+// smallest in size and so the most exact one; the others stand as far behind it as their logits.
+// Equal scores go to the lower beam, then in the order of the row.
+template <typename T>
+__global__ void beam_merge_kernel(BeamArgs a) {
+  extern __shared__ uint64_t beam_cand[];  // [warp][w][m]
+  const int lane = threadIdx.x & 31;
+  const int64_t b = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  uint64_t* cand = beam_cand + threadIdx.x / 32 * (a.w * a.m);
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (b >= a.B) return;
+  float score = -INFINITY, first = 0.f;
+  bool ended = false;
+  if (lane < a.w) {
+    score = a.scores[b * a.w + lane];
+    ended = a.ended && a.ended[b * a.w + lane];
+    first = a.top_logp[(b * a.w + lane) * a.m];
+  }
+  const bool dead = score == -INFINITY;
+  const bool bad = !(score < INFINITY) || (!dead && !ended && !(first == first));
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
+    if (lane < a.m) {
+      a.out[b * a.m + lane] = __int_as_float(0x7fffffff);
+      a.parent[b * a.m + lane] = -1;
+      a.token[b * a.m + lane] = -1;
+    }
+    return;
+  }
+  for (int c0 = 0; c0 < a.w * a.m; c0 += 32) {
+    const int c = c0 + lane, i = min(c / a.m, a.w - 1), j = c % a.m;
+    const float s = __shfl_sync(0xffffffffu, score, i);
+    const float lp = __shfl_sync(0xffffffffu, first, i);
+    const bool e = __shfl_sync(0xffffffffu, (int)ended, i);
+    if (c >= a.w * a.m) continue;
+    uint64_t key = 0;
+    if (e) {
+      if (j == 0) key = double_order((double)s);
+    } else if (s != -INFINITY) {
+      const int64_t row = b * a.w + i;
+      const int k0 = a.top_idx[row * a.m], k = a.top_idx[row * a.m + j];
+      if (k >= 0) {
+        const T* z = (const T*)a.Z + row * a.ld;
+        const double d = (double)to_f32(z[k]) - (double)to_f32(z[k0]);
+        key = double_order((double)s + ((double)lp + d * (double)a.scale));
+      }
+    }
+    cand[c] = key;
+  }
+  __syncwarp();
+  int pos = 0, my_parent = -1, my_rank = 0;
+  double my_score = -INFINITY;
+  uint64_t head = lane < a.w ? cand[lane * a.m] : 0;
+  for (int j = 0; j < a.m; j++) {
+    const uint64_t best = warp_max_key(head);
+    if (best == 0) break;
+    const int from = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+    const int rank = __shfl_sync(0xffffffffu, pos, from);
+    if (lane == j) {
+      my_score = order_double(best);
+      my_parent = from;
+      my_rank = rank;
+    }
+    if (lane == from) head = ++pos < a.m ? cand[lane * a.m + pos] : 0;
+  }
+  const bool end = __shfl_sync(0xffffffffu, (int)ended, max(my_parent, 0));
+  if (lane < a.m) {
+    a.out[b * a.m + lane] = (float)my_score;
+    a.parent[b * a.m + lane] = my_parent;
+    a.token[b * a.m + lane] = my_parent < 0 ? -1
+                              : end         ? a.end_id
+                                            : a.top_idx[(b * a.w + my_parent) * a.m + my_rank];
+  }
+}
+
+// ------------------------------------------------------------------ states after their parents
+// In place: a thread owns a column of a group, the same few bytes of all its beams, and has read
+// every beam's source before it writes any.  Beams that stay where they are are neither read
+// (unless another wants them) nor written.
+struct BeamState {
+  char* base;
+  int64_t row_stride, outer_stride;  // bytes
+  uint32_t outer, inner, per_pos;    // pieces of a row; columns of a piece and of a position
+  int by_len;
+};
+
+constexpr int kStates = 32;  // of one launch
+constexpr int kReorderThreads = 256;
+constexpr int kReorderGroups = 1024;  // looked at in one go
+
+struct ReorderArgs {
+  BeamState state[kStates];
+  const int32_t* parent;  // B x w
+  const int32_t* lens;    // B, may be null
+  int64_t B;
+  int w;
+  uint32_t* flags;
+};
+
+// kW: at least w.  Blocks y: a state; blocks x share out its tiles of 256 columns, of the groups in
+// which a beam moves, up to their lengths.
+template <typename Vec, int kW>
+__global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(ReorderArgs a) {
+  __shared__ uint32_t upto[kReorderGroups];  // tiles of the groups up to and with this one
+  __shared__ uint32_t warp_total[kReorderThreads / 32];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const BeamState st = a.state[blockIdx.y];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  constexpr int kEach = kReorderGroups / kReorderThreads;
+  auto length = [&](int64_t b) {  // columns of a piece that are used
+    if (!a.lens || !st.by_len) return st.inner;
+    const int most = (int)(st.inner / st.per_pos), n = a.lens[b];
+    return (uint32_t)max(0, min(n, most)) * st.per_pos;
+  };
+  for (int64_t b0 = 0; b0 < a.B; b0 += kReorderGroups) {
+    uint32_t mine[kEach], total = 0;
+#pragma unroll
+    for (int q = 0; q < kEach; q++) {
+      const int64_t b = b0 + t * kEach + q;
+      uint32_t tiles = 0;
+      if (b < a.B) {
+        bool moves = false;
+        for (int i = 0; i < a.w; i++) {
+          const int p = a.parent[b * a.w + i];
+          if ((unsigned)p < (unsigned)a.w) moves |= p != i;
+          else if (p != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+        }
+        if (a.lens && st.by_len && a.flags &&
+            (a.lens[b] < 0 || a.lens[b] > (int)(st.inner / st.per_pos)))
+          atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+        if (moves)
+          tiles = (uint32_t)(((uint64_t)st.outer * length(b) + kReorderThreads - 1) /
+                             kReorderThreads);
+      }
+      total += tiles;
+      mine[q] = total;
+    }
+    uint32_t scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_total[w] = scan;
+    __syncthreads();
+    uint32_t before = scan - total;
+    for (int q = 0; q < w; q++) before += warp_total[q];
+#pragma unroll
+    for (int q = 0; q < kEach; q++) upto[t * kEach + q] = before + mine[q];
+    __syncthreads();
+    const uint32_t all = upto[kReorderGroups - 1];
+    for (uint32_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
+      int lo = 0, hi = kReorderGroups - 1;  // the first group with upto > tile
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (upto[mid] > tile) hi = mid;
+        else lo = mid + 1;
+      }
+      const int64_t b = b0 + lo;
+      const uint32_t len = length(b);
+      const uint64_t c = (uint64_t)(tile - (lo ? upto[lo - 1] : 0)) * kReorderThreads + t;
+      if (c >= (uint64_t)st.outer * len) continue;
+      const uint32_t o = (uint32_t)c / len;  // (below 2^32: checked on the host)
+      char* p = st.base + b * a.w * st.row_stride + o * st.outer_stride +
+                ((uint64_t)c - (uint64_t)o * len) * sizeof(Vec);
+      Vec v[kW];
+      uint32_t moved = 0;
+#pragma unroll
+      for (int i = 0; i < kW; i++) {
+        const int from = i < a.w ? a.parent[b * a.w + i] : -1;
+        if ((unsigned)from < (unsigned)a.w && from != i) {
+          moved |= 1u << i;
+          v[i] = *reinterpret_cast<const Vec*>(p + from * st.row_stride);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kW; i++)
+        if (moved >> i & 1) *reinterpret_cast<Vec*>(p + i * st.row_stride) = v[i];
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace scem

@@ -1,0 +1,395 @@
+// route.cuh -- how a router loads its experts, and the router's gradient: kernels of
+// gmm_route_loss and gmm_route_backward.
+//
+// p = softmax(scale x) over the K experts of a row.  Per segment of rows, over its L rows that
+// count:
+//   load_k = 1/L sum_n p_nk     counts_k = how often idx names k
+//   balance = K sum_k (counts_k / (m L)) load_k        z = 1/L sum_n lse_n^2
+// and for upstream gradients dbalance, dz (per segment) and dresp (of the weights that
+// gmm_route gave, r = p of the chosen or q = p over the chosen's sum):
+//   dx_k = scale [ p_k (g_k - sum_i p_i g_i + 2 dz/L lse - R) + sum_j [idx_j = k] a_j ],
+//   g_k = dbalance K counts_k / (m L^2),
+//   a_j = p_j dresp_j, R = sum_j a_j      or   a_j = q_j (dresp_j - sum_i q_i dresp_i), R = 0.
+//
+// A row sits in the registers of 8 to 32 lanes, as in row_short_kernel, and is read once.
+#pragma once
+
+#include "rows.cuh"
+
+namespace scem {
+
+constexpr int kRouteMostK = 1024;
+constexpr int kRouteThreads = 256;
+constexpr int kRouteWarps = kRouteThreads / 32;
+
+struct RouteArgs {
+  const void* Z;
+  int64_t N, ld;
+  int K;
+  float scale;
+  const int32_t* idx;      // N x m
+  int m;
+  const uint8_t* mask;     // N, may be null: 0 is a row that does not count
+  const int32_t* offsets;  // S + 1, may be null: one segment
+  int S;
+  int64_t rows;            // of a CTA (loss) or of a warp (gradient)
+  uint32_t* flags;         // may be null
+};
+
+// The segment of row r: the last one that begins at r or before (the first, if none does).  By a
+// whole warp; any answer in [0, S) for offsets that do not ascend.
+__device__ __forceinline__ int segment_of(const int32_t* offsets, int S, int64_t r) {
+  if (!offsets) return 0;
+  int lo = 0, n = S;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = min((int)(threadIdx.x & 31) * step, n - 1);
+    const uint32_t here = __ballot_sync(0xffffffffu, offsets[lo + at] <= r);
+    const int f = here ? 31 - __clz(here) : 0;  // the last probe at r or before
+    const int from = min(f * step, n - 1);
+    lo += from;
+    n = min(step, n - from);
+  }
+  return lo;
+}
+
+// What a piece of a segment (its rows in one CTA) leaves: K sums of p, K counts, the sum of
+// lse^2 and the number of rows.
+__host__ __device__ __forceinline__ int64_t route_slot(int K) { return 2 * (int64_t)K + 2; }
+
+// The exponentials of a row relative to its largest logit.
+template <int kLanes, int kEl, typename T>
+struct RouteRow {
+  static constexpr int V = Vec16<T>::n;
+  static constexpr int kChunks = kEl / V;
+  float y[kEl];   // e^{z - largest z}
+  float S, xm;
+  float ref;
+  bool bad, empty;
+
+  __device__ __forceinline__ void make(const uint4 (&r)[kChunks], float scale) {
+    xm = max_nan(Vec16<T>::max_of(r), -INFINITY);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) xm = max_nan(xm, __shfl_xor_sync(0xffffffffu, xm, o));
+    const float z = xm * scale;
+    bad = !(z < INFINITY);
+    empty = z == -INFINITY;
+    ref = fmaxf(xm, -FLT_MAX);
+    const float c = scale * kLog2e;
+    S = 0.f;
+#pragma unroll
+    for (int v = 0; v < kChunks; v++) {
+      float x[V];
+      Vec16<T>::unpack(r[v], x);
+#pragma unroll
+      for (int e = 0; e < V; e++) {
+        y[v * V + e] = ex2((x[e] - ref) * c);
+        S += y[v * V + e];
+      }
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+  }
+  __device__ __forceinline__ float lse(float scale) const { return fmaf(xm, scale, logf(S)); }
+};
+
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ------------------------------------------------------------------ load and losses
+// A CTA takes `rows` rows.  For each segment that they meet, in order, column sums stay in
+// registers until the segment or the rows end; the sums of piece (CTA c, segment s) go to slot
+// c + s, which no other piece has: from piece to piece c or s grows, or both.
+template <typename T, int kLanes, int kEl, bool kVec>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_load_kernel(RouteArgs a, float* part) {
+  constexpr int kRows = 32 / kLanes;
+  constexpr int V = Vec16<T>::n;
+  constexpr int kChunks = kEl / V;
+  constexpr int kPlaces = kLanes * kEl;
+  __shared__ float sums[kRouteWarps][kPlaces];
+  __shared__ uint32_t hist[kPlaces];
+  __shared__ float zsum[kRouteWarps];
+  __shared__ uint32_t rsum[kRouteWarps];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5, l = lane % kLanes;
+  grid_dependents_launch();
+  const int64_t r0 = blockIdx.x * a.rows, r1 = min(r0 + a.rows, a.N);
+  int s = segment_of(a.offsets, a.S, r0);
+  for (int i = t; i < a.K; i += kRouteThreads) hist[i] = 0;
+  __syncthreads();
+  for (; s < a.S; s++) {
+    int64_t lo = r0, hi = r1;
+    if (a.offsets) {
+      lo = max(r0, (int64_t)a.offsets[s]);
+      hi = min(r1, (int64_t)a.offsets[s + 1]);
+      if (a.offsets[s] >= r1) break;
+    }
+    if (lo >= hi) continue;  // (the same for all threads)
+    float acc[kEl] = {};
+    float zs = 0.f;
+    uint32_t live_rows = 0;
+    for (int64_t n0 = lo + w * kRows; n0 < hi; n0 += kRouteWarps * kRows) {
+      const int64_t n = n0 + lane / kLanes;
+      const bool in = n < hi;
+      const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
+      uint4 r[kChunks];
+#pragma unroll
+      for (int c = 0; c < kChunks; c++)
+        r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
+      const int k = in && l < a.m ? a.idx[n * a.m + l] : -1;
+      const bool out = !in || (a.mask && !a.mask[n]);
+      if (out) {  // as if all its classes were masked
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) r[c] = Vec16<T>::neg_inf();
+      }
+      RouteRow<kLanes, kEl, T> q;
+      q.make(r, a.scale);
+      const float inv = q.empty ? 0.f : 1.f / q.S;
+#pragma unroll
+      for (int e = 0; e < kEl; e++) acc[e] = fmaf(q.y[e], inv, acc[e]);
+      if (!q.empty) {
+        if (l == 0) {
+          const float z = q.lse(a.scale);
+          zs = fmaf(z, z, zs);
+          live_rows++;
+          if (q.bad && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
+        }
+        if ((unsigned)k < (unsigned)a.K) atomicAdd(&hist[k], 1u);
+        else if (k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEl; e++) {
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+    }
+    zs = warp_sum(zs);
+    live_rows = __reduce_add_sync(0xffffffffu, live_rows);
+    if (lane < kLanes) {
+#pragma unroll
+      for (int e = 0; e < kEl; e++)  // (entry e of lane l is of this class)
+        sums[w][((e / V) * kLanes + l) * V + e % V] = acc[e];
+    }
+    if (lane == 0) zsum[w] = zs, rsum[w] = live_rows;
+    __syncthreads();
+    float* slot = part + (blockIdx.x + (int64_t)s) * route_slot(a.K);
+    for (int k = t; k < a.K; k += kRouteThreads) {
+      float p = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRouteWarps; i++) p += sums[i][k];
+      slot[k] = p;
+      reinterpret_cast<uint32_t*>(slot)[a.K + k] = hist[k];
+      hist[k] = 0;
+    }
+    if (t == 0) {
+      float z = 0.f;
+      uint32_t n = 0;
+      for (int i = 0; i < kRouteWarps; i++) z += zsum[i], n += rsum[i];
+      slot[2 * a.K] = z;
+      reinterpret_cast<uint32_t*>(slot)[2 * a.K + 1] = n;
+    }
+    __syncthreads();
+  }
+}
+
+struct RouteLossOut {
+  float *balance, *z, *load;
+  int32_t *counts, *rows;
+};
+
+// One CTA per segment adds up its slots, in order, in 64 bits.  Threads: `cols` columns (a power
+// of two) times groups that take every so many slots.
+constexpr int kReduceThreads = 512;
+__global__ void __launch_bounds__(kReduceThreads)
+    route_reduce_kernel(RouteArgs a, const float* part, RouteLossOut o, int cols) {
+  __shared__ double sh[kReduceThreads];
+  __shared__ uint32_t shc[kReduceThreads];
+  __shared__ double total[2];
+  __shared__ uint32_t rows;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const int t = threadIdx.x, s = blockIdx.x;
+  const int groups = kReduceThreads / cols, g = t / cols, col = t % cols;
+  int64_t lo = 0, hi = a.N;
+  if (a.offsets) {
+    lo = a.offsets[s];
+    hi = a.offsets[s + 1];
+  }
+  const bool legal = lo >= 0 && lo <= hi && hi <= a.N;
+  if (!legal && t == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+  const int64_t size = route_slot(a.K);
+  const int64_t first = legal && hi > lo ? lo / a.rows + s : 0;
+  const int count = legal && hi > lo ? (int)((hi - 1) / a.rows - lo / a.rows) + 1 : 0;
+  part += first * size;
+  if (t < 32) {
+    double z = 0.0;
+    uint32_t n = 0;
+    for (int q = t; q < count; q += 32) {
+      z += part[q * size + 2 * a.K];
+      n += reinterpret_cast<const uint32_t*>(part)[q * size + 2 * a.K + 1];
+    }
+    z = warp_sum(z);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (t == 0) total[0] = z, rows = n;
+  }
+  __syncthreads();
+  const double L = rows > 0 ? (double)rows : 1.0;
+  double balance = 0.0;
+  for (int k0 = 0; k0 < a.K; k0 += cols) {
+    const int k = k0 + col;
+    double p = 0.0;
+    uint32_t c = 0;
+    if (k < a.K) {
+#pragma unroll 8
+      for (int q = g; q < count; q += groups) {
+        p += part[q * size + k];
+        c += reinterpret_cast<const uint32_t*>(part)[q * size + a.K + k];
+      }
+    }
+    sh[t] = p;
+    shc[t] = c;
+    __syncthreads();
+    if (g == 0 && k < a.K) {
+      for (int i = 1; i < groups; i++) p += sh[i * cols + col], c += shc[i * cols + col];
+      if (o.load) o.load[(int64_t)s * a.K + k] = (float)(p / L);
+      if (o.counts) o.counts[(int64_t)s * a.K + k] = (int32_t)c;
+      balance += (double)c * p;
+    }
+    __syncthreads();
+  }
+  balance = warp_sum(balance);
+  if ((t & 31) == 0) sh[t >> 5] = balance;
+  __syncthreads();
+  if (t == 0) {
+    balance = 0.0;
+    for (int i = 0; i < kReduceThreads / 32; i++) balance += sh[i];
+    const float nan = __int_as_float(0x7fffffff);
+    if (o.balance) o.balance[s] = legal ? (float)(balance * a.K / (a.m * L * L)) : nan;
+    if (o.z) o.z[s] = legal ? (float)(total[0] / L) : nan;
+    if (o.rows) o.rows[s] = (int32_t)rows;
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+struct RouteGradArgs {
+  RouteArgs r;
+  const float* dresp;       // N x m, may be null
+  int renorm;
+  const int32_t *counts, *live;  // S x K and S; null without dbalance and dz
+  const float *dbalance, *dz;    // S each, may be null
+  void* dZ;
+  int64_t ldd;
+};
+
+// A warp takes `rows` consecutive rows, 32 / kLanes at a time; the counts of the segment stay in
+// registers while it lasts.
+template <typename T, int kLanes, int kEl, bool kVec>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_grad_kernel(RouteGradArgs g) {
+  constexpr int kRows = 32 / kLanes;
+  constexpr int V = Vec16<T>::n;
+  constexpr int kChunks = kEl / V;
+  const RouteArgs& a = g.r;
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
+  const int64_t warp = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  const int64_t r0 = warp * a.rows, r1 = min(r0 + a.rows, a.N);
+  if (r0 >= r1) return;
+  const bool losses = g.dbalance || g.dz;
+  int s = losses ? segment_of(a.offsets, a.S, r0) : 0, have = -1;
+  float cnt[kEl];
+  float coef = 0.f, pull = 0.f;
+#pragma unroll
+  for (int e = 0; e < kEl; e++) cnt[e] = 0.f;
+  for (int64_t n0 = r0; n0 < r1; n0 += kRows) {
+    const int64_t n = n0 + lane / kLanes;
+    const bool in = n < r1;
+    const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
+    uint4 r[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; c++)
+      r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
+    int k = -1;
+    float d = 0.f;
+    if (g.dresp && in && l < a.m) {
+      k = a.idx[n * a.m + l];
+      d = g.dresp[n * a.m + l];
+    }
+    const bool legal = (unsigned)k < (unsigned)a.K;
+    if (!legal && k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+    const float xk = legal ? to_f32(row[k]) : -INFINITY;
+    bool counts = losses && in && !(a.mask && !a.mask[n]);
+    if (counts && a.offsets) {
+      while (s + 1 < a.S && n >= a.offsets[s + 1]) s++;
+      counts = n >= a.offsets[s] && n < a.offsets[s + 1];
+    }
+    if (counts && s != have) {
+      have = s;
+      const float L = (float)max(g.live[s], 1);
+      coef = g.dbalance ? g.dbalance[s] * (float)a.K / ((float)a.m * L * L) : 0.f;
+      pull = g.dz ? 2.f * g.dz[s] / L : 0.f;
+      if (g.dbalance) {
+        const int32_t* of = g.counts + (int64_t)s * a.K;
+#pragma unroll
+        for (int e = 0; e < kEl; e++) {
+          const int ke = ((e / V) * kLanes + l) * V + e % V;
+          cnt[e] = ke < a.K ? (float)of[ke] : 0.f;
+        }
+      }
+    }
+    RouteRow<kLanes, kEl, T> q;
+    q.make(r, a.scale);
+    const float c = a.scale * kLog2e, inv = 1.f / q.S;
+    // the chosen: their weights and what they pull on
+    const float top = a.m > 0 && g.renorm ? fmaxf(group_max<kLanes>(xk), -FLT_MAX) : q.ref;
+    const float ek = legal ? ex2((xk - top) * c) : 0.f;
+    const float over = g.renorm ? group_sum<kLanes>(ek) : q.S;
+    const float wk = ek > 0.f || !(ek == ek) ? ek / over : 0.f;
+    const float wd = legal ? wk * d : 0.f;
+    const float R = group_sum<kLanes>(wd);
+    const float add = g.renorm ? fmaf(-wk, R, wd) : wd;
+    float dot = 0.f;
+#pragma unroll
+    for (int e = 0; e < kEl; e++) dot = fmaf(q.y[e], cnt[e], dot);
+    dot = group_sum<kLanes>(dot) * inv;
+    const float cf = counts ? coef : 0.f;
+    const float base = (counts ? pull * q.lse(a.scale) - coef * dot : 0.f) - (g.renorm ? 0.f : R);
+    const bool chosen = __ballot_sync(0xffffffffu, legal) >> (lane - l) & group_mask<kLanes>();
+    const bool live = !q.empty && (counts || chosen);
+    if (q.bad && live && l == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
+    // (a row with a NaN is NaN throughout, also where only some classes are pulled on)
+    const float nan = q.bad ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+    for (int e = 0; e < kEl; e++) q.y[e] = q.y[e] * inv * fmaf(cf, cnt[e], base) + nan;
+    for (int j = 0; j < (g.dresp ? a.m : 0); j++) {
+      const int kj = __shfl_sync(0xffffffffu, legal ? k : -1, (lane - l) + j);
+      const float aj = __shfl_sync(0xffffffffu, add, (lane - l) + j);
+      const int v = kj / V;
+      if (kj >= 0 && v % kLanes == l) {
+        const int at = v / kLanes * V + kj % V;
+#pragma unroll
+        for (int e = 0; e < kEl; e++)
+          if (e == at) q.y[e] += aj;
+      }
+    }
+    __syncwarp();
+    if (!in) continue;
+    T* out = (T*)g.dZ + n * g.ldd;
+#pragma unroll
+    for (int v = 0; v < kChunks; v++) {
+      float x[V];
+#pragma unroll
+      for (int e = 0; e < V; e++) x[e] = live ? q.y[v * V + e] * a.scale : 0.f;
+      const int k0 = (v * kLanes + l) * V;
+      if (kVec && k0 + V <= a.K) {
+        *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e++)
+          if (k0 + e < a.K) from_f32(out + k0 + e, x[e]);
+      }
+    }
+  }
+}
+
+}  // namespace scem

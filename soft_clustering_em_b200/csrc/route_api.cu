@@ -1,0 +1,166 @@
+// route_api.cu -- host side of gmm_route_loss and gmm_route_backward: argument checks and
+// launches.
+#include <math.h>
+
+#include <algorithm>
+
+#include "api_common.h"
+#include "route.cuh"
+
+using namespace scem;
+
+namespace {
+
+constexpr int32_t kMostSegments = 1 << 20;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+size_t elem(int32_t t) { return t == GMM_F32 ? 4 : 2; }
+
+gmm_status check_route(const gmm_rows* r, int32_t m, int32_t S) {
+  if (!r) return GMM_ERR_INVALID_ARG;
+  if (r->N < 0 || r->K < 1 || r->ld < r->K || m < 1 || m > kMaxTopM || S < 0)
+    return GMM_ERR_INVALID_ARG;
+  if (r->dtype != GMM_F32 && r->dtype != GMM_BF16 && r->dtype != GMM_F16)
+    return GMM_ERR_INVALID_ARG;
+  if (!(r->scale > 0.f) || !isfinite(r->scale)) return GMM_ERR_INVALID_ARG;
+  if (!isfinite(r->scale * kLog2e) || r->K > kRouteMostK || S > kMostSegments ||
+      r->N >= ((int64_t)1 << 31) / m || r->ld > kMaxStride ||
+      (double)r->N * (double)r->ld > 1e18)
+    return GMM_ERR_UNSUPPORTED;
+  return GMM_OK;
+}
+
+// CTAs of the loss and the rows of each.
+struct LossPlan {
+  int64_t chunks, rows;
+};
+LossPlan loss_plan(int64_t N) {
+  LossPlan p;
+  p.chunks = std::max<int64_t>(1, std::min<int64_t>((N + 31) / 32, 296));
+  p.rows = std::max<int64_t>(1, (N + p.chunks - 1) / p.chunks);
+  return p;
+}
+
+size_t loss_bytes(const gmm_rows* r, int32_t S) {
+  return (size_t)(loss_plan(r->N).chunks + std::max(S, 1)) * route_slot(r->K) * 4;
+}
+
+template <typename T, int kLanes, int kEl>
+gmm_status load_launch(const RouteArgs& a, float* part, bool vec, unsigned grid, cudaStream_t st) {
+  if (vec)
+    route_load_kernel<T, kLanes, kEl, true><<<grid, kRouteThreads, 0, st>>>(a, part);
+  else
+    route_load_kernel<T, kLanes, kEl, false><<<grid, kRouteThreads, 0, st>>>(a, part);
+  return api_launched(1);
+}
+
+// Lanes and places per row: those of gmm_route's rows.
+template <typename T>
+gmm_status load_dispatch(const RouteArgs& a, float* part, unsigned grid, cudaStream_t st) {
+  const bool vec = (uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0;
+  if (a.K <= 64) return load_launch<T, 8, 8>(a, part, vec, grid, st);
+  if (a.K <= 128) return load_launch<T, 8, 16>(a, part, vec, grid, st);
+  if (a.K <= 256) return load_launch<T, 8, 32>(a, part, vec, grid, st);
+  if (a.K <= 512) return load_launch<T, 16, 32>(a, part, vec, grid, st);
+  return load_launch<T, 32, 32>(a, part, vec, grid, st);
+}
+
+template <typename T, int kLanes, int kEl>
+gmm_status grad_launch(RouteGradArgs g, bool vec, cudaStream_t st) {
+  int sms = 0;
+  gmm_status s = api_device_sms(&sms);
+  if (s != GMM_OK) return s;
+  constexpr int kRows = 32 / kLanes;
+  const int64_t warps = std::min<int64_t>((g.r.N + kRows - 1) / kRows, (int64_t)sms * 16);
+  g.r.rows = ((g.r.N + warps - 1) / warps + kRows - 1) / kRows * kRows;
+  const unsigned grid =
+      (unsigned)((g.r.N + g.r.rows * kRouteWarps - 1) / (g.r.rows * kRouteWarps));
+  if (vec)
+    route_grad_kernel<T, kLanes, kEl, true><<<grid, kRouteThreads, 0, st>>>(g);
+  else
+    route_grad_kernel<T, kLanes, kEl, false><<<grid, kRouteThreads, 0, st>>>(g);
+  return api_launched(1);
+}
+
+template <typename T>
+gmm_status grad_dispatch(const RouteGradArgs& g, cudaStream_t st) {
+  const bool vec = (uintptr_t)g.r.Z % 16 == 0 && g.r.ld * sizeof(T) % 16 == 0 &&
+                   (uintptr_t)g.dZ % 16 == 0 && g.ldd * sizeof(T) % 16 == 0;
+  if (g.r.K <= 64) return grad_launch<T, 8, 8>(g, vec, st);
+  if (g.r.K <= 128) return grad_launch<T, 8, 16>(g, vec, st);
+  if (g.r.K <= 256) return grad_launch<T, 8, 32>(g, vec, st);
+  if (g.r.K <= 512) return grad_launch<T, 16, 32>(g, vec, st);
+  return grad_launch<T, 32, 32>(g, vec, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+gmm_status gmm_route_loss_workspace_size(const gmm_rows* r, int32_t S, size_t* bytes) {
+  gmm_status s = check_route(r, 1, S);
+  if (s != GMM_OK) return s;
+  if (!bytes) return GMM_ERR_INVALID_ARG;
+  *bytes = loss_bytes(r, S);
+  return GMM_OK;
+}
+
+gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, int32_t m,
+                          const uint8_t* mask, const int32_t* offsets, int32_t S, float* balance,
+                          float* z, float* load, int32_t* counts, int32_t* rows,
+                          uint32_t* dev_flags, void* ws, size_t ws_bytes, void* stream) {
+  gmm_status s = check_route(r, m, S);
+  if (s != GMM_OK) return s;
+  if (!offsets && S != 1) return GMM_ERR_INVALID_ARG;
+  if (S == 0) return GMM_OK;
+  if (!balance && !z && !load && !counts && !rows) return GMM_ERR_INVALID_ARG;
+  if (r->N > 0 && (!Z || !idx)) return GMM_ERR_INVALID_ARG;
+  if ((uintptr_t)Z % elem(r->dtype) != 0) return GMM_ERR_UNSUPPORTED;
+  if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < loss_bytes(r, S)) return GMM_ERR_WORKSPACE;
+  const LossPlan plan = loss_plan(r->N);
+  const RouteArgs a = {Z,    r->N,    r->ld, r->K,      r->scale, idx, m,
+                       mask, offsets, S,     plan.rows, dev_flags};
+  cudaStream_t st = (cudaStream_t)stream;
+  if (r->N > 0) {
+    const unsigned grid = (unsigned)((r->N + plan.rows - 1) / plan.rows);
+    s = r->dtype == GMM_F32    ? load_dispatch<float>(a, (float*)ws, grid, st)
+        : r->dtype == GMM_BF16 ? load_dispatch<__nv_bfloat16>(a, (float*)ws, grid, st)
+                               : load_dispatch<__half>(a, (float*)ws, grid, st);
+    if (s != GMM_OK) return s;
+  }
+  int cols = 32;
+  while (cols < r->K && cols < kReduceThreads) cols *= 2;
+  const RouteLossOut o = {balance, z, load, counts, rows};
+  return api_launch_next(route_reduce_kernel, dim3((unsigned)S), kReduceThreads, 0, st, a,
+                         (const float*)ws, o, cols);
+}
+
+gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* idx, int32_t m,
+                              const float* dresp, int32_t renorm, const int32_t* counts,
+                              const int32_t* rows, const float* dbalance, const float* dz,
+                              const uint8_t* mask, const int32_t* offsets, int32_t S, void* dZ,
+                              int64_t ldd, uint32_t* dev_flags, void* stream) {
+  gmm_status s = check_route(r, m, S);
+  if (s != GMM_OK) return s;
+  if (ldd < r->K) return GMM_ERR_INVALID_ARG;
+  if (ldd > kMaxStride || (double)r->N * (double)ldd > 1e18) return GMM_ERR_UNSUPPORTED;
+  if (!dresp && !dbalance && !dz) return GMM_ERR_INVALID_ARG;
+  const bool losses = dbalance || dz;
+  if (losses && !offsets && S != 1) return GMM_ERR_INVALID_ARG;
+  if (losses && offsets && S < 1) return GMM_ERR_INVALID_ARG;
+  if (r->N == 0) return GMM_OK;
+  if (!Z || !dZ || (dresp && !idx) || (dbalance && !counts) || (losses && !rows))
+    return GMM_ERR_INVALID_ARG;
+  if (dZ == Z && ldd != r->ld) return GMM_ERR_INVALID_ARG;
+  if ((uintptr_t)Z % elem(r->dtype) != 0 || (uintptr_t)dZ % elem(r->dtype) != 0)
+    return GMM_ERR_UNSUPPORTED;
+  const RouteArgs a = {Z,    r->N,    r->ld, r->K, r->scale, idx, m,
+                       mask, offsets, S,     0,    dev_flags};
+  const RouteGradArgs g = {a, dresp, renorm != 0, counts, rows, dbalance, dz, dZ, ldd};
+  cudaStream_t st = (cudaStream_t)stream;
+  if (r->dtype == GMM_F32) return grad_dispatch<float>(g, st);
+  if (r->dtype == GMM_BF16) return grad_dispatch<__nv_bfloat16>(g, st);
+  return grad_dispatch<__half>(g, st);
+}
+
+}  // extern "C"

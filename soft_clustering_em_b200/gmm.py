@@ -8,6 +8,7 @@ raises -- there is no fallback implementation.
 """
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -29,6 +30,9 @@ EXPORTS = ("gmm_workspace_size", "gmm_plan", "gmm_init", "gmm_init_rows", "gmm_e
            "gmm_estep_stats", "gmm_mstep", "gmm_fit", "gmm_loglik",
            "gmm_assign_topm", "gmm_ivf_workspace_size", "gmm_ivf_build", "gmm_logprobs",
            "gmm_logprobs_backward", "gmm_route", "gmm_moe_workspace_size", "gmm_moe",
+           "gmm_route_loss_workspace_size", "gmm_route_loss", "gmm_route_backward", "gmm_embed",
+           "gmm_embed_workspace_size", "gmm_embed_backward", "gmm_beam_workspace_size",
+           "gmm_beam_select", "gmm_beam_reorder",
            "gmm_device_status",
            "gmm_trace_fused", "gmm_set_wait_budget", "gmm_launch_count", "gmm_status_string")
 
@@ -53,6 +57,19 @@ class gmm_moe_problem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("m", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class gmm_embed_problem(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("m", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class gmm_beam_state(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("outer", ctypes.c_int64), ("outer_stride", ctypes.c_int64),
+                ("count", ctypes.c_int64), ("pos_bytes", ctypes.c_int64),
+                ("by_len", ctypes.c_int32)]
 
 
 class GmmError(RuntimeError):
@@ -99,6 +116,16 @@ def load_library(path: str = LIB_PATH):
     lib.gmm_route.argtypes = [PR, P, I32, I32, P, P, P, P]
     lib.gmm_moe_workspace_size.argtypes = [PM, ctypes.POINTER(SZ)]
     lib.gmm_moe.argtypes = [PM, P, P, P, P, P, P, P, SZ, P]
+    PE = ctypes.POINTER(gmm_embed_problem)
+    lib.gmm_route_loss_workspace_size.argtypes = [PR, I32, ctypes.POINTER(SZ)]
+    lib.gmm_route_loss.argtypes = [PR, P, P, I32, P, P, I32, P, P, P, P, P, P, P, SZ, P]
+    lib.gmm_route_backward.argtypes = [PR, P, P, I32, P, I32, P, P, P, P, P, P, I32, P, I64, P, P]
+    lib.gmm_embed.argtypes = [PE, P, P, P, P, P, P]
+    lib.gmm_embed_workspace_size.argtypes = [PE, ctypes.POINTER(SZ)]
+    lib.gmm_embed_backward.argtypes = [PE, P, P, P, P, P, I32, I64, I32, P, P, P, SZ, P]
+    lib.gmm_beam_workspace_size.argtypes = [PR, I32, I32, ctypes.POINTER(SZ)]
+    lib.gmm_beam_select.argtypes = [PR, P, I32, P, P, I32, I32, P, P, P, P, P, SZ, P]
+    lib.gmm_beam_reorder.argtypes = [I64, I32, P, P, I32, P, P, P]
     lib.gmm_device_status.argtypes = [P, SZ, P, ctypes.POINTER(ctypes.c_uint32), I32]
     lib.gmm_trace_fused.argtypes = [P, P]
     lib.gmm_set_wait_budget.argtypes = [ctypes.c_uint64]
@@ -602,6 +629,321 @@ def gmm_moe(X, idx, resp, W_up, W_down, act=GMM_ACT_SILU, out=None, ws=None, str
     if dev_flags is not None:
         dev_flags |= ws[:4].view(torch.int32)
     return out
+
+
+class RouteLoss(NamedTuple):
+    """Results of gmm_route_loss for S segments of rows and K experts."""
+
+    balance: torch.Tensor  # S
+    z: torch.Tensor        # S
+    load: torch.Tensor     # S x K: mean probabilities
+    counts: torch.Tensor   # S x K int32: choices
+    rows: torch.Tensor     # S int32: rows that count
+
+
+def _segments(Z, idx, mask, offsets):
+    """Checks of what says which rows count where; returns the number of segments."""
+    N = Z.shape[0]
+    if idx is not None:
+        if idx.dim() != 2:
+            raise ValueError("idx must be N x m")
+        _vector(idx, (N, idx.shape[1]), torch.int32, "idx")
+    if mask is not None:
+        _vector(mask, (N,), torch.bool if mask.dtype == torch.bool else torch.uint8, "mask")
+    if offsets is None:
+        return 1
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be S + 1 row numbers")
+    _vector(offsets, tuple(offsets.shape), torch.int32, "offsets")
+    return offsets.shape[0] - 1
+
+
+def _bytes(size_fn, what, *args):
+    n = ctypes.c_size_t(0)
+    _check(size_fn(*args, ctypes.byref(n)), what)
+    return int(n.value)
+
+
+def _workspace(ws, size, device):
+    """A workspace of `size` bytes, allocated when ws is None."""
+    return torch.empty(size(), dtype=torch.uint8, device=device) if ws is None else ws
+
+
+def gmm_route_loss(Z, idx, offsets=None, mask=None, scale=1.0, ws=None, dev_flags=None,
+                   stream=None) -> RouteLoss:
+    """How the assignment idx loads the experts, the balance loss K sum_k counts_k / (m L) load_k
+    (1 for an even load) and the mean squared log-sum-exp z, for each segment of rows.
+
+    Z: N x K router logits (K <= 1024), float32, bfloat16 or float16, any row stride; idx: N x m
+    int32 as gmm_route returns it, -1 for an unused choice.  offsets: S + 1 int32, segment s is
+    rows offsets[s] to offsets[s + 1]; None: one segment of all rows.  mask: N bool or uint8, 0
+    for rows that do not count.  ws: a uint8 device tensor of gmm_route_loss_workspace_size bytes
+    (allocated here when None).  dev_flags (1 int32 device tensor, optional) collects the device
+    status bits.  stream (None: the current one) runs the call and owns the results.
+    """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_route_loss(Z, idx, offsets, mask, scale, ws, dev_flags)
+    r = _rows(Z, scale)
+    _same_device(Z, idx, offsets, mask, ws, dev_flags)
+    S = _segments(Z, idx, mask, offsets)
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    K = Z.shape[1]
+    real = torch.empty(S * (K + 2), dtype=torch.float32, device=Z.device)
+    whole = torch.empty(S * (K + 1), dtype=torch.int32, device=Z.device)
+    ws = _workspace(ws, lambda: gmm_route_loss_workspace_size(Z, S, scale), Z.device)
+    at, wh = real.data_ptr(), whole.data_ptr()
+    _launch(load_library().gmm_route_loss, "gmm_route_loss", Z.device, ctypes.byref(r),
+            Z.data_ptr(), idx.data_ptr(), idx.shape[1], _address(mask), _address(offsets), S,
+            at + 4 * S * K, at + 4 * S * (K + 1), at, wh, wh + 4 * S * K, _address(dev_flags),
+            ws.data_ptr(), ws.numel())
+    load, balance, z = real.split((S * K, S, S))
+    counts, rows = whole.split((S * K, S))
+    return RouteLoss(balance, z, load.view(S, K), counts.view(S, K), rows)
+
+
+def gmm_route_loss_workspace_size(Z, S=1, scale=1.0) -> int:
+    """Bytes of gmm_route_loss's workspace for logits like Z and S segments."""
+    return _bytes(load_library().gmm_route_loss_workspace_size, "gmm_route_loss_workspace_size",
+                  ctypes.byref(_rows(Z, scale)), S)
+
+
+def gmm_route_backward(Z, idx, dresp=None, renorm=False, counts=None, rows=None, dbalance=None,
+                       dz=None, offsets=None, mask=None, scale=1.0, out=None, dev_flags=None,
+                       stream=None):
+    """Gradient with respect to the router logits Z of gmm_route's weights, for dresp (N x m
+    float32, or None), and of gmm_route_loss's losses, for dbalance and dz (S float32, or None).
+
+    idx, renorm, offsets, mask, scale as the forward calls took or gave them; counts and rows as
+    gmm_route_loss returned them (with dbalance or dz), or summed over the shards of a batch.
+    out: N x K of Z's type to write to, Z itself included; allocated when None.
+    """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_route_backward(Z, idx, dresp, renorm, counts, rows, dbalance, dz, offsets,
+                                      mask, scale, out, dev_flags)
+    r = _rows(Z, scale)
+    _same_device(Z, idx, dresp, counts, rows, dbalance, dz, offsets, mask, out, dev_flags)
+    S = _segments(Z, idx, mask, offsets)
+    N, K = Z.shape
+    m = idx.shape[1]
+    _vector(dresp, (N, m), torch.float32, "dresp")
+    _vector(counts, (S, K), torch.int32, "counts")
+    _vector(rows, (S,), torch.int32, "rows")
+    _vector(dbalance, (S,), torch.float32, "dbalance")
+    _vector(dz, (S,), torch.float32, "dz")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    if out is None:
+        out = torch.empty(N, K, dtype=Z.dtype, device=Z.device)
+    o = _rows(out, 1.0)
+    if out.dtype != Z.dtype or out.shape != Z.shape:
+        raise ValueError("out must have the shape and type of Z")
+    _launch(load_library().gmm_route_backward, "gmm_route_backward", Z.device, ctypes.byref(r),
+            Z.data_ptr(), idx.data_ptr(), m, _address(dresp), int(bool(renorm)), _address(counts),
+            _address(rows), _address(dbalance), _address(dz), _address(mask), _address(offsets),
+            S, out.data_ptr(), o.ld, _address(dev_flags))
+    return out
+
+
+def _choices(idx, resp, N):
+    """Checks an assignment of N rows, N x m or N (m = 1); returns m."""
+    if idx.dim() not in (1, 2):
+        raise ValueError("idx must be N or N x m")
+    if idx.shape[0] != N:
+        raise ValueError(f"idx must have {N} rows, got {idx.shape[0]}")
+    _vector(idx, tuple(idx.shape), torch.int32, "idx")
+    _vector(resp, tuple(idx.shape), torch.float32, "resp")
+    return idx.shape[1] if idx.dim() == 2 else 1
+
+
+def _ld(t, name):
+    """Elements from one row to the next of a matrix with a unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with a unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def embed_problem(idx, K, scale, ldw, Y) -> gmm_embed_problem:
+    """The problem of a gmm_embed or gmm_embed_backward call on these tensors."""
+    if Y.dtype not in _DTYPES:
+        raise TypeError(f"rows must be float32, bfloat16 or float16, got {Y.dtype}")
+    N, D = Y.shape
+    m = idx.shape[1] if idx.dim() == 2 else 1
+    return gmm_embed_problem(N, m, K, D, _DTYPES[Y.dtype], scale, ldw, _ld(Y, "Y"))
+
+
+def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=None):
+    """scale * sum_j resp_nj W[idx_nj]: the embedding of tokens (idx: N int32), or points put
+    together from a codebook's or mixture's entries (idx, resp: N x m, as gmm_assign_topm and
+    gmm_route return them; m <= 8).
+
+    W: K x D float32, bfloat16 or float16, any row stride.  A choice of -1 is unused; resp None is
+    weights of 1.  Returns N x D of W's type (into out when given).
+    """
+    if stream is not None:
+        with _on(stream, W):
+            return gmm_embed(W, idx, resp, scale, out, dev_flags)
+    _same_device(W, idx, resp, out, dev_flags)
+    N = idx.shape[0]
+    _choices(idx, resp, N)
+    ldw = _ld(W, "W")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    if out is None:
+        out = torch.empty(N, W.shape[1], dtype=W.dtype, device=W.device)
+    if out.dtype != W.dtype or out.shape != (N, W.shape[1]):
+        raise ValueError("out must be N x D of W's type")
+    p = embed_problem(idx, W.shape[0], scale, ldw, out)
+    _launch(load_library().gmm_embed, "gmm_embed", W.device, ctypes.byref(p), W.data_ptr(),
+            idx.data_ptr(), _address(resp), out.data_ptr(), _address(dev_flags))
+    return out
+
+
+def gmm_embed_workspace_size(p: gmm_embed_problem) -> int:
+    return _bytes(load_library().gmm_embed_workspace_size, "gmm_embed_workspace_size",
+                  ctypes.byref(p))
+
+
+def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accumulate=False,
+                       ws=None, dev_flags=None, stream=None):
+    """(dW, dresp): the gradients of gmm_embed(W, idx, resp, scale) for its upstream gradient dY
+    (N x D).
+
+    dW: K x D of dY's type, or in out (of dY's type or float32); with accumulate it is added to
+    what out holds, and rows that idx does not name are not touched.  dresp: of resp's shape, None
+    unless W is given.  ws: a uint8 device tensor of gmm_embed_workspace_size bytes (allocated here
+    when None).
+    """
+    if stream is not None:
+        with _on(stream, dY):
+            return gmm_embed_backward(dY, idx, K, resp, W, scale, out, accumulate, ws, dev_flags)
+    _same_device(dY, idx, resp, W, out, ws, dev_flags)
+    ldy = _ld(dY, "dY")
+    N, D = dY.shape
+    _choices(idx, resp, N)
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    K = int(K)
+    if W is not None and (W.dtype != dY.dtype or W.shape != (K, D)):
+        raise ValueError("W must be K x D of dY's type")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to out, which is missing")
+        out = torch.empty(K, D, dtype=dY.dtype, device=dY.device)
+    if out.dtype not in (dY.dtype, torch.float32) or out.shape != (K, D):
+        raise ValueError("out must be K x D of dY's type or float32")
+    dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=dY.device)
+    p = embed_problem(idx, K, scale, D if W is None else _ld(W, "W"), dY)
+    ws = _workspace(ws, lambda: gmm_embed_workspace_size(p), dY.device)
+    _launch(load_library().gmm_embed_backward, "gmm_embed_backward", dY.device, ctypes.byref(p),
+            dY.data_ptr(), idx.data_ptr(), _address(resp), _address(W), out.data_ptr(),
+            _DTYPES[out.dtype], _ld(out, "out"), int(bool(accumulate)), _address(dresp),
+            _address(dev_flags), ws.data_ptr(), ws.numel())
+    return out, dresp
+
+
+class BeamStep(NamedTuple):
+    """Results of gmm_beam_select for B groups, m candidates each."""
+
+    scores: torch.Tensor  # B x m
+    parent: torch.Tensor  # B x m int32: the candidate's beam, in its group
+    token: torch.Tensor   # B x m int32
+
+
+def gmm_beam_workspace_size(Z, w, m, scale=1.0) -> int:
+    """Bytes of gmm_beam_select's workspace for logits like Z, w beams and m candidates."""
+    return _bytes(load_library().gmm_beam_workspace_size, "gmm_beam_workspace_size",
+                  ctypes.byref(_rows(Z, scale)), w, m)
+
+
+def gmm_beam_select(Z, scores, m=None, ended=None, end_id=0, scale=1.0, ws=None, dev_flags=None,
+                    stream=None) -> BeamStep:
+    """The m best continuations of each group of beams (m None: as many as beams), by
+    scores[b, i] + log p of row b * w + i.
+
+    Z: (B * w) x K logits, float32, bfloat16 or float16, any row stride; the logits are scale * Z.
+    scores: B x w float32, -inf for no beam.  ended: B x w bool or uint8; a beam that has ended has
+    the one candidate (itself, end_id) with its score as it is.  Candidates that run out have -inf,
+    -1, -1.  w and m <= 32.  ws: a uint8 device tensor of gmm_beam_workspace_size bytes (allocated
+    here when None).
+    """
+    if stream is not None:
+        with _on(stream, Z):
+            return gmm_beam_select(Z, scores, m, ended, end_id, scale, ws, dev_flags)
+    r = _rows(Z, scale)
+    _same_device(Z, scores, ended, ws, dev_flags)
+    if scores.dim() != 2 or scores.numel() != Z.shape[0]:
+        raise ValueError("scores must be B x w for B * w rows of logits")
+    B, w = scores.shape
+    _vector(scores, (B, w), torch.float32, "scores")
+    if ended is not None:
+        _vector(ended, (B, w), torch.bool if ended.dtype == torch.bool else torch.uint8, "ended")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    m = w if m is None else int(m)
+    ws = _workspace(ws, lambda: gmm_beam_workspace_size(Z, w, m, scale), Z.device)
+    out = torch.empty(B, m, dtype=torch.float32, device=Z.device)
+    parent, token = torch.empty(2, B, m, dtype=torch.int32, device=Z.device).unbind(0)
+    _launch(load_library().gmm_beam_select, "gmm_beam_select", Z.device, ctypes.byref(r),
+            Z.data_ptr(), w, scores.data_ptr(), _address(ended), int(end_id), m, out.data_ptr(),
+            parent.data_ptr(), token.data_ptr(), _address(dev_flags), ws.data_ptr(), ws.numel())
+    return BeamStep(out, parent, token)
+
+
+_STATE = struct.Struct("=6qi4x")  # gmm_beam_state
+
+
+def _state(t, rows, dim):
+    """A tensor of `rows` rows as gmm_beam_state; dim: the dimension of its positions."""
+    if t.dim() < 1 or t.shape[0] != rows:
+        raise ValueError(f"a state must have {rows} rows, got {tuple(t.shape)}")
+    size, shape, stride = t.element_size(), t.shape, t.stride()
+    inner = 1 if dim is None else dim
+    dense = 1  # elements of the dimensions behind, which must lie densely
+    for d in range(t.dim() - 1, inner - 1, -1):
+        if shape[d] > 1 and stride[d] != dense:
+            raise ValueError("a state must be dense from its positions on")
+        dense *= shape[d]
+    outer, outer_stride = 1, 0
+    for d in range(inner - 1, 0, -1):
+        if shape[d] == 1:
+            continue
+        if outer > 1 and stride[d] != outer * outer_stride:
+            raise ValueError("the dimensions before a state's positions must lie evenly")
+        outer_stride = stride[d] if outer == 1 else outer_stride
+        outer *= shape[d]
+    count = 1 if dim is None else shape[dim]
+    per = dense // count if count else 0
+    return (t.data_ptr(), stride[0] * size, outer, outer_stride * size, count, per * size,
+            int(dim is not None))
+
+
+def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream=None):
+    """The beams' states after their parents, in place: state[b, i] <- state[b, parent[b, i]].
+
+    states: a tensor or a list of tensors of B * w rows each (a cache (B * w, heads, positions,
+    width), token ids (B * w, positions), any type); parent: B x w int32, a beam of the same group,
+    -1 to leave one as it is.  dim: the dimension of the positions, for all states or a list with
+    one for each, None for states without; lens (B int32): how many positions of a group are used,
+    those behind are left as they are.  w <= 32.
+    """
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    if stream is not None:
+        with _on(stream, parent):
+            return gmm_beam_reorder(states, parent, lens, dim, dev_flags)
+    _same_device(parent, lens, dev_flags, *states)
+    if parent.dim() != 2:
+        raise ValueError("parent must be B x w")
+    B, w = parent.shape
+    _vector(parent, (B, w), torch.int32, "parent")
+    _vector(lens, (B,), torch.int32, "lens")
+    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    dims = list(dim) if isinstance(dim, (list, tuple)) else [dim] * len(states)
+    if len(dims) != len(states):
+        raise ValueError("dim must be one for each state")
+    for t, d in zip(states, dims):
+        if d is not None and not 0 < d < t.dim():
+            raise ValueError("dim must be a dimension of the state behind its rows")
+    packed = b"".join([_STATE.pack(*_state(t, B * w, d)) for t, d in zip(states, dims)])
+    _launch(load_library().gmm_beam_reorder, "gmm_beam_reorder", parent.device, B, w,
+            parent.data_ptr(), _address(lens), len(states), packed, _address(dev_flags))
 
 
 def gmm_device_status(ws, clear=True, stream=None):
