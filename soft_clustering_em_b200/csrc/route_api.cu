@@ -144,11 +144,11 @@ gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* i
   if (s != GMM_OK) return s;
   if (ldd < r->K) return GMM_ERR_INVALID_ARG;
   if (ldd > kMaxStride || (double)r->N * (double)ldd > 1e18) return GMM_ERR_UNSUPPORTED;
-  if (!dresp && !dbalance && !dz) return GMM_ERR_INVALID_ARG;
   const bool losses = dbalance || dz;
   if (losses && !offsets && S != 1) return GMM_ERR_INVALID_ARG;
   if (losses && offsets && S < 1) return GMM_ERR_INVALID_ARG;
   if (r->N == 0) return GMM_OK;
+  if (!dresp && !losses) return GMM_ERR_INVALID_ARG;
   if (!Z || !dZ || (dresp && !idx) || (dbalance && !counts) || (losses && !rows))
     return GMM_ERR_INVALID_ARG;
   if (dZ == Z && ldd != r->ld) return GMM_ERR_INVALID_ARG;

@@ -654,7 +654,7 @@ def _segments(Z, idx, mask, offsets):
         return 1
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be S + 1 row numbers")
-    _vector(offsets, tuple(offsets.shape), torch.int32, "offsets")
+    _vector(offsets, offsets.shape, torch.int32, "offsets")
     return offsets.shape[0] - 1
 
 
@@ -745,15 +745,15 @@ def gmm_route_backward(Z, idx, dresp=None, renorm=False, counts=None, rows=None,
     return out
 
 
-def _choices(idx, resp, N):
-    """Checks an assignment of N rows, N x m or N (m = 1); returns m."""
+def _choices(idx, resp, N=None):
+    """Checks an assignment of N rows (None: any), N x m or N (m = 1); returns its rows."""
     if idx.dim() not in (1, 2):
         raise ValueError("idx must be N or N x m")
-    if idx.shape[0] != N:
+    if N is not None and idx.shape[0] != N:
         raise ValueError(f"idx must have {N} rows, got {idx.shape[0]}")
-    _vector(idx, tuple(idx.shape), torch.int32, "idx")
-    _vector(resp, tuple(idx.shape), torch.float32, "resp")
-    return idx.shape[1] if idx.dim() == 2 else 1
+    _vector(idx, idx.shape, torch.int32, "idx")
+    _vector(resp, idx.shape, torch.float32, "resp")
+    return idx.shape[0]
 
 
 def _ld(t, name):
@@ -784,8 +784,7 @@ def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=Non
         with _on(stream, W):
             return gmm_embed(W, idx, resp, scale, out, dev_flags)
     _same_device(W, idx, resp, out, dev_flags)
-    N = idx.shape[0]
-    _choices(idx, resp, N)
+    N = _choices(idx, resp)
     ldw = _ld(W, "W")
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
     if out is None:

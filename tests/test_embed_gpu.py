@@ -1,0 +1,281 @@
+"""gmm_embed and gmm_embed_backward on the GPU against oracle/assignments.py.
+
+Tolerances, for u = 2^-24 and sums of c float32 terms one after another: (c + 4) u times the sum of
+the terms' magnitudes (each product and each addition rounds once, and the scale), then half a step
+of the result's type relative to the value, and half its smallest step (float16 2^-25, bfloat16
+2^-134).  A class that is named n times is summed in chunks of at most 128 and the chunks' sums over
+8 warps in turn: c <= min(n, 128) + n / 128 + 8.  dresp: a lane adds up D / 8 terms, then 5 levels.
+"""
+import numpy as np
+import pytest
+
+from oracle import assignments as A
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+LEAST = {"f32": 2.0 ** -150, "bf16": 2.0 ** -134, "f16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def G():
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from soft_clustering_em_b200 import build
+    from soft_clustering_em_b200 import gmm
+
+    build.build()
+    gmm.load_library()
+    return gmm
+
+
+def _t(dtype):
+    import torch
+
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+
+
+def _rows(rng, N, D, dtype, pad=0, shift=0):
+    """N x D numbers in rows of D + pad, `shift` entries into a buffer of NaN; and their values."""
+    import torch
+
+    buf = torch.full((N * (D + pad) + shift + 64,), float("nan"), dtype=_t(dtype), device="cuda")
+    x = buf[shift:shift + N * (D + pad)].view(N, D + pad)[:, :D]
+    x.copy_(torch.from_numpy(rng.normal(size=(N, D)).astype(np.float32)))
+    return x, x.double().cpu().numpy()
+
+
+def _assignment(rng, N, m, K, weights):
+    import torch
+
+    idx = rng.integers(0, K, (N, m)).astype(np.int32)
+    idx[rng.random((N, m)) < 0.1] = -1
+    if N > 4:
+        idx[1] = -1               # a row without choices
+        idx[2] = idx[0]           # the same choices in two rows
+        idx[3] = idx[3, 0]        # and the same choice m times in one
+        idx[-1] = K - 1
+    r = rng.normal(size=(N, m)).astype(np.float32) if weights else None
+    return (torch.from_numpy(idx).cuda(), None if r is None else torch.from_numpy(r).cuda(),
+            idx, r)
+
+
+def _near(got, want, tol, what=""):
+    got = got.double().cpu().numpy() if hasattr(got, "cpu") else got
+    off = np.abs(got - want) - tol
+    assert (off <= 0).all(), (what, off.max(), np.unravel_index(off.argmax(), off.shape))
+
+
+def _depth(named):
+    return (np.minimum(named, 128) + named / 128 + 8)[:, None]
+
+
+SHAPES = [  # N, m, K, D, pad, shift
+    (1, 1, 1, 1, 0, 0), (1, 1, 50, 8, 0, 0), (3, 2, 7, 5, 0, 0), (33, 1, 100, 64, 0, 0),
+    (257, 3, 300, 96, 8, 0), (500, 8, 40, 24, 0, 1), (1000, 1, 2000, 257, 3, 0),
+    (70, 2, 10, 2048, 0, 0), (64, 1, 9, 8200, 0, 0), (900, 4, 5000, 100, 4, 2),
+    (5000, 1, 3, 16, 0, 0), (2, 1, 70000, 40, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,m,K,D,pad,shift", SHAPES)
+def test_lookup(G, N, m, K, D, pad, shift, dtype):
+    rng = np.random.default_rng(N + D)
+    W, w = _rows(rng, K, D, dtype, pad, shift)
+    idx, resp, i, r = _assignment(rng, N, m, K, m > 1 or N % 2)
+    want, size = A.embed(w, i, r, 1.25)
+    tol = (m + 4) * U * size + HALF[dtype] * np.abs(want) + LEAST[dtype]
+    _near(G.gmm_embed(W, idx, resp, scale=1.25), want, tol)
+    if m == 1:
+        _near(G.gmm_embed(W, idx[:, 0].contiguous(), None if resp is None else resp[:, 0].contiguous(),
+                          scale=1.25), want, tol)
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
+                                       ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("N,m,K,D,pad,shift", SHAPES)
+def test_gradient(G, N, m, K, D, pad, shift, dtype, out, add):
+    rng = np.random.default_rng(N + D + 1)
+    dY, dy = _rows(rng, N, D, dtype, pad, shift)
+    idx, resp, i, r = _assignment(rng, N, m, K, m > 1 or N % 2)
+    dW, old = _rows(rng, K, D, out, pad, shift)
+    want, size, named = A.embed_backward(dy, i, K, r, 0.75)
+    tol = (_depth(named) + 4) * U * size
+    if add:
+        want = want + old
+        tol = tol + U * np.abs(want)
+    tol = tol + HALF[out] * np.abs(want) + LEAST[out]
+    before = dW.clone()
+    got, none = G.gmm_embed_backward(dY, idx, K, resp, scale=0.75, out=dW, accumulate=add)
+    assert none is None and got is dW
+    if add:  # rows that nothing names are not touched
+        tol[named == 0] = 0
+    _near(dW, want, tol)
+    again = before.clone()
+    again, _ = G.gmm_embed_backward(dY, idx, K, resp, scale=0.75, out=again, accumulate=add)
+    if not (pad or shift):
+        assert (again == dW).all()  # from run to run
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,m,K,D,pad,shift", SHAPES)
+def test_gradient_of_the_weights(G, N, m, K, D, pad, shift, dtype):
+    rng = np.random.default_rng(N + D + 2)
+    dY, dy = _rows(rng, N, D, dtype, pad, shift)
+    W, w = _rows(rng, K, D, dtype, pad, shift)
+    idx, resp, i, r = _assignment(rng, N, m, K, True)
+    dW, dresp = G.gmm_embed_backward(dY, idx, K, resp, W=W, scale=0.75)
+    want, size = A.embed_dresp(dy, w, i, 0.75)
+    _near(dresp, want, (D / 8 + 12) * U * size)
+    want, size, named = A.embed_backward(dy, i, K, r, 0.75)
+    _near(dW, want, (_depth(named) + 4) * U * size + HALF[dtype] * np.abs(want) + LEAST[dtype])
+
+
+@pytest.mark.parametrize("N,K,D,how", [
+    (20000, 5, 64, "one"), (20000, 100, 40, "two"), (300_000, 1000, 8, "skewed"),
+    (70_000, 1 << 21, 4, "skewed"), (1000, 1 << 20, 3, "skewed"), (131_073, 30, 16, "one"),
+    (2048, 1023, 8, "all"), (4096, 1024, 8, "all"),
+])
+def test_lists_of_all_lengths(G, N, K, D, how):
+    """A class that has every choice, runs that end on a chunk's border, one to three digits."""
+    import torch
+
+    rng = np.random.default_rng(N)
+    dY, dy = _rows(rng, N, D, "f32")
+    i = {"one": np.full(N, K - 1), "two": np.where(np.arange(N) < N // 2, 3, 97),
+         "skewed": np.minimum((K ** rng.random(N)).astype(np.int64) - 1, K - 1),
+         "all": np.arange(N)[::-1] % K}[how].astype(np.int32)
+    got, _ = G.gmm_embed_backward(dY, torch.from_numpy(i).cuda(), K)
+    want, size, named = A.embed_backward(dy, i, K)
+    _near(got, want, (_depth(named) + 4) * U * size + HALF["f32"] * np.abs(want))
+    got2, _ = G.gmm_embed_backward(dY, torch.from_numpy(i).cuda(), K)
+    assert torch.equal(got, got2)
+
+
+def test_nothing_to_look_up(G):
+    import torch
+
+    W = torch.ones(5, 8, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert G.gmm_embed(W, none).shape == (0, 8)
+    out = torch.full((5, 8), 3.0, device="cuda")
+    G.gmm_embed_backward(W[:0], none, 5, out=out, accumulate=True)
+    assert (out == 3).all()
+    G.gmm_embed_backward(W[:0], none, 5, out=out)
+    assert (out == 0).all()
+    idx = torch.full((7,), -1, dtype=torch.int32, device="cuda")
+    assert (G.gmm_embed(W, idx) == 0).all()
+    G.gmm_embed_backward(torch.full((7, 8), float("nan"), device="cuda"), idx, 5, out=out)
+    assert (out == 0).all()
+
+
+def test_bad_indices_are_left_out_and_told(G):
+    import torch
+
+    W = torch.randn(6, 16, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = torch.tensor([[0, 5], [2, -1]], dtype=torch.int32, device="cuda")
+    G.gmm_embed(W, good, dev_flags=flags)
+    G.gmm_embed_backward(W[:2], good, 6, W=W, dev_flags=flags)
+    assert flags.item() == 0
+    bad = torch.tensor([[0, 6], [-2, 2]], dtype=torch.int32, device="cuda")
+    Y = G.gmm_embed(W, bad, dev_flags=flags)
+    assert flags.item() == G.GMM_DEVFLAG_BAD_INDEX
+    assert torch.equal(Y, W[[0, 2]])
+    flags.zero_()
+    dW, dresp = G.gmm_embed_backward(W[:2], bad, 6, W=W, dev_flags=flags)
+    assert flags.item() == G.GMM_DEVFLAG_BAD_INDEX
+    assert torch.equal(dW[[0, 2]], W[[0, 1]]) and (dW[[1, 3, 4, 5]] == 0).all()
+    assert (dresp[[0, 1], [1, 0]] == 0).all()
+
+
+def test_a_nan_reaches_only_what_it_is_part_of(G):
+    import torch
+
+    W = torch.ones(4, 24, device="cuda", dtype=torch.bfloat16)
+    W[1] = float("nan")
+    W[3] = float("inf")
+    idx = torch.tensor([[0, 2], [1, 2], [-1, 0], [3, 0]], dtype=torch.int32, device="cuda")
+    Y = G.gmm_embed(W, idx)
+    assert (Y[0] == 2).all() and Y[1].isnan().all() and (Y[2] == 1).all() and Y[3].isinf().all()
+    dY = torch.ones(4, 24, device="cuda")
+    dY[1] = float("nan")
+    dW, _ = G.gmm_embed_backward(dY, idx, 4)
+    assert (dW[0] == 3).all() and dW[1].isnan().all() and dW[2].isnan().all() and (dW[3] == 1).all()
+
+
+def test_tables_beyond_32_bits(G):
+    """Rows whose offsets pass 2^32 bytes and 2^31 elements."""
+    import torch
+
+    K, D = 70_000, 32_768  # 2.3e9 bfloat16
+    W = torch.zeros(K, D, dtype=torch.bfloat16, device="cuda")
+    idx = torch.tensor([K - 1, 0, 65_537], dtype=torch.int32, device="cuda")
+    W[idx.long()] = torch.randn(3, D, device="cuda").bfloat16()
+    Y = G.gmm_embed(W, idx)
+    assert torch.equal(Y, W[idx.long()])
+    dW, _ = G.gmm_embed_backward(Y, idx, K, out=W.fill_(1.0))
+    assert torch.equal(dW[idx.long()], Y)
+    assert dW.count_nonzero() == Y.count_nonzero()
+
+
+def test_captured_and_on_another_stream(G):
+    import torch
+
+    rng = np.random.default_rng(3)
+    N, K, D = 300, 500, 64
+    dY, _ = _rows(rng, N, D, "f32")
+    W, _ = _rows(rng, K, D, "f32")
+    idx = torch.from_numpy(rng.integers(0, K, N).astype(np.int32)).cuda()
+    want = G.gmm_embed(W, idx), G.gmm_embed_backward(dY, idx, K)[0]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    got = G.gmm_embed(W, idx, stream=other), G.gmm_embed_backward(dY, idx, K, stream=other)[0]
+    other.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    p = G.embed_problem(idx, K, 1.0, D, dY)
+    ws = torch.empty(G.gmm_embed_workspace_size(p), dtype=torch.uint8, device="cuda")
+    graph, Y, dW = torch.cuda.CUDAGraph(), torch.empty_like(want[0]), torch.empty_like(want[1])
+    with torch.cuda.graph(graph):
+        G.gmm_embed(W, idx, out=Y)
+        G.gmm_embed_backward(dY, idx, K, out=dW, ws=ws)
+    for seed in (4, 5):
+        new = torch.from_numpy(np.random.default_rng(seed).integers(0, K, N).astype(np.int32))
+        idx.copy_(new)
+        ws.fill_(255)  # any content
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, W[idx.long()])
+        assert torch.equal(dW, G.gmm_embed_backward(dY, idx, K)[0])
+
+
+def test_refusals(G):
+    import torch
+
+    W = torch.zeros(6, 8, device="cuda")
+    idx = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    dY = torch.zeros(4, 8, device="cuda")
+    for bad in (lambda: G.gmm_embed(W, idx.long()), lambda: G.gmm_embed(W, idx.cpu()),
+                lambda: G.gmm_embed(W.double(), idx), lambda: G.gmm_embed(W.t(), idx),
+                lambda: G.gmm_embed(W, idx, torch.zeros(4, device="cuda")),
+                lambda: G.gmm_embed(W, idx.t()), lambda: G.gmm_embed(W, idx, out=dY.half()),
+                lambda: G.gmm_embed(W, idx[0, 0]),
+                lambda: G.gmm_embed_backward(dY, idx[:3], 6),
+                lambda: G.gmm_embed_backward(dY, idx, 6, W=W.half()),
+                lambda: G.gmm_embed_backward(dY, idx, 7, W=W),
+                lambda: G.gmm_embed_backward(dY, idx, 6, accumulate=True),
+                lambda: G.gmm_embed_backward(dY, idx, 6, out=W.half()),
+                lambda: G.gmm_embed_backward(dY, idx, 6, out=W[:5])):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    with pytest.raises(G.GmmError):
+        G.gmm_embed(W, torch.zeros(4, 9, dtype=torch.int32, device="cuda"))
+    with pytest.raises(G.GmmError):
+        G.gmm_embed(W, idx, scale=float("nan"))
+    with pytest.raises(G.GmmError):
+        G.gmm_embed_backward(dY, idx, 6, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
