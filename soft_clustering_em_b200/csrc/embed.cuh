@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "sm100_prims.cuh"
 #include "vec16.cuh"
 
 namespace scem {
@@ -77,9 +78,9 @@ struct Unit {
 };
 
 // ------------------------------------------------------------------ lookup
-// A thread takes kPer units of the N x units outputs, 256 apart, so that kPer choices and then
-// kPer units are on their way at once.
-template <typename T, bool kVec, int kPer>
+// A thread takes kPer units of the N x units outputs, 256 apart, so that the choices of kPer rows
+// and then kPer * kM units are on their way at once.  kM: at least m.
+template <typename T, bool kVec, int kM, int kPer>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   using U = Unit<T, kVec>;
   const int64_t first = (int64_t)blockIdx.x * (kPer * kEmbedThreads);
@@ -88,69 +89,46 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   const uint32_t unit0 = (uint32_t)(first - row0 * a.units) + threadIdx.x;
   int64_t row[kPer];
   int unit[kPer];
+  int k[kPer][kM];
+  float w[kPer][kM];
+  typename U::Raw r[kPer][kM];
 #pragma unroll
   for (int p = 0; p < kPer; p++) {
     const uint32_t i = unit0 + p * kEmbedThreads;
-    // (exact: below 1,025 units i is below 2^12, and rows of more are passed at most once)
+    // (exact: up to 1,024 units i is below 2^11, and rows of more are passed at most once)
     const uint32_t q = a.units > kPer * kEmbedThreads ? i >= (uint32_t)a.units
                        : a.units == 1                 ? i
                                                       : __umulhi(i, a.magic);
     row[p] = row0 + q;
     unit[p] = (int)(i - q * a.units);
-  }
-  auto legal = [&](int k) {
-    if ((unsigned)k < (unsigned)a.K) return true;
-    if (k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    return false;
-  };
-  if (a.m == 1) {
-    int k[kPer];
-    typename U::Raw r[kPer];
-    float w[kPer];
 #pragma unroll
-    for (int p = 0; p < kPer; p++) k[p] = row[p] < a.N ? a.idx[row[p]] : -1;
-#pragma unroll
-    for (int p = 0; p < kPer; p++) w[p] = a.resp && row[p] < a.N ? a.resp[row[p]] : 1.f;
-#pragma unroll
-    for (int p = 0; p < kPer; p++) {
-      const bool ok = legal(k[p]);
-      r[p] = ok ? U::load((const T*)a.W + k[p] * a.ldw, unit[p], a.D) : U::zero();
-      if (!ok) w[p] = 0.f;
+    for (int j = 0; j < kM; j++) {
+      const bool live = row[p] < a.N && (kM == 1 || j < a.m);
+      const int64_t at = kM == 1 ? row[p] : row[p] * a.m + j;
+      k[p][j] = live ? a.idx[at] : -1;
+      w[p][j] = live && a.resp ? a.resp[at] : 1.f;
     }
-#pragma unroll
-    for (int p = 0; p < kPer; p++) {
-      if (row[p] >= a.N) continue;
-      float x[U::n];
-      U::unpack(r[p], x);
-#pragma unroll
-      for (int e = 0; e < U::n; e++) x[e] = x[e] * w[p] * a.scale;
-      U::store((T*)a.Y + row[p] * a.ldy, unit[p], a.D, x);
-    }
-    return;
   }
-#pragma unroll 1
+#pragma unroll
+  for (int p = 0; p < kPer; p++) {
+#pragma unroll
+    for (int j = 0; j < kM; j++) {
+      const bool ok = (unsigned)k[p][j] < (unsigned)a.K;
+      if (!ok && k[p][j] != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+      r[p][j] = ok ? U::load((const T*)a.W + k[p][j] * a.ldw, unit[p], a.D) : U::zero();
+      if (!ok) w[p][j] = 0.f;
+    }
+  }
+#pragma unroll
   for (int p = 0; p < kPer; p++) {
     if (row[p] >= a.N) return;
     float y[U::n] = {};
-#pragma unroll 1
-    for (int j0 = 0; j0 < a.m; j0 += 4) {
-      typename U::Raw r[4];
-      float w[4];
-      const int64_t at = row[p] * a.m + j0;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int k = j0 + j < a.m ? a.idx[at + j] : -1;
-        const bool ok = legal(k);
-        w[j] = !ok ? 0.f : a.resp ? a.resp[at + j] : 1.f;
-        r[j] = ok ? U::load((const T*)a.W + k * a.ldw, unit[p], a.D) : U::zero();
-      }
+    for (int j = 0; j < kM; j++) {
+      float x[U::n];
+      U::unpack(r[p][j], x);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        float x[U::n];
-        U::unpack(r[j], x);
-#pragma unroll
-        for (int e = 0; e < U::n; e++) y[e] = fmaf(w[j], x[e], y[e]);
-      }
+      for (int e = 0; e < U::n; e++) y[e] = kM == 1 ? w[p][j] * x[e] : fmaf(w[p][j], x[e], y[e]);
     }
 #pragma unroll
     for (int e = 0; e < U::n; e++) y[e] *= a.scale;
@@ -161,49 +139,88 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
 // ------------------------------------------------------------------ choices sorted by class
 // A stable sort of the M = N m choices by class, least significant digit first, one to three
 // digits of up to kSortBits bits.  A choice of no class gets class K and ends up behind all
-// others.  Per digit two kernels: each CTA counts the digits of its contiguous tile, then (all
-// counts known) places its entries.  Warps take contiguous parts of a tile, 32 entries at a
-// time; equal digits are ranked by a match across the warp.
+// others.  Warps take contiguous parts of the choices, 32 at a time; equal digits are ranked by a
+// match across the warp.
+//
+// Up to kSortCluster choices one cluster of CTAs does all of it, with its barriers between the
+// steps, and leaves the other SMs to whatever else the gradient needs.  Beyond, two kernels per
+// digit: each CTA counts the digits of its contiguous tile, then (all counts known) places its
+// entries.
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;
 constexpr int kSortTiles = 148;  // most tiles
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr uint32_t kSortCluster = 1u << 17;
+
+// A choice on its way: its class and its place in idx.
+using Choice = uint2;
 
 struct SortArgs {
-  const int32_t* idx;       // the first digit: the choices themselves
-  const uint32_t *key, *src;  // later digits: what the one before wrote
-  uint32_t *key_out, *src_out;
-  uint32_t* counts;         // tiles x bins
-  uint8_t* seen;            // K bytes, may be null: which classes are named
+  const int32_t* idx;  // the first digit: the choices themselves
+  const Choice* in;    // later digits: what the one before wrote
+  Choice* out;
+  uint32_t* counts;    // tiles x bins
   uint32_t M;
-  uint32_t per_warp;        // entries, a multiple of 32
+  uint32_t per_warp;          // entries, a multiple of 32
   int K, shift, bits;
   uint32_t* flags;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
-  if (!a.idx) return a.key[i];
-  const int k = a.idx[i];
-  return (unsigned)k < (unsigned)a.K ? (uint32_t)k : (uint32_t)a.K;
+// Entries i0 + 32 b + lane of a warp's part, b < kSortBatch, all on their way at once; class K where
+// there is none.
+constexpr int kSortBatch = 8;
+__device__ __forceinline__ void sort_fetch(const int32_t* idx, const Choice* in, uint64_t i0,
+                                           uint64_t end, uint32_t K, uint32_t* flags,
+                                           Choice (&c)[kSortBatch]) {
+  i0 += threadIdx.x & 31;
+#pragma unroll
+  for (int b = 0; b < kSortBatch; b++) {
+    const uint64_t i = i0 + 32 * b;
+    c[b] = make_uint2(K, 0);
+    if (i < end) c[b] = idx ? make_uint2((uint32_t)idx[i], (uint32_t)i) : __ldcg(in + i);
+  }
+  if (!idx) return;
+#pragma unroll
+  for (int b = 0; b < kSortBatch; b++) {
+    if (c[b].x < K) continue;
+    if (c[b].x != 0xffffffffu && i0 + 32 * b < end && flags)
+      atomicOr(flags, GMM_DEVFLAG_BAD_INDEX);
+    c[b].x = K;
+  }
+}
+
+// The warp's 32 entries to their places, in order: `next` holds where each bin's next entry goes.
+__device__ __forceinline__ void sort_put(uint32_t* next, bool live, Choice c, uint32_t bin,
+                                         Choice* out) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t equal = __match_any_sync(0xffffffffu, live ? bin : 0xffffffffu);
+  const uint32_t rank = __popc(equal & ((1u << lane) - 1u));
+  uint32_t at = 0;
+  if (live) at = next[bin] + rank;
+  __syncwarp();
+  if (live && rank == 0) next[bin] = at + __popc(equal);
+  __syncwarp();
+  if (live) out[at] = c;
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   __shared__ uint32_t hist[1 << kSortBits];
   const int bins = 1 << a.bits;
-  grid_dependents_launch();
   for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
-  grid_dependency_wait();
-  if (a.seen)  // (set by the kernel after this one)
-    for (int k = blockIdx.x * kSortThreads + threadIdx.x; k < a.K; k += gridDim.x * kSortThreads)
-      a.seen[k] = 0;
   __syncthreads();
-  const uint64_t begin = (uint64_t)blockIdx.x * kSortWarps * a.per_warp;
-  const uint64_t end = min(begin + (uint64_t)kSortWarps * a.per_warp, (uint64_t)a.M);
-  for (uint64_t i = begin + threadIdx.x; i < end; i += kSortThreads) {
-    const uint32_t k = sort_key(a, (uint32_t)i);
-    if (a.idx && k == (uint32_t)a.K && a.idx[i] != -1 && a.flags)
-      atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    atomicAdd(&hist[(k >> a.shift) & (bins - 1)], 1u);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const uint64_t begin = ((uint64_t)blockIdx.x * kSortWarps + threadIdx.x / 32) * a.per_warp;
+  const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
+  for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+    Choice c[kSortBatch];
+    sort_fetch(a.idx, a.in, i0, end, (uint32_t)a.K, a.flags, c);
+#pragma unroll
+    for (int b = 0; b < kSortBatch; b++)
+      if (i0 + 32 * b + (threadIdx.x & 31) < end)
+        atomicAdd(&hist[(c[b].x >> a.shift) & (bins - 1)], 1u);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += kSortThreads)
@@ -212,33 +229,45 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   extern __shared__ uint32_t place[];  // [warp][bin]: where the warp's next entry of bin goes
-  __shared__ uint32_t sums[kSortWarps];
+  __shared__ uint32_t sums[kSortWarps], of_bin[2][kSortThreads];
   const int bins = 1 << a.bits, t = threadIdx.x, lane = t & 31, w = t >> 5;
-  grid_dependents_launch();
   for (int i = t; i < kSortWarps * bins; i += kSortThreads) place[i] = 0;
   __syncthreads();
   grid_dependency_wait();
-  const uint64_t begin = ((uint64_t)blockIdx.x * kSortWarps + w) * a.per_warp;
+  grid_dependents_launch();
+  const uint64_t begin = min(((uint64_t)blockIdx.x * kSortWarps + w) * a.per_warp, (uint64_t)a.M);
   const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
   uint32_t* mine = place + w * bins;
-  for (uint64_t i0 = begin; i0 < end; i0 += 32) {
-    const uint64_t i = i0 + lane;
-    if (i < end) atomicAdd(&mine[(sort_key(a, (uint32_t)i) >> a.shift) & (bins - 1)], 1u);
+  Choice c[kSortBatch];
+  for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+    sort_fetch(a.idx, a.in, i0, end, (uint32_t)a.K, nullptr, c);
+#pragma unroll
+    for (int b = 0; b < kSortBatch; b++)
+      if (i0 + 32 * b + lane < end) atomicAdd(&mine[(c[b].x >> a.shift) & (bins - 1)], 1u);
   }
-  __syncthreads();
   // Bins in order over the threads: entries of lower bins, then of the same bin in earlier
-  // tiles, then in earlier warps.
+  // tiles, then in earlier warps.  With few bins several threads share a bin's tiles.
+  const int cols = min(bins, kSortThreads), groups = kSortThreads / cols;
+  const int col = t & (cols - 1), tiles = (int)gridDim.x;
   uint32_t carry = 0;
-  for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
-    const int b = b0 + t;
+  for (int b0 = 0; b0 < bins; b0 += cols) {
     uint32_t before = 0, all = 0;
-    if (b < bins) {
-#pragma unroll 8
-      for (int tile = 0; tile < (int)gridDim.x; tile++) {
-        const uint32_t c = a.counts[tile * bins + b];
-        all += c;
-        before += tile < (int)blockIdx.x ? c : 0u;
+#pragma unroll 16
+    for (int tile = t / cols; tile < tiles; tile += groups) {
+      const uint32_t n = a.counts[tile * bins + b0 + col];
+      all += n;
+      before += tile < (int)blockIdx.x ? n : 0u;
+    }
+    of_bin[0][t] = all;
+    of_bin[1][t] = before;
+    __syncthreads();
+    if (t < cols) {
+      for (int g = 1; g < groups; g++) {
+        all += of_bin[0][g * cols + t];
+        before += of_bin[1][g * cols + t];
       }
+    } else {
+      all = 0;
     }
     uint32_t scan = all;  // inclusive over the CTA
 #pragma unroll
@@ -254,34 +283,162 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
       total += sums[q];
     }
     carry += total;
-    if (b < bins) {
+    if (t < cols) {
       uint32_t at = lower + scan - all + before;
-      for (int q = 0; q < kSortWarps; q++) {
-        const uint32_t c = place[q * bins + b];
-        place[q * bins + b] = at;
-        at += c;
+#pragma unroll
+      for (int q0 = 0; q0 < kSortWarps; q0 += 8) {
+        uint32_t n[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) n[q] = place[(q0 + q) * bins + b0 + t];
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+          place[(q0 + q) * bins + b0 + t] = at;
+          at += n[q];
+        }
       }
     }
     __syncthreads();
   }
-  for (uint64_t i0 = begin; i0 < end; i0 += 32) {
-    const uint64_t i = i0 + lane;
-    const bool live = i < end;
-    const uint32_t k = live ? sort_key(a, (uint32_t)i) : 0u;
-    const uint32_t bin = (k >> a.shift) & (bins - 1);
-    const uint32_t equal = __match_any_sync(0xffffffffu, live ? bin : 0xffffffffu);
-    const uint32_t rank = __popc(equal & ((1u << lane) - 1u));
-    uint32_t at = 0;
-    if (live) at = mine[bin] + rank;
-    __syncwarp();
-    if (live && rank == 0) mine[bin] = at + __popc(equal);
-    __syncwarp();
-    if (live) {
-      a.key_out[at] = k;
-      a.src_out[at] = a.idx ? (uint32_t)i : a.src[i];
-      if (a.seen && k < (uint32_t)a.K) a.seen[k] = 1;
+  for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+    if (a.per_warp > 32 * kSortBatch)  // (else they are still here)
+      sort_fetch(a.idx, a.in, i0, end, (uint32_t)a.K, nullptr, c);
+#pragma unroll
+    for (int b = 0; b < kSortBatch; b++) {
+      if (i0 + 32 * b >= end) break;  // (the same for the warp)
+      sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> a.shift) & (bins - 1), a.out);
     }
   }
+}
+
+// All digits by one cluster: per warp and bin first the counts, then the places.  The counts of
+// the CTAs meet in shared memory.
+struct SortAllArgs {
+  const int32_t* idx;
+  Choice* list[2];  // digit i writes buffer i & 1
+  uint32_t M, per_warp;
+  int K, passes, bits;
+  uint32_t* flags;
+};
+
+__global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAllArgs a) {
+  extern __shared__ uint32_t place[];  // [warp][bin], then the CTA's counts [bin]
+  __shared__ uint32_t sums[kClusterWarps];
+  const int bins = 1 << a.bits, t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const uint32_t rank = sm100::cluster_ctarank(), ctas = sm100::cluster_nctarank();
+  uint32_t* mine = place + w * bins;
+  uint32_t* total = place + kClusterWarps * bins;
+  const uint64_t begin = min(((uint64_t)rank * kClusterWarps + w) * a.per_warp, (uint64_t)a.M);
+  const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (int pass = 0; pass < a.passes; pass++) {
+    const int shift = pass * a.bits;
+    const int32_t* idx = pass == 0 ? a.idx : nullptr;
+    const Choice* in = a.list[(pass + 1) & 1];
+    Choice c[kSortBatch];
+    for (int i = lane; i < bins; i += 32) mine[i] = 0;
+    __syncwarp();
+    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+      sort_fetch(idx, in, i0, end, (uint32_t)a.K, a.flags, c);
+#pragma unroll
+      for (int b = 0; b < kSortBatch; b++)
+        if (i0 + 32 * b + lane < end) atomicAdd(&mine[(c[b].x >> shift) & (bins - 1)], 1u);
+    }
+    __syncthreads();
+    for (int b = t; b < bins; b += kClusterThreads) {
+      uint32_t n = 0;
+#pragma unroll 8
+      for (int q = 0; q < kClusterWarps; q++) n += place[q * bins + b];
+      total[b] = n;
+    }
+    __syncwarp();
+    sm100::cluster_sync();
+    static_assert((1 << kSortBits) <= kClusterThreads, "a thread for each bin");
+    uint32_t before = 0, all = 0;
+    if (t < bins) {
+#pragma unroll 8
+      for (uint32_t r = 0; r < ctas; r++) {
+        uint32_t n;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(n)
+                     : "r"(sm100::map_to_rank(sm100::smem_u32(total + t), r))
+                     : "memory");
+        all += n;
+        before += r < rank ? n : 0u;
+      }
+    }
+    uint32_t scan = all;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) sums[w] = scan;
+    __syncthreads();
+    uint32_t lower = lane < w ? sums[lane] : 0u;
+    lower = __reduce_add_sync(0xffffffffu, lower);
+    if (t < bins) {
+      uint32_t at = lower + scan - all + before;
+      for (int q0 = 0; q0 < kClusterWarps; q0 += 8) {
+        uint32_t n[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) n[q] = place[(q0 + q) * bins + t];
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+          place[(q0 + q) * bins + t] = at;
+          at += n[q];
+        }
+      }
+    }
+    __syncthreads();
+    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+      if (a.per_warp > 32 * kSortBatch)  // (else they are still here)
+        sort_fetch(idx, in, i0, end, (uint32_t)a.K, nullptr, c);
+#pragma unroll
+      for (int b = 0; b < kSortBatch; b++) {
+        if (i0 + 32 * b >= end) break;  // (the same for the warp)
+        sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> shift) & (bins - 1),
+                 a.list[pass & 1]);
+      }
+    }
+    // what the others placed is visible, and nobody's counts are read any more
+    __syncwarp();
+    sm100::cluster_sync();
+  }
+}
+
+// ------------------------------------------------------------------ rows of zeros
+// Pieces of a row, one per warp.  Does not wait for the sort before it in the stream, only ends
+// after it: nothing that is written here is read or written there, and what came before the sort
+// is done when it lets this kernel start.
+constexpr int kFillPiece = 16384;  // bytes
+// CTAs per SM of a kernel that goes on beside the sort and ends after it: all of them are resident
+// at once, also beside the sort's (one that waits keeps its place).
+constexpr int kBesideCtas = 4;
+struct FillArgs {
+  char* base;
+  uint64_t rows, row_bytes, stride;  // bytes
+  uint64_t parts;                    // pieces per row
+};
+
+__global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(FillArgs a) {
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const uint64_t pieces = a.rows * a.parts;
+  for (uint64_t i = (uint64_t)blockIdx.x * (kEmbedThreads / 32) + threadIdx.x / 32; i < pieces;
+       i += (uint64_t)gridDim.x * (kEmbedThreads / 32)) {
+    const uint64_t row = a.rows == 1 ? 0 : a.parts == 1 ? i : i / a.parts;
+    const uint64_t part = i - row * a.parts;
+    char* p = a.base + row * a.stride + part * kFillPiece;
+    const uint32_t n = (uint32_t)min((uint64_t)kFillPiece, a.row_bytes - part * kFillPiece);
+    const uint32_t head = min(n, (uint32_t)(-(uintptr_t)p & 15u)), body = (n - head) / 16;
+    if (lane < head) p[lane] = 0;
+    uint4* v = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 4
+    for (uint32_t u = lane; u < body; u += 32) v[u] = make_uint4(0, 0, 0, 0);
+    if (lane < n - head - body * 16) p[head + body * 16 + lane] = 0;
+  }
+  grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ sums by class
@@ -293,8 +450,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
 struct EmbedGradArgs {
   const void* dY;
   const float* resp;       // may be null
-  const uint32_t *key, *src;
-  const uint8_t* seen;     // null: dW is added to
+  const Choice* list;      // sorted
   void* dW;
   float* part;             // chunks x 2 x width
   int64_t ldy, ldd;
@@ -302,7 +458,7 @@ struct EmbedGradArgs {
   uint32_t M, chunk, chunks;
   int K, D, units, lanes, width;
   float scale;
-  int m;
+  int m, add;
 };
 
 template <typename T, typename TO, bool kVec>
@@ -314,7 +470,7 @@ __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, i
 #pragma unroll
   for (int e = 0; e < n; e++) x[e] = sum[e] * a.scale;
   if constexpr (std::is_same<T, TO>::value) {
-    if (!a.seen) {
+    if (a.add) {
       float old[n];
       Unit<T, kVec>::unpack(Unit<T, kVec>::load(row, u, a.D), old);
 #pragma unroll
@@ -327,7 +483,7 @@ __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, i
       if (kVec && u * n + e + 4 <= a.D) {
         float4* p = reinterpret_cast<float4*>(row + u * n + e);
         float4 v = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        if (!a.seen) {
+        if (a.add) {
           const float4 o = *p;
           v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
         }
@@ -335,55 +491,76 @@ __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, i
       } else {
 #pragma unroll
         for (int i = e; i < e + 4 && i < n; i++)
-          if (u * n + i < a.D) row[u * n + i] = a.seen ? x[i] : x[i] + row[u * n + i];
+          if (u * n + i < a.D) row[u * n + i] = a.add ? x[i] + row[u * n + i] : x[i];
       }
     }
   }
 }
 
 constexpr int kGradBatch = 8;
+constexpr int kGradChunk = 128;  // most choices per chunk
 
+// Shared memory: what the CTA's choices say (class, row of dY, weight), read once.
 template <typename T, typename TO, bool kVec>
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedGradArgs a) {
+__global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradArgs a) {
   using U = Unit<T, kVec>;
-  grid_dependents_launch();
-  grid_dependency_wait();
+  extern __shared__ uint32_t stage[];
   const int l = threadIdx.x & (a.lanes - 1);
-  const uint32_t c = blockIdx.x * (kEmbedThreads / a.lanes) + threadIdx.x / a.lanes;
+  const uint32_t groups = kEmbedThreads / a.lanes, g = threadIdx.x / a.lanes;
+  const uint32_t per = groups * a.chunk;  // of the CTA
+  uint32_t* key = stage;
+  uint32_t* row = stage + per;
+  float* weight = reinterpret_cast<float*>(stage + 2 * per);
+  const uint32_t first = blockIdx.x * per;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (uint32_t i = threadIdx.x; i < per; i += kEmbedThreads) {
+    uint32_t k = (uint32_t)a.K, n = 0;
+    float w = 0.f;
+    if (first + i < a.M) {
+      const Choice c = a.list[first + i];
+      const uint32_t s = c.y;
+      k = c.x;
+      n = a.m == 1 ? s : (uint32_t)((s * a.by_m) >> 34);
+      w = !a.resp ? 1.f : k < (uint32_t)a.K ? a.resp[s] : 0.f;
+    }
+    key[i] = k;
+    row[i] = n;
+    weight[i] = w;
+  }
+  const uint32_t c = blockIdx.x * groups + g, begin = c * a.chunk;
+  const uint32_t none = 0xffffffffu;
+  uint32_t before = none, after = none;
+  if (c < a.chunks) {
+    if (begin > 0) before = a.list[begin - 1].x;
+    if (begin + a.chunk < a.M) after = a.list[begin + a.chunk].x;
+  }
+  __syncthreads();
   const int u = blockIdx.y * a.lanes + l;
   if (c >= a.chunks || u >= a.units) return;
-  const uint32_t begin = c * a.chunk, end = min(begin + a.chunk, a.M);
-  bool came_in = begin > 0 && a.key[begin - 1] == a.key[begin];
+  key += g * a.chunk;
+  row += g * a.chunk;
+  weight += g * a.chunk;
+  bool came_in = before == key[0];
   float sum[U::n] = {};
-  for (uint32_t i = begin; i < end; i += kGradBatch) {
-    uint32_t k[kGradBatch + 1], s[kGradBatch];
+  for (uint32_t i = 0; i < a.chunk; i += kGradBatch) {  // (a multiple of the batch)
     typename U::Raw r[kGradBatch];
-    float w[kGradBatch];
+#pragma unroll
+    for (int b = 0; b < kGradBatch; b++)
+      r[b] = key[i + b] < (uint32_t)a.K
+                 ? U::load((const T*)a.dY + (int64_t)row[i + b] * a.ldy, u, a.D)
+                 : U::zero();
 #pragma unroll
     for (int b = 0; b < kGradBatch; b++) {
-      k[b] = i + b < end ? a.key[i + b] : a.K;
-      s[b] = i + b < end ? a.src[i + b] : 0u;
-    }
-    // (the entry behind the batch, in the next chunk or not)
-    k[kGradBatch] = i + kGradBatch < a.M ? a.key[i + kGradBatch] : a.K;
-#pragma unroll
-    for (int b = 0; b < kGradBatch; b++) {
-      const bool live = k[b] < (uint32_t)a.K;
-      const int64_t n = a.m == 1 ? s[b] : (int64_t)((s[b] * a.by_m) >> 34);
-      r[b] = live ? U::load((const T*)a.dY + n * a.ldy, u, a.D) : U::zero();
-      w[b] = live && a.resp ? a.resp[s[b]] : 1.f;
-    }
-#pragma unroll
-    for (int b = 0; b < kGradBatch; b++) {
-      if (k[b] >= (uint32_t)a.K) continue;
+      const uint32_t k = key[i + b];
+      if (k >= (uint32_t)a.K) return;  // the choices of no class are the last ones
+      const float w = weight[i + b];
       float x[U::n];
       U::unpack(r[b], x);
 #pragma unroll
-      for (int e = 0; e < U::n; e++) sum[e] = fmaf(w[b], x[e], sum[e]);
-      const bool last = i + b + 1 == end;
-      // (past `end` inside a batch k says none: look at the entry itself)
-      const bool goes_on =
-          last ? end < a.M && a.key[end] == k[b] : k[b + 1] == k[b];
+      for (int e = 0; e < U::n; e++) sum[e] = fmaf(w, x[e], sum[e]);
+      const bool last = i + b + 1 == a.chunk;
+      const bool goes_on = (last ? after : key[i + b + 1]) == k;
       if (goes_on && !last) continue;
       if (came_in || goes_on) {
         float* p = a.part + ((int64_t)c * 2 + (came_in ? 0 : 1)) * a.width + u * U::n;
@@ -396,7 +573,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedGradArgs 
           p[0] = sum[0];
         }
       } else {
-        write_grad<T, TO, kVec>(a, k[b], u, sum);
+        write_grad<T, TO, kVec>(a, k, u, sum);
       }
       came_in = false;
 #pragma unroll
@@ -405,71 +582,99 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(EmbedGradArgs 
   }
 }
 
-// Blocks [0, chunks): the sums of the run that begins in a chunk and goes on behind it, 32 units
-// at a time by 8 warps, which share out the run's chunks.  Blocks behind those: rows of classes
-// that nothing names get zeros.
-constexpr int kFillRows = 64;
+// The sums of runs that chunks' borders cut.  A warp looks at a chunk, for 32 units (blocks y): does a run
+// begin in it and go on behind it?  It adds up a run of a few chunks by itself; longer ones
+// are shared out over the CTA's warps.
+constexpr int kJoinShort = 8;  // chunks
 
 template <typename T, typename TO, bool kVec>
-__global__ void __launch_bounds__(kEmbedThreads) embed_finish_kernel(EmbedGradArgs a,
-                                                                     uint32_t joins) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs a) {
   using U = Unit<T, kVec>;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   constexpr int kWarps = kEmbedThreads / 32;
-  grid_dependency_wait();
-  if (blockIdx.x >= joins) {
-    const int k0 = (int)(blockIdx.x - joins) * kFillRows;
-    constexpr int V = kVec ? 16 / (int)sizeof(TO) : 1;
-    const int units = (a.D + V - 1) / V;
-    const int per = units >= 256 ? 256 : units > 16 ? 32 : 8;  // threads of a row
-    const int l = threadIdx.x & (per - 1);
-    for (int q = threadIdx.x / per; q < kFillRows && k0 + q < a.K; q += kEmbedThreads / per) {
-      if (a.seen[k0 + q]) continue;
-      TO* row = (TO*)a.dW + (int64_t)(k0 + q) * a.ldd;
-      const float zero[V] = {};
-      for (int u = l; u < units; u += per) Unit<TO, kVec>::store(row, u, a.D, zero);
-    }
-    return;
-  }
   __shared__ float sh[kWarps][32 * U::n];
-  const uint32_t c = blockIdx.x;
-  const uint32_t begin = c * a.chunk, end = begin + a.chunk;
-  if (end >= a.M) return;
-  const uint32_t k = a.key[end - 1];
-  if (k >= (uint32_t)a.K || a.key[end] != k) return;                   // nothing goes on
-  if (a.key[begin] == k && begin > 0 && a.key[begin - 1] == k) return;  // it began before
-  // the run's last chunk: the first whose last entry is of another class, or the last of all
-  uint32_t lo = c + 1, hi = a.chunks - 1;
-  while (lo < hi) {
-    const uint32_t step = (hi - lo + 31) / 32, at = min(lo + step * lane, hi);
-    const bool past = at == hi || a.key[(uint64_t)(at + 1) * a.chunk] != k;
-    const int f = __ffs(__ballot_sync(0xffffffffu, past)) - 1;
-    const uint32_t found = f < 0 ? hi : min(lo + step * f, hi);
-    const uint32_t from = f == 0 ? lo : f < 0 ? lo + step * 31 + 1 : lo + step * (f - 1) + 1;
-    hi = found;
-    lo = min(from, hi);
+  __shared__ uint32_t long_chunk[kWarps], long_last[kWarps];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const uint32_t c = blockIdx.x * kWarps + w;
+  const uint64_t begin = (uint64_t)c * a.chunk, end = begin + a.chunk;
+  const int u = blockIdx.y * 32 + lane;
+  auto part = [&](uint32_t q, bool tail, float (&x)[U::n]) {
+    const float* p = a.part + ((int64_t)q * 2 + tail) * a.width + u * U::n;
+    if constexpr (kVec) {
+#pragma unroll
+      for (int e = 0; e < U::n; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + e);
+        x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+      }
+    } else {
+      x[0] = p[0];
+    }
+  };
+  uint32_t k = (uint32_t)a.K, last = 0;
+  bool mine = false;
+  if (end < a.M) {
+    k = a.list[end - 1].x;
+    const uint32_t next = a.list[end].x, head = a.list[begin].x;
+    const uint32_t before = begin > 0 ? a.list[begin - 1].x : 0xffffffffu;
+    mine = k < (uint32_t)a.K && next == k && !(head == k && before == k);
   }
-  const uint32_t last = lo;
-  for (int u0 = 0; u0 < a.units; u0 += 32) {
-    const int u = u0 + lane;
+  if (mine) {
+    // the run's last chunk: the first behind c whose own next entry is of another class
+    uint32_t lo = c + 1, hi = a.chunks - 1;
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32, at = min(lo + step * lane, hi);
+      const bool past = at == hi || a.list[(uint64_t)(at + 1) * a.chunk].x != k;
+      const int f = __ffs(__ballot_sync(0xffffffffu, past)) - 1;
+      const uint32_t found = f < 0 ? hi : min(lo + step * f, hi);
+      const uint32_t from = f == 0 ? lo : f < 0 ? lo + step * 31 + 1 : lo + step * (f - 1) + 1;
+      hi = found;
+      lo = min(from, hi);
+    }
+    last = lo;
+    if (last - c <= kJoinShort && u < a.units) {
+      float sum[U::n], x[kJoinShort][U::n];
+      part(c, true, sum);
+#pragma unroll
+      for (int q = 0; q < kJoinShort; q++)
+        if (c + 1 + q <= last) part(c + 1 + q, false, x[q]);
+#pragma unroll
+      for (int q = 0; q < kJoinShort; q++) {
+        if (c + 1 + q > last) continue;
+#pragma unroll
+        for (int e = 0; e < U::n; e++) sum[e] += x[q][e];
+      }
+      write_grad<T, TO, kVec>(a, k, u, sum);
+    }
+  }
+  const bool is_long = mine && last - c > kJoinShort;
+  if (lane == 0) {
+    long_chunk[w] = is_long ? c : 0xffffffffu;
+    long_last[w] = last;
+  }
+  if (__syncthreads_or(is_long) == 0) return;
+  for (int q = 0; q < kWarps; q++) {
+    const uint32_t from = long_chunk[q], to = long_last[q];
+    if (from == 0xffffffffu) continue;  // (the same for all threads)
     float sum[U::n] = {};
     if (u < a.units) {
-#pragma unroll 4
-      for (uint32_t q = c + w; q <= last; q += kWarps) {
-        const float* p = a.part + ((int64_t)q * 2 + (q == c ? 1 : 0)) * a.width + u * U::n;
+#pragma unroll 8
+      for (uint32_t i = from + w; i <= to; i += kWarps) {
+        float x[U::n];
+        part(i, i == from, x);
 #pragma unroll
-        for (int e = 0; e < U::n; e++) sum[e] += p[e];
+        for (int e = 0; e < U::n; e++) sum[e] += x[e];
       }
     }
 #pragma unroll
     for (int e = 0; e < U::n; e++) sh[w][lane * U::n + e] = sum[e];
     __syncthreads();
     if (w == 0 && u < a.units) {
-      for (int q = 1; q < kWarps; q++) {
+      for (int i = 1; i < kWarps; i++) {
 #pragma unroll
-        for (int e = 0; e < U::n; e++) sum[e] += sh[q][lane * U::n + e];
+        for (int e = 0; e < U::n; e++) sum[e] += sh[i][lane * U::n + e];
       }
-      write_grad<T, TO, kVec>(a, k, u, sum);
+      write_grad<T, TO, kVec>(a, a.list[((uint64_t)from + 1) * a.chunk].x, u, sum);
     }
     __syncthreads();
   }
@@ -477,6 +682,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_finish_kernel(EmbedGradAr
 
 // ------------------------------------------------------------------ gradient of the weights
 // A group of 8 or 32 lanes per row n: <dY_n, W[idx_nj]> for its m choices, in a fixed order.
+// (Like the rows of zeros it goes on beside the sort, and ends after it.)
 struct EmbedDotArgs {
   const void *W, *dY;
   const int32_t* idx;
@@ -488,40 +694,55 @@ struct EmbedDotArgs {
 };
 
 template <typename T, bool kVec, int kLanes, int kMost>
-__global__ void __launch_bounds__(kEmbedThreads) embed_dot_kernel(EmbedDotArgs a) {
+__global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(EmbedDotArgs a) {
   using U = Unit<T, kVec>;
+  constexpr int kAhead = kMost == 1 ? 4 : kMost == 2 ? 2 : 1;  // units of a lane on their way at once
   grid_dependents_launch();
-  grid_dependency_wait();
   const int l = threadIdx.x % kLanes;
   const int64_t step = (int64_t)gridDim.x * (kEmbedThreads / kLanes);
-  for (int64_t n0 = ((int64_t)blockIdx.x * kEmbedThreads + threadIdx.x) / 32 * (32 / kLanes);
-       n0 < a.N; n0 += step) {  // (whole warps)
-    const int64_t n = n0 + (threadIdx.x & 31) / kLanes;
+  int64_t n = ((int64_t)blockIdx.x * kEmbedThreads + threadIdx.x) / kLanes;
+  int next[kMost];  // the choices of the row after this one
+  auto choices = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < kMost; j++) next[j] = row < a.N && j < a.m ? a.idx[row * a.m + j] : -1;
+  };
+  choices(n);
+  for (; __any_sync(0xffffffffu, n < a.N); n += step) {  // (whole warps)
     int k[kMost];
     float dot[kMost] = {};
 #pragma unroll
     for (int j = 0; j < kMost; j++) {
-      k[j] = n < a.N && j < a.m ? a.idx[n * a.m + j] : -1;
+      k[j] = next[j];
       if ((unsigned)k[j] >= (unsigned)a.K) {
         if (k[j] != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
         k[j] = -1;
       }
     }
+    choices(n + step);
     if (n < a.N) {
-      for (int u = l; u < a.units; u += kLanes) {
-        const typename U::Raw y = U::load((const T*)a.dY + n * a.ldy, u, a.D);
-        typename U::Raw r[kMost];
+      const T* dy = (const T*)a.dY + n * a.ldy;
+      for (int u0 = l; u0 < a.units; u0 += kAhead * kLanes) {
+        typename U::Raw y[kAhead], r[kAhead][kMost];
 #pragma unroll
-        for (int j = 0; j < kMost; j++)
-          r[j] = k[j] >= 0 ? U::load((const T*)a.W + k[j] * a.ldw, u, a.D) : U::zero();
-        float yx[U::n];
-        U::unpack(y, yx);
+        for (int i = 0; i < kAhead; i++) {
+          const int u = u0 + i * kLanes;
+          y[i] = u < a.units ? U::load(dy, u, a.D) : U::zero();
 #pragma unroll
-        for (int j = 0; j < kMost; j++) {
-          float x[U::n];
-          U::unpack(r[j], x);
+          for (int j = 0; j < kMost; j++)
+            r[i][j] = u < a.units && k[j] >= 0 ? U::load((const T*)a.W + k[j] * a.ldw, u, a.D)
+                                               : U::zero();
+        }
 #pragma unroll
-          for (int e = 0; e < U::n; e++) dot[j] = fmaf(yx[e], x[e], dot[j]);
+        for (int i = 0; i < kAhead; i++) {
+          float yx[U::n];
+          U::unpack(y[i], yx);
+#pragma unroll
+          for (int j = 0; j < kMost; j++) {
+            float x[U::n];
+            U::unpack(r[i][j], x);
+#pragma unroll
+            for (int e = 0; e < U::n; e++) dot[j] = fmaf(yx[e], x[e], dot[j]);
+          }
         }
       }
     }
@@ -533,6 +754,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_dot_kernel(EmbedDotArgs a
       if (l == 0 && n < a.N && j < a.m) a.dresp[n * a.m + j] = k[j] < 0 ? 0.f : dot[j] * a.scale;
     }
   }
+  grid_dependency_wait();
 }
 
 }  // namespace scem

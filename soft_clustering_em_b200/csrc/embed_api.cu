@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "api_common.h"
 #include "embed.cuh"
@@ -45,13 +46,17 @@ gmm_status embed_launch(EmbedArgs a, cudaStream_t st) {
   a.units = (a.D + V - 1) / V;
   a.magic = a.units > 1 ? (uint32_t)((((uint64_t)1 << 32) + a.units - 1) / a.units) : 0;
   const int64_t all = a.N * a.units;
-  // one unit per thread while that leaves SMs without work
-  if (all <= (int64_t)sms * 2 * kEmbedThreads) {
-    embed_kernel<T, kVec, 1><<<(unsigned)((all + 255) / 256), kEmbedThreads, 0, st>>>(a);
-  } else {
-    embed_kernel<T, kVec, 4><<<(unsigned)((all + 1023) / 1024), kEmbedThreads, 0, st>>>(a);
-  }
-  return api_launched(1);
+  auto go = [&](auto kern, int per) {
+    const int64_t grid = (all + per * kEmbedThreads - 1) / (per * kEmbedThreads);
+    kern<<<(unsigned)grid, kEmbedThreads, 0, st>>>(a);
+    return api_launched(1);
+  };
+  // one unit per thread while more would leave SMs without work
+  const bool few = all <= (int64_t)sms * 2 * kEmbedThreads;
+  if (a.m == 1) return few ? go(embed_kernel<T, kVec, 1, 1>, 1) : go(embed_kernel<T, kVec, 1, 4>, 4);
+  if (a.m == 2) return few ? go(embed_kernel<T, kVec, 2, 1>, 1) : go(embed_kernel<T, kVec, 2, 4>, 4);
+  if (a.m <= 4) return few ? go(embed_kernel<T, kVec, 4, 1>, 1) : go(embed_kernel<T, kVec, 4, 2>, 2);
+  return go(embed_kernel<T, kVec, kMaxTopM, 1>, 1);
 }
 
 template <typename T>
@@ -62,11 +67,16 @@ gmm_status embed_vec(const EmbedArgs& a, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------- the gradient
-// Digits of the sort: as few as hold the classes 0 .. K (K: none).
+// Digits of the sort: as few as hold the classes 0 .. K (K: none); tiles and a warp's choices for
+// two kernels per digit.
 struct SortPlan {
   int passes, bits;
   uint32_t tiles, per_warp;
 };
+
+uint32_t part_of(uint32_t M, uint32_t warps) {  // a warp's choices: whole rounds of 32
+  return std::max(32u, (M / warps + (M % warps != 0) + 31) / 32 * 32);
+}
 
 SortPlan sort_plan(uint32_t M, int K) {
   int bits = 1;
@@ -75,21 +85,54 @@ SortPlan sort_plan(uint32_t M, int K) {
   s.passes = (bits + kSortBits - 1) / kSortBits;
   s.bits = (bits + s.passes - 1) / s.passes;
   s.tiles = std::max(1u, std::min<uint32_t>(kSortTiles, (M + kSortThreads - 1) / kSortThreads));
-  const uint32_t warps = s.tiles * kSortWarps;
-  s.per_warp = std::max(32u, (M / warps + (M % warps != 0) + 31) / 32 * 32);
+  s.per_warp = part_of(M, s.tiles * kSortWarps);
   return s;
+}
+
+size_t cluster_smem(int bits) { return ((size_t)(kClusterWarps + 1) << bits) * 4; }
+
+// CTAs of the sorting cluster: 16 where the device has room for one, else 8.  Asked once per
+// device.
+bool cluster_size(int* C) {
+  static std::atomic<int> known[64];
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return false;
+  const bool keep = device >= 0 && device < 64;
+  if (keep && (*C = known[device].load()) != 0) return true;
+  const int smem = (int)cluster_smem(kSortBits);
+  if (cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess ||
+      cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                           1) != cudaSuccess)
+    return false;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  *C = cudaOccupancyMaxActiveClusters(&n, sort_cluster_kernel, &cfg) == cudaSuccess && n > 0 ? 16
+                                                                                             : 8;
+  cudaGetLastError();  // (a size that is not supported is no error of the call)
+  if (keep) known[device] = *C;
+  return true;
 }
 
 // Choices per chunk.  More, and fewer runs are cut; fewer, and there are more CTAs.
 uint32_t grad_chunk(uint32_t M) {
   uint32_t c = 16;
-  while (c < 128 && M / c > 8192) c *= 2;
+  while (c < kGradChunk && M / c > 4096) c *= 2;
   return c;
 }
 
-// Workspace: two buffers of sorted classes and their places, counts, seen classes, cut sums.
+// Workspace: two buffers of sorted classes and their places, counts, cut sums.
 struct GradLayout {
-  size_t key[2], src[2], counts, seen, part, total;
+  size_t list[2], counts, part, total;
   uint32_t chunk, chunks;
   int width;
 };
@@ -104,12 +147,8 @@ GradLayout grad_layout(const gmm_embed_problem* p) {
     off = align_up(off + bytes, 256);
     return at;
   };
-  for (int i = 0; i < 2; i++) {
-    L.key[i] = take((size_t)M * 4);
-    L.src[i] = take((size_t)M * 4);
-  }
+  for (int i = 0; i < 2; i++) L.list[i] = take((size_t)M * sizeof(Choice));
   L.counts = take(((size_t)s.tiles << s.bits) * 4);
-  L.seen = take(p->K);
   L.chunk = grad_chunk(M);
   L.chunks = M / L.chunk + (M % L.chunk != 0);
   L.width = (p->D + 7) / 8 * 8;
@@ -132,8 +171,62 @@ struct GradCall {
   cudaStream_t st;
 };
 
+// The choices sorted by class, in *list.
+gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const Choice** list) {
+  const SortPlan plan = sort_plan(M, g.p->K);
+  Choice* lists[2] = {(Choice*)(g.ws + L.list[0]), (Choice*)(g.ws + L.list[1])};
+  *list = lists[(plan.passes - 1) & 1];
+  if (M <= kSortCluster) {
+    int C = 0;
+    if (!cluster_size(&C)) return api_launched(0), GMM_ERR_CUDA;
+    const SortAllArgs a = {g.idx,  {lists[0], lists[1]}, M,         part_of(M, C * kClusterWarps),
+                           g.p->K, plan.passes,          plan.bits, g.flags};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = cluster_smem(plan.bits);
+    cfg.stream = g.st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, sort_cluster_kernel, a) != cudaSuccess)
+      return api_launched(0), GMM_ERR_CUDA;
+    return api_launched(1);
+  }
+  if (cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSortWarps * (4 << kSortBits)) != cudaSuccess)
+    return api_launched(0), GMM_ERR_CUDA;
+  for (int i = 0; i < plan.passes; i++) {
+    SortArgs o = {};
+    o.idx = i == 0 ? g.idx : nullptr;
+    o.in = lists[(i + 1) & 1];
+    o.out = lists[i & 1];
+    o.counts = (uint32_t*)(g.ws + L.counts);
+    o.M = M;
+    o.per_warp = plan.per_warp;
+    o.K = g.p->K;
+    o.bits = plan.bits;
+    o.shift = i * plan.bits;
+    o.flags = g.flags;
+    gmm_status s;
+    if ((s = api_launch_next(sort_count_kernel, dim3(plan.tiles), kSortThreads, 0, g.st, o)) !=
+        GMM_OK)
+      return s;
+    if ((s = api_launch_next(sort_place_kernel, dim3(plan.tiles), kSortThreads,
+                             kSortWarps * ((size_t)4 << plan.bits), g.st, o)) != GMM_OK)
+      return s;
+  }
+  return GMM_OK;
+}
+
+// `first`: nothing of this call is before it in the stream (it does not wait at its start).
 template <typename T, bool kVec>
-gmm_status dot_launch(const GradCall& g) {
+gmm_status dot_launch(const GradCall& g, bool first) {
   const gmm_embed_problem* p = g.p;
   constexpr int V = Unit<T, kVec>::n;
   EmbedDotArgs a = {g.W,  g.dY, g.idx, g.dresp, p->N, p->ldw, p->ldy,
@@ -143,10 +236,12 @@ gmm_status dot_launch(const GradCall& g) {
   if (s != GMM_OK) return s;
   auto go = [&](auto kern, int lanes) {
     const int rows = kEmbedThreads / lanes;
-    const int64_t blocks = std::min<int64_t>((p->N + rows - 1) / rows, (int64_t)sms * 64);
-    return api_launch_next(kern, dim3((unsigned)blocks), kEmbedThreads, 0, g.st, a);
+    const int64_t blocks = std::min<int64_t>((p->N + rows - 1) / rows, sms * kBesideCtas);
+    if (!first) return api_launch_next(kern, dim3((unsigned)blocks), kEmbedThreads, 0, g.st, a);
+    kern<<<(unsigned)blocks, kEmbedThreads, 0, g.st>>>(a);
+    return api_launched(1);
   };
-  if (a.units <= 16) {
+  if (a.units <= 64) {  // 8 lanes of up to 8 units: 4 rows per warp
     if (p->m == 1) return go(embed_dot_kernel<T, kVec, 8, 1>, 8);
     if (p->m == 2) return go(embed_dot_kernel<T, kVec, 8, 2>, 8);
     return go(embed_dot_kernel<T, kVec, 8, kMaxTopM>, 8);
@@ -156,17 +251,42 @@ gmm_status dot_launch(const GradCall& g) {
   return go(embed_dot_kernel<T, kVec, 32, kMaxTopM>, 32);
 }
 
+template <typename T>
+gmm_status dot_vec(const GradCall& g, bool first) {
+  if (!g.dresp || g.p->N == 0) return GMM_OK;
+  return aligned_rows(g.W, g.p->ldw, sizeof(T)) && aligned_rows(g.dY, g.p->ldy, sizeof(T))
+             ? dot_launch<T, true>(g, first)
+             : dot_launch<T, false>(g, first);
+}
+
+gmm_status fill_launch(const GradCall& g, size_t size) {
+  int sms = 0;
+  gmm_status s = api_device_sms(&sms);
+  if (s != GMM_OK) return s;
+  const uint64_t K = g.p->K, D = g.p->D;
+  const bool one = g.ldd == g.p->D;  // one long row
+  FillArgs a = {(char*)g.dW, one ? 1 : K, (one ? K * D : D) * size, (uint64_t)g.ldd * size, 0};
+  a.parts = (a.row_bytes + kFillPiece - 1) / kFillPiece;
+  const uint64_t blocks = (a.rows * a.parts + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32);
+  return api_launch_next(embed_fill_kernel, dim3((unsigned)std::min<uint64_t>(blocks, sms * kBesideCtas)),
+                         kEmbedThreads, 0, g.st, a);
+}
+
+// Stream order: the sort; beside it the weights' gradient and rows of zeros; then the sums.
 template <typename T, typename TO, bool kVec>
 gmm_status grad_launch(const GradCall& g) {
   const gmm_embed_problem* p = g.p;
   const GradLayout L = grad_layout(p);
   const uint32_t M = (uint32_t)(p->N * p->m);
-  const SortPlan plan = sort_plan(M, p->K);
   constexpr int V = Unit<T, kVec>::n;
   EmbedGradArgs a = {};
+  gmm_status s;
+  if ((s = sort_launch(g, L, M, &a.list)) != GMM_OK) return s;
+  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
+  if (!g.add && (s = fill_launch(g, sizeof(TO))) != GMM_OK) return s;
+  if (M == 0) return GMM_OK;
   a.dY = g.dY;
   a.resp = g.resp;
-  a.seen = g.add ? nullptr : (const uint8_t*)(g.ws + L.seen);
   a.dW = g.dW;
   a.part = (float*)(g.ws + L.part);
   a.ldy = p->ldy;
@@ -183,61 +303,22 @@ gmm_status grad_launch(const GradCall& g) {
   a.width = L.width;
   a.scale = p->scale;
   a.m = p->m;
-
-  gmm_status s;
-  if (cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSortWarps * (4 << kSortBits)) != cudaSuccess)
-    return api_launched(0), GMM_ERR_CUDA;
-  for (int i = 0; i < plan.passes; i++) {
-    SortArgs o = {};
-    o.idx = i == 0 ? g.idx : nullptr;
-    o.key = a.key;
-    o.src = a.src;
-    o.key_out = (uint32_t*)(g.ws + L.key[i & 1]);
-    o.src_out = (uint32_t*)(g.ws + L.src[i & 1]);
-    o.counts = (uint32_t*)(g.ws + L.counts);
-    o.seen = i == 0 && !g.add ? (uint8_t*)(g.ws + L.seen) : nullptr;
-    o.M = M;
-    o.per_warp = plan.per_warp;
-    o.K = p->K;
-    o.bits = plan.bits;
-    o.shift = i * plan.bits;
-    o.flags = g.flags;
-    if ((s = api_launch_next(sort_count_kernel, dim3(plan.tiles), kSortThreads, 0, g.st, o)) != GMM_OK)
-      return s;
-    if ((s = api_launch_next(sort_place_kernel, dim3(plan.tiles), kSortThreads,
-                         kSortWarps * ((size_t)4 << plan.bits), g.st, o)) != GMM_OK)
-      return s;
-    a.key = o.key_out;
-    a.src = o.src_out;
-  }
-  if (M > 0) {
-    const unsigned groups = kEmbedThreads / a.lanes;
-    const dim3 grid((a.chunks + groups - 1) / groups, (a.units + a.lanes - 1) / a.lanes);
-    if ((s = api_launch_next(embed_sum_kernel<T, TO, kVec>, grid, kEmbedThreads, 0, g.st, a)) !=
-        GMM_OK)
-      return s;
-  }
-  const unsigned fill = g.add ? 0 : (unsigned)((p->K + kFillRows - 1) / kFillRows);
-  if (a.chunks + fill > 0 &&
-      (s = api_launch_next(embed_finish_kernel<T, TO, kVec>, dim3(a.chunks + fill), kEmbedThreads, 0,
-                       g.st, a, a.chunks)) != GMM_OK)
+  a.add = g.add;
+  const unsigned groups = kEmbedThreads / a.lanes;
+  const dim3 grid((a.chunks + groups - 1) / groups, (a.units + a.lanes - 1) / a.lanes);
+  if ((s = api_launch_next(embed_sum_kernel<T, TO, kVec>, grid, kEmbedThreads,
+                           (size_t)groups * a.chunk * 12, g.st, a)) != GMM_OK)
     return s;
-  return GMM_OK;
+  constexpr int kWarps = kEmbedThreads / 32;
+  return api_launch_next(embed_join_kernel<T, TO, kVec>,
+                         dim3((a.chunks + kWarps - 1) / kWarps, (a.units + 31) / 32),
+                         kEmbedThreads, 0, g.st, a);
 }
 
 template <typename T>
 gmm_status grad_types(const GradCall& g, bool wide) {
-  const gmm_embed_problem* p = g.p;
-  gmm_status s = GMM_OK;
-  if (g.dresp && p->N > 0) {
-    s = aligned_rows(g.W, p->ldw, sizeof(T)) && aligned_rows(g.dY, p->ldy, sizeof(T))
-            ? dot_launch<T, true>(g)
-            : dot_launch<T, false>(g);
-    if (s != GMM_OK) return s;
-  }
-  if (!g.dW) return GMM_OK;
-  const bool vec = aligned_rows(g.dY, p->ldy, sizeof(T)) &&
+  if (!g.dW) return dot_vec<T>(g, true);
+  const bool vec = aligned_rows(g.dY, g.p->ldy, sizeof(T)) &&
                    aligned_rows(g.dW, g.ldd, wide ? sizeof(float) : sizeof(T));
   if (wide) return vec ? grad_launch<T, float, true>(g) : grad_launch<T, float, false>(g);
   return vec ? grad_launch<T, T, true>(g) : grad_launch<T, T, false>(g);
