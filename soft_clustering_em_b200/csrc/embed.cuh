@@ -26,8 +26,7 @@ struct EmbedArgs {
   int64_t N, ldw, ldy;
   int m, K, D;
   float scale;
-  int units;       // of kEl elements per row
-  uint32_t magic;  // ceil(2^32 / units)
+  int units, lane_bits;
   uint32_t* flags;
 };
 
@@ -78,61 +77,57 @@ struct Unit {
 };
 
 // ------------------------------------------------------------------ lookup
-// A thread takes kPer units of the N x units outputs, 256 apart, so that the choices of kPer rows
-// and then kPer * kM units are on their way at once.  kM: at least m.
+// 2^lane_bits lanes per row; a lane takes kPer units of it, a row's lanes apart, so that a row's
+// choices and addresses are formed once for kPer * kM units, all on their way at once.  Blocks y:
+// where a row has more units than that.  kM: at least m.
 template <typename T, bool kVec, int kM, int kPer>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   using U = Unit<T, kVec>;
-  const int64_t first = (int64_t)blockIdx.x * (kPer * kEmbedThreads);
-  const int64_t row0 = first <= 0xffffffffll ? (int64_t)((uint32_t)first / (uint32_t)a.units)
-                                             : first / a.units;
-  const uint32_t unit0 = (uint32_t)(first - row0 * a.units) + threadIdx.x;
-  int64_t row[kPer];
-  int unit[kPer];
-  int k[kPer][kM];
-  float w[kPer][kM];
+  const int lanes = 1 << a.lane_bits, l = threadIdx.x & (lanes - 1);
+  const int64_t row =
+      (int64_t)blockIdx.x * (kEmbedThreads >> a.lane_bits) + (threadIdx.x >> a.lane_bits);
+  const int u0 = (int)(blockIdx.y * kPer << a.lane_bits) + l;
+  if (row >= a.N) return;
+  int k[kM];
+  float w[kM];
+#pragma unroll
+  for (int j = 0; j < kM; j++) {
+    const bool live = kM == 1 || j < a.m;
+    const int64_t at = kM == 1 ? row : row * a.m + j;
+    k[j] = live ? a.idx[at] : -1;
+    w[j] = live && a.resp ? a.resp[at] : 1.f;
+  }
   typename U::Raw r[kPer][kM];
 #pragma unroll
-  for (int p = 0; p < kPer; p++) {
-    const uint32_t i = unit0 + p * kEmbedThreads;
-    // (exact: up to 1,024 units i is below 2^11, and rows of more are passed at most once)
-    const uint32_t q = a.units > kPer * kEmbedThreads ? i >= (uint32_t)a.units
-                       : a.units == 1                 ? i
-                                                      : __umulhi(i, a.magic);
-    row[p] = row0 + q;
-    unit[p] = (int)(i - q * a.units);
+  for (int j = 0; j < kM; j++) {
+    const bool ok = (unsigned)k[j] < (unsigned)a.K;
+    if (!ok) {
+      if (k[j] != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+      w[j] = 0.f;
+    }
+    const T* from = (const T*)a.W + (ok ? k[j] : 0) * a.ldw;
 #pragma unroll
-    for (int j = 0; j < kM; j++) {
-      const bool live = row[p] < a.N && (kM == 1 || j < a.m);
-      const int64_t at = kM == 1 ? row[p] : row[p] * a.m + j;
-      k[p][j] = live ? a.idx[at] : -1;
-      w[p][j] = live && a.resp ? a.resp[at] : 1.f;
+    for (int p = 0; p < kPer; p++) {
+      const int u = u0 + (p << a.lane_bits);
+      r[p][j] = ok && u < a.units ? U::load(from, u, a.D) : U::zero();
     }
   }
+  T* to = (T*)a.Y + row * a.ldy;
 #pragma unroll
   for (int p = 0; p < kPer; p++) {
-#pragma unroll
-    for (int j = 0; j < kM; j++) {
-      const bool ok = (unsigned)k[p][j] < (unsigned)a.K;
-      if (!ok && k[p][j] != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-      r[p][j] = ok ? U::load((const T*)a.W + k[p][j] * a.ldw, unit[p], a.D) : U::zero();
-      if (!ok) w[p][j] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < kPer; p++) {
-    if (row[p] >= a.N) return;
+    const int u = u0 + (p << a.lane_bits);
+    if (u >= a.units) return;
     float y[U::n] = {};
 #pragma unroll
     for (int j = 0; j < kM; j++) {
       float x[U::n];
       U::unpack(r[p][j], x);
 #pragma unroll
-      for (int e = 0; e < U::n; e++) y[e] = kM == 1 ? w[p][j] * x[e] : fmaf(w[p][j], x[e], y[e]);
+      for (int e = 0; e < U::n; e++) y[e] = kM == 1 ? w[j] * x[e] : fmaf(w[j], x[e], y[e]);
     }
 #pragma unroll
     for (int e = 0; e < U::n; e++) y[e] *= a.scale;
-    U::store((T*)a.Y + row[p] * a.ldy, unit[p], a.D, y);
+    U::store(to, u, a.D, y);
   }
 }
 

@@ -44,19 +44,31 @@ gmm_status embed_launch(EmbedArgs a, cudaStream_t st) {
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
   a.units = (a.D + V - 1) / V;
-  a.magic = a.units > 1 ? (uint32_t)((((uint64_t)1 << 32) + a.units - 1) / a.units) : 0;
-  const int64_t all = a.N * a.units;
-  auto go = [&](auto kern, int per) {
-    const int64_t grid = (all + per * kEmbedThreads - 1) / (per * kEmbedThreads);
-    kern<<<(unsigned)grid, kEmbedThreads, 0, st>>>(a);
+  const bool few = a.N * a.units <= (int64_t)sms * 2 * kEmbedThreads;
+  // Units of a lane: one while more would leave SMs without work, else up to 4 (2 or 1 of 4 or 8
+  // choices), and the lanes that waste the fewest places; of those, the fewest lanes.
+  auto go = [&](auto one, auto more, int most) {
+    const int per = few ? 1 : most;
+    a.lane_bits = 8;
+    int64_t least = INT64_MAX;
+    for (int bits = 8; bits >= 0; bits--) {
+      const int64_t lanes = (int64_t)1 << bits, blocks = (a.units + per * lanes - 1) / (per * lanes);
+      const int64_t places = (a.units + lanes - 1) / lanes * lanes;
+      if (blocks > 1 && bits < 6) break;
+      if (places <= least) least = places, a.lane_bits = bits;
+    }
+    const int rows = kEmbedThreads >> a.lane_bits, width = per << a.lane_bits;
+    const dim3 grid((unsigned)((a.N + rows - 1) / rows), (a.units + width - 1) / width);
+    if (few)
+      one<<<grid, kEmbedThreads, 0, st>>>(a);
+    else
+      more<<<grid, kEmbedThreads, 0, st>>>(a);
     return api_launched(1);
   };
-  // one unit per thread while more would leave SMs without work
-  const bool few = all <= (int64_t)sms * 2 * kEmbedThreads;
-  if (a.m == 1) return few ? go(embed_kernel<T, kVec, 1, 1>, 1) : go(embed_kernel<T, kVec, 1, 4>, 4);
-  if (a.m == 2) return few ? go(embed_kernel<T, kVec, 2, 1>, 1) : go(embed_kernel<T, kVec, 2, 4>, 4);
-  if (a.m <= 4) return few ? go(embed_kernel<T, kVec, 4, 1>, 1) : go(embed_kernel<T, kVec, 4, 2>, 2);
-  return go(embed_kernel<T, kVec, kMaxTopM, 1>, 1);
+  if (a.m == 1) return go(embed_kernel<T, kVec, 1, 1>, embed_kernel<T, kVec, 1, 4>, 4);
+  if (a.m == 2) return go(embed_kernel<T, kVec, 2, 1>, embed_kernel<T, kVec, 2, 4>, 4);
+  if (a.m <= 4) return go(embed_kernel<T, kVec, 4, 1>, embed_kernel<T, kVec, 4, 2>, 2);
+  return go(embed_kernel<T, kVec, kMaxTopM, 1>, embed_kernel<T, kVec, kMaxTopM, 1>, 1);
 }
 
 template <typename T>
@@ -337,7 +349,7 @@ gmm_status gmm_embed(const gmm_embed_problem* p, const void* W, const int32_t* i
   if ((uintptr_t)W % elem(p->dtype) != 0 || (uintptr_t)Y % elem(p->dtype) != 0)
     return GMM_ERR_UNSUPPORTED;
   const EmbedArgs a = {W,    idx,  resp, Y,        p->N, p->ldw, p->ldy,
-                       p->m, p->K, p->D, p->scale, 0,    0,      dev_flags};
+                       p->m, p->K, p->D, p->scale, 0,    0,    dev_flags};
   cudaStream_t st = (cudaStream_t)stream;
   if (p->dtype == GMM_F32) return embed_vec<float>(a, st);
   if (p->dtype == GMM_BF16) return embed_vec<__nv_bfloat16>(a, st);

@@ -104,7 +104,7 @@ __device__ __forceinline__ float group_sum(float v) {
 // registers until the segment or the rows end; the sums of piece (CTA c, segment s) go to slot
 // c + s, which no other piece has: from piece to piece c or s grows, or both.
 template <typename T, int kLanes, int kEl, bool kVec>
-__global__ void __launch_bounds__(kRouteThreads, 2) route_load_kernel(RouteArgs a, float* part) {
+__global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_load_kernel(RouteArgs a, float* part) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
   constexpr int kChunks = kEl / V;
@@ -199,19 +199,23 @@ struct RouteLossOut {
   int32_t *counts, *rows;
 };
 
-// One CTA per segment adds up its slots, in order, in 64 bits.  Threads: `cols` columns (a power
-// of two) times groups that take every so many slots.
+// A cluster per segment adds up its slots, in order, in 64 bits; each CTA has a share of the
+// experts.  Threads: `cols` columns (a power of two) times groups that take every so many slots.
 constexpr int kReduceThreads = 512;
+constexpr int kReduceWarps = kReduceThreads / 32;
 __global__ void __launch_bounds__(kReduceThreads)
     route_reduce_kernel(RouteArgs a, const float* part, RouteLossOut o, int cols) {
   __shared__ double sh[kReduceThreads];
   __shared__ uint32_t shc[kReduceThreads];
-  __shared__ double total[2];
-  __shared__ uint32_t rows;
-  grid_dependents_launch();
+  __shared__ double zs[kReduceWarps];
+  __shared__ uint32_t rs[kReduceWarps];
+  __shared__ double mine;  // of balance, read by the cluster's first CTA
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
+  const int s = blockIdx.x / ctas;
+  const int groups = kReduceThreads / cols, g = t / cols, col = t & (cols - 1);
   grid_dependency_wait();
-  const int t = threadIdx.x, s = blockIdx.x;
-  const int groups = kReduceThreads / cols, g = t / cols, col = t % cols;
+  grid_dependents_launch();
   int64_t lo = 0, hi = a.N;
   if (a.offsets) {
     lo = a.offsets[s];
@@ -223,21 +227,22 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int64_t first = legal && hi > lo ? lo / a.rows + s : 0;
   const int count = legal && hi > lo ? (int)((hi - 1) / a.rows - lo / a.rows) + 1 : 0;
   part += first * size;
-  if (t < 32) {
-    double z = 0.0;
-    uint32_t n = 0;
-    for (int q = t; q < count; q += 32) {
-      z += part[q * size + 2 * a.K];
-      n += reinterpret_cast<const uint32_t*>(part)[q * size + 2 * a.K + 1];
-    }
-    z = warp_sum(z);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (t == 0) total[0] = z, rows = n;
+  double z = 0.0;
+  uint32_t n = 0;
+  for (int q = t; q < count; q += kReduceThreads) {
+    z += part[q * size + 2 * a.K];
+    n += reinterpret_cast<const uint32_t*>(part)[q * size + 2 * a.K + 1];
   }
+  z = warp_sum(z);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) zs[w] = z, rs[w] = n;
   __syncthreads();
-  const double L = rows > 0 ? (double)rows : 1.0;
+  z = 0.0;
+  n = 0;
+  for (int i = 0; i < kReduceWarps; i++) z += zs[i], n += rs[i];
+  const double L = n > 0 ? (double)n : 1.0;
   double balance = 0.0;
-  for (int k0 = 0; k0 < a.K; k0 += cols) {
+  for (int k0 = rank * cols; k0 < a.K; k0 += ctas * cols) {
     const int k = k0 + col;
     double p = 0.0;
     uint32_t c = 0;
@@ -260,16 +265,31 @@ __global__ void __launch_bounds__(kReduceThreads)
     __syncthreads();
   }
   balance = warp_sum(balance);
-  if ((t & 31) == 0) sh[t >> 5] = balance;
+  if (lane == 0) zs[w] = balance;
   __syncthreads();
   if (t == 0) {
     balance = 0.0;
-    for (int i = 0; i < kReduceThreads / 32; i++) balance += sh[i];
+    for (int i = 0; i < kReduceWarps; i++) balance += zs[i];
+    mine = balance;
+  }
+  __syncwarp();
+  sm100::cluster_sync();
+  if (rank == 0 && t == 0) {
+    for (int r = 1; r < ctas; r++) {
+      double v;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                   : "=d"(v)
+                   : "r"(sm100::map_to_rank(sm100::smem_u32(&mine), r))
+                   : "memory");
+      balance += v;
+    }
     const float nan = __int_as_float(0x7fffffff);
     if (o.balance) o.balance[s] = legal ? (float)(balance * a.K / (a.m * L * L)) : nan;
-    if (o.z) o.z[s] = legal ? (float)(total[0] / L) : nan;
-    if (o.rows) o.rows[s] = (int32_t)rows;
+    if (o.z) o.z[s] = legal ? (float)(z / L) : nan;
+    if (o.rows) o.rows[s] = (int32_t)n;
   }
+  __syncwarp();
+  sm100::cluster_sync();  // `mine` is read until here
 }
 
 // ------------------------------------------------------------------ gradient
@@ -286,7 +306,7 @@ struct RouteGradArgs {
 // A warp takes `rows` consecutive rows, 32 / kLanes at a time; the counts of the segment stay in
 // registers while it lasts.
 template <typename T, int kLanes, int kEl, bool kVec>
-__global__ void __launch_bounds__(kRouteThreads, 2) route_grad_kernel(RouteGradArgs g) {
+__global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_kernel(RouteGradArgs g) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
   constexpr int kChunks = kEl / V;
@@ -361,33 +381,35 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_grad_kernel(RouteGradA
     const float nan = q.bad ? __int_as_float(0x7fffffff) : 0.f;
 #pragma unroll
     for (int e = 0; e < kEl; e++) q.y[e] = q.y[e] * inv * fmaf(cf, cnt[e], base) + nan;
+    // what a chosen class gets beside that, from every choice that names it
+    float more = 0.f;
     for (int j = 0; j < (g.dresp ? a.m : 0); j++) {
-      const int kj = __shfl_sync(0xffffffffu, legal ? k : -1, (lane - l) + j);
+      const int kj = __shfl_sync(0xffffffffu, k, (lane - l) + j);
       const float aj = __shfl_sync(0xffffffffu, add, (lane - l) + j);
-      const int v = kj / V;
-      if (kj >= 0 && v % kLanes == l) {
-        const int at = v / kLanes * V + kj % V;
-#pragma unroll
-        for (int e = 0; e < kEl; e++)
-          if (e == at) q.y[e] += aj;
-      }
+      if (kj == k) more += aj;
     }
     __syncwarp();
-    if (!in) continue;
-    T* out = (T*)g.dZ + n * g.ldd;
+    T* out = (T*)g.dZ + (in ? n : n0) * g.ldd;
 #pragma unroll
     for (int v = 0; v < kChunks; v++) {
       float x[V];
 #pragma unroll
       for (int e = 0; e < V; e++) x[e] = live ? q.y[v * V + e] * a.scale : 0.f;
       const int k0 = (v * kLanes + l) * V;
-      if (kVec && k0 + V <= a.K) {
+      if (kVec && in && k0 + V <= a.K) {
         *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
       } else {
 #pragma unroll
         for (int e = 0; e < V; e++)
-          if (k0 + e < a.K) from_f32(out + k0 + e, x[e]);
+          if (in && k0 + e < a.K) from_f32(out + k0 + e, x[e]);
       }
+    }
+    __syncwarp();
+    // the chosen classes' entries once more, by the lanes that hold the choices
+    if (legal && live) {
+      const float ck = counts && g.dbalance ? (float)g.counts[(int64_t)s * a.K + k] : 0.f;
+      const float pk = ex2((xk - q.ref) * c) * inv;
+      from_f32(out + k, (fmaf(pk, fmaf(cf, ck, base), more) + nan) * a.scale);
     }
   }
 }

@@ -36,7 +36,7 @@ struct LossPlan {
 };
 LossPlan loss_plan(int64_t N) {
   LossPlan p;
-  p.chunks = std::max<int64_t>(1, std::min<int64_t>((N + 31) / 32, 296));
+  p.chunks = std::max<int64_t>(1, std::min<int64_t>((N + 31) / 32, 444));
   p.rows = std::max<int64_t>(1, (N + p.chunks - 1) / p.chunks);
   return p;
 }
@@ -54,14 +54,14 @@ gmm_status load_launch(const RouteArgs& a, float* part, bool vec, unsigned grid,
   return api_launched(1);
 }
 
-// Lanes and places per row: those of gmm_route's rows.
+// Lanes and places per row: up to 16 places, so that three CTAs are resident.
 template <typename T>
 gmm_status load_dispatch(const RouteArgs& a, float* part, unsigned grid, cudaStream_t st) {
   const bool vec = (uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0;
   if (a.K <= 64) return load_launch<T, 8, 8>(a, part, vec, grid, st);
   if (a.K <= 128) return load_launch<T, 8, 16>(a, part, vec, grid, st);
-  if (a.K <= 256) return load_launch<T, 8, 32>(a, part, vec, grid, st);
-  if (a.K <= 512) return load_launch<T, 16, 32>(a, part, vec, grid, st);
+  if (a.K <= 256) return load_launch<T, 16, 16>(a, part, vec, grid, st);
+  if (a.K <= 512) return load_launch<T, 32, 16>(a, part, vec, grid, st);
   return load_launch<T, 32, 32>(a, part, vec, grid, st);
 }
 
@@ -88,8 +88,8 @@ gmm_status grad_dispatch(const RouteGradArgs& g, cudaStream_t st) {
                    (uintptr_t)g.dZ % 16 == 0 && g.ldd * sizeof(T) % 16 == 0;
   if (g.r.K <= 64) return grad_launch<T, 8, 8>(g, vec, st);
   if (g.r.K <= 128) return grad_launch<T, 8, 16>(g, vec, st);
-  if (g.r.K <= 256) return grad_launch<T, 8, 32>(g, vec, st);
-  if (g.r.K <= 512) return grad_launch<T, 16, 32>(g, vec, st);
+  if (g.r.K <= 256) return grad_launch<T, 16, 16>(g, vec, st);
+  if (g.r.K <= 512) return grad_launch<T, 32, 16>(g, vec, st);
   return grad_launch<T, 32, 32>(g, vec, st);
 }
 
@@ -128,11 +128,26 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
                                : load_dispatch<__half>(a, (float*)ws, grid, st);
     if (s != GMM_OK) return s;
   }
+  // a cluster per segment: 32 experts to a CTA, up to 8 CTAs
+  const int ctas = std::min(8, (r->K + 31) / 32);
   int cols = 32;
-  while (cols < r->K && cols < kReduceThreads) cols *= 2;
+  while (cols * ctas < r->K) cols *= 2;
   const RouteLossOut o = {balance, z, load, counts, rows};
-  return api_launch_next(route_reduce_kernel, dim3((unsigned)S), kReduceThreads, 0, st, a,
-                         (const float*)ws, o, cols);
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S * ctas);
+  cfg.blockDim = dim3(kReduceThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, route_reduce_kernel, a, (const float*)ws, o, cols) != cudaSuccess)
+    return api_launched(0), GMM_ERR_CUDA;
+  return api_launched(1);
 }
 
 gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* idx, int32_t m,
