@@ -124,41 +124,43 @@ __global__ void beam_merge_kernel(BeamArgs a) {
 struct BeamState {
   char* base;
   int64_t row_stride, outer_stride;  // bytes
-  uint32_t outer, inner, per_pos;    // pieces of a row; columns of a piece and of a position
-  int by_len;
 };
 
-constexpr int kStates = 32;  // of one launch
+constexpr int kStates = 64;  // of one launch
 constexpr int kReorderThreads = 256;
 constexpr int kReorderGroups = 1024;  // looked at in one go
 
+// States of one shape.
 struct ReorderArgs {
   BeamState state[kStates];
   const int32_t* parent;  // B x w
-  const int32_t* lens;    // B, may be null
+  const int32_t* lens;    // B, or null: all positions are used
   int64_t B;
-  int w;
+  int n, w;
+  uint32_t outer, inner, per_pos;  // pieces of a row; columns of a piece and of a position
   uint32_t* flags;
 };
 
-// kW: at least w.  Blocks y: a state; blocks x share out its tiles of 256 columns, of the groups in
-// which a beam moves, up to their lengths.
+// CTAs per SM: all of a launch are resident at once.
+constexpr int reorder_ctas(int w) { return w <= 4 ? 6 : w <= 8 ? 4 : w <= 16 ? 2 : 1; }
+
+// kW: at least w.  The blocks share out tiles of 256 columns: of the groups in which a beam moves, up
+// to their lengths, for every state.
 template <typename Vec, int kW>
-__global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(ReorderArgs a) {
+__global__ void __launch_bounds__(kReorderThreads, reorder_ctas(kW))
+    beam_reorder_kernel(ReorderArgs a) {
   __shared__ uint32_t upto[kReorderGroups];  // tiles of the groups up to and with this one
   __shared__ uint32_t warp_total[kReorderThreads / 32];
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-  const BeamState st = a.state[blockIdx.y];
-  grid_dependents_launch();
   grid_dependency_wait();
+  grid_dependents_launch();
   constexpr int kEach = kReorderGroups / kReorderThreads;
+  const int positions = (int)(a.inner / a.per_pos);
   auto length = [&](int64_t b) {  // columns of a piece that are used
-    if (!a.lens || !st.by_len) return st.inner;
-    const int most = (int)(st.inner / st.per_pos), n = a.lens[b];
-    return (uint32_t)max(0, min(n, most)) * st.per_pos;
+    return a.lens ? (uint32_t)max(0, min(a.lens[b], positions)) * a.per_pos : a.inner;
   };
   for (int64_t b0 = 0; b0 < a.B; b0 += kReorderGroups) {
-    uint32_t mine[kEach], total = 0;
+    uint32_t tiles_to[kEach], total = 0;
 #pragma unroll
     for (int q = 0; q < kEach; q++) {
       const int64_t b = b0 + t * kEach + q;
@@ -170,15 +172,14 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(ReorderAr
           if ((unsigned)p < (unsigned)a.w) moves |= p != i;
           else if (p != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
         }
-        if (a.lens && st.by_len && a.flags &&
-            (a.lens[b] < 0 || a.lens[b] > (int)(st.inner / st.per_pos)))
+        if (a.lens && a.flags && (unsigned)a.lens[b] > (unsigned)positions)
           atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
         if (moves)
-          tiles = (uint32_t)(((uint64_t)st.outer * length(b) + kReorderThreads - 1) /
+          tiles = (uint32_t)(((uint64_t)a.outer * length(b) + kReorderThreads - 1) /
                              kReorderThreads);
       }
       total += tiles;
-      mine[q] = total;
+      tiles_to[q] = total;
     }
     uint32_t scan = total;
 #pragma unroll
@@ -191,36 +192,55 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(ReorderAr
     uint32_t before = scan - total;
     for (int q = 0; q < w; q++) before += warp_total[q];
 #pragma unroll
-    for (int q = 0; q < kEach; q++) upto[t * kEach + q] = before + mine[q];
+    for (int q = 0; q < kEach; q++) upto[t * kEach + q] = before + tiles_to[q];
     __syncthreads();
-    const uint32_t all = upto[kReorderGroups - 1];
-    for (uint32_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
-      int lo = 0, hi = kReorderGroups - 1;  // the first group with upto > tile
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (upto[mid] > tile) hi = mid;
-        else lo = mid + 1;
+    // this block's share: consecutive tiles, so that it seldom comes to another group
+    const uint64_t all = upto[kReorderGroups - 1], every = all * a.n;
+    uint64_t tile = every * blockIdx.x / gridDim.x;
+    const uint64_t stop = every * (blockIdx.x + 1) / gridDim.x;
+    int state = -1, group = 0;
+    uint32_t here = 0, first = 0, upper = 0;  // the tile in its state; those of its group
+    uint32_t len = 0, moved = 0;
+    int mine = 0;
+    int64_t b = 0;
+    for (; tile < stop; tile++, here++) {
+      if (state < 0 || here >= upper) {  // (the same for all threads)
+        if (state < 0 || here >= all) {
+          state = (int)(tile / all);
+          here = (uint32_t)(tile - state * all);
+          group = 0;
+          int hi = kReorderGroups - 1;  // the first group with upto > here
+          while (group < hi) {
+            const int mid = (group + hi) / 2;
+            if (upto[mid] > here) hi = mid;
+            else group = mid + 1;
+          }
+        } else {
+          do group++;
+          while (upto[group] <= here);
+        }
+        first = group ? upto[group - 1] : 0;
+        upper = upto[group];
+        b = b0 + group;
+        len = length(b);
+        mine = lane < a.w ? a.parent[b * a.w + lane] : -1;  // a parent per lane
+        moved = __ballot_sync(0xffffffffu, (unsigned)mine < (unsigned)a.w && mine != lane);
       }
-      const int64_t b = b0 + lo;
-      const uint32_t len = length(b);
-      const uint64_t c = (uint64_t)(tile - (lo ? upto[lo - 1] : 0)) * kReorderThreads + t;
-      if (c >= (uint64_t)st.outer * len) continue;
-      const uint32_t o = (uint32_t)c / len;  // (below 2^32: checked on the host)
-      char* p = st.base + b * a.w * st.row_stride + o * st.outer_stride +
+      const uint64_t c = (uint64_t)(here - first) * kReorderThreads + t;
+      const bool in = c < (uint64_t)a.outer * len;
+      const uint32_t o = in ? (uint32_t)c / len : 0;  // (below 2^32: checked on the host)
+      const int64_t stride = a.state[state].row_stride;
+      char* p = a.state[state].base + b * a.w * stride + o * a.state[state].outer_stride +
                 ((uint64_t)c - (uint64_t)o * len) * sizeof(Vec);
       Vec v[kW];
-      uint32_t moved = 0;
 #pragma unroll
       for (int i = 0; i < kW; i++) {
-        const int from = i < a.w ? a.parent[b * a.w + i] : -1;
-        if ((unsigned)from < (unsigned)a.w && from != i) {
-          moved |= 1u << i;
-          v[i] = *reinterpret_cast<const Vec*>(p + from * st.row_stride);
-        }
+        const int from = __shfl_sync(0xffffffffu, mine, i);
+        if (in && (moved >> i & 1)) v[i] = *reinterpret_cast<const Vec*>(p + from * stride);
       }
 #pragma unroll
       for (int i = 0; i < kW; i++)
-        if (moved >> i & 1) *reinterpret_cast<Vec*>(p + i * st.row_stride) = v[i];
+        if (in && (moved >> i & 1)) *reinterpret_cast<Vec*>(p + i * stride) = v[i];
     }
     __syncthreads();
   }

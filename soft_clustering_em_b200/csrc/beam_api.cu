@@ -25,19 +25,25 @@ gmm_status merge_launch(const BeamArgs& a, cudaStream_t st) {
                          32 * warps, (size_t)warps * a.w * a.m * 8, st, a);
 }
 
-template <typename Vec>
-gmm_status reorder_launch(const ReorderArgs& a, int n, uint64_t tiles, cudaStream_t st) {
+// As many CTAs as are resident at once: each finds its tiles once.
+template <typename Vec, int kW>
+gmm_status reorder_launch(const ReorderArgs& a, cudaStream_t st) {
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
-  const unsigned x = (unsigned)std::max<uint64_t>(
-      1, std::min<uint64_t>(tiles, ((uint64_t)sms * 16 + n - 1) / n));
-  const dim3 grid(x, n);
-  auto go = [&](auto kern) { return api_launch_next(kern, grid, kReorderThreads, 0, st, a); };
-  if (a.w <= 4) return go(beam_reorder_kernel<Vec, 4>);
-  if (a.w <= 8) return go(beam_reorder_kernel<Vec, 8>);
-  if (a.w <= 16) return go(beam_reorder_kernel<Vec, 16>);
-  return go(beam_reorder_kernel<Vec, 32>);
+  const double tiles = (double)a.n * a.B *
+                       (((double)a.outer * a.inner + kReorderThreads - 1) / kReorderThreads);
+  const unsigned grid =
+      (unsigned)std::max(1.0, std::min(tiles, (double)sms * reorder_ctas(kW)));
+  return api_launch_next(beam_reorder_kernel<Vec, kW>, dim3(grid), kReorderThreads, 0, st, a);
+}
+
+template <typename Vec>
+gmm_status reorder_width(const ReorderArgs& a, cudaStream_t st) {
+  return a.w <= 4    ? reorder_launch<Vec, 4>(a, st)
+         : a.w <= 8  ? reorder_launch<Vec, 8>(a, st)
+         : a.w <= 16 ? reorder_launch<Vec, 16>(a, st)
+                     : reorder_launch<Vec, 32>(a, st);
 }
 
 // Bytes of a column: 16, 4 or 1, the most that every address of the state is a multiple of.
@@ -105,41 +111,48 @@ gmm_status gmm_beam_reorder(int64_t B, int32_t w, const int32_t* parent, const i
         (double)B * w * (double)s.row_stride > 1e18 ||
         (double)s.outer * (double)s.outer_stride > 1e18)
       return GMM_ERR_UNSUPPORTED;
-    // tiles of a whole launch are counted in 32 bits, 1,024 groups at a time
+    // tiles are counted in 32 bits, 1,024 groups at a time
     if (std::min<double>(B, kReorderGroups) * (row / column_bytes(s) / kReorderThreads + 1) >=
-        4294967296.0)
+        2147483648.0)
       return GMM_ERR_UNSUPPORTED;
   }
   if (B == 0 || n == 0) return GMM_OK;
   if (!parent) return GMM_ERR_INVALID_ARG;
-  for (int bytes : {16, 4, 1}) {
+  // One launch for the states of a shape, up to kStates of them.  (A state that has been taken is
+  // one with an earlier state of its shape: no memory is needed to tell.)
+  auto empty = [&](const gmm_beam_state& s) {
+    return s.outer == 0 || s.count == 0 || s.pos_bytes == 0;
+  };
+  auto alike = [&](const gmm_beam_state& s, const gmm_beam_state& q) {
+    return s.outer == q.outer && s.count == q.count && s.pos_bytes == q.pos_bytes &&
+           (lens == nullptr || (s.by_len != 0) == (q.by_len != 0)) &&
+           column_bytes(s) == column_bytes(q);
+  };
+  for (int i = 0; i < n; i++) {
+    bool taken = empty(states[i]);
+    for (int j = 0; j < i && !taken; j++) taken = !empty(states[j]) && alike(states[i], states[j]);
+    if (taken) continue;
+    const int bytes = column_bytes(states[i]);
     ReorderArgs a = {};
     a.parent = parent;
-    a.lens = lens;
+    a.lens = states[i].by_len ? lens : nullptr;
     a.B = B;
     a.w = w;
+    a.outer = (uint32_t)states[i].outer;
+    a.per_pos = (uint32_t)(states[i].pos_bytes / bytes);
+    a.inner = (uint32_t)states[i].count * a.per_pos;
     a.flags = dev_flags;
-    int have = 0;
-    uint64_t tiles = 0;
-    for (int i = 0; i <= n; i++) {
-      if (have == kStates || (i == n && have > 0)) {
+    for (int j = i; j <= n; j++) {
+      if (a.n == kStates || (j == n && a.n > 0)) {
         cudaStream_t st = (cudaStream_t)stream;
-        const gmm_status s = bytes == 16  ? reorder_launch<uint4>(a, have, tiles, st)
-                             : bytes == 4 ? reorder_launch<uint32_t>(a, have, tiles, st)
-                                          : reorder_launch<uint8_t>(a, have, tiles, st);
+        const gmm_status s = bytes == 16  ? reorder_width<uint4>(a, st)
+                             : bytes == 4 ? reorder_width<uint32_t>(a, st)
+                                          : reorder_width<uint8_t>(a, st);
         if (s != GMM_OK) return s;
-        have = 0;
-        tiles = 0;
+        a.n = 0;
       }
-      if (i == n) break;
-      const gmm_beam_state& s = states[i];
-      if (s.outer == 0 || s.count == 0 || s.pos_bytes == 0 || column_bytes(s) != bytes) continue;
-      const uint32_t per = (uint32_t)(s.pos_bytes / bytes);
-      a.state[have++] = {(char*)s.base,       s.row_stride, s.outer_stride, (uint32_t)s.outer,
-                         (uint32_t)s.count * per, per,          s.by_len};
-      const uint64_t row = (uint64_t)s.outer * s.count * per;
-      tiles = std::max<uint64_t>(tiles, (uint64_t)B * ((row + kReorderThreads - 1) /
-                                                       kReorderThreads));
+      if (j < n && alike(states[j], states[i]))
+        a.state[a.n++] = {(char*)states[j].base, states[j].row_stride, states[j].outer_stride};
     }
   }
   return GMM_OK;

@@ -30,9 +30,11 @@ struct EmbedArgs {
   uint32_t* flags;
 };
 
-// A unit of a row: 16 bytes of T (kVec, rows start on 16 bytes), or one element.
-template <typename T, bool kVec>
+// A unit of a row: one element (kMode 0), or 16 bytes of T where rows start on 16 bytes, the last
+// unit perhaps a part (1) or whole as well (2: D is a multiple).
+template <typename T, int kMode>
 struct Unit {
+  static constexpr bool kVec = kMode > 0;
   static constexpr int n = kVec ? Vec16<T>::n : 1;
   using Raw = typename std::conditional<kVec, uint4, T>::type;
   static __device__ __forceinline__ Raw zero() {
@@ -41,8 +43,10 @@ struct Unit {
   }
   // unit u of a row of D elements; what is behind the row is 0
   static __device__ __forceinline__ Raw load(const T* row, int u, int D) {
-    if constexpr (kVec) {
-      if (u * n + n <= D) return load16(row + u * n);
+    if constexpr (!kVec) {
+      return row[u];
+    } else {
+      if (kMode == 2 || u * n + n <= D) return load16(row + u * n);
       union {
         uint4 r;
         T x[n];
@@ -52,8 +56,6 @@ struct Unit {
       for (int e = 0; e < n; e++)
         if (u * n + e < D) part.x[e] = row[u * n + e];
       return part.r;
-    } else {
-      return row[u];
     }
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[n]) {
@@ -61,17 +63,16 @@ struct Unit {
     else x[0] = to_f32(r);
   }
   static __device__ __forceinline__ void store(T* row, int u, int D, const float (&x)[n]) {
-    if constexpr (kVec) {
-      const uint4 r = Vec16<T>::pack(x);
-      if (u * n + n <= D) {
-        *reinterpret_cast<uint4*>(row + u * n) = r;
-        return;
-      }
-#pragma unroll
-      for (int e = 0; e < n; e++)
-        if (u * n + e < D) from_f32(row + u * n + e, x[e]);
-    } else {
+    if constexpr (!kVec) {
       from_f32(row + u, x[0]);
+    } else {
+      if (kMode == 2 || u * n + n <= D) {
+        *reinterpret_cast<uint4*>(row + u * n) = Vec16<T>::pack(x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < n; e++)
+          if (u * n + e < D) from_f32(row + u * n + e, x[e]);
+      }
     }
   }
 };
@@ -80,9 +81,9 @@ struct Unit {
 // 2^lane_bits lanes per row; a lane takes kPer units of it, a row's lanes apart, so that a row's
 // choices and addresses are formed once for kPer * kM units, all on their way at once.  Blocks y:
 // where a row has more units than that.  kM: at least m.
-template <typename T, bool kVec, int kM, int kPer>
+template <typename T, int kMode, int kM, int kPer>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
-  using U = Unit<T, kVec>;
+  using U = Unit<T, kMode>;
   const int lanes = 1 << a.lane_bits, l = threadIdx.x & (lanes - 1);
   const int64_t row =
       (int64_t)blockIdx.x * (kEmbedThreads >> a.lane_bits) + (threadIdx.x >> a.lane_bits);
@@ -456,10 +457,10 @@ struct EmbedGradArgs {
   int m, add;
 };
 
-template <typename T, typename TO, bool kVec>
+template <typename T, typename TO, int kMode>
 __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, int u,
-                                           const float (&sum)[Unit<T, kVec>::n]) {
-  constexpr int n = Unit<T, kVec>::n;
+                                           const float (&sum)[Unit<T, kMode>::n]) {
+  constexpr int n = Unit<T, kMode>::n;
   TO* row = (TO*)a.dW + (int64_t)k * a.ldd;
   float x[n];
 #pragma unroll
@@ -467,15 +468,15 @@ __device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, i
   if constexpr (std::is_same<T, TO>::value) {
     if (a.add) {
       float old[n];
-      Unit<T, kVec>::unpack(Unit<T, kVec>::load(row, u, a.D), old);
+      Unit<T, kMode>::unpack(Unit<T, kMode>::load(row, u, a.D), old);
 #pragma unroll
       for (int e = 0; e < n; e++) x[e] += old[e];
     }
-    Unit<T, kVec>::store(row, u, a.D, x);
+    Unit<T, kMode>::store(row, u, a.D, x);
   } else {  // a float32 gradient of narrower rows: 32 bytes per unit
 #pragma unroll
     for (int e = 0; e < n; e += 4) {
-      if (kVec && u * n + e + 4 <= a.D) {
+      if (kMode == 2 || (kMode == 1 && u * n + e + 4 <= a.D)) {
         float4* p = reinterpret_cast<float4*>(row + u * n + e);
         float4 v = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         if (a.add) {
@@ -496,9 +497,9 @@ constexpr int kGradBatch = 8;
 constexpr int kGradChunk = 128;  // most choices per chunk
 
 // Shared memory: what the CTA's choices say (class, row of dY, weight), read once.
-template <typename T, typename TO, bool kVec>
+template <typename T, typename TO, int kMode>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradArgs a) {
-  using U = Unit<T, kVec>;
+  using U = Unit<T, kMode>;
   extern __shared__ uint32_t stage[];
   const int l = threadIdx.x & (a.lanes - 1);
   const uint32_t groups = kEmbedThreads / a.lanes, g = threadIdx.x / a.lanes;
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
       if (goes_on && !last) continue;
       if (came_in || goes_on) {
         float* p = a.part + ((int64_t)c * 2 + (came_in ? 0 : 1)) * a.width + u * U::n;
-        if constexpr (kVec) {
+        if constexpr (U::kVec) {
 #pragma unroll
           for (int e = 0; e < U::n; e += 4)
             *reinterpret_cast<float4*>(p + e) =
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
           p[0] = sum[0];
         }
       } else {
-        write_grad<T, TO, kVec>(a, k, u, sum);
+        write_grad<T, TO, kMode>(a, k, u, sum);
       }
       came_in = false;
 #pragma unroll
@@ -582,9 +583,9 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
 // are shared out over the CTA's warps.
 constexpr int kJoinShort = 8;  // chunks
 
-template <typename T, typename TO, bool kVec>
+template <typename T, typename TO, int kMode>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs a) {
-  using U = Unit<T, kVec>;
+  using U = Unit<T, kMode>;
   constexpr int kWarps = kEmbedThreads / 32;
   __shared__ float sh[kWarps][32 * U::n];
   __shared__ uint32_t long_chunk[kWarps], long_last[kWarps];
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
   const int u = blockIdx.y * 32 + lane;
   auto part = [&](uint32_t q, bool tail, float (&x)[U::n]) {
     const float* p = a.part + ((int64_t)q * 2 + tail) * a.width + u * U::n;
-    if constexpr (kVec) {
+    if constexpr (U::kVec) {
 #pragma unroll
       for (int e = 0; e < U::n; e += 4) {
         const float4 v = *reinterpret_cast<const float4*>(p + e);
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
 #pragma unroll
         for (int e = 0; e < U::n; e++) sum[e] += x[q][e];
       }
-      write_grad<T, TO, kVec>(a, k, u, sum);
+      write_grad<T, TO, kMode>(a, k, u, sum);
     }
   }
   const bool is_long = mine && last - c > kJoinShort;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
 #pragma unroll
         for (int e = 0; e < U::n; e++) sum[e] += sh[i][lane * U::n + e];
       }
-      write_grad<T, TO, kVec>(a, a.list[((uint64_t)from + 1) * a.chunk].x, u, sum);
+      write_grad<T, TO, kMode>(a, a.list[((uint64_t)from + 1) * a.chunk].x, u, sum);
     }
     __syncthreads();
   }
@@ -688,9 +689,9 @@ struct EmbedDotArgs {
   uint32_t* flags;
 };
 
-template <typename T, bool kVec, int kLanes, int kMost>
+template <typename T, int kMode, int kLanes, int kMost>
 __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(EmbedDotArgs a) {
-  using U = Unit<T, kVec>;
+  using U = Unit<T, kMode>;
   constexpr int kAhead = kMost == 1 ? 4 : kMost == 2 ? 2 : 1;  // units of a lane on their way at once
   grid_dependents_launch();
   const int l = threadIdx.x % kLanes;

@@ -36,46 +36,64 @@ gmm_status check_embed(const gmm_embed_problem* p) {
 bool aligned_rows(const void* base, int64_t ld, size_t size) {
   return (uintptr_t)base % 16 == 0 && ld * size % 16 == 0;
 }
+// How rows of D elements are taken (Unit).
+template <typename T>
+int unit_mode(bool aligned, int D) {
+  return !aligned ? 0 : D % Vec16<T>::n != 0 ? 1 : 2;
+}
 
-template <typename T, bool kVec>
+template <typename T, int kMode>
 gmm_status embed_launch(EmbedArgs a, cudaStream_t st) {
-  constexpr int V = Unit<T, kVec>::n;
+  constexpr int V = Unit<T, kMode>::n;
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
   a.units = (a.D + V - 1) / V;
   const bool few = a.N * a.units <= (int64_t)sms * 2 * kEmbedThreads;
-  // Units of a lane: one while more would leave SMs without work, else up to 4 (2 or 1 of 4 or 8
-  // choices), and the lanes that waste the fewest places; of those, the fewest lanes.
-  auto go = [&](auto one, auto more, int most) {
-    const int per = few ? 1 : most;
-    a.lane_bits = 8;
+  // Lanes of a row: of the shapes with up to `most` units per lane, the one that wastes the fewest
+  // places; of those, the fewest lanes.  One unit per lane while more would leave SMs without work.
+  int per = 1;
+  auto shape = [&](int most) {
     int64_t least = INT64_MAX;
     for (int bits = 8; bits >= 0; bits--) {
-      const int64_t lanes = (int64_t)1 << bits, blocks = (a.units + per * lanes - 1) / (per * lanes);
-      const int64_t places = (a.units + lanes - 1) / lanes * lanes;
-      if (blocks > 1 && bits < 6) break;
-      if (places <= least) least = places, a.lane_bits = bits;
+      const int64_t lanes = (int64_t)1 << bits, each = (a.units + lanes - 1) / lanes;
+      if (each > most && bits < 6) break;
+      if (each * lanes <= least) {
+        least = each * lanes;
+        a.lane_bits = bits;
+        per = (int)std::min<int64_t>(each, most);
+      }
     }
+  };
+  auto go = [&](auto kern) {
     const int rows = kEmbedThreads >> a.lane_bits, width = per << a.lane_bits;
     const dim3 grid((unsigned)((a.N + rows - 1) / rows), (a.units + width - 1) / width);
-    if (few)
-      one<<<grid, kEmbedThreads, 0, st>>>(a);
-    else
-      more<<<grid, kEmbedThreads, 0, st>>>(a);
+    kern<<<grid, kEmbedThreads, 0, st>>>(a);
     return api_launched(1);
   };
-  if (a.m == 1) return go(embed_kernel<T, kVec, 1, 1>, embed_kernel<T, kVec, 1, 4>, 4);
-  if (a.m == 2) return go(embed_kernel<T, kVec, 2, 1>, embed_kernel<T, kVec, 2, 4>, 4);
-  if (a.m <= 4) return go(embed_kernel<T, kVec, 4, 1>, embed_kernel<T, kVec, 4, 2>, 2);
-  return go(embed_kernel<T, kVec, kMaxTopM, 1>, embed_kernel<T, kVec, kMaxTopM, 1>, 1);
+  shape(few ? 1 : a.m <= 2 ? 4 : a.m <= 4 ? 2 : 1);
+  if (a.m == 1)
+    return per == 1   ? go(embed_kernel<T, kMode, 1, 1>)
+           : per == 2 ? go(embed_kernel<T, kMode, 1, 2>)
+           : per == 3 ? go(embed_kernel<T, kMode, 1, 3>)
+                      : go(embed_kernel<T, kMode, 1, 4>);
+  if (a.m == 2)
+    return per == 1   ? go(embed_kernel<T, kMode, 2, 1>)
+           : per == 2 ? go(embed_kernel<T, kMode, 2, 2>)
+           : per == 3 ? go(embed_kernel<T, kMode, 2, 3>)
+                      : go(embed_kernel<T, kMode, 2, 4>);
+  if (a.m <= 4)
+    return per == 1 ? go(embed_kernel<T, kMode, 4, 1>) : go(embed_kernel<T, kMode, 4, 2>);
+  return go(embed_kernel<T, kMode, kMaxTopM, 1>);
 }
 
 template <typename T>
 gmm_status embed_vec(const EmbedArgs& a, cudaStream_t st) {
-  return aligned_rows(a.W, a.ldw, sizeof(T)) && aligned_rows(a.Y, a.ldy, sizeof(T))
-             ? embed_launch<T, true>(a, st)
-             : embed_launch<T, false>(a, st);
+  const bool aligned = aligned_rows(a.W, a.ldw, sizeof(T)) && aligned_rows(a.Y, a.ldy, sizeof(T));
+  const int mode = unit_mode<T>(aligned, a.D);
+  return mode == 0   ? embed_launch<T, 0>(a, st)
+         : mode == 1 ? embed_launch<T, 1>(a, st)
+                     : embed_launch<T, 2>(a, st);
 }
 
 // ---------------------------------------------------------------- the gradient
@@ -135,11 +153,21 @@ bool cluster_size(int* C) {
   return true;
 }
 
-// Choices per chunk.  More, and fewer runs are cut; fewer, and there are more CTAs.
-uint32_t grad_chunk(uint32_t M) {
-  uint32_t c = 16;
-  while (c < kGradChunk && M / c > 4096) c *= 2;
-  return c;
+// Lanes of a group of the sums, for rows of so many units.
+int grad_lanes(int units) {
+  int lanes = 8;
+  while (lanes < kEmbedThreads && lanes < units) lanes *= 2;
+  return lanes;
+}
+
+// Choices per chunk: as few as leave no more CTAs than are resident at once (3 on each of 148 SMs),
+// between 16 and 128.  (131,072 x 2,048 bf16 from 16,384 choices: 122 us in chunks of 16, 2.3
+// turns of the CTAs, 116 in chunks of 40.)
+uint32_t grad_chunk(const gmm_embed_problem* p, uint32_t M) {
+  const int units = (int)((p->D * elem(p->dtype) + 15) / 16), lanes = grad_lanes(units);
+  const uint64_t slices = (units + lanes - 1) / lanes, groups = kEmbedThreads / lanes;
+  const uint64_t most = std::max<uint64_t>(1, 3 * 148 * groups / slices);
+  return (uint32_t)std::min<uint64_t>(kGradChunk, std::max<uint64_t>(16, (M / most + 8) / 8 * 8));
 }
 
 // Workspace: two buffers of sorted classes and their places, counts, cut sums.
@@ -161,7 +189,7 @@ GradLayout grad_layout(const gmm_embed_problem* p) {
   };
   for (int i = 0; i < 2; i++) L.list[i] = take((size_t)M * sizeof(Choice));
   L.counts = take(((size_t)s.tiles << s.bits) * 4);
-  L.chunk = grad_chunk(M);
+  L.chunk = grad_chunk(p, M);
   L.chunks = M / L.chunk + (M % L.chunk != 0);
   L.width = (p->D + 7) / 8 * 8;
   L.part = take((size_t)L.chunks * 2 * L.width * 4);
@@ -237,10 +265,10 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const
 }
 
 // `first`: nothing of this call is before it in the stream (it does not wait at its start).
-template <typename T, bool kVec>
+template <typename T, int kMode>
 gmm_status dot_launch(const GradCall& g, bool first) {
   const gmm_embed_problem* p = g.p;
-  constexpr int V = Unit<T, kVec>::n;
+  constexpr int V = Unit<T, kMode>::n;
   EmbedDotArgs a = {g.W,  g.dY, g.idx, g.dresp, p->N, p->ldw, p->ldy,
                     p->m, p->K, p->D,  (p->D + V - 1) / V, p->scale, g.flags};
   int sms = 0;
@@ -254,21 +282,24 @@ gmm_status dot_launch(const GradCall& g, bool first) {
     return api_launched(1);
   };
   if (a.units <= 64) {  // 8 lanes of up to 8 units: 4 rows per warp
-    if (p->m == 1) return go(embed_dot_kernel<T, kVec, 8, 1>, 8);
-    if (p->m == 2) return go(embed_dot_kernel<T, kVec, 8, 2>, 8);
-    return go(embed_dot_kernel<T, kVec, 8, kMaxTopM>, 8);
+    if (p->m == 1) return go(embed_dot_kernel<T, kMode, 8, 1>, 8);
+    if (p->m == 2) return go(embed_dot_kernel<T, kMode, 8, 2>, 8);
+    return go(embed_dot_kernel<T, kMode, 8, kMaxTopM>, 8);
   }
-  if (p->m == 1) return go(embed_dot_kernel<T, kVec, 32, 1>, 32);
-  if (p->m == 2) return go(embed_dot_kernel<T, kVec, 32, 2>, 32);
-  return go(embed_dot_kernel<T, kVec, 32, kMaxTopM>, 32);
+  if (p->m == 1) return go(embed_dot_kernel<T, kMode, 32, 1>, 32);
+  if (p->m == 2) return go(embed_dot_kernel<T, kMode, 32, 2>, 32);
+  return go(embed_dot_kernel<T, kMode, 32, kMaxTopM>, 32);
 }
 
 template <typename T>
 gmm_status dot_vec(const GradCall& g, bool first) {
   if (!g.dresp || g.p->N == 0) return GMM_OK;
-  return aligned_rows(g.W, g.p->ldw, sizeof(T)) && aligned_rows(g.dY, g.p->ldy, sizeof(T))
-             ? dot_launch<T, true>(g, first)
-             : dot_launch<T, false>(g, first);
+  const bool aligned =
+      aligned_rows(g.W, g.p->ldw, sizeof(T)) && aligned_rows(g.dY, g.p->ldy, sizeof(T));
+  const int mode = unit_mode<T>(aligned, g.p->D);
+  return mode == 0   ? dot_launch<T, 0>(g, first)
+         : mode == 1 ? dot_launch<T, 1>(g, first)
+                     : dot_launch<T, 2>(g, first);
 }
 
 gmm_status fill_launch(const GradCall& g, size_t size) {
@@ -285,12 +316,12 @@ gmm_status fill_launch(const GradCall& g, size_t size) {
 }
 
 // Stream order: the sort; beside it the weights' gradient and rows of zeros; then the sums.
-template <typename T, typename TO, bool kVec>
+template <typename T, typename TO, int kMode>
 gmm_status grad_launch(const GradCall& g) {
   const gmm_embed_problem* p = g.p;
   const GradLayout L = grad_layout(p);
   const uint32_t M = (uint32_t)(p->N * p->m);
-  constexpr int V = Unit<T, kVec>::n;
+  constexpr int V = Unit<T, kMode>::n;
   EmbedGradArgs a = {};
   gmm_status s;
   if ((s = sort_launch(g, L, M, &a.list)) != GMM_OK) return s;
@@ -310,30 +341,36 @@ gmm_status grad_launch(const GradCall& g) {
   a.K = p->K;
   a.D = p->D;
   a.units = (p->D + V - 1) / V;
-  a.lanes = 8;
-  while (a.lanes < kEmbedThreads && a.lanes < a.units) a.lanes *= 2;
+  a.lanes = grad_lanes(a.units);
   a.width = L.width;
   a.scale = p->scale;
   a.m = p->m;
   a.add = g.add;
   const unsigned groups = kEmbedThreads / a.lanes;
   const dim3 grid((a.chunks + groups - 1) / groups, (a.units + a.lanes - 1) / a.lanes);
-  if ((s = api_launch_next(embed_sum_kernel<T, TO, kVec>, grid, kEmbedThreads,
+  if ((s = api_launch_next(embed_sum_kernel<T, TO, kMode>, grid, kEmbedThreads,
                            (size_t)groups * a.chunk * 12, g.st, a)) != GMM_OK)
     return s;
   constexpr int kWarps = kEmbedThreads / 32;
-  return api_launch_next(embed_join_kernel<T, TO, kVec>,
+  return api_launch_next(embed_join_kernel<T, TO, kMode>,
                          dim3((a.chunks + kWarps - 1) / kWarps, (a.units + 31) / 32),
                          kEmbedThreads, 0, g.st, a);
+}
+
+template <typename T, typename TO>
+gmm_status grad_vec(const GradCall& g) {
+  const bool aligned = aligned_rows(g.dY, g.p->ldy, sizeof(T)) &&
+                       aligned_rows(g.dW, g.ldd, sizeof(TO));
+  const int mode = unit_mode<T>(aligned, g.p->D);
+  return mode == 0   ? grad_launch<T, TO, 0>(g)
+         : mode == 1 ? grad_launch<T, TO, 1>(g)
+                     : grad_launch<T, TO, 2>(g);
 }
 
 template <typename T>
 gmm_status grad_types(const GradCall& g, bool wide) {
   if (!g.dW) return dot_vec<T>(g, true);
-  const bool vec = aligned_rows(g.dY, g.p->ldy, sizeof(T)) &&
-                   aligned_rows(g.dW, g.ldd, wide ? sizeof(float) : sizeof(T));
-  if (wide) return vec ? grad_launch<T, float, true>(g) : grad_launch<T, float, false>(g);
-  return vec ? grad_launch<T, T, true>(g) : grad_launch<T, T, false>(g);
+  return wide ? grad_vec<T, float>(g) : grad_vec<T, T>(g);
 }
 
 }  // namespace

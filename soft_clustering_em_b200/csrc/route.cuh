@@ -56,6 +56,14 @@ __device__ __forceinline__ int segment_of(const int32_t* offsets, int S, int64_t
 // lse^2 and the number of rows.
 __host__ __device__ __forceinline__ int64_t route_slot(int K) { return 2 * (int64_t)K + 2; }
 
+// Vector k0 of a row of K classes, masked classes behind its end.  kMode: the row's entries one by one
+// (0); 16 bytes, the last vector perhaps a part (1) or whole (2: K is a multiple).
+template <typename T, int kMode>
+__device__ __forceinline__ uint4 route_vec(const T* row, int k0, int K) {
+  if constexpr (kMode < 2) return load_row_vec<T, kMode == 1>(row, k0, K);
+  return k0 < K ? load16(row + k0) : Vec16<T>::neg_inf();
+}
+
 // The exponentials of a row relative to its largest logit.
 template <int kLanes, int kEl, typename T>
 struct RouteRow {
@@ -74,18 +82,24 @@ struct RouteRow {
     bad = !(z < INFINITY);
     empty = z == -INFINITY;
     ref = fmaxf(xm, -FLT_MAX);
-    const float c = scale * kLog2e;
-    S = 0.f;
+    const F2 c2 = f2(scale * kLog2e, scale * kLog2e), ref2 = f2(-ref, -ref);
+    F2 S2 = f2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < kChunks; v++) {
       float x[V];
       Vec16<T>::unpack(r[v], x);
 #pragma unroll
-      for (int e = 0; e < V; e++) {
-        y[v * V + e] = ex2((x[e] - ref) * c);
-        S += y[v * V + e];
+      for (int e = 0; e < V; e += 2) {
+        float t0, t1;
+        f2_get(f2_mul(f2_add(f2(x[e], x[e + 1]), ref2), c2), t0, t1);
+        y[v * V + e] = ex2(t0);
+        y[v * V + e + 1] = ex2(t1);
+        S2 = f2_add(S2, f2(y[v * V + e], y[v * V + e + 1]));
       }
     }
+    float s0, s1;
+    f2_get(S2, s0, s1);
+    S = s0 + s1;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
   }
@@ -103,7 +117,7 @@ __device__ __forceinline__ float group_sum(float v) {
 // A CTA takes `rows` rows.  For each segment that they meet, in order, column sums stay in
 // registers until the segment or the rows end; the sums of piece (CTA c, segment s) go to slot
 // c + s, which no other piece has: from piece to piece c or s grows, or both.
-template <typename T, int kLanes, int kEl, bool kVec>
+template <typename T, int kLanes, int kEl, int kMode>
 __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_load_kernel(RouteArgs a, float* part) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
@@ -130,25 +144,34 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_load_k
     float acc[kEl] = {};
     float zs = 0.f;
     uint32_t live_rows = 0;
-    for (int64_t n0 = lo + w * kRows; n0 < hi; n0 += kRouteWarps * kRows) {
+    uint4 next[kChunks];  // the rows after these are on their way
+    int next_k = -1;
+    bool next_out = false;
+    auto fetch = [&](int64_t n0) {
       const int64_t n = n0 + lane / kLanes;
       const bool in = n < hi;
       const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
-      uint4 r[kChunks];
 #pragma unroll
       for (int c = 0; c < kChunks; c++)
-        r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
-      const int k = in && l < a.m ? a.idx[n * a.m + l] : -1;
-      const bool out = !in || (a.mask && !a.mask[n]);
-      if (out) {  // as if all its classes were masked
+        next[c] = route_vec<T, kMode>(row, (c * kLanes + l) * V, a.K);
+      next_k = in && l < a.m ? a.idx[n * a.m + l] : -1;
+      next_out = !in || (a.mask && !a.mask[n]);
+    };
+    if (lo + w * kRows < hi) fetch(lo + w * kRows);
+    for (int64_t n0 = lo + w * kRows; n0 < hi; n0 += kRouteWarps * kRows) {
+      uint4 r[kChunks];
 #pragma unroll
-        for (int c = 0; c < kChunks; c++) r[c] = Vec16<T>::neg_inf();
-      }
+      for (int c = 0; c < kChunks; c++)  // (a row that is out: as if all its classes were masked)
+        r[c] = next_out ? Vec16<T>::neg_inf() : next[c];
+      const int k = next_k;
+      if (n0 + kRouteWarps * kRows < hi) fetch(n0 + kRouteWarps * kRows);
       RouteRow<kLanes, kEl, T> q;
       q.make(r, a.scale);
       const float inv = q.empty ? 0.f : 1.f / q.S;
+      const F2 inv2 = f2(inv, inv);
 #pragma unroll
-      for (int e = 0; e < kEl; e++) acc[e] = fmaf(q.y[e], inv, acc[e]);
+      for (int e = 0; e < kEl; e += 2)
+        f2_get(f2_fma(f2(q.y[e], q.y[e + 1]), inv2, f2(acc[e], acc[e + 1])), acc[e], acc[e + 1]);
       if (!q.empty) {
         if (l == 0) {
           const float z = q.lse(a.scale);
@@ -214,13 +237,13 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
   const int s = blockIdx.x / ctas;
   const int groups = kReduceThreads / cols, g = t / cols, col = t & (cols - 1);
-  grid_dependency_wait();
-  grid_dependents_launch();
   int64_t lo = 0, hi = a.N;
-  if (a.offsets) {
+  if (a.offsets) {  // (from before the kernel that leaves the sums)
     lo = a.offsets[s];
     hi = a.offsets[s + 1];
   }
+  grid_dependency_wait();
+  grid_dependents_launch();
   const bool legal = lo >= 0 && lo <= hi && hi <= a.N;
   if (!legal && t == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
   const int64_t size = route_slot(a.K);
@@ -305,7 +328,7 @@ struct RouteGradArgs {
 
 // A warp takes `rows` consecutive rows, 32 / kLanes at a time; the counts of the segment stay in
 // registers while it lasts.
-template <typename T, int kLanes, int kEl, bool kVec>
+template <typename T, int kLanes, int kEl, int kMode>
 __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_kernel(RouteGradArgs g) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
@@ -321,24 +344,39 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
   float coef = 0.f, pull = 0.f;
 #pragma unroll
   for (int e = 0; e < kEl; e++) cnt[e] = 0.f;
+  uint4 next[kChunks];  // the rows after these are on their way
+  int next_k = -1;
+  float next_d = 0.f;
+  bool next_out = false;
+  auto fetch = [&](int64_t n0) {
+    const int64_t n = n0 + lane / kLanes;
+    const bool in = n < r1;
+    const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
+#pragma unroll
+    for (int c = 0; c < kChunks; c++)
+      next[c] = route_vec<T, kMode>(row, (c * kLanes + l) * V, a.K);
+    next_k = -1;
+    if (g.dresp && in && l < a.m) {
+      next_k = a.idx[n * a.m + l];
+      next_d = g.dresp[n * a.m + l];
+    }
+    next_out = a.mask && in && !a.mask[n];
+  };
+  fetch(r0);
   for (int64_t n0 = r0; n0 < r1; n0 += kRows) {
     const int64_t n = n0 + lane / kLanes;
     const bool in = n < r1;
     const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
     uint4 r[kChunks];
 #pragma unroll
-    for (int c = 0; c < kChunks; c++)
-      r[c] = load_row_vec<T, kVec>(row, (c * kLanes + l) * V, a.K);
-    int k = -1;
-    float d = 0.f;
-    if (g.dresp && in && l < a.m) {
-      k = a.idx[n * a.m + l];
-      d = g.dresp[n * a.m + l];
-    }
+    for (int c = 0; c < kChunks; c++) r[c] = next[c];
+    const int k = next_k;
+    const float d = next_d;
+    bool counts = losses && in && !next_out;
     const bool legal = (unsigned)k < (unsigned)a.K;
     if (!legal && k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
     const float xk = legal ? to_f32(row[k]) : -INFINITY;
-    bool counts = losses && in && !(a.mask && !a.mask[n]);
+    if (n0 + kRows < r1) fetch(n0 + kRows);
     if (counts && a.offsets) {
       while (s + 1 < a.S && n >= a.offsets[s + 1]) s++;
       counts = n >= a.offsets[s] && n < a.offsets[s + 1];
@@ -368,25 +406,40 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
     const float wd = legal ? wk * d : 0.f;
     const float R = group_sum<kLanes>(wd);
     const float add = g.renorm ? fmaf(-wk, R, wd) : wd;
-    float dot = 0.f;
+    F2 dot2 = f2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < kEl; e++) dot = fmaf(q.y[e], cnt[e], dot);
-    dot = group_sum<kLanes>(dot) * inv;
+    for (int e = 0; e < kEl; e += 2)
+      dot2 = f2_fma(f2(q.y[e], q.y[e + 1]), f2(cnt[e], cnt[e + 1]), dot2);
+    float dot, dot1;
+    f2_get(dot2, dot, dot1);
+    dot = group_sum<kLanes>(dot + dot1) * inv;
     const float cf = counts ? coef : 0.f;
     const float base = (counts ? pull * q.lse(a.scale) - coef * dot : 0.f) - (g.renorm ? 0.f : R);
     const bool chosen = __ballot_sync(0xffffffffu, legal) >> (lane - l) & group_mask<kLanes>();
     const bool live = !q.empty && (counts || chosen);
     if (q.bad && live && l == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
-    // (a row with a NaN is NaN throughout, also where only some classes are pulled on)
-    const float nan = q.bad ? __int_as_float(0x7fffffff) : 0.f;
+    // (a row with a NaN is NaN throughout: so is the sum of its exponentials)
+    const F2 to2 = f2(inv * a.scale, inv * a.scale), cf2 = f2(cf, cf), base2 = f2(base, base);
 #pragma unroll
-    for (int e = 0; e < kEl; e++) q.y[e] = q.y[e] * inv * fmaf(cf, cnt[e], base) + nan;
+    for (int e = 0; e < kEl; e += 2)
+      f2_get(f2_mul(f2_mul(f2(q.y[e], q.y[e + 1]), to2),
+                    f2_fma(cf2, f2(cnt[e], cnt[e + 1]), base2)),
+             q.y[e], q.y[e + 1]);
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < kEl; e++) q.y[e] = 0.f;
+    }
     // what a chosen class gets beside that, from every choice that names it
-    float more = 0.f;
-    for (int j = 0; j < (g.dresp ? a.m : 0); j++) {
-      const int kj = __shfl_sync(0xffffffffu, k, (lane - l) + j);
-      const float aj = __shfl_sync(0xffffffffu, add, (lane - l) + j);
-      if (kj == k) more += aj;
+    float more = add;
+    const uint32_t same = __match_any_sync(
+        0xffffffffu, legal ? (lane - l) << 16 | k : -1 - lane);  // (K is below 2^16)
+    if (__any_sync(0xffffffffu, (same & (same - 1u)) != 0u)) {  // a class named twice
+      more = 0.f;
+      for (int j = 0; j < a.m; j++) {
+        const int kj = __shfl_sync(0xffffffffu, k, (lane - l) + j);
+        const float aj = __shfl_sync(0xffffffffu, add, (lane - l) + j);
+        if (kj == k) more += aj;
+      }
     }
     __syncwarp();
     T* out = (T*)g.dZ + (in ? n : n0) * g.ldd;
@@ -394,9 +447,11 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
     for (int v = 0; v < kChunks; v++) {
       float x[V];
 #pragma unroll
-      for (int e = 0; e < V; e++) x[e] = live ? q.y[v * V + e] * a.scale : 0.f;
+      for (int e = 0; e < V; e++) x[e] = q.y[v * V + e];
       const int k0 = (v * kLanes + l) * V;
-      if (kVec && in && k0 + V <= a.K) {
+      if constexpr (kMode == 2) {
+        if (in && k0 < a.K) *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
+      } else if (kMode == 1 && in && k0 + V <= a.K) {
         *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
       } else {
 #pragma unroll
@@ -409,7 +464,7 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
     if (legal && live) {
       const float ck = counts && g.dbalance ? (float)g.counts[(int64_t)s * a.K + k] : 0.f;
       const float pk = ex2((xk - q.ref) * c) * inv;
-      from_f32(out + k, (fmaf(pk, fmaf(cf, ck, base), more) + nan) * a.scale);
+      from_f32(out + k, fmaf(pk, fmaf(cf, ck, base), more) * a.scale);
     }
   }
 }

@@ -45,52 +45,59 @@ size_t loss_bytes(const gmm_rows* r, int32_t S) {
   return (size_t)(loss_plan(r->N).chunks + std::max(S, 1)) * route_slot(r->K) * 4;
 }
 
+// How rows of K classes are taken (route_vec).
+template <typename T>
+int route_mode(bool aligned, int K) {
+  return !aligned ? 0 : K % Vec16<T>::n != 0 ? 1 : 2;
+}
+
 template <typename T, int kLanes, int kEl>
-gmm_status load_launch(const RouteArgs& a, float* part, bool vec, unsigned grid, cudaStream_t st) {
-  if (vec)
-    route_load_kernel<T, kLanes, kEl, true><<<grid, kRouteThreads, 0, st>>>(a, part);
-  else
-    route_load_kernel<T, kLanes, kEl, false><<<grid, kRouteThreads, 0, st>>>(a, part);
+gmm_status load_launch(const RouteArgs& a, float* part, int mode, unsigned grid, cudaStream_t st) {
+  auto kern = mode == 0   ? route_load_kernel<T, kLanes, kEl, 0>
+              : mode == 1 ? route_load_kernel<T, kLanes, kEl, 1>
+                          : route_load_kernel<T, kLanes, kEl, 2>;
+  kern<<<grid, kRouteThreads, 0, st>>>(a, part);
   return api_launched(1);
 }
 
 // Lanes and places per row: up to 16 places, so that three CTAs are resident.
 template <typename T>
 gmm_status load_dispatch(const RouteArgs& a, float* part, unsigned grid, cudaStream_t st) {
-  const bool vec = (uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0;
-  if (a.K <= 64) return load_launch<T, 8, 8>(a, part, vec, grid, st);
-  if (a.K <= 128) return load_launch<T, 8, 16>(a, part, vec, grid, st);
-  if (a.K <= 256) return load_launch<T, 16, 16>(a, part, vec, grid, st);
-  if (a.K <= 512) return load_launch<T, 32, 16>(a, part, vec, grid, st);
-  return load_launch<T, 32, 32>(a, part, vec, grid, st);
+  const int mode = route_mode<T>((uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0, a.K);
+  if (a.K <= 64) return load_launch<T, 8, 8>(a, part, mode, grid, st);
+  if (a.K <= 128) return load_launch<T, 8, 16>(a, part, mode, grid, st);
+  if (a.K <= 256) return load_launch<T, 16, 16>(a, part, mode, grid, st);
+  if (a.K <= 512) return load_launch<T, 32, 16>(a, part, mode, grid, st);
+  return load_launch<T, 32, 32>(a, part, mode, grid, st);
 }
 
 template <typename T, int kLanes, int kEl>
-gmm_status grad_launch(RouteGradArgs g, bool vec, cudaStream_t st) {
+gmm_status grad_launch(RouteGradArgs g, int mode, cudaStream_t st) {
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
   constexpr int kRows = 32 / kLanes;
-  const int64_t warps = std::min<int64_t>((g.r.N + kRows - 1) / kRows, (int64_t)sms * 16);
+  const int64_t warps = std::min<int64_t>((g.r.N + kRows - 1) / kRows, (int64_t)sms * kRouteWarps * (kEl <= 16 ? 3 : 2));
   g.r.rows = ((g.r.N + warps - 1) / warps + kRows - 1) / kRows * kRows;
   const unsigned grid =
       (unsigned)((g.r.N + g.r.rows * kRouteWarps - 1) / (g.r.rows * kRouteWarps));
-  if (vec)
-    route_grad_kernel<T, kLanes, kEl, true><<<grid, kRouteThreads, 0, st>>>(g);
-  else
-    route_grad_kernel<T, kLanes, kEl, false><<<grid, kRouteThreads, 0, st>>>(g);
+  auto kern = mode == 0   ? route_grad_kernel<T, kLanes, kEl, 0>
+              : mode == 1 ? route_grad_kernel<T, kLanes, kEl, 1>
+                          : route_grad_kernel<T, kLanes, kEl, 2>;
+  kern<<<grid, kRouteThreads, 0, st>>>(g);
   return api_launched(1);
 }
 
 template <typename T>
 gmm_status grad_dispatch(const RouteGradArgs& g, cudaStream_t st) {
-  const bool vec = (uintptr_t)g.r.Z % 16 == 0 && g.r.ld * sizeof(T) % 16 == 0 &&
-                   (uintptr_t)g.dZ % 16 == 0 && g.ldd * sizeof(T) % 16 == 0;
-  if (g.r.K <= 64) return grad_launch<T, 8, 8>(g, vec, st);
-  if (g.r.K <= 128) return grad_launch<T, 8, 16>(g, vec, st);
-  if (g.r.K <= 256) return grad_launch<T, 16, 16>(g, vec, st);
-  if (g.r.K <= 512) return grad_launch<T, 32, 16>(g, vec, st);
-  return grad_launch<T, 32, 32>(g, vec, st);
+  const int mode = route_mode<T>((uintptr_t)g.r.Z % 16 == 0 && g.r.ld * sizeof(T) % 16 == 0 &&
+                                     (uintptr_t)g.dZ % 16 == 0 && g.ldd * sizeof(T) % 16 == 0,
+                                 g.r.K);
+  if (g.r.K <= 64) return grad_launch<T, 8, 8>(g, mode, st);
+  if (g.r.K <= 128) return grad_launch<T, 8, 16>(g, mode, st);
+  if (g.r.K <= 256) return grad_launch<T, 16, 16>(g, mode, st);
+  if (g.r.K <= 512) return grad_launch<T, 32, 16>(g, mode, st);
+  return grad_launch<T, 32, 32>(g, mode, st);
 }
 
 }  // namespace

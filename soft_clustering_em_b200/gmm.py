@@ -7,6 +7,7 @@ does no arithmetic of its own.  The library must be built
 raises -- there is no fallback implementation.
 """
 import ctypes
+import functools
 import os
 import struct
 from typing import NamedTuple, Optional
@@ -664,9 +665,21 @@ def _bytes(size_fn, what, *args):
     return int(n.value)
 
 
-def _workspace(ws, size, device):
-    """A workspace of `size` bytes, allocated when ws is None."""
-    return torch.empty(size(), dtype=torch.uint8, device=device) if ws is None else ws
+@functools.lru_cache(maxsize=4096)
+def _route_loss_bytes(N, K, S):
+    return _bytes(load_library().gmm_route_loss_workspace_size, "gmm_route_loss_workspace_size",
+                  ctypes.byref(gmm_rows(N, K, K, GMM_F32, 1.0)), S)
+
+
+@functools.lru_cache(maxsize=4096)
+def _embed_bytes(N, m, K, D, dtype):
+    return gmm_embed_workspace_size(gmm_embed_problem(N, m, K, D, dtype, 1.0, D, D))
+
+
+@functools.lru_cache(maxsize=4096)
+def _beam_bytes(N, w, m):
+    return _bytes(load_library().gmm_beam_workspace_size, "gmm_beam_workspace_size",
+                  ctypes.byref(gmm_rows(N, 1, 1, GMM_F32, 1.0)), w, m)
 
 
 def gmm_route_loss(Z, idx, offsets=None, mask=None, scale=1.0, ws=None, dev_flags=None,
@@ -688,24 +701,25 @@ def gmm_route_loss(Z, idx, offsets=None, mask=None, scale=1.0, ws=None, dev_flag
     _same_device(Z, idx, offsets, mask, ws, dev_flags)
     S = _segments(Z, idx, mask, offsets)
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
-    K = Z.shape[1]
-    real = torch.empty(S * (K + 2), dtype=torch.float32, device=Z.device)
-    whole = torch.empty(S * (K + 1), dtype=torch.int32, device=Z.device)
-    ws = _workspace(ws, lambda: gmm_route_loss_workspace_size(Z, S, scale), Z.device)
-    at, wh = real.data_ptr(), whole.data_ptr()
-    _launch(load_library().gmm_route_loss, "gmm_route_loss", Z.device, ctypes.byref(r),
+    N, K = Z.shape
+    device = Z.device
+    if ws is None:
+        ws = torch.empty(_route_loss_bytes(N, K, S), dtype=torch.uint8, device=device)
+    balance = torch.empty(S, dtype=torch.float32, device=device)
+    z = torch.empty(S, dtype=torch.float32, device=device)
+    load = torch.empty(S, K, dtype=torch.float32, device=device)
+    counts = torch.empty(S, K, dtype=torch.int32, device=device)
+    rows = torch.empty(S, dtype=torch.int32, device=device)
+    _launch(load_library().gmm_route_loss, "gmm_route_loss", device, ctypes.byref(r),
             Z.data_ptr(), idx.data_ptr(), idx.shape[1], _address(mask), _address(offsets), S,
-            at + 4 * S * K, at + 4 * S * (K + 1), at, wh, wh + 4 * S * K, _address(dev_flags),
-            ws.data_ptr(), ws.numel())
-    load, balance, z = real.split((S * K, S, S))
-    counts, rows = whole.split((S * K, S))
-    return RouteLoss(balance, z, load.view(S, K), counts.view(S, K), rows)
+            balance.data_ptr(), z.data_ptr(), load.data_ptr(), counts.data_ptr(), rows.data_ptr(),
+            _address(dev_flags), ws.data_ptr(), ws.numel())
+    return RouteLoss(balance, z, load, counts, rows)
 
 
-def gmm_route_loss_workspace_size(Z, S=1, scale=1.0) -> int:
-    """Bytes of gmm_route_loss's workspace for logits like Z and S segments."""
-    return _bytes(load_library().gmm_route_loss_workspace_size, "gmm_route_loss_workspace_size",
-                  ctypes.byref(_rows(Z, scale)), S)
+def gmm_route_loss_workspace_size(Z, S=1) -> int:
+    """Bytes of gmm_route_loss's workspace for N x K logits like Z and S segments."""
+    return _route_loss_bytes(*Z.shape, S)
 
 
 def gmm_route_backward(Z, idx, dresp=None, renorm=False, counts=None, rows=None, dbalance=None,
@@ -831,7 +845,8 @@ def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accum
         raise ValueError("out must be K x D of dY's type or float32")
     dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=dY.device)
     p = embed_problem(idx, K, scale, D if W is None else _ld(W, "W"), dY)
-    ws = _workspace(ws, lambda: gmm_embed_workspace_size(p), dY.device)
+    if ws is None:
+        ws = torch.empty(_embed_bytes(N, p.m, K, D, p.dtype), dtype=torch.uint8, device=dY.device)
     _launch(load_library().gmm_embed_backward, "gmm_embed_backward", dY.device, ctypes.byref(p),
             dY.data_ptr(), idx.data_ptr(), _address(resp), _address(W), out.data_ptr(),
             _DTYPES[out.dtype], _ld(out, "out"), int(bool(accumulate)), _address(dresp),
@@ -847,10 +862,9 @@ class BeamStep(NamedTuple):
     token: torch.Tensor   # B x m int32
 
 
-def gmm_beam_workspace_size(Z, w, m, scale=1.0) -> int:
+def gmm_beam_workspace_size(Z, w, m) -> int:
     """Bytes of gmm_beam_select's workspace for logits like Z, w beams and m candidates."""
-    return _bytes(load_library().gmm_beam_workspace_size, "gmm_beam_workspace_size",
-                  ctypes.byref(_rows(Z, scale)), w, m)
+    return _beam_bytes(Z.shape[0], w, m)
 
 
 def gmm_beam_select(Z, scores, m=None, ended=None, end_id=0, scale=1.0, ws=None, dev_flags=None,
@@ -877,9 +891,12 @@ def gmm_beam_select(Z, scores, m=None, ended=None, end_id=0, scale=1.0, ws=None,
         _vector(ended, (B, w), torch.bool if ended.dtype == torch.bool else torch.uint8, "ended")
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
     m = w if m is None else int(m)
-    ws = _workspace(ws, lambda: gmm_beam_workspace_size(Z, w, m, scale), Z.device)
-    out = torch.empty(B, m, dtype=torch.float32, device=Z.device)
-    parent, token = torch.empty(2, B, m, dtype=torch.int32, device=Z.device).unbind(0)
+    device = Z.device
+    if ws is None:
+        ws = torch.empty(_beam_bytes(Z.shape[0], w, m), dtype=torch.uint8, device=device)
+    out = torch.empty(B, m, dtype=torch.float32, device=device)
+    parent = torch.empty(B, m, dtype=torch.int32, device=device)
+    token = torch.empty(B, m, dtype=torch.int32, device=device)
     _launch(load_library().gmm_beam_select, "gmm_beam_select", Z.device, ctypes.byref(r),
             Z.data_ptr(), w, scores.data_ptr(), _address(ended), int(end_id), m, out.data_ptr(),
             parent.data_ptr(), token.data_ptr(), _address(dev_flags), ws.data_ptr(), ws.numel())
