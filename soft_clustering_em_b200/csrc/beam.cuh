@@ -40,39 +40,28 @@ __device__ __forceinline__ double order_double(uint64_t o) {
                 : __longlong_as_double((long long)(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
 }
 
-// A warp per group, a lane per beam.  Scores are 64 bits wide: those of different rows lie close
-// together, and in 32 bits a log p of -15 is rounded by 5e-7.  A row's first log p is the
-// smallest in size and so the most exact one; the others stand as far behind it as their logits.
-// Equal scores go to the lower beam, then in the order of the row.
+// A CTA per group: its threads form the candidates' scores, a warp with a lane per beam merges them.
+// Scores are 64 bits wide: those of different rows lie close together, and in 32 bits a log p of
+// -15 is rounded by 5e-7.  A row's first log p is the smallest in size and so the most exact one;
+// the others stand as far behind it as their logits.  Equal scores go to the lower beam, then in
+// the order of the row.
+constexpr int kMergeThreads = 128;
 template <typename T>
-__global__ void beam_merge_kernel(BeamArgs a) {
-  extern __shared__ uint64_t beam_cand[];  // [warp][w][m]
-  const int lane = threadIdx.x & 31;
-  const int64_t b = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-  uint64_t* cand = beam_cand + threadIdx.x / 32 * (a.w * a.m);
-  grid_dependents_launch();
-  grid_dependency_wait();
-  if (b >= a.B) return;
-  float score = -INFINITY, first = 0.f;
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
+  __shared__ uint64_t cand[kMostBeams * kMaxAlt];  // [beam][m]
+  const int t = threadIdx.x, lane = t & 31;
+  const int64_t b = blockIdx.x;
+  float score = -INFINITY;
   bool ended = false;
-  if (lane < a.w) {
+  if (lane < a.w) {  // (from before the kernel that finds the rows' best classes)
     score = a.scores[b * a.w + lane];
     ended = a.ended && a.ended[b * a.w + lane];
-    first = a.top_logp[(b * a.w + lane) * a.m];
   }
-  const bool dead = score == -INFINITY;
-  const bool bad = !(score < INFINITY) || (!dead && !ended && !(first == first));
-  if (__any_sync(0xffffffffu, bad)) {
-    if (lane == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
-    if (lane < a.m) {
-      a.out[b * a.m + lane] = __int_as_float(0x7fffffff);
-      a.parent[b * a.m + lane] = -1;
-      a.token[b * a.m + lane] = -1;
-    }
-    return;
-  }
-  for (int c0 = 0; c0 < a.w * a.m; c0 += 32) {
-    const int c = c0 + lane, i = min(c / a.m, a.w - 1), j = c % a.m;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const float first = lane < a.w ? a.top_logp[(b * a.w + lane) * a.m] : 0.f;
+  for (int c0 = 0; c0 < a.w * a.m; c0 += kMergeThreads) {
+    const int c = c0 + t, i = min(c / a.m, a.w - 1), j = c % a.m;
     const float s = __shfl_sync(0xffffffffu, score, i);
     const float lp = __shfl_sync(0xffffffffu, first, i);
     const bool e = __shfl_sync(0xffffffffu, (int)ended, i);
@@ -91,7 +80,19 @@ __global__ void beam_merge_kernel(BeamArgs a) {
     }
     cand[c] = key;
   }
-  __syncwarp();
+  __syncthreads();
+  if (t >= 32) return;
+  const bool dead = score == -INFINITY;
+  const bool bad = !(score < INFINITY) || (!dead && !ended && !(first == first));
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
+    if (lane < a.m) {
+      a.out[b * a.m + lane] = __int_as_float(0x7fffffff);
+      a.parent[b * a.m + lane] = -1;
+      a.token[b * a.m + lane] = -1;
+    }
+    return;
+  }
   int pos = 0, my_parent = -1, my_rank = 0;
   double my_score = -INFINITY;
   uint64_t head = lane < a.w ? cand[lane * a.m] : 0;

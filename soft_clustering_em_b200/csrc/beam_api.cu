@@ -20,9 +20,7 @@ gmm_status check_select(const gmm_rows* r, int32_t w, int32_t m) {
 
 template <typename T>
 gmm_status merge_launch(const BeamArgs& a, cudaStream_t st) {
-  const int warps = a.w * a.m > 256 ? 1 : 4;
-  return api_launch_next(beam_merge_kernel<T>, dim3((unsigned)((a.B + warps - 1) / warps)),
-                         32 * warps, (size_t)warps * a.w * a.m * 8, st, a);
+  return api_launch_next(beam_merge_kernel<T>, dim3((unsigned)a.B), kMergeThreads, 0, st, a);
 }
 
 // As many CTAs as are resident at once: each finds its tiles once.

@@ -224,15 +224,16 @@ struct RouteLossOut {
 
 // A cluster per segment adds up its slots, in order, in 64 bits; each CTA has a share of the
 // experts.  Threads: `cols` columns (a power of two) times groups that take every so many slots.
-constexpr int kReduceThreads = 512;
+constexpr int kReduceThreads = 1024;
 constexpr int kReduceWarps = kReduceThreads / 32;
+constexpr int kReduceCtas = 8;  // most
 __global__ void __launch_bounds__(kReduceThreads)
     route_reduce_kernel(RouteArgs a, const float* part, RouteLossOut o, int cols) {
   __shared__ double sh[kReduceThreads];
   __shared__ uint32_t shc[kReduceThreads];
-  __shared__ double zs[kReduceWarps];
+  __shared__ double zs[kReduceWarps], bs[kReduceWarps];
   __shared__ uint32_t rs[kReduceWarps];
-  __shared__ double mine;  // of balance, read by the cluster's first CTA
+  __shared__ double of_cta[kReduceCtas];  // balance of each CTA's experts, in the first CTA
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
   const int s = blockIdx.x / ctas;
@@ -256,16 +257,8 @@ __global__ void __launch_bounds__(kReduceThreads)
     z += part[q * size + 2 * a.K];
     n += reinterpret_cast<const uint32_t*>(part)[q * size + 2 * a.K + 1];
   }
-  z = warp_sum(z);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0) zs[w] = z, rs[w] = n;
-  __syncthreads();
-  z = 0.0;
-  n = 0;
-  for (int i = 0; i < kReduceWarps; i++) z += zs[i], n += rs[i];
-  const double L = n > 0 ? (double)n : 1.0;
-  double balance = 0.0;
-  for (int k0 = rank * cols; k0 < a.K; k0 += ctas * cols) {
+  double balance = 0.0, L = 1.0;
+  for (int k0 = rank * cols; k0 < a.K || k0 == rank * cols; k0 += ctas * cols) {
     const int k = k0 + col;
     double p = 0.0;
     uint32_t c = 0;
@@ -278,7 +271,18 @@ __global__ void __launch_bounds__(kReduceThreads)
     }
     sh[t] = p;
     shc[t] = c;
+    if (k0 == rank * cols) {
+      z = warp_sum(z);
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) zs[w] = z, rs[w] = n;
+    }
     __syncthreads();
+    if (k0 == rank * cols) {
+      z = 0.0;
+      n = 0;
+      for (int i = 0; i < kReduceWarps; i++) z += zs[i], n += rs[i];
+      L = n > 0 ? (double)n : 1.0;
+    }
     if (g == 0 && k < a.K) {
       for (int i = 1; i < groups; i++) p += sh[i * cols + col], c += shc[i * cols + col];
       if (o.load) o.load[(int64_t)s * a.K + k] = (float)(p / L);
@@ -288,31 +292,26 @@ __global__ void __launch_bounds__(kReduceThreads)
     __syncthreads();
   }
   balance = warp_sum(balance);
-  if (lane == 0) zs[w] = balance;
+  if (lane == 0) bs[w] = balance;
   __syncthreads();
   if (t == 0) {
     balance = 0.0;
-    for (int i = 0; i < kReduceWarps; i++) balance += zs[i];
-    mine = balance;
+    for (int i = 0; i < kReduceWarps; i++) balance += bs[i];
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                     sm100::map_to_rank(sm100::smem_u32(of_cta + rank), 0)),
+                 "d"(balance)
+                 : "memory");
   }
   __syncwarp();
   sm100::cluster_sync();
   if (rank == 0 && t == 0) {
-    for (int r = 1; r < ctas; r++) {
-      double v;
-      asm volatile("ld.shared::cluster.f64 %0, [%1];"
-                   : "=d"(v)
-                   : "r"(sm100::map_to_rank(sm100::smem_u32(&mine), r))
-                   : "memory");
-      balance += v;
-    }
+    balance = 0.0;
+    for (int r = 0; r < ctas; r++) balance += of_cta[r];
     const float nan = __int_as_float(0x7fffffff);
     if (o.balance) o.balance[s] = legal ? (float)(balance * a.K / (a.m * L * L)) : nan;
     if (o.z) o.z[s] = legal ? (float)(z / L) : nan;
     if (o.rows) o.rows[s] = (int32_t)n;
   }
-  __syncwarp();
-  sm100::cluster_sync();  // `mine` is read until here
 }
 
 // ------------------------------------------------------------------ gradient

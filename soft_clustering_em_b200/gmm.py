@@ -800,12 +800,13 @@ def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=Non
     _same_device(W, idx, resp, out, dev_flags)
     N = _choices(idx, resp)
     ldw = _ld(W, "W")
+    K, D = W.shape
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
     if out is None:
-        out = torch.empty(N, W.shape[1], dtype=W.dtype, device=W.device)
-    if out.dtype != W.dtype or out.shape != (N, W.shape[1]):
+        out = torch.empty(N, D, dtype=W.dtype, device=W.device)
+    elif out.dtype != W.dtype or out.shape != (N, D):
         raise ValueError("out must be N x D of W's type")
-    p = embed_problem(idx, W.shape[0], scale, ldw, out)
+    p = embed_problem(idx, K, scale, ldw, out)
     _launch(load_library().gmm_embed, "gmm_embed", W.device, ctypes.byref(p), W.data_ptr(),
             idx.data_ptr(), _address(resp), out.data_ptr(), _address(dev_flags))
     return out
@@ -906,14 +907,16 @@ def gmm_beam_select(Z, scores, m=None, ended=None, end_id=0, scale=1.0, ws=None,
 _STATE = struct.Struct("=6qi4x")  # gmm_beam_state
 
 
-def _state(t, rows, dim):
-    """A tensor of `rows` rows as gmm_beam_state; dim: the dimension of its positions."""
-    if t.dim() < 1 or t.shape[0] != rows:
-        raise ValueError(f"a state must have {rows} rows, got {tuple(t.shape)}")
-    size, shape, stride = t.element_size(), t.shape, t.stride()
+@functools.lru_cache(maxsize=4096)
+def _state_layout(shape, stride, size, rows, dim):
+    """A tensor's rows as gmm_beam_state, without the address; dim: that of its positions."""
+    if len(shape) < 1 or shape[0] != rows:
+        raise ValueError(f"a state must have {rows} rows, got {shape}")
+    if dim is not None and not 0 < dim < len(shape):
+        raise ValueError("dim must be a dimension of the state behind its rows")
     inner = 1 if dim is None else dim
     dense = 1  # elements of the dimensions behind, which must lie densely
-    for d in range(t.dim() - 1, inner - 1, -1):
+    for d in range(len(shape) - 1, inner - 1, -1):
         if shape[d] > 1 and stride[d] != dense:
             raise ValueError("a state must be dense from its positions on")
         dense *= shape[d]
@@ -927,8 +930,11 @@ def _state(t, rows, dim):
         outer *= shape[d]
     count = 1 if dim is None else shape[dim]
     per = dense // count if count else 0
-    return (t.data_ptr(), stride[0] * size, outer, outer_stride * size, count, per * size,
-            int(dim is not None))
+    return stride[0] * size, outer, outer_stride * size, count, per * size, int(dim is not None)
+
+
+def _state(t, rows, dim):
+    return (t.data_ptr(), *_state_layout(t.shape, t.stride(), t.element_size(), rows, dim))
 
 
 def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream=None):
@@ -954,9 +960,6 @@ def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream
     dims = list(dim) if isinstance(dim, (list, tuple)) else [dim] * len(states)
     if len(dims) != len(states):
         raise ValueError("dim must be one for each state")
-    for t, d in zip(states, dims):
-        if d is not None and not 0 < d < t.dim():
-            raise ValueError("dim must be a dimension of the state behind its rows")
     packed = b"".join([_STATE.pack(*_state(t, B * w, d)) for t, d in zip(states, dims)])
     _launch(load_library().gmm_beam_reorder, "gmm_beam_reorder", parent.device, B, w,
             parent.data_ptr(), _address(lens), len(states), packed, _address(dev_flags))
