@@ -142,11 +142,12 @@ struct ReorderArgs {
   uint32_t* flags;
 };
 
-// CTAs per SM: all of a launch are resident at once.
-constexpr int reorder_ctas(int w) { return w <= 4 ? 6 : w <= 8 ? 4 : w <= 16 ? 2 : 1; }
+// Columns of a thread in a tile, and CTAs per SM: all of a launch are resident at once.
+constexpr int reorder_cols(int w) { return w <= 2 ? 4 : w <= 4 ? 2 : 1; }
+constexpr int reorder_ctas(int w) { return w <= 8 ? 3 : w <= 16 ? 2 : 1; }
 
-// kW: at least w.  The blocks share out tiles of 256 columns: of the groups in which a beam moves, up
-// to their lengths, for every state.
+// kW: at least w.  The blocks share out tiles of columns: of the groups in which a beam moves, up to
+// their lengths, for every state.
 template <typename Vec, int kW>
 __global__ void __launch_bounds__(kReorderThreads, reorder_ctas(kW))
     beam_reorder_kernel(ReorderArgs a) {
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kReorderThreads, reorder_ctas(kW))
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   grid_dependency_wait();
   grid_dependents_launch();
-  constexpr int kEach = kReorderGroups / kReorderThreads;
+  constexpr int kEach = kReorderGroups / kReorderThreads, kCols = reorder_cols(kW);
+  constexpr int kTile = kCols * kReorderThreads;
   const int positions = (int)(a.inner / a.per_pos);
   auto length = [&](int64_t b) {  // columns of a piece that are used
     return a.lens ? (uint32_t)max(0, min(a.lens[b], positions)) * a.per_pos : a.inner;
@@ -176,8 +178,7 @@ __global__ void __launch_bounds__(kReorderThreads, reorder_ctas(kW))
         if (a.lens && a.flags && (unsigned)a.lens[b] > (unsigned)positions)
           atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
         if (moves)
-          tiles = (uint32_t)(((uint64_t)a.outer * length(b) + kReorderThreads - 1) /
-                             kReorderThreads);
+          tiles = (uint32_t)(((uint64_t)a.outer * length(b) + kTile - 1) / kTile);
       }
       total += tiles;
       tiles_to[q] = total;
@@ -227,21 +228,31 @@ __global__ void __launch_bounds__(kReorderThreads, reorder_ctas(kW))
         mine = lane < a.w ? a.parent[b * a.w + lane] : -1;  // a parent per lane
         moved = __ballot_sync(0xffffffffu, (unsigned)mine < (unsigned)a.w && mine != lane);
       }
-      const uint64_t c = (uint64_t)(here - first) * kReorderThreads + t;
-      const bool in = c < (uint64_t)a.outer * len;
-      const uint32_t o = in ? (uint32_t)c / len : 0;  // (below 2^32: checked on the host)
       const int64_t stride = a.state[state].row_stride;
-      char* p = a.state[state].base + b * a.w * stride + o * a.state[state].outer_stride +
-                ((uint64_t)c - (uint64_t)o * len) * sizeof(Vec);
-      Vec v[kW];
+      char* p[kCols];
+      bool in[kCols];
+      Vec v[kCols][kW];
+#pragma unroll
+      for (int q = 0; q < kCols; q++) {
+        const uint64_t c = (uint64_t)(here - first) * kTile + q * kReorderThreads + t;
+        in[q] = c < (uint64_t)a.outer * len;
+        const uint32_t o = in[q] ? (uint32_t)c / len : 0;  // (below 2^32: checked on the host)
+        p[q] = a.state[state].base + b * a.w * stride + o * a.state[state].outer_stride +
+               ((uint64_t)c - (uint64_t)o * len) * sizeof(Vec);
+      }
 #pragma unroll
       for (int i = 0; i < kW; i++) {
         const int from = __shfl_sync(0xffffffffu, mine, i);
-        if (in && (moved >> i & 1)) v[i] = *reinterpret_cast<const Vec*>(p + from * stride);
+#pragma unroll
+        for (int q = 0; q < kCols; q++)
+          if (in[q] && (moved >> i & 1)) v[q][i] = *reinterpret_cast<const Vec*>(p[q] + from * stride);
       }
 #pragma unroll
-      for (int i = 0; i < kW; i++)
-        if (in && (moved >> i & 1)) *reinterpret_cast<Vec*>(p + i * stride) = v[i];
+      for (int i = 0; i < kW; i++) {
+#pragma unroll
+        for (int q = 0; q < kCols; q++)
+          if (in[q] && (moved >> i & 1)) *reinterpret_cast<Vec*>(p[q] + i * stride) = v[q][i];
+      }
     }
     __syncthreads();
   }

@@ -29,8 +29,8 @@ gmm_status reorder_launch(const ReorderArgs& a, cudaStream_t st) {
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
-  const double tiles = (double)a.n * a.B *
-                       (((double)a.outer * a.inner + kReorderThreads - 1) / kReorderThreads);
+  constexpr int kTile = kReorderThreads * reorder_cols(kW);
+  const double tiles = (double)a.n * a.B * (((double)a.outer * a.inner + kTile - 1) / kTile);
   const unsigned grid =
       (unsigned)std::max(1.0, std::min(tiles, (double)sms * reorder_ctas(kW)));
   return api_launch_next(beam_reorder_kernel<Vec, kW>, dim3(grid), kReorderThreads, 0, st, a);
@@ -38,7 +38,8 @@ gmm_status reorder_launch(const ReorderArgs& a, cudaStream_t st) {
 
 template <typename Vec>
 gmm_status reorder_width(const ReorderArgs& a, cudaStream_t st) {
-  return a.w <= 4    ? reorder_launch<Vec, 4>(a, st)
+  return a.w <= 2    ? reorder_launch<Vec, 2>(a, st)
+         : a.w <= 4  ? reorder_launch<Vec, 4>(a, st)
          : a.w <= 8  ? reorder_launch<Vec, 8>(a, st)
          : a.w <= 16 ? reorder_launch<Vec, 16>(a, st)
                      : reorder_launch<Vec, 32>(a, st);
