@@ -144,17 +144,18 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   while (cols * ctas < r->K) cols *= 2;
   const RouteLossOut o = {balance, z, load, counts, rows};
   cudaLaunchAttribute attr[2] = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S * ctas);
   cfg.blockDim = dim3(kReduceThreads);
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  // (it reads the offsets before it waits: they are there when the kernel above has started)
+  cfg.numAttrs = r->N > 0 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, route_reduce_kernel, a, (const float*)ws, o, cols) != cudaSuccess)
     return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
