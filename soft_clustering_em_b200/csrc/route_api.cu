@@ -30,19 +30,22 @@ gmm_status check_route(const gmm_rows* r, int32_t m, int32_t S) {
   return GMM_OK;
 }
 
-// CTAs of the loss and the rows of each.
+// CTAs of the loss and the rows of each: at least 32 rows, or about a segment's where those are
+// shorter (a CTA takes a segment after the other, 1 us each), and three CTAs on each of 148 SMs at
+// most.
 struct LossPlan {
   int64_t chunks, rows;
 };
-LossPlan loss_plan(int64_t N) {
+LossPlan loss_plan(int64_t N, int32_t S) {
   LossPlan p;
-  p.chunks = std::max<int64_t>(1, std::min<int64_t>((N + 31) / 32, 444));
+  p.chunks = std::max<int64_t>((N + 31) / 32, std::min<int64_t>(N, S));
+  p.chunks = std::max<int64_t>(1, std::min<int64_t>(p.chunks, 444));
   p.rows = std::max<int64_t>(1, (N + p.chunks - 1) / p.chunks);
   return p;
 }
 
 size_t loss_bytes(const gmm_rows* r, int32_t S) {
-  return (size_t)(loss_plan(r->N).chunks + std::max(S, 1)) * route_slot(r->K) * 4;
+  return (size_t)(loss_plan(r->N, S).chunks + std::max(S, 1)) * route_slot(r->K) * 4;
 }
 
 // How rows of K classes are taken (route_vec).
@@ -127,7 +130,7 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   if (r->N > 0 && (!Z || !idx)) return GMM_ERR_INVALID_ARG;
   if ((uintptr_t)Z % elem(r->dtype) != 0) return GMM_ERR_UNSUPPORTED;
   if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < loss_bytes(r, S)) return GMM_ERR_WORKSPACE;
-  const LossPlan plan = loss_plan(r->N);
+  const LossPlan plan = loss_plan(r->N, S);
   const RouteArgs a = {Z,    r->N,    r->ld, r->K,      r->scale, idx, m,
                        mask, offsets, S,     plan.rows, dev_flags};
   cudaStream_t st = (cudaStream_t)stream;
