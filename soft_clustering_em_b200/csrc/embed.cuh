@@ -30,23 +30,40 @@ struct EmbedArgs {
   uint32_t* flags;
 };
 
-// A unit of a row: one element (kMode 0), or 16 bytes of T where rows start on 16 bytes, the last
-// unit perhaps a part (1) or whole as well (2: D is a multiple).
+// What a lane takes of a row at once, a unit.  kMode 1 and 2, rows that start on 16 bytes: 16 bytes of T,
+// the last unit perhaps a part (1) or whole as well (2: D is a multiple).  kMode 0, rows that start
+// anywhere: four elements, as far apart as there are lanes, so that a warp's accesses lie together.
 template <typename T, int kMode>
 struct Unit {
   static constexpr bool kVec = kMode > 0;
-  static constexpr int n = kVec ? Vec16<T>::n : 1;
-  using Raw = typename std::conditional<kVec, uint4, T>::type;
-  static __device__ __forceinline__ Raw zero() {
-    if constexpr (kVec) return make_uint4(0, 0, 0, 0);
-    else return T(0.f);
+  static constexpr int n = kVec ? Vec16<T>::n : 4;
+  struct Elements {
+    T x[n];
+  };
+  using Raw = typename std::conditional<kVec, uint4, Elements>::type;
+  // The first element of lane l, of `lanes` that take units first, first + 1, ...
+  static __device__ __forceinline__ int at(int first, int l, int lanes) {
+    return kVec ? (first + l) * n : first * n + l;
   }
-  // unit u of a row of D elements; what is behind the row is 0
-  static __device__ __forceinline__ Raw load(const T* row, int u, int D) {
-    if constexpr (!kVec) {
-      return row[u];
+  static __device__ __forceinline__ Raw zero() {
+    if constexpr (kVec) {
+      return make_uint4(0, 0, 0, 0);
     } else {
-      if (kMode == 2 || u * n + n <= D) return load16(row + u * n);
+      Raw r;
+#pragma unroll
+      for (int e = 0; e < n; e++) r.x[e] = T(0.f);
+      return r;
+    }
+  }
+  // The unit at element i of a row of D; what is behind the row is 0.
+  static __device__ __forceinline__ Raw load(const T* row, int i, int lanes, int D) {
+    if constexpr (!kVec) {
+      Raw r;
+#pragma unroll
+      for (int e = 0; e < n; e++) r.x[e] = i + e * lanes < D ? row[i + e * lanes] : T(0.f);
+      return r;
+    } else {
+      if (kMode == 2 || i + n <= D) return load16(row + i);
       union {
         uint4 r;
         T x[n];
@@ -54,24 +71,31 @@ struct Unit {
       part.r = zero();
 #pragma unroll
       for (int e = 0; e < n; e++)
-        if (u * n + e < D) part.x[e] = row[u * n + e];
+        if (i + e < D) part.x[e] = row[i + e];
       return part.r;
     }
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[n]) {
-    if constexpr (kVec) Vec16<T>::unpack(r, x);
-    else x[0] = to_f32(r);
-  }
-  static __device__ __forceinline__ void store(T* row, int u, int D, const float (&x)[n]) {
-    if constexpr (!kVec) {
-      from_f32(row + u, x[0]);
+    if constexpr (kVec) {
+      Vec16<T>::unpack(r, x);
     } else {
-      if (kMode == 2 || u * n + n <= D) {
-        *reinterpret_cast<uint4*>(row + u * n) = Vec16<T>::pack(x);
+#pragma unroll
+      for (int e = 0; e < n; e++) x[e] = to_f32(r.x[e]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int i, int lanes, int D,
+                                               const float (&x)[n]) {
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int e = 0; e < n; e++)
+        if (i + e * lanes < D) from_f32(row + i + e * lanes, x[e]);
+    } else {
+      if (kMode == 2 || i + n <= D) {
+        *reinterpret_cast<uint4*>(row + i) = Vec16<T>::pack(x);
       } else {
 #pragma unroll
         for (int e = 0; e < n; e++)
-          if (u * n + e < D) from_f32(row + u * n + e, x[e]);
+          if (i + e < D) from_f32(row + i + e, x[e]);
       }
     }
   }
@@ -87,16 +111,16 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   const int lanes = 1 << a.lane_bits, l = threadIdx.x & (lanes - 1);
   const int64_t row =
       (int64_t)blockIdx.x * (kEmbedThreads >> a.lane_bits) + (threadIdx.x >> a.lane_bits);
-  const int u0 = (int)(blockIdx.y * kPer << a.lane_bits) + l;
+  auto at = [&](int p) { return U::at((int)(blockIdx.y * kPer + p) << a.lane_bits, l, lanes); };
   if (row >= a.N) return;
   int k[kM];
   float w[kM];
 #pragma unroll
   for (int j = 0; j < kM; j++) {
     const bool live = kM == 1 || j < a.m;
-    const int64_t at = kM == 1 ? row : row * a.m + j;
-    k[j] = live ? a.idx[at] : -1;
-    w[j] = live && a.resp ? a.resp[at] : 1.f;
+    const int64_t c = kM == 1 ? row : row * a.m + j;
+    k[j] = live ? a.idx[c] : -1;
+    w[j] = live && a.resp ? a.resp[c] : 1.f;
   }
   typename U::Raw r[kPer][kM];
 #pragma unroll
@@ -108,16 +132,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
     }
     const T* from = (const T*)a.W + (ok ? k[j] : 0) * a.ldw;
 #pragma unroll
-    for (int p = 0; p < kPer; p++) {
-      const int u = u0 + (p << a.lane_bits);
-      r[p][j] = ok && u < a.units ? U::load(from, u, a.D) : U::zero();
-    }
+    for (int p = 0; p < kPer; p++)
+      r[p][j] = ok && at(p) < a.D ? U::load(from, at(p), lanes, a.D) : U::zero();
   }
   T* to = (T*)a.Y + row * a.ldy;
 #pragma unroll
   for (int p = 0; p < kPer; p++) {
-    const int u = u0 + (p << a.lane_bits);
-    if (u >= a.units) return;
+    if (at(p) >= a.D) return;
     float y[U::n] = {};
 #pragma unroll
     for (int j = 0; j < kM; j++) {
@@ -128,7 +149,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < U::n; e++) y[e] *= a.scale;
-    U::store(to, u, a.D, y);
+    U::store(to, at(p), lanes, a.D, y);
   }
 }
 
@@ -142,7 +163,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
 // steps, and leaves the other SMs to whatever else the gradient needs.  Beyond, two kernels per
 // digit: each CTA counts the digits of its contiguous tile, then (all counts known) places its
 // entries.
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 10;
 constexpr int kSortTiles = 148;  // most tiles
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   uint32_t carry = 0;
   for (int b0 = 0; b0 < bins; b0 += cols) {
     uint32_t before = 0, all = 0;
-#pragma unroll 16
+#pragma unroll 24
     for (int tile = t / cols; tile < tiles; tile += groups) {
       const uint32_t n = a.counts[tile * bins + b0 + col];
       all += n;
@@ -457,39 +478,59 @@ struct EmbedGradArgs {
   int m, add;
 };
 
+// Adds to float32 memory without waiting for what is there.  (An element is added to once in a call, so
+// this is old + x rounded once, whatever the order; subnormal values count as 0.)
+__device__ __forceinline__ void red_add(float* p, float x) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory");
+}
+__device__ __forceinline__ void red_add4(float* p, float4 x) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x.x),
+               "f"(x.y), "f"(x.z), "f"(x.w)
+               : "memory");
+}
+
+// scale * sum to, or added to, row k's unit at element i.
 template <typename T, typename TO, int kMode>
-__device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, int u,
+__device__ __forceinline__ void write_grad(const EmbedGradArgs& a, uint32_t k, int i, int lanes,
                                            const float (&sum)[Unit<T, kMode>::n]) {
   constexpr int n = Unit<T, kMode>::n;
   TO* row = (TO*)a.dW + (int64_t)k * a.ldd;
   float x[n];
 #pragma unroll
   for (int e = 0; e < n; e++) x[e] = sum[e] * a.scale;
-  if constexpr (std::is_same<T, TO>::value) {
+  if constexpr (std::is_same<TO, float>::value) {  // (units of T: 16 or 32 bytes of dW)
+    if constexpr (kMode == 0) {
+#pragma unroll
+      for (int e = 0; e < n; e++) {
+        if (i + e * lanes >= a.D) continue;
+        if (a.add) red_add(row + i + e * lanes, x[e]);
+        else row[i + e * lanes] = x[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < n; e += 4) {
+        const float4 v = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (kMode == 2 || i + e + 4 <= a.D) {
+          if (a.add) red_add4(row + i + e, v);
+          else *reinterpret_cast<float4*>(row + i + e) = v;
+        } else {
+#pragma unroll
+          for (int q = e; q < e + 4; q++) {
+            if (i + q >= a.D) continue;
+            if (a.add) red_add(row + i + q, x[q]);
+            else row[i + q] = x[q];
+          }
+        }
+      }
+    }
+  } else {
     if (a.add) {
       float old[n];
-      Unit<T, kMode>::unpack(Unit<T, kMode>::load(row, u, a.D), old);
+      Unit<T, kMode>::unpack(Unit<T, kMode>::load(row, i, lanes, a.D), old);
 #pragma unroll
       for (int e = 0; e < n; e++) x[e] += old[e];
     }
-    Unit<T, kMode>::store(row, u, a.D, x);
-  } else {  // a float32 gradient of narrower rows: 32 bytes per unit
-#pragma unroll
-    for (int e = 0; e < n; e += 4) {
-      if (kMode == 2 || (kMode == 1 && u * n + e + 4 <= a.D)) {
-        float4* p = reinterpret_cast<float4*>(row + u * n + e);
-        float4 v = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        if (a.add) {
-          const float4 o = *p;
-          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-        }
-        *p = v;
-      } else {
-#pragma unroll
-        for (int i = e; i < e + 4 && i < n; i++)
-          if (u * n + i < a.D) row[u * n + i] = a.add ? x[i] + row[u * n + i] : x[i];
-      }
-    }
+    Unit<T, kMode>::store(row, i, lanes, a.D, x);
   }
 }
 
@@ -532,8 +573,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
     if (begin + a.chunk < a.M) after = a.list[begin + a.chunk].x;
   }
   __syncthreads();
-  const int u = blockIdx.y * a.lanes + l;
-  if (c >= a.chunks || u >= a.units) return;
+  const int at = U::at(blockIdx.y * a.lanes, l, a.lanes);
+  if (c >= a.chunks || at >= a.D) return;
   key += g * a.chunk;
   row += g * a.chunk;
   weight += g * a.chunk;
@@ -544,7 +585,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
 #pragma unroll
     for (int b = 0; b < kGradBatch; b++)
       r[b] = key[i + b] < (uint32_t)a.K
-                 ? U::load((const T*)a.dY + (int64_t)row[i + b] * a.ldy, u, a.D)
+                 ? U::load((const T*)a.dY + (int64_t)row[i + b] * a.ldy, at, a.lanes, a.D)
                  : U::zero();
 #pragma unroll
     for (int b = 0; b < kGradBatch; b++) {
@@ -559,17 +600,19 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
       const bool goes_on = (last ? after : key[i + b + 1]) == k;
       if (goes_on && !last) continue;
       if (came_in || goes_on) {
-        float* p = a.part + ((int64_t)c * 2 + (came_in ? 0 : 1)) * a.width + u * U::n;
+        float* p = a.part + ((int64_t)c * 2 + (came_in ? 0 : 1)) * a.width + at;
         if constexpr (U::kVec) {
 #pragma unroll
           for (int e = 0; e < U::n; e += 4)
             *reinterpret_cast<float4*>(p + e) =
                 make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
         } else {
-          p[0] = sum[0];
+#pragma unroll
+          for (int e = 0; e < U::n; e++)
+            if (at + e * a.lanes < a.D) p[e * a.lanes] = sum[e];
         }
       } else {
-        write_grad<T, TO, kMode>(a, k, u, sum);
+        write_grad<T, TO, kMode>(a, k, at, a.lanes, sum);
       }
       came_in = false;
 #pragma unroll
@@ -594,9 +637,9 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
   grid_dependents_launch();
   const uint32_t c = blockIdx.x * kWarps + w;
   const uint64_t begin = (uint64_t)c * a.chunk, end = begin + a.chunk;
-  const int u = blockIdx.y * 32 + lane;
+  const int at = U::at(blockIdx.y * 32, lane, 32);
   auto part = [&](uint32_t q, bool tail, float (&x)[U::n]) {
-    const float* p = a.part + ((int64_t)q * 2 + tail) * a.width + u * U::n;
+    const float* p = a.part + ((int64_t)q * 2 + tail) * a.width + at;
     if constexpr (U::kVec) {
 #pragma unroll
       for (int e = 0; e < U::n; e += 4) {
@@ -604,7 +647,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
         x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
       }
     } else {
-      x[0] = p[0];
+#pragma unroll
+      for (int e = 0; e < U::n; e++) x[e] = at + e * 32 < a.D ? p[e * 32] : 0.f;
     }
   };
   uint32_t k = (uint32_t)a.K, last = 0;
@@ -619,8 +663,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
     // the run's last chunk: the first behind c whose own next entry is of another class
     uint32_t lo = c + 1, hi = a.chunks - 1;
     while (lo < hi) {
-      const uint32_t step = (hi - lo + 31) / 32, at = min(lo + step * lane, hi);
-      const bool past = at == hi || a.list[(uint64_t)(at + 1) * a.chunk].x != k;
+      const uint32_t step = (hi - lo + 31) / 32, probe = min(lo + step * lane, hi);
+      const bool past = probe == hi || a.list[(uint64_t)(probe + 1) * a.chunk].x != k;
       const int f = __ffs(__ballot_sync(0xffffffffu, past)) - 1;
       const uint32_t found = f < 0 ? hi : min(lo + step * f, hi);
       const uint32_t from = f == 0 ? lo : f < 0 ? lo + step * 31 + 1 : lo + step * (f - 1) + 1;
@@ -628,7 +672,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
       lo = min(from, hi);
     }
     last = lo;
-    if (last - c <= kJoinShort && u < a.units) {
+    if (last - c <= kJoinShort && at < a.D) {
       float sum[U::n], x[kJoinShort][U::n];
       part(c, true, sum);
 #pragma unroll
@@ -640,7 +684,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
 #pragma unroll
         for (int e = 0; e < U::n; e++) sum[e] += x[q][e];
       }
-      write_grad<T, TO, kMode>(a, k, u, sum);
+      write_grad<T, TO, kMode>(a, k, at, 32, sum);
     }
   }
   const bool is_long = mine && last - c > kJoinShort;
@@ -653,7 +697,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
     const uint32_t from = long_chunk[q], to = long_last[q];
     if (from == 0xffffffffu) continue;  // (the same for all threads)
     float sum[U::n] = {};
-    if (u < a.units) {
+    if (at < a.D) {
 #pragma unroll 8
       for (uint32_t i = from + w; i <= to; i += kWarps) {
         float x[U::n];
@@ -665,20 +709,20 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
 #pragma unroll
     for (int e = 0; e < U::n; e++) sh[w][lane * U::n + e] = sum[e];
     __syncthreads();
-    if (w == 0 && u < a.units) {
+    if (w == 0 && at < a.D) {
       for (int i = 1; i < kWarps; i++) {
 #pragma unroll
         for (int e = 0; e < U::n; e++) sum[e] += sh[i][lane * U::n + e];
       }
-      write_grad<T, TO, kMode>(a, a.list[((uint64_t)from + 1) * a.chunk].x, u, sum);
+      write_grad<T, TO, kMode>(a, a.list[((uint64_t)from + 1) * a.chunk].x, at, 32, sum);
     }
     __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------ gradient of the weights
-// A group of 8 or 32 lanes per row n: <dY_n, W[idx_nj]> for its m choices, in a fixed order.
-// (Like the rows of zeros it goes on beside the sort, and ends after it.)
+// A group of 8, 32 or (for few rows) all 256 lanes per row n: <dY_n, W[idx_nj]> for its m choices, in a
+// fixed order.  (Like the rows of zeros it goes on beside the sort, and ends after it.)
 struct EmbedDotArgs {
   const void *W, *dY;
   const int32_t* idx;
@@ -692,7 +736,10 @@ struct EmbedDotArgs {
 template <typename T, int kMode, int kLanes, int kMost>
 __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(EmbedDotArgs a) {
   using U = Unit<T, kMode>;
-  constexpr int kAhead = kMost == 1 ? 4 : kMost == 2 ? 2 : 1;  // units of a lane on their way at once
+  // units of a lane on their way at once
+  constexpr int kAhead = kMost == 1 ? 4 : kMost == 2 ? 2 : 1;
+  constexpr int kWarps = kLanes / 32;  // of a row, where it has more than one
+  __shared__ float sh[kLanes > 32 ? kWarps : 1][kMost];
   grid_dependents_launch();
   const int l = threadIdx.x % kLanes;
   const int64_t step = (int64_t)gridDim.x * (kEmbedThreads / kLanes);
@@ -703,7 +750,7 @@ __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(E
     for (int j = 0; j < kMost; j++) next[j] = row < a.N && j < a.m ? a.idx[row * a.m + j] : -1;
   };
   choices(n);
-  for (; __any_sync(0xffffffffu, n < a.N); n += step) {  // (whole warps)
+  for (; __any_sync(0xffffffffu, n < a.N); n += step) {  // (whole warps; the CTA, if it has one row)
     int k[kMost];
     float dot[kMost] = {};
 #pragma unroll
@@ -717,16 +764,17 @@ __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(E
     choices(n + step);
     if (n < a.N) {
       const T* dy = (const T*)a.dY + n * a.ldy;
-      for (int u0 = l; u0 < a.units; u0 += kAhead * kLanes) {
+      for (int u0 = 0; u0 < a.units; u0 += kAhead * kLanes) {
         typename U::Raw y[kAhead], r[kAhead][kMost];
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
-          const int u = u0 + i * kLanes;
-          y[i] = u < a.units ? U::load(dy, u, a.D) : U::zero();
+          const int at = U::at(u0 + i * kLanes, l, kLanes);
+          y[i] = at < a.D ? U::load(dy, at, kLanes, a.D) : U::zero();
 #pragma unroll
           for (int j = 0; j < kMost; j++)
-            r[i][j] = u < a.units && k[j] >= 0 ? U::load((const T*)a.W + k[j] * a.ldw, u, a.D)
-                                               : U::zero();
+            r[i][j] = at < a.D && k[j] >= 0
+                          ? U::load((const T*)a.W + k[j] * a.ldw, at, kLanes, a.D)
+                          : U::zero();
         }
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
@@ -745,10 +793,27 @@ __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(E
 #pragma unroll
     for (int j = 0; j < kMost; j++) {
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1)
+      for (int o = (kLanes < 32 ? kLanes : 32) / 2; o > 0; o >>= 1)
         dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-      if (l == 0 && n < a.N && j < a.m) a.dresp[n * a.m + j] = k[j] < 0 ? 0.f : dot[j] * a.scale;
     }
+    if constexpr (kLanes > 32) {
+      if (l % 32 == 0) {
+#pragma unroll
+        for (int j = 0; j < kMost; j++) sh[l / 32][j] = dot[j];
+      }
+      __syncthreads();
+      if (l == 0) {
+#pragma unroll
+        for (int j = 0; j < kMost; j++) {
+#pragma unroll
+          for (int w = 1; w < kWarps; w++) dot[j] += sh[w][j];
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kMost; j++)
+      if (l == 0 && n < a.N && j < a.m) a.dresp[n * a.m + j] = k[j] < 0 ? 0.f : dot[j] * a.scale;
   }
   grid_dependency_wait();
 }

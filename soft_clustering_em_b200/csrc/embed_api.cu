@@ -160,14 +160,16 @@ int grad_lanes(int units) {
   return lanes;
 }
 
-// Choices per chunk: as few as leave no more CTAs than are resident at once (3 on each of 148 SMs),
-// between 16 and 128.  (131,072 x 2,048 bf16 from 16,384 choices: 122 us in chunks of 16, 2.3
-// turns of the CTAs, 116 in chunks of 40.)
+// Choices per chunk: as few as leave no more CTAs than are resident at once (3 on each of 148 SMs), or
+// whole turns of those, between 16 and 128.  (131,072 x 2,048 bf16 from 16,384 choices: 122 us in
+// chunks of 16, 2.3 turns of the CTAs, 116 in chunks of 40.)
 uint32_t grad_chunk(const gmm_embed_problem* p, uint32_t M) {
   const int units = (int)((p->D * elem(p->dtype) + 15) / 16), lanes = grad_lanes(units);
   const uint64_t slices = (units + lanes - 1) / lanes, groups = kEmbedThreads / lanes;
   const uint64_t most = std::max<uint64_t>(1, 3 * 148 * groups / slices);
-  return (uint32_t)std::min<uint64_t>(kGradChunk, std::max<uint64_t>(16, (M / most + 8) / 8 * 8));
+  const uint64_t turns = (M + most * kGradChunk - 1) / (most * kGradChunk);
+  const uint64_t chunk = turns == 0 ? 0 : (M + most * turns - 1) / (most * turns);
+  return (uint32_t)std::min<uint64_t>(kGradChunk, std::max<uint64_t>(16, (chunk + 7) / 8 * 8));
 }
 
 // Workspace: two buffers of sorted classes and their places, counts, cut sums.
@@ -217,8 +219,9 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const
   Choice* lists[2] = {(Choice*)(g.ws + L.list[0]), (Choice*)(g.ws + L.list[1])};
   *list = lists[(plan.passes - 1) & 1];
   if (M <= kSortCluster) {
-    int C = 0;
-    if (!cluster_size(&C)) return api_launched(0), GMM_ERR_CUDA;
+    int most = 0, C = 1;  // 1,024 choices, one round of its warps, per CTA
+    if (!cluster_size(&most)) return api_launched(0), GMM_ERR_CUDA;
+    while (C < most && (uint32_t)C * kClusterThreads < M) C *= 2;
     const SortAllArgs a = {g.idx,  {lists[0], lists[1]}, M,         part_of(M, C * kClusterWarps),
                            g.p->K, plan.passes,          plan.bits, g.flags};
     cudaLaunchAttribute attr[2] = {};
@@ -281,14 +284,18 @@ gmm_status dot_launch(const GradCall& g, bool first) {
     kern<<<(unsigned)blocks, kEmbedThreads, 0, g.st>>>(a);
     return api_launched(1);
   };
-  if (a.units <= 64) {  // 8 lanes of up to 8 units: 4 rows per warp
-    if (p->m == 1) return go(embed_dot_kernel<T, kMode, 8, 1>, 8);
-    if (p->m == 2) return go(embed_dot_kernel<T, kMode, 8, 2>, 8);
-    return go(embed_dot_kernel<T, kMode, 8, kMaxTopM>, 8);
-  }
-  if (p->m == 1) return go(embed_dot_kernel<T, kMode, 32, 1>, 32);
-  if (p->m == 2) return go(embed_dot_kernel<T, kMode, 32, 2>, 32);
-  return go(embed_dot_kernel<T, kMode, 32, kMaxTopM>, 32);
+  auto lanes = [&](auto one, auto two, auto four, auto most, int n) {
+    return p->m == 1 ? go(one, n) : p->m == 2 ? go(two, n) : p->m <= 4 ? go(four, n) : go(most, n);
+  };
+  if (a.units <= 64)  // 8 lanes of up to 8 units: 4 rows per warp
+    return lanes(embed_dot_kernel<T, kMode, 8, 1>, embed_dot_kernel<T, kMode, 8, 2>,
+                 embed_dot_kernel<T, kMode, 8, 4>, embed_dot_kernel<T, kMode, 8, kMaxTopM>, 8);
+  if (p->N >= (int64_t)sms * kBesideCtas)
+    return lanes(embed_dot_kernel<T, kMode, 32, 1>, embed_dot_kernel<T, kMode, 32, 2>,
+                 embed_dot_kernel<T, kMode, 32, 4>, embed_dot_kernel<T, kMode, 32, kMaxTopM>, 32);
+  // few rows: a CTA for each (8 rows of 5,987 fp16 that start anywhere: 177 us with a warp each)
+  return lanes(embed_dot_kernel<T, kMode, 256, 1>, embed_dot_kernel<T, kMode, 256, 2>,
+               embed_dot_kernel<T, kMode, 256, 4>, embed_dot_kernel<T, kMode, 256, kMaxTopM>, 256);
 }
 
 template <typename T>
