@@ -83,6 +83,8 @@ struct Unit {
       for (int e = 0; e < n; e++) x[e] = to_f32(r.x[e]);
     }
   }
+  // kStream: not read again soon by this kernel (the table stays in L2).
+  template <bool kStream = false>
   static __device__ __forceinline__ void store(T* row, int i, int lanes, int D,
                                                const float (&x)[n]) {
     if constexpr (!kVec) {
@@ -91,7 +93,8 @@ struct Unit {
         if (i + e * lanes < D) from_f32(row + i + e * lanes, x[e]);
     } else {
       if (kMode == 2 || i + n <= D) {
-        *reinterpret_cast<uint4*>(row + i) = Vec16<T>::pack(x);
+        if (kStream) __stcs(reinterpret_cast<uint4*>(row + i), Vec16<T>::pack(x));
+        else *reinterpret_cast<uint4*>(row + i) = Vec16<T>::pack(x);
       } else {
 #pragma unroll
         for (int e = 0; e < n; e++)
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < U::n; e++) y[e] *= a.scale;
-    U::store(to, at(p), lanes, a.D, y);
+    U::template store<true>(to, at(p), lanes, a.D, y);
   }
 }
 
@@ -179,6 +182,7 @@ struct SortArgs {
   const Choice* in;    // later digits: what the one before wrote
   Choice* out;
   uint32_t* counts;    // tiles x bins
+  uint8_t* seen;       // K bytes with the first digit, or null: which classes are named
   uint32_t M;
   uint32_t per_warp;          // entries, a multiple of 32
   int K, shift, bits;
@@ -208,6 +212,12 @@ __device__ __forceinline__ void sort_fetch(const int32_t* idx, const Choice* in,
   }
 }
 
+// K bytes of 0 (on 16 bytes, room up to the next 16), by threads of index t of n.
+__device__ __forceinline__ void clear_seen(uint8_t* seen, int K, int t, int n) {
+  uint4* v = reinterpret_cast<uint4*>(seen);
+  for (int i = t; i < (K + 15) / 16; i += n) v[i] = make_uint4(0, 0, 0, 0);
+}
+
 // The warp's 32 entries to their places, in order: `next` holds where each bin's next entry goes.
 __device__ __forceinline__ void sort_put(uint32_t* next, bool live, Choice c, uint32_t bin,
                                          Choice* out) {
@@ -229,6 +239,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
+  if (a.seen)
+    clear_seen(a.seen, a.K, blockIdx.x * kSortThreads + threadIdx.x, gridDim.x * kSortThreads);
   const uint64_t begin = ((uint64_t)blockIdx.x * kSortWarps + threadIdx.x / 32) * a.per_warp;
   const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
   for (uint64_t i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
@@ -322,6 +334,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
 #pragma unroll
     for (int b = 0; b < kSortBatch; b++) {
       if (i0 + 32 * b >= end) break;  // (the same for the warp)
+      if (a.seen && c[b].x < (uint32_t)a.K) a.seen[c[b].x] = 1;
       sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> a.shift) & (bins - 1), a.out);
     }
   }
@@ -332,6 +345,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
 struct SortAllArgs {
   const int32_t* idx;
   Choice* list[2];  // digit i writes buffer i & 1
+  uint8_t* seen;    // K bytes, or null: which classes are named
   uint32_t M, per_warp;
   int K, passes, bits;
   uint32_t* flags;
@@ -348,6 +362,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
   const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
   grid_dependency_wait();
   grid_dependents_launch();
+  if (a.seen) clear_seen(a.seen, a.K, rank * kClusterThreads + t, ctas * kClusterThreads);
   for (int pass = 0; pass < a.passes; pass++) {
     const int shift = pass * a.bits;
     const int32_t* idx = pass == 0 ? a.idx : nullptr;
@@ -414,6 +429,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
 #pragma unroll
       for (int b = 0; b < kSortBatch; b++) {
         if (i0 + 32 * b >= end) break;  // (the same for the warp)
+        if (idx && a.seen && c[b].x < (uint32_t)a.K) a.seen[c[b].x] = 1;
         sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> shift) & (bins - 1),
                  a.list[pass & 1]);
       }
@@ -425,9 +441,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
 }
 
 // ------------------------------------------------------------------ rows of zeros
-// Pieces of a row, one per warp.  Does not wait for the sort before it in the stream, only ends
-// after it: nothing that is written here is read or written there, and what came before the sort
-// is done when it lets this kernel start.
+// Rows [0, rows) beside the sort, before it is known which are named; pieces of a row, one per warp.
+// Does not wait for the sort before it in the stream, only ends after it: nothing that is written
+// here is read or written there, and what came before the sort is done when it lets this kernel
+// start.  (The rows behind, of classes that nothing names, get their zeros with the sums.)
 constexpr int kFillPiece = 16384;  // bytes
 // CTAs per SM of a kernel that goes on beside the sort and ends after it: all of them are resident
 // at once, also beside the sort's (one that waits keeps its place).
@@ -438,22 +455,26 @@ struct FillArgs {
   uint64_t parts;                    // pieces per row
 };
 
+// n bytes of 0, by a warp.
+__device__ __forceinline__ void zero_bytes(char* p, uint64_t n) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t head = (uint32_t)min(n, (uint64_t)(-(uintptr_t)p & 15u));
+  const uint64_t body = (n - head) / 16;
+  if (lane < head) p[lane] = 0;
+  uint4* v = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 4
+  for (uint64_t u = lane; u < body; u += 32) v[u] = make_uint4(0, 0, 0, 0);
+  if (lane < n - head - body * 16) p[head + body * 16 + lane] = 0;
+}
+
 __global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(FillArgs a) {
   grid_dependents_launch();
-  const int lane = threadIdx.x & 31;
   const uint64_t pieces = a.rows * a.parts;
   for (uint64_t i = (uint64_t)blockIdx.x * (kEmbedThreads / 32) + threadIdx.x / 32; i < pieces;
        i += (uint64_t)gridDim.x * (kEmbedThreads / 32)) {
     const uint64_t row = a.rows == 1 ? 0 : a.parts == 1 ? i : i / a.parts;
-    const uint64_t part = i - row * a.parts;
-    char* p = a.base + row * a.stride + part * kFillPiece;
-    const uint32_t n = (uint32_t)min((uint64_t)kFillPiece, a.row_bytes - part * kFillPiece);
-    const uint32_t head = min(n, (uint32_t)(-(uintptr_t)p & 15u)), body = (n - head) / 16;
-    if (lane < head) p[lane] = 0;
-    uint4* v = reinterpret_cast<uint4*>(p + head);
-#pragma unroll 4
-    for (uint32_t u = lane; u < body; u += 32) v[u] = make_uint4(0, 0, 0, 0);
-    if (lane < n - head - body * 16) p[head + body * 16 + lane] = 0;
+    const uint64_t at = (i - row * a.parts) * kFillPiece;
+    zero_bytes(a.base + row * a.stride + at, min((uint64_t)kFillPiece, a.row_bytes - at));
   }
   grid_dependency_wait();
 }
@@ -476,6 +497,11 @@ struct EmbedGradArgs {
   int K, D, units, lanes, width;
   float scale;
   int m, add;
+  // zeros for rows from fill_from on that `seen` does not name: blocks of fill_rows rows, the first
+  // fill_first of them before the sums' blocks, the others behind
+  const uint8_t* seen;
+  int fill_from, fill_rows;
+  uint32_t fill_first, sum_blocks;
 };
 
 // Adds to float32 memory without waiting for what is there.  (An element is added to once in a call, so
@@ -542,15 +568,25 @@ template <typename T, typename TO, int kMode>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradArgs a) {
   using U = Unit<T, kMode>;
   extern __shared__ uint32_t stage[];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  uint32_t block = blockIdx.x - a.fill_first;
+  if (block >= a.sum_blocks) {  // (the first ones wrap around)
+    if (blockIdx.y != 0) return;
+    block = blockIdx.x < a.fill_first ? blockIdx.x : blockIdx.x - a.sum_blocks;
+    const int64_t k0 = a.fill_from + (int64_t)block * a.fill_rows;
+    for (int q = threadIdx.x / 32; q < a.fill_rows && k0 + q < a.K; q += kEmbedThreads / 32)
+      if (!a.seen[k0 + q])
+        zero_bytes((char*)((TO*)a.dW + (k0 + q) * a.ldd), (uint64_t)a.D * sizeof(TO));
+    return;
+  }
   const int l = threadIdx.x & (a.lanes - 1);
   const uint32_t groups = kEmbedThreads / a.lanes, g = threadIdx.x / a.lanes;
   const uint32_t per = groups * a.chunk;  // of the CTA
   uint32_t* key = stage;
   uint32_t* row = stage + per;
   float* weight = reinterpret_cast<float*>(stage + 2 * per);
-  const uint32_t first = blockIdx.x * per;
-  grid_dependency_wait();
-  grid_dependents_launch();
+  const uint32_t first = block * per;
   for (uint32_t i = threadIdx.x; i < per; i += kEmbedThreads) {
     uint32_t k = (uint32_t)a.K, n = 0;
     float w = 0.f;
@@ -565,7 +601,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
     row[i] = n;
     weight[i] = w;
   }
-  const uint32_t c = blockIdx.x * groups + g, begin = c * a.chunk;
+  const uint32_t c = block * groups + g, begin = c * a.chunk;
   const uint32_t none = 0xffffffffu;
   uint32_t before = none, after = none;
   if (c < a.chunks) {

@@ -172,9 +172,9 @@ uint32_t grad_chunk(const gmm_embed_problem* p, uint32_t M) {
   return (uint32_t)std::min<uint64_t>(kGradChunk, std::max<uint64_t>(16, (chunk + 7) / 8 * 8));
 }
 
-// Workspace: two buffers of sorted classes and their places, counts, cut sums.
+// Workspace: two buffers of sorted choices, counts, named classes, cut sums.
 struct GradLayout {
-  size_t list[2], counts, part, total;
+  size_t list[2], counts, seen, part, total;
   uint32_t chunk, chunks;
   int width;
 };
@@ -191,6 +191,7 @@ GradLayout grad_layout(const gmm_embed_problem* p) {
   };
   for (int i = 0; i < 2; i++) L.list[i] = take((size_t)M * sizeof(Choice));
   L.counts = take(((size_t)s.tiles << s.bits) * 4);
+  L.seen = take(p->K);
   L.chunk = grad_chunk(p, M);
   L.chunks = M / L.chunk + (M % L.chunk != 0);
   L.width = (p->D + 7) / 8 * 8;
@@ -217,12 +218,13 @@ struct GradCall {
 gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const Choice** list) {
   const SortPlan plan = sort_plan(M, g.p->K);
   Choice* lists[2] = {(Choice*)(g.ws + L.list[0]), (Choice*)(g.ws + L.list[1])};
+  uint8_t* seen = g.add ? nullptr : (uint8_t*)(g.ws + L.seen);
   *list = lists[(plan.passes - 1) & 1];
   if (M <= kSortCluster) {
     int most = 0, C = 1;  // 1,024 choices, one round of its warps, per CTA
     if (!cluster_size(&most)) return api_launched(0), GMM_ERR_CUDA;
     while (C < most && (uint32_t)C * kClusterThreads < M) C *= 2;
-    const SortAllArgs a = {g.idx,  {lists[0], lists[1]}, M,         part_of(M, C * kClusterWarps),
+    const SortAllArgs a = {g.idx,  {lists[0], lists[1]}, seen,      M, part_of(M, C * kClusterWarps),
                            g.p->K, plan.passes,          plan.bits, g.flags};
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -250,6 +252,7 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const
     o.in = lists[(i + 1) & 1];
     o.out = lists[i & 1];
     o.counts = (uint32_t*)(g.ws + L.counts);
+    o.seen = i == 0 ? seen : nullptr;
     o.M = M;
     o.per_warp = plan.per_warp;
     o.K = g.p->K;
@@ -309,17 +312,26 @@ gmm_status dot_vec(const GradCall& g, bool first) {
                      : dot_launch<T, 2>(g, first);
 }
 
-gmm_status fill_launch(const GradCall& g, size_t size) {
+gmm_status fill_launch(const GradCall& g, size_t size, uint64_t rows) {
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
-  const uint64_t K = g.p->K, D = g.p->D;
+  const uint64_t D = g.p->D;
   const bool one = g.ldd == g.p->D;  // one long row
-  FillArgs a = {(char*)g.dW, one ? 1 : K, (one ? K * D : D) * size, (uint64_t)g.ldd * size, 0};
+  FillArgs a = {(char*)g.dW, one ? 1 : rows, (one ? rows * D : D) * size, (uint64_t)g.ldd * size,
+                0};
   a.parts = (a.row_bytes + kFillPiece - 1) / kFillPiece;
   const uint64_t blocks = (a.rows * a.parts + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32);
-  return api_launch_next(embed_fill_kernel, dim3((unsigned)std::min<uint64_t>(blocks, sms * kBesideCtas)),
+  return api_launch_next(embed_fill_kernel,
+                         dim3((unsigned)std::min<uint64_t>(blocks, sms * kBesideCtas)),
                          kEmbedThreads, 0, g.st, a);
+}
+
+// Rows that get their zeros beside the sort: what goes through while it runs (6 GB in a ms, from 12 us on
+// 1 us more for every 8,192 choices).  All of them where there are no sums.
+uint64_t beside_rows(const gmm_embed_problem* p, uint32_t M, size_t size) {
+  const uint64_t rows = (uint64_t)(6e6 * (12.0 + M / 8192.0) / ((double)p->D * size));
+  return M == 0 ? p->K : std::min<uint64_t>(p->K, std::max<uint64_t>(rows, 1));
 }
 
 // Stream order: the sort; beside it the weights' gradient and rows of zeros; then the sums.
@@ -333,7 +345,8 @@ gmm_status grad_launch(const GradCall& g) {
   gmm_status s;
   if ((s = sort_launch(g, L, M, &a.list)) != GMM_OK) return s;
   if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
-  if (!g.add && (s = fill_launch(g, sizeof(TO))) != GMM_OK) return s;
+  const uint64_t beside = g.add ? p->K : beside_rows(p, M, sizeof(TO));
+  if (!g.add && (s = fill_launch(g, sizeof(TO), beside)) != GMM_OK) return s;
   if (M == 0) return GMM_OK;
   a.dY = g.dY;
   a.resp = g.resp;
@@ -354,7 +367,16 @@ gmm_status grad_launch(const GradCall& g) {
   a.m = p->m;
   a.add = g.add;
   const unsigned groups = kEmbedThreads / a.lanes;
-  const dim3 grid((a.chunks + groups - 1) / groups, (a.units + a.lanes - 1) / a.lanes);
+  a.sum_blocks = (a.chunks + groups - 1) / groups;
+  // the other rows' zeros: blocks of about 128 KB, one per SM ahead of the sums' so that the memory
+  // is busy while those wait for it
+  const uint64_t left = p->K - beside, bytes = (uint64_t)p->D * sizeof(TO);
+  a.seen = (const uint8_t*)(g.ws + L.seen);
+  a.fill_from = (int)beside;
+  a.fill_rows = (int)std::max<uint64_t>(8, std::min<uint64_t>(4096, (131072 / bytes + 7) / 8 * 8));
+  const uint32_t fill = (uint32_t)((left + a.fill_rows - 1) / a.fill_rows);
+  a.fill_first = std::min(fill, 148u);
+  const dim3 grid(a.sum_blocks + fill, (a.units + a.lanes - 1) / a.lanes);
   if ((s = api_launch_next(embed_sum_kernel<T, TO, kMode>, grid, kEmbedThreads,
                            (size_t)groups * a.chunk * 12, g.st, a)) != GMM_OK)
     return s;

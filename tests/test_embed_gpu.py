@@ -209,6 +209,27 @@ def test_a_nan_reaches_only_what_it_is_part_of(G):
     assert (dW[0] == 3).all() and dW[1].isnan().all() and dW[2].isnan().all() and (dW[3] == 1).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,D,pad,shift", [(60_000, 1000, 0, 0), (60_000, 1000, 8, 0),
+                                           (150_001, 301, 0, 0), (150_001, 301, 2, 1),
+                                           (1_000_003, 64, 0, 0)])
+@pytest.mark.parametrize("M", [1, 3000, 150_000])
+def test_large_tables_are_written_throughout(G, K, D, pad, shift, dtype, M):
+    """Ones summed are counts (whole numbers up to 256 in bfloat16), everywhere else zeros: also in
+    the rows that are written after the sort, and not between the rows."""
+    import torch
+
+    idx = torch.randint(0, K, (M,), device="cuda", dtype=torch.int32)
+    idx[::7] = K - 1 - idx[::7] // 1000
+    buf = torch.full((K * (D + pad) + shift + 64,), float("nan"), dtype=_t(dtype), device="cuda")
+    out = buf[shift:shift + K * (D + pad)].view(K, D + pad)[:, :D]
+    dY = torch.ones(1, D, dtype=_t(dtype), device="cuda").expand(M, D).contiguous()
+    G.gmm_embed_backward(dY, idx, K, out=out)
+    want = torch.bincount(idx.long(), minlength=K).to(_t(dtype))
+    assert torch.equal(out, want[:, None].expand(K, D))
+    assert buf.isnan().sum() == buf.numel() - K * D
+
+
 def test_tables_beyond_32_bits(G):
     """Rows whose offsets pass 2^32 bytes and 2^31 elements."""
     import torch
