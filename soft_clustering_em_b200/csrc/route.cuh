@@ -224,11 +224,11 @@ struct RouteLossOut {
 
 // A cluster per segment adds up its slots, in order, in 64 bits; each CTA has a share of the
 // experts.  Threads: `cols` columns (a power of two) times groups that take every so many slots.
-constexpr int kReduceThreads = 1024;  // most
-constexpr int kReduceWarps = kReduceThreads / 32;
 constexpr int kReduceCtas = 8;  // most
+template <int kReduceThreads>
 __global__ void __launch_bounds__(kReduceThreads)
     route_reduce_kernel(RouteArgs a, const float* part, RouteLossOut o, int cols) {
+  constexpr int kReduceWarps = kReduceThreads / 32;
   __shared__ double sh[kReduceThreads];
   __shared__ uint32_t shc[kReduceThreads];
   __shared__ double zs[kReduceWarps], bs[kReduceWarps];
@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
   const int s = blockIdx.x / ctas;
-  const int threads = (int)blockDim.x, groups = threads / cols, g = t / cols, col = t & (cols - 1);
+  const int groups = kReduceThreads / cols, g = t / cols, col = t & (cols - 1);
+  // (the others of the cluster have started when its first CTA's memory is written below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   int64_t lo = 0, hi = a.N;
   if (a.offsets) {  // (from before the kernel that leaves the sums)
     lo = a.offsets[s];
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kReduceThreads)
   part += first * size;
   double z = 0.0;
   uint32_t n = 0;
-  for (int q = t; q < count; q += threads) {
+  for (int q = t; q < count; q += kReduceThreads) {
     z += part[q * size + 2 * a.K];
     n += reinterpret_cast<const uint32_t*>(part)[q * size + 2 * a.K + 1];
   }
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kReduceThreads)
     if (k0 == rank * cols) {
       z = 0.0;
       n = 0;
-      for (int i = 0; i < threads / 32; i++) z += zs[i], n += rs[i];
+      for (int i = 0; i < kReduceWarps; i++) z += zs[i], n += rs[i];
       L = n > 0 ? (double)n : 1.0;
     }
     if (g == 0 && k < a.K) {
@@ -294,9 +296,10 @@ __global__ void __launch_bounds__(kReduceThreads)
   balance = warp_sum(balance);
   if (lane == 0) bs[w] = balance;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (t == 0) {
     balance = 0.0;
-    for (int i = 0; i < threads / 32; i++) balance += bs[i];
+    for (int i = 0; i < kReduceWarps; i++) balance += bs[i];
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
                      sm100::map_to_rank(sm100::smem_u32(of_cta + rank), 0)),
                  "d"(balance)

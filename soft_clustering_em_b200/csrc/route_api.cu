@@ -142,9 +142,9 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
     if (s != GMM_OK) return s;
   }
   // a cluster per segment: 32 experts to a CTA, up to 8 CTAs, of 1,024 threads, while all segments'
-  // are resident at once (64 segments of 7,152 rows of 244: 35 us in clusters of 8, 17 in twos)
+  // are resident at once (64 segments of 7,152 rows of 244: 35 us in clusters of 8, 12 in twos)
   const int ctas = std::max(1, std::min({kReduceCtas, (r->K + 31) / 32, 148 / S}));
-  const int threads = (int64_t)S * ctas > 296 ? 256 : kReduceThreads;
+  const int threads = (int64_t)S * ctas > 296 ? 256 : 1024;
   int cols = 32;
   while (cols * ctas < r->K && cols < threads) cols *= 2;
   const RouteLossOut o = {balance, z, load, counts, rows};
@@ -161,7 +161,8 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   cfg.attrs = attr;
   // (it reads the offsets before it waits: they are there when the kernel above has started)
   cfg.numAttrs = r->N > 0 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, route_reduce_kernel, a, (const float*)ws, o, cols) != cudaSuccess)
+  auto kern = threads == 256 ? route_reduce_kernel<256> : route_reduce_kernel<1024>;
+  if (cudaLaunchKernelEx(&cfg, kern, a, (const float*)ws, o, cols) != cudaSuccess)
     return api_launched(0), GMM_ERR_CUDA;
   return api_launched(1);
 }
