@@ -218,6 +218,12 @@ __device__ __forceinline__ void clear_seen(uint8_t* seen, int K, int t, int n) {
   for (int i = t; i < (K + 15) / 16; i += n) v[i] = make_uint4(0, 0, 0, 0);
 }
 
+// A class that is named.  (Looked at first: a frequent one would have a hundred thousand stores wait for
+// one place in memory.)
+__device__ __forceinline__ void mark_seen(uint8_t* seen, uint32_t k) {
+  if (!seen[k]) seen[k] = 1;
+}
+
 // The warp's 32 entries to their places, in order: `next` holds where each bin's next entry goes.
 __device__ __forceinline__ void sort_put(uint32_t* next, bool live, Choice c, uint32_t bin,
                                          Choice* out) {
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
 #pragma unroll
     for (int b = 0; b < kSortBatch; b++) {
       if (i0 + 32 * b >= end) break;  // (the same for the warp)
-      if (a.seen && c[b].x < (uint32_t)a.K) a.seen[c[b].x] = 1;
+      if (a.seen && c[b].x < (uint32_t)a.K) mark_seen(a.seen, c[b].x);
       sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> a.shift) & (bins - 1), a.out);
     }
   }
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
 #pragma unroll
       for (int b = 0; b < kSortBatch; b++) {
         if (i0 + 32 * b >= end) break;  // (the same for the warp)
-        if (idx && a.seen && c[b].x < (uint32_t)a.K) a.seen[c[b].x] = 1;
+        if (idx && a.seen && c[b].x < (uint32_t)a.K) mark_seen(a.seen, c[b].x);
         sort_put(mine, i0 + 32 * b + lane < end, c[b], (c[b].x >> shift) & (bins - 1),
                  a.list[pass & 1]);
       }
@@ -666,14 +672,14 @@ template <typename T, typename TO, int kMode>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs a) {
   using U = Unit<T, kMode>;
   constexpr int kWarps = kEmbedThreads / 32;
-  __shared__ float sh[kWarps][32 * U::n];
+  __shared__ float sh[kEmbedThreads][U::n];
   __shared__ uint32_t long_chunk[kWarps], long_last[kWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_dependents_launch();
   const uint32_t c = blockIdx.x * kWarps + w;
   const uint64_t begin = (uint64_t)c * a.chunk, end = begin + a.chunk;
-  const int at = U::at(blockIdx.y * 32, lane, 32);
+  int at = U::at(blockIdx.y * 32, lane, 32);
   auto part = [&](uint32_t q, bool tail, float (&x)[U::n]) {
     const float* p = a.part + ((int64_t)q * 2 + tail) * a.width + at;
     if constexpr (U::kVec) {
@@ -729,13 +735,20 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
     long_last[w] = last;
   }
   if (__syncthreads_or(is_long) == 0) return;
+  // as many threads of a row as it has lanes; groups of those take every so many chunks
+  const int first = blockIdx.y * 32 * U::n, rest = a.D - first;
+  const int used = U::kVec ? (rest + U::n - 1) / U::n : rest;
+  int lanes = 32;
+  while (lanes / 2 >= used) lanes /= 2;
+  const int ul = threadIdx.x & (lanes - 1), g = threadIdx.x / lanes, groups = kEmbedThreads / lanes;
+  at = U::at(blockIdx.y * 32, ul, 32);
   for (int q = 0; q < kWarps; q++) {
     const uint32_t from = long_chunk[q], to = long_last[q];
     if (from == 0xffffffffu) continue;  // (the same for all threads)
     float sum[U::n] = {};
     if (at < a.D) {
 #pragma unroll 8
-      for (uint32_t i = from + w; i <= to; i += kWarps) {
+      for (uint32_t i = from + g; i <= to; i += groups) {
         float x[U::n];
         part(i, i == from, x);
 #pragma unroll
@@ -743,12 +756,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
       }
     }
 #pragma unroll
-    for (int e = 0; e < U::n; e++) sh[w][lane * U::n + e] = sum[e];
+    for (int e = 0; e < U::n; e++) sh[threadIdx.x][e] = sum[e];
     __syncthreads();
-    if (w == 0 && at < a.D) {
-      for (int i = 1; i < kWarps; i++) {
+    if (g == 0 && at < a.D) {
+#pragma unroll 4
+      for (int i = 1; i < groups; i++) {
 #pragma unroll
-        for (int e = 0; e < U::n; e++) sum[e] += sh[i][lane * U::n + e];
+        for (int e = 0; e < U::n; e++) sum[e] += sh[i * lanes + ul][e];
       }
       write_grad<T, TO, kMode>(a, a.list[((uint64_t)from + 1) * a.chunk].x, at, 32, sum);
     }

@@ -215,10 +215,11 @@ struct GradCall {
 };
 
 // The choices sorted by class, in *list.
-gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, const Choice** list) {
+// `seen`: K bytes for which classes are named, or null.
+gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, uint8_t* seen,
+                       const Choice** list) {
   const SortPlan plan = sort_plan(M, g.p->K);
   Choice* lists[2] = {(Choice*)(g.ws + L.list[0]), (Choice*)(g.ws + L.list[1])};
-  uint8_t* seen = g.add ? nullptr : (uint8_t*)(g.ws + L.seen);
   *list = lists[(plan.passes - 1) & 1];
   if (M <= kSortCluster) {
     int most = 0, C = 1;  // 1,024 choices, one round of its warps, per CTA
@@ -343,9 +344,10 @@ gmm_status grad_launch(const GradCall& g) {
   constexpr int V = Unit<T, kMode>::n;
   EmbedGradArgs a = {};
   gmm_status s;
-  if ((s = sort_launch(g, L, M, &a.list)) != GMM_OK) return s;
-  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
   const uint64_t beside = g.add ? p->K : beside_rows(p, M, sizeof(TO));
+  uint8_t* seen = beside < (uint64_t)p->K ? (uint8_t*)(g.ws + L.seen) : nullptr;
+  if ((s = sort_launch(g, L, M, seen, &a.list)) != GMM_OK) return s;
+  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
   if (!g.add && (s = fill_launch(g, sizeof(TO), beside)) != GMM_OK) return s;
   if (M == 0) return GMM_OK;
   a.dY = g.dY;
@@ -371,7 +373,7 @@ gmm_status grad_launch(const GradCall& g) {
   // the other rows' zeros: blocks of about 128 KB, one per SM ahead of the sums' so that the memory
   // is busy while those wait for it
   const uint64_t left = p->K - beside, bytes = (uint64_t)p->D * sizeof(TO);
-  a.seen = (const uint8_t*)(g.ws + L.seen);
+  a.seen = seen;
   a.fill_from = (int)beside;
   a.fill_rows = (int)std::max<uint64_t>(8, std::min<uint64_t>(4096, (131072 / bytes + 7) / 8 * 8));
   const uint32_t fill = (uint32_t)((left + a.fill_rows - 1) / a.fill_rows);

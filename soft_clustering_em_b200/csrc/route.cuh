@@ -56,13 +56,52 @@ __device__ __forceinline__ int segment_of(const int32_t* offsets, int S, int64_t
 // lse^2 and the number of rows.
 __host__ __device__ __forceinline__ int64_t route_slot(int K) { return 2 * (int64_t)K + 2; }
 
-// Vector k0 of a row of K classes, masked classes behind its end.  kMode: the row's entries one by one
-// (0); 16 bytes, the last vector perhaps a part (1) or whole (2: K is a multiple).
-template <typename T, int kMode>
-__device__ __forceinline__ uint4 route_vec(const T* row, int k0, int K) {
-  if constexpr (kMode < 2) return load_row_vec<T, kMode == 1>(row, k0, K);
-  return k0 < K ? load16(row + k0) : Vec16<T>::neg_inf();
-}
+// How the classes of a row lie in the registers of kLanes lanes, in vectors of 16 bytes of T.  kMode 1 and
+// 2, rows that start on 16 bytes: as in memory, the row's last vector perhaps a part (1) or whole
+// (2: K is a multiple).  kMode 0, rows that start anywhere: entry e of lane l is class e kLanes + l,
+// so that the lanes' accesses lie together.
+template <typename T, int kLanes, int kMode>
+struct RouteMap {
+  static constexpr int V = Vec16<T>::n;
+  static __device__ __forceinline__ int class_of(int e, int l) {
+    return kMode == 0 ? e * kLanes + l : (e / V * kLanes + l) * V + e % V;
+  }
+  // vector c of lane l, masked classes behind the row's end
+  static __device__ __forceinline__ uint4 load(const T* row, int c, int l, int K) {
+    const int k0 = (c * kLanes + l) * V;
+    if constexpr (kMode == 2) {
+      return k0 < K ? load16(row + k0) : Vec16<T>::neg_inf();
+    } else if constexpr (kMode == 1) {
+      return load_row_vec<T, true>(row, k0, K);
+    } else {
+      union {
+        uint4 r;
+        T x[V];
+      } u;
+      u.r = Vec16<T>::neg_inf();
+#pragma unroll
+      for (int e = 0; e < V; e++) {
+        const int k = class_of(c * V + e, l);
+        if (k < K) u.x[e] = row[k];
+      }
+      return u.r;
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int c, int l, int K, const float (&x)[V]) {
+    const int k0 = (c * kLanes + l) * V;
+    if constexpr (kMode == 2) {
+      if (k0 < K) *reinterpret_cast<uint4*>(row + k0) = Vec16<T>::pack(x);
+    } else if (kMode == 1 && k0 + V <= K) {
+      *reinterpret_cast<uint4*>(row + k0) = Vec16<T>::pack(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e++) {
+        const int k = class_of(c * V + e, l);
+        if (k < K) from_f32(row + k, x[e]);
+      }
+    }
+  }
+};
 
 // The exponentials of a row relative to its largest logit.
 template <int kLanes, int kEl, typename T>
@@ -153,7 +192,7 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_load_k
       const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
 #pragma unroll
       for (int c = 0; c < kChunks; c++)
-        next[c] = route_vec<T, kMode>(row, (c * kLanes + l) * V, a.K);
+        next[c] = RouteMap<T, kLanes, kMode>::load(row, c, l, a.K);
       next_k = in && l < a.m ? a.idx[n * a.m + l] : -1;
       next_out = !in || (a.mask && !a.mask[n]);
     };
@@ -192,8 +231,8 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_load_k
     live_rows = __reduce_add_sync(0xffffffffu, live_rows);
     if (lane < kLanes) {
 #pragma unroll
-      for (int e = 0; e < kEl; e++)  // (entry e of lane l is of this class)
-        sums[w][((e / V) * kLanes + l) * V + e % V] = acc[e];
+      for (int e = 0; e < kEl; e++)
+        sums[w][RouteMap<T, kLanes, kMode>::class_of(e, l)] = acc[e];
     }
     if (lane == 0) zsum[w] = zs, rsum[w] = live_rows;
     __syncthreads();
@@ -356,7 +395,7 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
     const T* row = (const T*)a.Z + (in ? n : n0) * a.ld;
 #pragma unroll
     for (int c = 0; c < kChunks; c++)
-      next[c] = route_vec<T, kMode>(row, (c * kLanes + l) * V, a.K);
+      next[c] = RouteMap<T, kLanes, kMode>::load(row, c, l, a.K);
     next_k = -1;
     if (g.dresp && in && l < a.m) {
       next_k = a.idx[n * a.m + l];
@@ -392,7 +431,7 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
         const int32_t* of = g.counts + (int64_t)s * a.K;
 #pragma unroll
         for (int e = 0; e < kEl; e++) {
-          const int ke = ((e / V) * kLanes + l) * V + e % V;
+          const int ke = RouteMap<T, kLanes, kMode>::class_of(e, l);
           cnt[e] = ke < a.K ? (float)of[ke] : 0.f;
         }
       }
@@ -450,16 +489,7 @@ __global__ void __launch_bounds__(kRouteThreads, kEl <= 16 ? 3 : 2) route_grad_k
       float x[V];
 #pragma unroll
       for (int e = 0; e < V; e++) x[e] = q.y[v * V + e];
-      const int k0 = (v * kLanes + l) * V;
-      if constexpr (kMode == 2) {
-        if (in && k0 < a.K) *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
-      } else if (kMode == 1 && in && k0 + V <= a.K) {
-        *reinterpret_cast<uint4*>(out + k0) = Vec16<T>::pack(x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; e++)
-          if (in && k0 + e < a.K) from_f32(out + k0 + e, x[e]);
-      }
+      if (in) RouteMap<T, kLanes, kMode>::store(out, v, l, a.K, x);
     }
     __syncwarp();
     // the chosen classes' entries once more, by the lanes that hold the choices
