@@ -667,6 +667,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
 // begin in it and go on behind it?  It adds up a run of a few chunks by itself; longer ones
 // are shared out over the CTA's warps.
 constexpr int kJoinShort = 8;  // chunks
+constexpr int kJoinBatch = 8;  // chunks on their way at once
 
 template <typename T, typename TO, int kMode>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs a) {
@@ -747,12 +748,19 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
     if (from == 0xffffffffu) continue;  // (the same for all threads)
     float sum[U::n] = {};
     if (at < a.D) {
-#pragma unroll 8
-      for (uint32_t i = from + g; i <= to; i += groups) {
-        float x[U::n];
-        part(i, i == from, x);
+      for (uint32_t i0 = from + g; i0 <= to; i0 += kJoinBatch * groups) {
+        float x[kJoinBatch][U::n];
 #pragma unroll
-        for (int e = 0; e < U::n; e++) sum[e] += x[e];
+        for (int b = 0; b < kJoinBatch; b++) {
+          const uint32_t i = i0 + b * groups;
+          if (i <= to) part(i, i == from, x[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < kJoinBatch; b++) {
+          if (i0 + b * groups > to) continue;
+#pragma unroll
+          for (int e = 0; e < U::n; e++) sum[e] += x[b][e];
+        }
       }
     }
 #pragma unroll
