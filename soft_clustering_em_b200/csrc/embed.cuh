@@ -287,11 +287,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
   uint32_t carry = 0;
   for (int b0 = 0; b0 < bins; b0 += cols) {
     uint32_t before = 0, all = 0;
-#pragma unroll 24
-    for (int tile = t / cols; tile < tiles; tile += groups) {
-      const uint32_t n = a.counts[tile * bins + b0 + col];
-      all += n;
-      before += tile < (int)blockIdx.x ? n : 0u;
+    constexpr int kAhead = 20;  // counts on their way at once
+    for (int tile0 = t / cols; tile0 < tiles; tile0 += kAhead * groups) {
+      uint32_t n[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; q++) {
+        const int tile = tile0 + q * groups;
+        n[q] = tile < tiles ? __ldcg(a.counts + tile * bins + b0 + col) : 0u;
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; q++) {
+        all += n[q];
+        before += tile0 + q * groups < (int)blockIdx.x ? n[q] : 0u;
+      }
     }
     of_bin[0][t] = all;
     of_bin[1][t] = before;
@@ -312,12 +320,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
     }
     if (lane == 31) sums[w] = scan;
     __syncthreads();
-    uint32_t lower = carry, total = 0;
-    for (int q = 0; q < kSortWarps; q++) {
-      if (q < w) lower += sums[q];
-      total += sums[q];
-    }
-    carry += total;
+    static_assert(kSortWarps == 32, "a lane for each warp's sum");
+    const uint32_t lower = carry + __reduce_add_sync(0xffffffffu, lane < w ? sums[lane] : 0u);
+    carry += __reduce_add_sync(0xffffffffu, sums[lane]);
     if (t < cols) {
       uint32_t at = lower + scan - all + before;
 #pragma unroll
