@@ -557,8 +557,8 @@ gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* i
  *           raises GMM_DEVFLAG_BAD_INDEX.  A row without choices is zeros.
  *   resp    device, N x m floats, or NULL.
  * Sums are formed in float32 and rounded once.  Rows may start anywhere (element-aligned); 16-byte
- * aligned ones are faster.  N = 0 does nothing.  GMM_ERR_UNSUPPORTED: K > 2^24, D > 2^20,
- * N * m >= 2^31, N * D > 10^12.
+ * aligned ones are faster.  Y must not overlap the inputs.  N = 0 does nothing.
+ * GMM_ERR_UNSUPPORTED: K > 2^24, D > 2^20, N * m >= 2^31, N * D > 10^12.
  */
 typedef struct {
   int64_t N;          /* rows of idx and Y, >= 0 */
@@ -580,7 +580,9 @@ gmm_status gmm_embed(const gmm_embed_problem* p, const void* W, const int32_t* i
  * does not change from run to run, and is rounded once.
  *   dW        device, K x D of dw_dtype (GMM_F32 or dtype), rows ldd apart, or NULL.  Every row is
  *             written, zeros where nothing names it; with accumulate != 0 the gradient is added to
- *             what is there, and rows that nothing names are not touched.
+ *             what is there (in float32; in a GMM_F32 dW subnormal values count as 0), and rows
+ *             that nothing names are not touched.  What lies between the rows stays as it is.  Must not
+ *             overlap the inputs.
  *   dresp     device, N x m floats, or NULL; needs W (else unused).
  *   ws        device workspace of gmm_embed_workspace_size bytes, 256-byte aligned, any content
  *             (only for dW).  Calls that share it must be ordered on one stream.
@@ -624,12 +626,12 @@ gmm_status gmm_beam_select(const gmm_rows* r, const void* Z, int32_t w, const fl
  *   lens     device, B int32, or NULL: used positions of the group's beams, for states with by_len;
  *            positions behind them are left as they are.  One outside [0, count] counts as the
  *            nearer end and raises GMM_DEVFLAG_BAD_INDEX.
- *   states   host array of n.  The row of beam (b, i) is base + (b w + i) row_stride; it has `outer`
- *            pieces outer_stride bytes apart (the heads of a cache), each of `count` positions of
- *            pos_bytes bytes.  Rows and pieces must not overlap.
+ *   states   host array of n.  The row of beam (b, i) is base + (b w + i) row_stride; it has
+ *            `outer` pieces outer_stride bytes apart (the heads of a cache), each of `count` positions of
+ *            pos_bytes bytes.  Rows and pieces must not overlap, nor states one another.
  * 1 <= w <= 32.  Nothing is read or written of groups whose beams all stay.  No workspace.
- * GMM_ERR_UNSUPPORTED: a row of 2^32 or more columns of 16 bytes (4 or 1 where an address, stride or
- * position is not a multiple of 16 bytes).
+ * GMM_ERR_UNSUPPORTED: a row of 2^32 or more columns of 16 bytes (4 or 1 where an address, stride
+ * or position is not a multiple of 16 bytes).
  */
 typedef struct {
   void* base;

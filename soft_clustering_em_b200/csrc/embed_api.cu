@@ -160,9 +160,9 @@ int grad_lanes(int units) {
   return lanes;
 }
 
-// Choices per chunk: as few as leave no more CTAs than are resident at once (3 on each of 148 SMs), or
-// whole turns of those, between 16 and 128.  (131,072 x 2,048 bf16 from 16,384 choices: 122 us in
-// chunks of 16, 2.3 turns of the CTAs, 116 in chunks of 40.)
+// Choices per chunk: as few as leave no more CTAs than are resident at once (3 on each of 148
+// SMs), or whole turns of those, between 16 and 128.  (131,072 x 2,048 bf16 from 16,384 choices:
+// 122 us in chunks of 16, 2.3 turns of the CTAs, 116 in chunks of 40.)
 uint32_t grad_chunk(const gmm_embed_problem* p, uint32_t M) {
   const int units = (int)((p->D * elem(p->dtype) + 15) / 16), lanes = grad_lanes(units);
   const uint64_t slices = (units + lanes - 1) / lanes, groups = kEmbedThreads / lanes;
@@ -225,8 +225,10 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, uint8
     int most = 0, C = 1;  // 1,024 choices, one round of its warps, per CTA
     if (!cluster_size(&most)) return api_launched(0), GMM_ERR_CUDA;
     while (C < most && (uint32_t)C * kClusterThreads < M) C *= 2;
-    const SortAllArgs a = {g.idx,  {lists[0], lists[1]}, seen,      M, part_of(M, C * kClusterWarps),
-                           g.p->K, plan.passes,          plan.bits, g.flags};
+    const SortAllArgs a = {g.idx,       {lists[0], lists[1]}, seen,
+                           M,           part_of(M, C * kClusterWarps),
+                           g.p->K,      plan.passes,          plan.bits,
+                           g.flags};
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -328,8 +330,8 @@ gmm_status fill_launch(const GradCall& g, size_t size, uint64_t rows) {
                          kEmbedThreads, 0, g.st, a);
 }
 
-// Rows that get their zeros beside the sort: what goes through while it runs (6 GB in a ms, from 12 us on
-// 1 us more for every 8,192 choices).  All of them where there are no sums.
+// Rows that get their zeros beside the sort: what goes through while it runs (6 GB in a ms, from
+// 12 us on 1 us more for every 8,192 choices).  All of them where there are no sums.
 uint64_t beside_rows(const gmm_embed_problem* p, uint32_t M, size_t size) {
   const uint64_t rows = (uint64_t)(6e6 * (12.0 + M / 8192.0) / ((double)p->D * size));
   return M == 0 ? p->K : std::min<uint64_t>(p->K, std::max<uint64_t>(rows, 1));

@@ -81,7 +81,8 @@ gmm_status grad_launch(RouteGradArgs g, int mode, cudaStream_t st) {
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
   constexpr int kRows = 32 / kLanes;
-  const int64_t warps = std::min<int64_t>((g.r.N + kRows - 1) / kRows, (int64_t)sms * kRouteWarps * (kEl <= 16 ? 3 : 2));
+  const int64_t warps = std::min<int64_t>((g.r.N + kRows - 1) / kRows,
+                                          (int64_t)sms * kRouteWarps * route_ctas(kEl));
   g.r.rows = ((g.r.N + warps - 1) / warps + kRows - 1) / kRows * kRows;
   const unsigned grid =
       (unsigned)((g.r.N + g.r.rows * kRouteWarps - 1) / (g.r.rows * kRouteWarps));

@@ -3,8 +3,9 @@
 Tolerances, for u = 2^-24 and sums of c float32 terms one after another: (c + 4) u times the sum of
 the terms' magnitudes (each product and each addition rounds once, and the scale), then half a step
 of the result's type relative to the value, and half its smallest step (float16 2^-25, bfloat16
-2^-134).  A class that is named n times is summed in chunks of at most 128 and the chunks' sums over
-8 warps in turn: c <= min(n, 128) + n / 128 + 8.  dresp: a lane adds up D / 8 terms, then 5 levels.
+2^-134).  A class that is named n times is summed in chunks of 16 to 128, the chunks' sums by 8 to
+256 groups in turn, and those by halves: c <= min(n, 128) + n / 128 + 8.  dresp: a lane adds up at
+most D / 8 terms, then up to 12 levels.
 """
 import numpy as np
 import pytest
@@ -91,8 +92,8 @@ def test_lookup(G, N, m, K, D, pad, shift, dtype):
     tol = (m + 4) * U * size + HALF[dtype] * np.abs(want) + LEAST[dtype]
     _near(G.gmm_embed(W, idx, resp, scale=1.25), want, tol)
     if m == 1:
-        _near(G.gmm_embed(W, idx[:, 0].contiguous(), None if resp is None else resp[:, 0].contiguous(),
-                          scale=1.25), want, tol)
+        one = [None if t is None else t[:, 0].contiguous() for t in (idx, resp)]
+        _near(G.gmm_embed(W, *one, scale=1.25), want, tol)
 
 
 @pytest.mark.parametrize("add", [False, True])
