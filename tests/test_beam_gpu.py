@@ -286,6 +286,47 @@ def test_captured_and_on_another_stream(G):
     assert all(torch.equal(p, q) for p, q in zip(r, G.gmm_beam_select(Z, s, 4)))
 
 
+def test_two_threads_on_two_streams(G):
+    """Calls at the same time, each with memory of its own, give what they give alone."""
+    import threading
+
+    import torch
+
+    def work(seed, stream):
+        rng = np.random.default_rng(seed)
+        with torch.cuda.stream(stream):
+            Z, _ = _logits(rng, 24, 3000, "bf16")
+            s = torch.from_numpy(rng.normal(size=(6, 4)).astype(np.float32)).cuda()
+            W = torch.from_numpy(rng.normal(size=(4000, 64)).astype(np.float32)).cuda()
+            ids = torch.from_numpy(rng.integers(0, 4000, 5000).astype(np.int32)).cuda()
+            cache = torch.from_numpy(rng.normal(size=(24, 2, 40, 16)).astype(np.float32)).cuda()
+            results = []
+            for _ in range(30):
+                r = G.gmm_beam_select(Z, s)
+                c = cache.clone()
+                G.gmm_beam_reorder(c, r.parent, None, 2)
+                x = G.gmm_embed(W, ids)
+                dW, _ = G.gmm_embed_backward(x, ids, 4000)
+                idx, _ = G.gmm_route(x, 4)
+                loss = G.gmm_route_loss(x, idx)
+                results.append((*r, c, x, dW, *loss))
+            stream.synchronize()
+        return results
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone = [work(i, streams[i])[0] for i in range(2)]
+    together = [None, None]
+    threads = [threading.Thread(target=lambda i=i: together.__setitem__(i, work(i, streams[i])))
+               for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for want, got in zip(alone, together):
+        for r in got:
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
 def test_refusals(G):
     import torch
 

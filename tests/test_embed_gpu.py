@@ -158,6 +158,26 @@ def test_lists_of_all_lengths(G, N, K, D, how):
     assert torch.equal(got, got2)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D,pad,shift", [(40, 8, 0), (41, 7, 0), (40, 3, 1), (300, 1, 0)])
+def test_results_in_rows_of_another_tensor(G, D, pad, shift, dtype):
+    """Aligned tables into rows that start anywhere and the other way; what lies between stays."""
+    import torch
+
+    rng = np.random.default_rng(D + pad)
+    N, K = 70, 30
+    for table in ((pad, shift), (0, 0)):
+        W, w = _rows(rng, K, D, dtype, *table)
+        idx, resp, i, r = _assignment(rng, N, 2, K, True)
+        buf = torch.full((N * (D + pad) + shift + 64,), 7.0, dtype=_t(dtype), device="cuda")
+        out = buf[shift:shift + N * (D + pad)].view(N, D + pad)[:, :D]
+        assert G.gmm_embed(W, idx, resp, out=out) is out
+        want, size = A.embed(w, i, r)
+        _near(out, want, 6 * U * size + HALF[dtype] * np.abs(want) + LEAST[dtype])
+        out.fill_(7.0)
+        assert (buf == 7).all()
+
+
 def test_nothing_to_look_up(G):
     import torch
 
@@ -292,12 +312,15 @@ def test_refusals(G):
                 lambda: G.gmm_embed_backward(dY, idx, 7, W=W),
                 lambda: G.gmm_embed_backward(dY, idx, 6, accumulate=True),
                 lambda: G.gmm_embed_backward(dY, idx, 6, out=W.half()),
-                lambda: G.gmm_embed_backward(dY, idx, 6, out=W[:5])):
+                lambda: G.gmm_embed_backward(dY, idx, 6, out=W[:5]),
+                lambda: G.gmm_embed_backward(dY[:, :1].expand(4, 8), idx, 6)):
         with pytest.raises((TypeError, ValueError)):
             bad()
     with pytest.raises(G.GmmError):
         G.gmm_embed(W, torch.zeros(4, 9, dtype=torch.int32, device="cuda"))
     with pytest.raises(G.GmmError):
         G.gmm_embed(W, idx, scale=float("nan"))
+    with pytest.raises(G.GmmError):  # one row for all
+        G.gmm_embed_backward(dY[:1].expand(4, 8), idx, 6)
     with pytest.raises(G.GmmError):
         G.gmm_embed_backward(dY, idx, 6, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))

@@ -160,6 +160,29 @@ def test_gradient(G, N, K, m, S, masks, pad, shift, dtype, renorm, what):
             assert torch.equal(flat, got)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,pad,shift", [(64, 8, 0), (64, 3, 0), (200, 0, 1), (1000, 5, 3)])
+def test_gradient_in_rows_of_another_tensor(G, K, pad, shift, dtype):
+    """Rows of Z that start on 16 bytes and of dZ that do not: the same to a rounding of the type
+    (vectors or single entries, the same arithmetic); what lies between the rows stays."""
+    import torch
+
+    N, m = 150, 4
+    Z, x, i, _, _, idx, _, _, _ = _case(K, N, K, m, dtype)
+    d, one = torch.randn(N, m, device="cuda"), torch.ones(1, device="cuda")
+    loss = G.gmm_route_loss(Z, idx)
+    args = (Z, idx, d, False, loss.counts, loss.rows, one, one)
+    want = G.gmm_route_backward(*args).double()
+    buf = torch.full((N * (K + pad) + shift + 64,), 7.0, dtype=_t(dtype), device="cuda")
+    out = buf[shift:shift + N * (K + pad)].view(N, K + pad)[:, :K]
+    assert G.gmm_route_backward(*args, out=out) is out
+    # sums over lanes in another order: (K / 8 + 30) u of a row's largest terms, and a rounding
+    tol = (K / 8 + 30) * U * 4 * want.abs().amax(1, keepdim=True) + 2 * HALF[dtype] * want.abs()
+    assert ((out.double() - want).abs() <= tol + LEAST[dtype]).all()
+    out.fill_(7.0)
+    assert (buf == 7).all()
+
+
 def test_gradient_is_what_the_losses_change_by(G):
     """Central differences of the library's own losses in float32: their error is that of the loss
     (a few 1e-7 of about 1) over the step, 1e-5 at a step of 0.05, plus the step's square times the
