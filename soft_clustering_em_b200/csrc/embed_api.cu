@@ -337,6 +337,23 @@ uint64_t beside_rows(const gmm_embed_problem* p, uint32_t M, size_t size) {
   return M == 0 ? p->K : std::min<uint64_t>(p->K, std::max<uint64_t>(rows, 1));
 }
 
+// Up to kFew choices, in one launch (and the weights' gradient in one before it).
+template <typename T, typename TO, int kMode>
+gmm_status few_launch(const GradCall& g, EmbedGradArgs a) {
+  const gmm_embed_problem* p = g.p;
+  gmm_status s = dot_vec<T>(g, true);
+  if (s != GMM_OK) return s;
+  const int groups = kEmbedThreads / a.lanes;
+  a.sum_blocks = (a.M + groups - 1) / groups;
+  const uint64_t bytes = (uint64_t)p->D * sizeof(TO);
+  a.fill_rows = (int)std::max<uint64_t>(8, std::min<uint64_t>(kFewRows, 131072 / bytes / 8 * 8));
+  const unsigned fill = g.add ? 0 : (unsigned)((p->K + a.fill_rows - 1) / a.fill_rows);
+  const EmbedFewArgs f = {a, g.idx, g.flags};
+  return api_launch_next(embed_few_kernel<T, TO, kMode>,
+                         dim3(a.sum_blocks + fill, (a.units + a.lanes - 1) / a.lanes),
+                         kEmbedThreads, 0, g.st, f);
+}
+
 // Stream order: the sort; beside it the weights' gradient and rows of zeros; then the sums.
 template <typename T, typename TO, int kMode>
 gmm_status grad_launch(const GradCall& g) {
@@ -346,12 +363,6 @@ gmm_status grad_launch(const GradCall& g) {
   constexpr int V = Unit<T, kMode>::n;
   EmbedGradArgs a = {};
   gmm_status s;
-  const uint64_t beside = g.add ? p->K : beside_rows(p, M, sizeof(TO));
-  uint8_t* seen = beside < (uint64_t)p->K ? (uint8_t*)(g.ws + L.seen) : nullptr;
-  if ((s = sort_launch(g, L, M, seen, &a.list)) != GMM_OK) return s;
-  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
-  if (!g.add && (s = fill_launch(g, sizeof(TO), beside)) != GMM_OK) return s;
-  if (M == 0) return GMM_OK;
   a.dY = g.dY;
   a.resp = g.resp;
   a.dW = g.dW;
@@ -370,6 +381,13 @@ gmm_status grad_launch(const GradCall& g) {
   a.scale = p->scale;
   a.m = p->m;
   a.add = g.add;
+  if (M > 0 && M <= kFew) return few_launch<T, TO, kMode>(g, a);
+  const uint64_t beside = g.add ? p->K : beside_rows(p, M, sizeof(TO));
+  uint8_t* seen = beside < (uint64_t)p->K ? (uint8_t*)(g.ws + L.seen) : nullptr;
+  if ((s = sort_launch(g, L, M, seen, &a.list)) != GMM_OK) return s;
+  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
+  if (!g.add && (s = fill_launch(g, sizeof(TO), beside)) != GMM_OK) return s;
+  if (M == 0) return GMM_OK;
   const unsigned groups = kEmbedThreads / a.lanes;
   a.sum_blocks = (a.chunks + groups - 1) / groups;
   // the other rows' zeros: blocks of about 128 KB, one per SM ahead of the sums' so that the memory
