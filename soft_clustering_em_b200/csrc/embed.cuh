@@ -61,8 +61,14 @@ struct Unit {
   static __device__ __forceinline__ Raw load(const T* row, int i, int lanes, int D) {
     if constexpr (!kVec) {
       Raw r;
+      const T* p = row + i;
+      if (i + (n - 1) * lanes < D) {
 #pragma unroll
-      for (int e = 0; e < n; e++) r.x[e] = i + e * lanes < D ? row[i + e * lanes] : T(0.f);
+        for (int e = 0; e < n; e++, p += lanes) r.x[e] = *p;
+      } else {
+#pragma unroll
+        for (int e = 0; e < n; e++, p += lanes) r.x[e] = i + e * lanes < D ? *p : T(0.f);
+      }
       return r;
     } else {
       if (kMode == 2 || i + n <= D) return load16(row + i);
@@ -90,9 +96,15 @@ struct Unit {
   static __device__ __forceinline__ void store(T* row, int i, int lanes, int D,
                                                const float (&x)[n]) {
     if constexpr (!kVec) {
+      T* p = row + i;
+      if (i + (n - 1) * lanes < D) {
 #pragma unroll
-      for (int e = 0; e < n; e++)
-        if (i + e * lanes < D) from_f32(row + i + e * lanes, x[e]);
+        for (int e = 0; e < n; e++, p += lanes) from_f32(p, x[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < n; e++, p += lanes)
+          if (i + e * lanes < D) from_f32(p, x[e]);
+      }
     } else {
       if (kMode == 2 || i + n <= D) {
         if (kStream) __stcs(reinterpret_cast<uint4*>(row + i), Vec16<T>::pack(x));
@@ -141,6 +153,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
       if (k[j] != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
       w[j] = 0.f;
     }
+    w[j] *= a.scale;
     const T* from = (const T*)a.W + (ok ? k[j] : 0) * a.ldw;
 #pragma unroll
     for (int p = 0; p < kPer; p++)
@@ -158,8 +171,6 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
 #pragma unroll
       for (int e = 0; e < U::n; e++) y[e] = kM == 1 ? w[j] * x[e] : fmaf(w[j], x[e], y[e]);
     }
-#pragma unroll
-    for (int e = 0; e < U::n; e++) y[e] *= a.scale;
     U::template store<true>(to, at(p), lanes, a.D, y);
   }
 }
