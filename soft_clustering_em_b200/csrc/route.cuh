@@ -158,6 +158,28 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // ------------------------------------------------------------------ load and losses
+struct RouteLossOut {
+  float *balance, *z, *load;
+  int32_t *counts, *rows;
+};
+
+// The results of segment s, by one thread each: of an expert (its sum of p and its choices; returns
+// its part of balance before scaling), and of the whole segment.
+__device__ __forceinline__ double write_expert(const RouteArgs& a, const RouteLossOut& o, int s,
+                                               int k, double p, uint32_t c, double L) {
+  if (o.load) o.load[(int64_t)s * a.K + k] = (float)(p / L);
+  if (o.counts) o.counts[(int64_t)s * a.K + k] = (int32_t)c;
+  return (double)c * p;
+}
+__device__ __forceinline__ void write_segment(const RouteArgs& a, const RouteLossOut& o, int s,
+                                              double balance, double z, uint32_t n, bool legal) {
+  const float nan = __int_as_float(0x7fffffff);
+  const double L = n > 0 ? (double)n : 1.0;
+  if (o.balance) o.balance[s] = legal ? (float)(balance * a.K / (a.m * L * L)) : nan;
+  if (o.z) o.z[s] = legal ? (float)(z / L) : nan;
+  if (o.rows) o.rows[s] = (int32_t)n;
+}
+
 // A CTA takes `rows` rows.  For each segment that they meet, in order, column sums stay in
 // registers until the segment or the rows end; the sums of piece (CTA c, segment s) go to slot
 // c + s, which no other piece has: from piece to piece c or s grows, or both.
@@ -165,9 +187,12 @@ __device__ __forceinline__ float group_sum(float v) {
 // 65,536 rows of 256 fp32, the joining kernel with it: 22 us (10.6 us of bytes), 16.5 of them this
 // kernel's, at 3.6 TB/s: few rows per warp, so that the first loads and the joining of the columns
 // weigh.  262,144 rows: 54 us (41).  65,536 of 1,024: 71 us (41).
-template <typename T, int kLanes, int kEl, int kMode>
+//
+// kDirect, for few rows: a CTA takes a segment and writes its results, in one launch.  (50 rows in
+// 64 segments: 3.5 us, 13 with the joining kernel.)
+template <typename T, int kLanes, int kEl, int kMode, bool kDirect>
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
-    route_load_kernel(RouteArgs a, float* part) {
+    route_load_kernel(RouteArgs a, float* part, RouteLossOut o) {
   constexpr int kRows = 32 / kLanes;
   constexpr int V = Vec16<T>::n;
   constexpr int kChunks = kEl / V;
@@ -176,20 +201,30 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
   __shared__ uint32_t hist[kPlaces];
   __shared__ float zsum[kRouteWarps];
   __shared__ uint32_t rsum[kRouteWarps];
+  __shared__ double bsum[kRouteWarps];  // with kDirect
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, l = lane % kLanes;
   grid_dependents_launch();
-  const int64_t r0 = blockIdx.x * a.rows, r1 = min(r0 + a.rows, a.N);
-  int s = segment_of(a.offsets, a.S, r0);
+  const int64_t r0 = kDirect ? 0 : blockIdx.x * a.rows;
+  const int64_t r1 = kDirect ? a.N : min(r0 + a.rows, a.N);
+  int s = kDirect ? (int)blockIdx.x : segment_of(a.offsets, a.S, r0);
+  const int s_end = kDirect ? s + 1 : a.S;
   for (int i = t; i < a.K; i += kRouteThreads) hist[i] = 0;
   __syncthreads();
-  for (; s < a.S; s++) {
+  for (; s < s_end; s++) {
     int64_t lo = r0, hi = r1;
+    bool legal = true;
     if (a.offsets) {
-      lo = max(r0, (int64_t)a.offsets[s]);
-      hi = min(r1, (int64_t)a.offsets[s + 1]);
-      if (a.offsets[s] >= r1) break;
+      const int64_t from = a.offsets[s], to = a.offsets[s + 1];
+      legal = from >= 0 && from <= to && to <= a.N;
+      lo = max(r0, from);
+      hi = min(r1, to);
+      if (!kDirect && from >= r1) break;
     }
-    if (lo >= hi) continue;  // (the same for all threads)
+    if (!kDirect && lo >= hi) continue;  // (the same for all threads)
+    if (kDirect && !legal) {
+      hi = lo = 0;
+      if (t == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+    }
     float acc[kEl] = {};
     float zs = 0.f;
     uint32_t live_rows = 0;
@@ -246,30 +281,42 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     }
     if (lane == 0) zsum[w] = zs, rsum[w] = live_rows;
     __syncthreads();
+    float z = 0.f;
+    uint32_t rows = 0;
+    for (int i = 0; i < kRouteWarps; i++) z += zsum[i], rows += rsum[i];
     float* slot = part + (blockIdx.x + (int64_t)s) * route_slot(a.K);
+    const double L = rows > 0 ? (double)rows : 1.0;
+    double balance = 0.0;
     for (int k = t; k < a.K; k += kRouteThreads) {
       float p = 0.f;
 #pragma unroll
       for (int i = 0; i < kRouteWarps; i++) p += sums[i][k];
-      slot[k] = p;
-      reinterpret_cast<uint32_t*>(slot)[a.K + k] = hist[k];
-      hist[k] = 0;
+      if constexpr (kDirect) {
+        balance += write_expert(a, o, s, k, p, hist[k], L);
+      } else {
+        slot[k] = p;
+        reinterpret_cast<uint32_t*>(slot)[a.K + k] = hist[k];
+        hist[k] = 0;
+      }
     }
-    if (t == 0) {
-      float z = 0.f;
-      uint32_t n = 0;
-      for (int i = 0; i < kRouteWarps; i++) z += zsum[i], n += rsum[i];
-      slot[2 * a.K] = z;
-      reinterpret_cast<uint32_t*>(slot)[2 * a.K + 1] = n;
+    if constexpr (kDirect) {
+      balance = warp_sum(balance);
+      if (lane == 0) bsum[w] = balance;
+      __syncthreads();
+      if (t == 0) {
+        balance = 0.0;
+        for (int i = 0; i < kRouteWarps; i++) balance += bsum[i];
+        write_segment(a, o, s, balance, z, rows, legal);
+      }
+    } else {
+      if (t == 0) {
+        slot[2 * a.K] = z;
+        reinterpret_cast<uint32_t*>(slot)[2 * a.K + 1] = rows;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
-
-struct RouteLossOut {
-  float *balance, *z, *load;
-  int32_t *counts, *rows;
-};
 
 // A cluster per segment adds up its slots, in order, in 64 bits; each CTA has a share of the
 // experts.  Threads: `cols` columns (a power of two) times groups that take every so many slots.
@@ -336,9 +383,7 @@ __global__ void __launch_bounds__(kReduceThreads)
     }
     if (g == 0 && k < a.K) {
       for (int i = 1; i < groups; i++) p += sh[i * cols + col], c += shc[i * cols + col];
-      if (o.load) o.load[(int64_t)s * a.K + k] = (float)(p / L);
-      if (o.counts) o.counts[(int64_t)s * a.K + k] = (int32_t)c;
-      balance += (double)c * p;
+      balance += write_expert(a, o, s, k, p, c, L);
     }
     __syncthreads();
   }
@@ -359,10 +404,7 @@ __global__ void __launch_bounds__(kReduceThreads)
   if (rank == 0 && t == 0) {
     balance = 0.0;
     for (int r = 0; r < ctas; r++) balance += of_cta[r];
-    const float nan = __int_as_float(0x7fffffff);
-    if (o.balance) o.balance[s] = legal ? (float)(balance * a.K / (a.m * L * L)) : nan;
-    if (o.z) o.z[s] = legal ? (float)(z / L) : nan;
-    if (o.rows) o.rows[s] = (int32_t)n;
+    write_segment(a, o, s, balance, z, n, legal);
   }
 }
 

@@ -54,25 +54,38 @@ int route_mode(bool aligned, int K) {
   return !aligned ? 0 : K % Vec16<T>::n != 0 ? 1 : 2;
 }
 
+// Whether the rows are few enough for one launch, a CTA per segment, in `*direct`: 8 turns of its
+// warps at most, should one segment have all.  (256 rows of 64: 6.7 us, 7.4 by two kernels; 512:
+// 10.4 and 7.5.)
 template <typename T, int kLanes, int kEl>
-gmm_status load_launch(const RouteArgs& a, float* part, int mode, unsigned grid, cudaStream_t st) {
-  auto kern = mode == 0   ? route_load_kernel<T, kLanes, kEl, 0>
-              : mode == 1 ? route_load_kernel<T, kLanes, kEl, 1>
-                          : route_load_kernel<T, kLanes, kEl, 2>;
-  kern<<<grid, kRouteThreads, 0, st>>>(a, part);
-  return api_launched(1);
+gmm_status load_launch(const RouteArgs& a, float* part, const RouteLossOut& o, int mode,
+                       bool* direct, cudaStream_t st) {
+  *direct = a.N <= 8 * kRouteWarps * (32 / kLanes);
+  auto go = [&](auto kern, int64_t grid) {
+    kern<<<(unsigned)grid, kRouteThreads, 0, st>>>(a, part, o);
+    return api_launched(1);
+  };
+  if (*direct)
+    return mode == 0   ? go(route_load_kernel<T, kLanes, kEl, 0, true>, a.S)
+           : mode == 1 ? go(route_load_kernel<T, kLanes, kEl, 1, true>, a.S)
+                       : go(route_load_kernel<T, kLanes, kEl, 2, true>, a.S);
+  const int64_t grid = (a.N + a.rows - 1) / a.rows;
+  return mode == 0   ? go(route_load_kernel<T, kLanes, kEl, 0, false>, grid)
+         : mode == 1 ? go(route_load_kernel<T, kLanes, kEl, 1, false>, grid)
+                     : go(route_load_kernel<T, kLanes, kEl, 2, false>, grid);
 }
 
 // Lanes and places per row.  Here up to 16 places, so that three CTAs are resident: 262,144 rows of
 // 256 fp32 take 54 us with 16 lanes of 16, 62 with 8 of 32.
 template <typename T>
-gmm_status load_dispatch(const RouteArgs& a, float* part, unsigned grid, cudaStream_t st) {
+gmm_status load_dispatch(const RouteArgs& a, float* part, const RouteLossOut& o, bool* direct,
+                         cudaStream_t st) {
   const int mode = route_mode<T>((uintptr_t)a.Z % 16 == 0 && a.ld * sizeof(T) % 16 == 0, a.K);
-  if (a.K <= 64) return load_launch<T, 8, 8>(a, part, mode, grid, st);
-  if (a.K <= 128) return load_launch<T, 8, 16>(a, part, mode, grid, st);
-  if (a.K <= 256) return load_launch<T, 16, 16>(a, part, mode, grid, st);
-  if (a.K <= 512) return load_launch<T, 32, 16>(a, part, mode, grid, st);
-  return load_launch<T, 32, 32>(a, part, mode, grid, st);
+  if (a.K <= 64) return load_launch<T, 8, 8>(a, part, o, mode, direct, st);
+  if (a.K <= 128) return load_launch<T, 8, 16>(a, part, o, mode, direct, st);
+  if (a.K <= 256) return load_launch<T, 16, 16>(a, part, o, mode, direct, st);
+  if (a.K <= 512) return load_launch<T, 32, 16>(a, part, o, mode, direct, st);
+  return load_launch<T, 32, 32>(a, part, o, mode, direct, st);
 }
 
 template <typename T, int kLanes, int kEl>
@@ -135,12 +148,13 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   const RouteArgs a = {Z,    r->N,    r->ld, r->K,      r->scale, idx, m,
                        mask, offsets, S,     plan.rows, dev_flags};
   cudaStream_t st = (cudaStream_t)stream;
+  const RouteLossOut o = {balance, z, load, counts, rows};
   if (r->N > 0) {
-    const unsigned grid = (unsigned)((r->N + plan.rows - 1) / plan.rows);
-    s = r->dtype == GMM_F32    ? load_dispatch<float>(a, (float*)ws, grid, st)
-        : r->dtype == GMM_BF16 ? load_dispatch<__nv_bfloat16>(a, (float*)ws, grid, st)
-                               : load_dispatch<__half>(a, (float*)ws, grid, st);
-    if (s != GMM_OK) return s;
+    bool direct = false;
+    s = r->dtype == GMM_F32    ? load_dispatch<float>(a, (float*)ws, o, &direct, st)
+        : r->dtype == GMM_BF16 ? load_dispatch<__nv_bfloat16>(a, (float*)ws, o, &direct, st)
+                               : load_dispatch<__half>(a, (float*)ws, o, &direct, st);
+    if (s != GMM_OK || direct) return s;
   }
   // a cluster per segment: 32 experts to a CTA, up to 8 CTAs, of 1,024 threads, while all segments'
   // are resident at once (64 segments of 7,152 rows of 244: 35 us in clusters of 8, 12 in twos)
@@ -148,7 +162,6 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   const int threads = (int64_t)S * ctas > 296 ? 256 : 1024;
   int cols = 32;
   while (cols * ctas < r->K && cols < threads) cols *= 2;
-  const RouteLossOut o = {balance, z, load, counts, rows};
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
