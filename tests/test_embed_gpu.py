@@ -230,6 +230,42 @@ def test_a_nan_reaches_only_what_it_is_part_of(G):
     assert (dW[0] == 3).all() and dW[1].isnan().all() and dW[2].isnan().all() and (dW[3] == 1).all()
 
 
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("K", [1, 2, 1023, 1024, 1 << 20])
+@pytest.mark.parametrize("M", [31, 127, 128, 129, 1023, 1024, 1025, 16_385, (1 << 17) - 1, 1 << 17,
+                               (1 << 17) + 1])
+def test_where_the_ways_to_sum_change(G, M, K, add):
+    """Numbers of choices beside those at which another path is taken, and digits of the sort; half
+    of the choices name one class.  Whole numbers: the sums are exact."""
+    import torch
+
+    D = 9
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    idx = torch.randint(-1, K, (M,), generator=g, device="cuda", dtype=torch.int32)
+    idx[::2] = K - 1
+    dY = torch.randint(-8, 9, (M, D), generator=g, device="cuda").float()
+    out = torch.full((K, D), 3.0, device="cuda")
+    G.gmm_embed_backward(dY, idx, K, out=out, accumulate=add)
+    want = torch.full((K + 1, D), 3.0 if add else 0.0, device="cuda", dtype=torch.float64)
+    want.index_add_(0, torch.where(idx < 0, K, idx).long(), dY.double())
+    assert torch.equal(out.double(), want[:K])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 128, 129, 591, 592, 593, 2000])
+@pytest.mark.parametrize("D", [8, 256, 264, 512, 520, 1031])
+def test_where_the_ways_to_multiply_change(G, N, D, dtype):
+    """Rows and widths beside those at which the weights' gradient takes other lanes."""
+    rng = np.random.default_rng(N + D)
+    for m in (1, 2, 3, 5):
+        dY, dy = _rows(rng, N, D, dtype)
+        W, w = _rows(rng, 50, D, dtype)
+        idx, resp, i, _ = _assignment(rng, N, m, 50, True)
+        _, dresp = G.gmm_embed_backward(dY, idx, 50, resp, W=W)
+        want, size = A.embed_dresp(dy, w, i)
+        _near(dresp, want, (D / 8 + 12) * U * size)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("K,D,pad,shift", [(60_000, 1000, 0, 0), (60_000, 1000, 8, 0),
                                            (150_001, 301, 0, 0), (150_001, 301, 2, 1),

@@ -81,6 +81,10 @@ CASES = [  # N, K, m, S, masks, pad, shift
     (2500, 256, 8, 7, True, 0, 0), (513, 300, 2, 2, False, 4, 3), (700, 512, 8, 0, True, 0, 0),
     (400, 1024, 1, 300, True, 0, 0), (64, 1023, 8, 1, True, 0, 0), (12_000, 16, 2, 900, True, 0, 0),
     (20_000, 33, 8, 0, False, 0, 0), (5, 3, 8, 1, True, 0, 0),
+    # beside the numbers of rows at which one launch becomes two
+    (256, 64, 2, 3, True, 0, 0), (257, 64, 2, 3, True, 0, 0), (128, 256, 2, 0, True, 0, 0),
+    (129, 256, 2, 0, True, 0, 0), (64, 600, 2, 2, True, 0, 0), (65, 600, 2, 2, True, 0, 0),
+    (200, 7, 2, 500, True, 0, 0),
 ]
 
 
