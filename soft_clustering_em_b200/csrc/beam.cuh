@@ -148,9 +148,11 @@ struct ReorderArgs {
   uint32_t* flags;
 };
 
-// Columns of a thread in a tile, and CTAs per SM: all of a launch are resident at once.
-constexpr int reorder_cols(int w) { return w <= 2 ? 4 : w <= 4 ? 2 : 1; }
-constexpr int reorder_ctas(int w) { return w <= 8 ? 3 : w <= 16 ? 2 : 1; }
+// Columns of a thread in a tile, and CTAs per SM: all of a launch are resident at once.  (16 groups
+// of 4 beams take 149 us with four columns and two CTAs, 175 with two and three; groups of 8 193 us
+// with one column and three CTAs, 200 with two and two.)
+constexpr int reorder_cols(int w) { return w <= 4 ? 4 : 1; }
+constexpr int reorder_ctas(int w) { return w <= 2 ? 3 : w <= 4 ? 2 : w <= 8 ? 3 : w <= 16 ? 2 : 1; }
 
 // kW: at least w.  The blocks share out tiles of columns: of the groups in which a beam moves, up
 // to their lengths, for every state.
