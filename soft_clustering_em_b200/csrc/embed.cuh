@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   const int64_t row =
       (int64_t)blockIdx.x * (kEmbedThreads >> a.lane_bits) + (threadIdx.x >> a.lane_bits);
   auto at = [&](int p) { return U::at((int)(blockIdx.y * kPer + p) << a.lane_bits, l, lanes); };
+  grid_dependency_wait();
+  grid_dependents_launch();
   if (row >= a.N) return;
   int k[kM];
   float w[kM];

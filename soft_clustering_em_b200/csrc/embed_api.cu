@@ -68,8 +68,7 @@ gmm_status embed_launch(EmbedArgs a, cudaStream_t st) {
   auto go = [&](auto kern) {
     const int rows = kEmbedThreads >> a.lane_bits, width = per << a.lane_bits;
     const dim3 grid((unsigned)((a.N + rows - 1) / rows), (a.units + width - 1) / width);
-    kern<<<grid, kEmbedThreads, 0, st>>>(a);
-    return api_launched(1);
+    return api_launch_next(kern, grid, kEmbedThreads, 0, st, a);
   };
   shape(few ? 1 : a.m <= 2 ? 4 : a.m <= 4 ? 2 : 1);
   if (a.m == 1)

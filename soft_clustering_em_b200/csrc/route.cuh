@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
   __shared__ uint32_t rsum[kRouteWarps];
   __shared__ double bsum[kRouteWarps];  // with kDirect
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, l = lane % kLanes;
+  grid_dependency_wait();
   grid_dependents_launch();
   const int64_t r0 = kDirect ? 0 : blockIdx.x * a.rows;
   const int64_t r1 = kDirect ? a.N : min(r0 + a.rows, a.N);
@@ -437,6 +438,8 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
   const int lane = threadIdx.x & 31, l = lane % kLanes;
   const int64_t warp = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
   const int64_t r0 = warp * a.rows, r1 = min(r0 + a.rows, a.N);
+  grid_dependency_wait();
+  grid_dependents_launch();
   if (r0 >= r1) return;
   const bool losses = g.dbalance || g.dz;
   int s = losses ? segment_of(a.offsets, a.S, r0) : 0, have = -1;

@@ -62,8 +62,7 @@ gmm_status load_launch(const RouteArgs& a, float* part, const RouteLossOut& o, i
                        bool* direct, cudaStream_t st) {
   *direct = a.N <= 8 * kRouteWarps * (32 / kLanes);
   auto go = [&](auto kern, int64_t grid) {
-    kern<<<(unsigned)grid, kRouteThreads, 0, st>>>(a, part, o);
-    return api_launched(1);
+    return api_launch_next(kern, dim3((unsigned)grid), kRouteThreads, 0, st, a, part, o);
   };
   if (*direct)
     return mode == 0   ? go(route_load_kernel<T, kLanes, kEl, 0, true>, a.S)
@@ -102,8 +101,7 @@ gmm_status grad_launch(RouteGradArgs g, int mode, cudaStream_t st) {
   auto kern = mode == 0   ? route_grad_kernel<T, kLanes, kEl, 0>
               : mode == 1 ? route_grad_kernel<T, kLanes, kEl, 1>
                           : route_grad_kernel<T, kLanes, kEl, 2>;
-  kern<<<grid, kRouteThreads, 0, st>>>(g);
-  return api_launched(1);
+  return api_launch_next(kern, dim3(grid), kRouteThreads, 0, st, g);
 }
 
 // Here few lanes, so that a warp has four rows to share its reductions and the rows' fixed part:
