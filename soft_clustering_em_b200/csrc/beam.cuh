@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
 //
 // Bound by memory.  16 groups of 8 beams, four caches of 8 x 1,024 x 128 bf16, 300 to 1,024
 // positions used: 191 to 209 us, 5.2 TB/s (157 us at the rate of a large copy; reads and writes
-// take turns on 16 streams per block).  2 groups of 32: 324 us (258).  16 of 4: 179 (125).
+// take turns on 16 streams per block).  2 groups of 32: 324 us (258).  16 of 4: 151 (125).
 struct BeamState {
   char* base;
   int64_t row_stride, outer_stride;  // bytes

@@ -123,10 +123,10 @@ struct Unit {
 // choices and addresses are formed once for kPer * kM units, all on their way at once.  Blocks y:
 // where a row has more units than that.  kM: at least m.
 //
-// 1e6 rows of 96 fp32, two of 4,096 entries each: 80 to 90 us (61 us of bytes), bound by
+// 1e6 rows of 96 fp32, two of 4,096 entries each: 79 to 89 us (61 us of bytes), bound by
 // instruction issue (2.9 of 4 a clock) and the writes; with a thread per unit, indices and
 // addresses formed for each, 117 to 209.  16,384 of 131,072 rows of 2,048 bf16: 13 us.  8 rows of
-// those: 1.5 us.  Rows that start anywhere go element by element: 239,198 of 185 bf16 take 46 us
+// those: 1.5 us.  Rows that start anywhere go element by element: 239,198 of 185 bf16 take 39 us
 // (14 us of bytes).
 template <typename T, int kMode, int kM, int kPer>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(FillArgs a) {
 // two of 4,096 entries each, added to what is there, and the weights' gradient: 74 to 76 us (13
 // us of bytes): sort 21, weights 22, sums 26, cut runs 6; bound by the sort's latency and by
 // reading each row of dY three times, out of L2 all but once.  (The weights' gradient with the
-// sums, dY read twice: 115; the sums over a group of lanes cost more than the reading.)
+// sums, dY read twice: 80; the sums over a group of lanes cost more than the reading.)
 struct EmbedGradArgs {
   const void* dY;
   const float* resp;       // may be null

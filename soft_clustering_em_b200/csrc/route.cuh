@@ -425,7 +425,7 @@ struct RouteGradArgs {
 // hold the choices: finding them in the registers of the lane that holds the class cost 32
 // compares for each (58 us, now 31, for the first of these).
 //
-// 65,536 rows of 256 fp32 with 8 choices: 31 to 37 us (21 us of bytes).  262,144: 111 us (83), 94
+// 65,536 rows of 256 fp32 with 8 choices: 31 to 35 us (21 us of bytes).  262,144: 111 us (83), 94
 // without the choices' entries.  65,536 of 1,024: 97 us (83).  Of 201 bf16, rows that start
 // anywhere: 35 us (9); of 200: 22.
 template <typename T, int kLanes, int kEl, int kMode>
