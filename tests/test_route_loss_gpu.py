@@ -164,6 +164,30 @@ def test_gradient(G, N, K, m, S, masks, pad, shift, dtype, renorm, what):
             assert torch.equal(flat, got)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("K", [3, 64, 250, 1000])
+def test_an_expert_named_twice(G, K, renorm):
+    """Choices that name the same expert: each counts, and its gradients add up."""
+    import torch
+
+    N, m = 60, 5
+    Z, x, i, _, _, idx, _, _, rng = _case(K + 9, N, K, m, "f32")
+    i[:, 1] = i[:, 0]
+    i[::3, 4] = i[::3, 0]
+    i[::4, 2:] = i[::4, 1:2]
+    i[::7, 3] = -1
+    i[5] = -1
+    idx.copy_(torch.from_numpy(i))
+    d = rng.normal(size=(N, m)).astype(np.float32)
+    loss = G.gmm_route_loss(Z, idx)
+    assert torch.equal(loss.counts[0].cpu(), torch.bincount(idx[idx >= 0].cpu(), minlength=K).int())
+    got = G.gmm_route_backward(Z, idx, torch.from_numpy(d).cuda(), renorm).double().cpu().numpy()
+    want, size = A.route_backward(x, i, d, renorm)
+    top = np.abs(x).max()
+    tol = (2 * _s(K) + (K / 8 + 30) * U + 8 * U * top) * size + HALF["f32"] * np.abs(want)
+    assert (np.abs(got - want) <= tol + LEAST["f32"]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("K,pad,shift", [(64, 8, 0), (64, 3, 0), (200, 0, 1), (1000, 5, 3)])
 def test_gradient_in_rows_of_another_tensor(G, K, pad, shift, dtype):
