@@ -63,13 +63,4 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Programmatic dependent launch: wait until the kernels before this one in the stream are done and
-// their writes visible; let the next kernel's blocks start (they wait in turn).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependents_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 }  // namespace scem

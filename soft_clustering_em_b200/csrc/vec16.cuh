@@ -1,5 +1,5 @@
 // vec16.cuh -- 16-byte vectors of fp32, bf16 and fp16, packed float pairs and a few
-// instructions that the row and expert kernels share.
+// instructions that the row, expert and lookup kernels share.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -168,6 +168,15 @@ __device__ __forceinline__ void from_f32(__half* p, float x) { *p = __float2half
 
 __device__ __forceinline__ uint4 load16(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
+}
+
+// Programmatic dependent launch: wait until the kernels before this one in the stream are done and
+// their writes visible; let the next kernel's blocks start (they wait in turn).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 }  // namespace scem
