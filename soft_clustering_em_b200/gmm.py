@@ -747,27 +747,31 @@ def gmm_route_backward(Z, idx, dresp=None, renorm=False, counts=None, rows=None,
     _vector(dbalance, (S,), torch.float32, "dbalance")
     _vector(dz, (S,), torch.float32, "dz")
     _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    device = Z.device
     if out is None:
-        out = torch.empty(N, K, dtype=Z.dtype, device=Z.device)
-    o = _rows(out, 1.0)
-    if out.dtype != Z.dtype or out.shape != Z.shape:
-        raise ValueError("out must have the shape and type of Z")
-    _launch(load_library().gmm_route_backward, "gmm_route_backward", Z.device, ctypes.byref(r),
+        out, ldd = torch.empty(N, K, dtype=Z.dtype, device=device), K
+    else:
+        if out.dtype != Z.dtype or out.shape != Z.shape:
+            raise ValueError("out must have the shape and type of Z")
+        ldd = _ld(out, "out")
+    _launch(load_library().gmm_route_backward, "gmm_route_backward", device, ctypes.byref(r),
             Z.data_ptr(), idx.data_ptr(), m, _address(dresp), int(bool(renorm)), _address(counts),
             _address(rows), _address(dbalance), _address(dz), _address(mask), _address(offsets),
-            S, out.data_ptr(), o.ld, _address(dev_flags))
+            S, out.data_ptr(), ldd, _address(dev_flags))
     return out
 
 
 def _choices(idx, resp, N=None):
-    """Checks an assignment of N rows (None: any), N x m or N (m = 1); returns its rows."""
-    if idx.dim() not in (1, 2):
+    """Checks an assignment of N rows (None: any), N x m or N (m = 1); returns N and m."""
+    shape = idx.shape
+    if len(shape) not in (1, 2):
         raise ValueError("idx must be N or N x m")
-    if N is not None and idx.shape[0] != N:
-        raise ValueError(f"idx must have {N} rows, got {idx.shape[0]}")
-    _vector(idx, idx.shape, torch.int32, "idx")
-    _vector(resp, idx.shape, torch.float32, "resp")
-    return idx.shape[0]
+    if N is not None and shape[0] != N:
+        raise ValueError(f"idx must have {N} rows, got {shape[0]}")
+    _vector(idx, shape, torch.int32, "idx")
+    if resp is not None:
+        _vector(resp, shape, torch.float32, "resp")
+    return shape if len(shape) == 2 else (shape[0], 1)
 
 
 def _ld(t, name):
@@ -777,13 +781,18 @@ def _ld(t, name):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+def _dtype(t):
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise TypeError(f"rows must be float32, bfloat16 or float16, got {t.dtype}")
+    return dtype
+
+
 def embed_problem(idx, K, scale, ldw, Y) -> gmm_embed_problem:
     """The problem of a gmm_embed or gmm_embed_backward call on these tensors."""
-    if Y.dtype not in _DTYPES:
-        raise TypeError(f"rows must be float32, bfloat16 or float16, got {Y.dtype}")
     N, D = Y.shape
     m = idx.shape[1] if idx.dim() == 2 else 1
-    return gmm_embed_problem(N, m, K, D, _DTYPES[Y.dtype], scale, ldw, _ld(Y, "Y"))
+    return gmm_embed_problem(N, m, K, D, _dtype(Y), scale, ldw, _ld(Y, "Y"))
 
 
 def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=None):
@@ -798,16 +807,18 @@ def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=Non
         with _on(stream, W):
             return gmm_embed(W, idx, resp, scale, out, dev_flags)
     _same_device(W, idx, resp, out, dev_flags)
-    N = _choices(idx, resp)
-    ldw = _ld(W, "W")
+    N, m = _choices(idx, resp)
+    ldw, ldy = _ld(W, "W"), None
     K, D = W.shape
-    _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    if dev_flags is not None:
+        _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    dtype, device = _dtype(W), W.device
     if out is None:
-        out = torch.empty(N, D, dtype=W.dtype, device=W.device)
+        out, ldy = torch.empty(N, D, dtype=W.dtype, device=device), D
     elif out.dtype != W.dtype or out.shape != (N, D):
         raise ValueError("out must be N x D of W's type")
-    p = embed_problem(idx, K, scale, ldw, out)
-    _launch(load_library().gmm_embed, "gmm_embed", W.device, ctypes.byref(p), W.data_ptr(),
+    p = gmm_embed_problem(N, m, K, D, dtype, scale, ldw, _ld(out, "out") if ldy is None else ldy)
+    _launch(load_library().gmm_embed, "gmm_embed", device, ctypes.byref(p), W.data_ptr(),
             idx.data_ptr(), _address(resp), out.data_ptr(), _address(dev_flags))
     return out
 
@@ -833,24 +844,30 @@ def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accum
     _same_device(dY, idx, resp, W, out, ws, dev_flags)
     ldy = _ld(dY, "dY")
     N, D = dY.shape
-    _choices(idx, resp, N)
-    _vector(dev_flags, (1,), torch.int32, "dev_flags")
-    K = int(K)
-    if W is not None and (W.dtype != dY.dtype or W.shape != (K, D)):
-        raise ValueError("W must be K x D of dY's type")
+    m = _choices(idx, resp, N)[1]
+    if dev_flags is not None:
+        _vector(dev_flags, (1,), torch.int32, "dev_flags")
+    K, dtype, device = int(K), _dtype(dY), dY.device
+    ldw = D
+    if W is not None:
+        if W.dtype != dY.dtype or W.shape != (K, D):
+            raise ValueError("W must be K x D of dY's type")
+        ldw = _ld(W, "W")
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to out, which is missing")
-        out = torch.empty(K, D, dtype=dY.dtype, device=dY.device)
-    if out.dtype not in (dY.dtype, torch.float32) or out.shape != (K, D):
-        raise ValueError("out must be K x D of dY's type or float32")
-    dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=dY.device)
-    p = embed_problem(idx, K, scale, D if W is None else _ld(W, "W"), dY)
+        out, ldd = torch.empty(K, D, dtype=dY.dtype, device=device), D
+    else:
+        if out.dtype not in (dY.dtype, torch.float32) or out.shape != (K, D):
+            raise ValueError("out must be K x D of dY's type or float32")
+        ldd = _ld(out, "out")
+    dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=device)
+    p = gmm_embed_problem(N, m, K, D, dtype, scale, ldw, ldy)
     if ws is None:
-        ws = torch.empty(_embed_bytes(N, p.m, K, D, p.dtype), dtype=torch.uint8, device=dY.device)
-    _launch(load_library().gmm_embed_backward, "gmm_embed_backward", dY.device, ctypes.byref(p),
+        ws = torch.empty(_embed_bytes(N, m, K, D, dtype), dtype=torch.uint8, device=device)
+    _launch(load_library().gmm_embed_backward, "gmm_embed_backward", device, ctypes.byref(p),
             dY.data_ptr(), idx.data_ptr(), _address(resp), _address(W), out.data_ptr(),
-            _DTYPES[out.dtype], _ld(out, "out"), int(bool(accumulate)), _address(dresp),
+            _DTYPES[out.dtype], ldd, int(bool(accumulate)), _address(dresp),
             _address(dev_flags), ws.data_ptr(), ws.numel())
     return out, dresp
 
