@@ -950,10 +950,6 @@ def _state_layout(shape, stride, size, rows, dim):
     return stride[0] * size, outer, outer_stride * size, count, per * size, int(dim is not None)
 
 
-def _state(t, rows, dim):
-    return (t.data_ptr(), *_state_layout(t.shape, t.stride(), t.element_size(), rows, dim))
-
-
 def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream=None):
     """The beams' states after their parents, in place: state[b, i] <- state[b, parent[b, i]].
 
@@ -977,7 +973,14 @@ def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream
     dims = list(dim) if isinstance(dim, (list, tuple)) else [dim] * len(states)
     if len(dims) != len(states):
         raise ValueError("dim must be one for each state")
-    packed = b"".join([_STATE.pack(*_state(t, B * w, d)) for t, d in zip(states, dims)])
+    packed, like, layout = [], None, None
+    for t, d in zip(states, dims):  # (caches mostly have one shape)
+        shape, stride = t.shape, t.stride()
+        if like is None or shape != like[0] or stride != like[1] or (t.dtype, d) != like[2:]:
+            like = shape, stride, t.dtype, d
+            layout = _state_layout(shape, stride, t.element_size(), B * w, d)
+        packed.append(_STATE.pack(t.data_ptr(), *layout))
+    packed = b"".join(packed)
     _launch(load_library().gmm_beam_reorder, "gmm_beam_reorder", parent.device, B, w,
             parent.data_ptr(), _address(lens), len(states), packed, _address(dev_flags))
 

@@ -199,20 +199,24 @@ def test_the_binding_packs_states_as_the_header_does():
     assert len(packed) == ctypes.sizeof(st) and bytes(st)[:52] == packed[:52]
 
 
+def layout(t, rows, dim):
+    return G._state_layout(t.shape, t.stride(), t.element_size(), rows, dim)
+
+
 def test_states_that_can_be_reordered():
     t = torch.zeros(6, 3, 5, 4)
-    assert G._state(t, 6, 2)[1:] == (240, 3, 80, 5, 16, 1)
-    assert G._state(t, 6, 1)[1:] == (240, 1, 0, 3, 80, 1)
-    assert G._state(t, 6, None)[1:] == (240, 1, 0, 1, 240, 0)
+    assert layout(t, 6, 2) == (240, 3, 80, 5, 16, 1)
+    assert layout(t, 6, 1) == (240, 1, 0, 3, 80, 1)
+    assert layout(t, 6, None) == (240, 1, 0, 1, 240, 0)
     layers = torch.zeros(2, 6, 3, 5, 4)[1]
-    assert G._state(layers, 6, 2)[1:] == (240, 3, 80, 5, 16, 1)
+    assert layout(layers, 6, 2) == (240, 3, 80, 5, 16, 1)
     with pytest.raises(ValueError):
-        G._state(t.transpose(2, 3), 6, 2)  # positions' widths do not lie densely
+        layout(t.transpose(2, 3), 6, 2)  # positions' widths do not lie densely
     with pytest.raises(ValueError):
-        G._state(t, 5, 2)
+        layout(t, 5, 2)
     by_position = torch.zeros(5, 6, 4).transpose(0, 1)  # positions first
     with pytest.raises(ValueError):
-        G._state(by_position, 6, 1)
+        layout(by_position, 6, 1)
 
 
 def test_binding_refuses_what_it_cannot_pass(lib):
