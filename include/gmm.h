@@ -628,7 +628,8 @@ gmm_status gmm_beam_select(const gmm_rows* r, const void* Z, int32_t w, const fl
  *            nearer end and raises GMM_DEVFLAG_BAD_INDEX.
  *   states   host array of n.  The row of beam (b, i) is base + (b w + i) row_stride; it has
  *            `outer` pieces outer_stride bytes apart (the heads of a cache), each of `count` positions of
- *            pos_bytes bytes.  Rows and pieces must not overlap, nor states one another.
+ *            pos_bytes bytes.  Rows and pieces must not overlap, nor states one
+ *            another (two of one base are refused).
  * 1 <= w <= 32.  Nothing is read or written of groups whose beams all stay.  No workspace.
  * GMM_ERR_UNSUPPORTED: a row of 2^32 or more columns of 16 bytes (4 or 1 where an address, stride
  * or position is not a multiple of 16 bytes).

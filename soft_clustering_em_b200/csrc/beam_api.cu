@@ -103,6 +103,9 @@ gmm_status gmm_beam_reorder(int64_t B, int32_t w, const int32_t* parent, const i
     const double row = (double)s.outer * (double)s.count * (double)s.pos_bytes;
     if (row == 0 || B == 0) continue;
     if (row > 1e18) return GMM_ERR_UNSUPPORTED;
+    for (int j = 0; j < i; j++)  // (one state named twice would be reordered twice at once)
+      if (states[j].base == s.base && states[j].outer && states[j].count && states[j].pos_bytes)
+        return GMM_ERR_INVALID_ARG;
     const int64_t piece = s.count * s.pos_bytes;  // (rows and pieces lie apart)
     if (!s.base || (B * w > 1 && s.row_stride < piece) || (s.outer > 1 && s.outer_stride < piece))
       return GMM_ERR_INVALID_ARG;

@@ -957,7 +957,8 @@ def gmm_beam_reorder(states, parent, lens=None, dim=None, dev_flags=None, stream
     width), token ids (B * w, positions), any type); parent: B x w int32, a beam of the same group,
     -1 to leave one as it is.  dim: the dimension of the positions, for all states or a list with
     one for each, None for states without; lens (B int32): how many positions of a group are used,
-    those behind are left as they are.  w <= 32.
+    those behind are left as they are.  w <= 32.  States must not overlap: one that serves twice is
+    named once.
     """
     states = [states] if isinstance(states, torch.Tensor) else list(states)
     if stream is not None:

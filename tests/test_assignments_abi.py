@@ -193,6 +193,14 @@ def test_reordering_arguments(lib):
     assert reorder(lib, n=0, parent=0) == OK
 
 
+def test_a_state_named_twice(lib):
+    for second in (state(), state(outer=1), state(pos=4)):
+        two = (type(second) * 2)(state(), second)
+        assert lib.gmm_beam_reorder(3, 2, P(16), P(0), 2, two, P(0), P(0)) == BAD
+    two = (type(second) * 2)(state(count=0), state(count=0))  # nothing in them
+    assert lib.gmm_beam_reorder(3, 2, P(16), P(0), 2, two, P(0), P(0)) == OK
+
+
 def test_the_binding_packs_states_as_the_header_does():
     st = state()
     packed = G._STATE.pack(16, 64, 2, 32, 4, 8, 1)
