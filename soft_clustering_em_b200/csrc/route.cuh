@@ -180,6 +180,16 @@ __device__ __forceinline__ void write_segment(const RouteArgs& a, const RouteLos
   if (o.rows) o.rows[s] = (int32_t)n;
 }
 
+// 32 bits of CTA r's shared memory, at the place of `here` in this one's.
+__device__ __forceinline__ uint32_t ld_cluster(const void* here, int r) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
+               : "r"(sm100::map_to_rank(sm100::smem_u32(here), r))
+               : "memory");
+  return v;
+}
+
 // A CTA takes `rows` rows.  For each segment that they meet, in order, column sums stay in
 // registers until the segment or the rows end; the sums of piece (CTA c, segment s) go to slot
 // c + s, which no other piece has: from piece to piece c or s grows, or both.
@@ -188,8 +198,9 @@ __device__ __forceinline__ void write_segment(const RouteArgs& a, const RouteLos
 // kernel's, at 3.6 TB/s: few rows per warp, so that the first loads and the joining of the columns
 // weigh.  262,144 rows: 54 us (41).  65,536 of 1,024: 71 us (41).
 //
-// kDirect, for few rows: a CTA takes a segment and writes its results, in one launch.  (50 rows in
-// 64 segments: 3.5 us, 13 with the joining kernel.)
+// kDirect, for few rows: a cluster of up to 8 CTAs takes a segment, and its first CTA adds up what
+// the others left in their shared memory and writes the results, in one launch.  (50 rows in 64
+// segments: 3.5 us, 13 with the joining kernel; 512 rows of 64: 4.7 and 7.0.)
 template <typename T, int kLanes, int kEl, int kMode, bool kDirect>
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     route_load_kernel(RouteArgs a, float* part, RouteLossOut o) {
@@ -201,13 +212,17 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
   __shared__ uint32_t hist[kPlaces];
   __shared__ float zsum[kRouteWarps];
   __shared__ uint32_t rsum[kRouteWarps];
-  __shared__ double bsum[kRouteWarps];  // with kDirect
+  __shared__ double bsum[kRouteWarps];  // with kDirect, and the CTA's z and rows
+  __shared__ float z_here;
+  __shared__ uint32_t rows_here;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, l = lane % kLanes;
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t r0 = kDirect ? 0 : blockIdx.x * a.rows;
   const int64_t r1 = kDirect ? a.N : min(r0 + a.rows, a.N);
-  int s = kDirect ? (int)blockIdx.x : segment_of(a.offsets, a.S, r0);
+  const int rank = kDirect ? (int)sm100::cluster_ctarank() : 0;
+  const int ctas = kDirect ? (int)sm100::cluster_nctarank() : 1;
+  int s = kDirect ? (int)blockIdx.x / ctas : segment_of(a.offsets, a.S, r0);
   const int s_end = kDirect ? s + 1 : a.S;
   for (int i = t; i < a.K; i += kRouteThreads) hist[i] = 0;
   __syncthreads();
@@ -225,6 +240,12 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     if (kDirect && !legal) {
       hi = lo = 0;
       if (t == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
+    }
+    if (kDirect) {  // the CTA's share: whole turns of its warps
+      constexpr int kTurn = kRouteWarps * kRows;
+      const int64_t per = ((hi - lo + ctas - 1) / ctas + kTurn - 1) / kTurn * kTurn;
+      lo = min(lo + rank * per, hi);
+      hi = min(lo + per, hi);
     }
     float acc[kEl] = {};
     float zs = 0.f;
@@ -285,30 +306,49 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     float z = 0.f;
     uint32_t rows = 0;
     for (int i = 0; i < kRouteWarps; i++) z += zsum[i], rows += rsum[i];
-    float* slot = part + (blockIdx.x + (int64_t)s) * route_slot(a.K);
-    const double L = rows > 0 ? (double)rows : 1.0;
-    double balance = 0.0;
+    float* slot = kDirect ? sums[0] : part + (blockIdx.x + (int64_t)s) * route_slot(a.K);
     for (int k = t; k < a.K; k += kRouteThreads) {
       float p = 0.f;
 #pragma unroll
       for (int i = 0; i < kRouteWarps; i++) p += sums[i][k];
-      if constexpr (kDirect) {
-        balance += write_expert(a, o, s, k, p, hist[k], L);
-      } else {
-        slot[k] = p;
+      slot[k] = p;
+      if constexpr (!kDirect) {
         reinterpret_cast<uint32_t*>(slot)[a.K + k] = hist[k];
         hist[k] = 0;
       }
     }
     if constexpr (kDirect) {
-      balance = warp_sum(balance);
-      if (lane == 0) bsum[w] = balance;
-      __syncthreads();
-      if (t == 0) {
-        balance = 0.0;
-        for (int i = 0; i < kRouteWarps; i++) balance += bsum[i];
-        write_segment(a, o, s, balance, z, rows, legal);
+      if (t == 0) z_here = z, rows_here = rows;
+      if (ctas > 1) sm100::cluster_sync();
+      else __syncthreads();
+      if (rank == 0) {
+        double z_all = z, balance = 0.0;
+        for (int r = 1; r < ctas; r++) {
+          z_all += __uint_as_float(ld_cluster(&z_here, r));
+          rows += ld_cluster(&rows_here, r);
+        }
+        const double L = rows > 0 ? (double)rows : 1.0;
+        for (int k = t; k < a.K; k += kRouteThreads) {
+          double p = sums[0][k];
+          uint32_t c = hist[k];
+#pragma unroll 7
+          for (int r = 1; r < ctas; r++) {
+            p += __uint_as_float(ld_cluster(&sums[0][k], r));
+            c += ld_cluster(&hist[k], r);
+          }
+          balance += write_expert(a, o, s, k, p, c, L);
+        }
+        balance = warp_sum(balance);
+        if (lane == 0) bsum[w] = balance;
+        __syncthreads();
+        if (t == 0) {
+          balance = 0.0;
+          for (int i = 0; i < kRouteWarps; i++) balance += bsum[i];
+          write_segment(a, o, s, balance, z_all, rows, legal);
+        }
       }
+      __syncwarp();
+      if (ctas > 1) sm100::cluster_sync();  // (shared memory is there until it has been read)
     } else {
       if (t == 0) {
         slot[2 * a.K] = z;

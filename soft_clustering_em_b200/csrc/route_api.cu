@@ -54,24 +54,41 @@ int route_mode(bool aligned, int K) {
   return !aligned ? 0 : K % Vec16<T>::n != 0 ? 1 : 2;
 }
 
-// Whether the rows are few enough for one launch, a CTA per segment, in `*direct`: 8 turns of its
-// warps at most, should one segment have all.  (256 rows of 64: 6.7 us, 7.4 by two kernels; 512:
-// 10.4 and 7.5.)
+// Whether the rows are few enough for one launch, a cluster of CTAs per segment, in `*direct`: 6
+// turns of its warps at most (8, should one of several segments have all).  CTAs: as many as that
+// takes, and one for each two turns of an average segment, up to 8 and to what is resident at
+// once.  (fp32, by one launch and by two: 512 rows of 64 4.6 and 7.0 us, 1,536 6.9 and 7.4, in 5
+// segments 5.1 and 8.8; 512 of 256 6.8 and 8.0, but 1,024 of those in 8 turns 9.3 and 8.1.)
 template <typename T, int kLanes, int kEl>
 gmm_status load_launch(const RouteArgs& a, float* part, const RouteLossOut& o, int mode,
                        bool* direct, cudaStream_t st) {
-  *direct = a.N <= 8 * kRouteWarps * (32 / kLanes);
-  auto go = [&](auto kern, int64_t grid) {
-    return api_launch_next(kern, dim3((unsigned)grid), kRouteThreads, 0, st, a, part, o);
-  };
-  if (*direct)
-    return mode == 0   ? go(route_load_kernel<T, kLanes, kEl, 0, true>, a.S)
-           : mode == 1 ? go(route_load_kernel<T, kLanes, kEl, 1, true>, a.S)
-                       : go(route_load_kernel<T, kLanes, kEl, 2, true>, a.S);
-  const int64_t grid = (a.N + a.rows - 1) / a.rows;
-  return mode == 0   ? go(route_load_kernel<T, kLanes, kEl, 0, false>, grid)
-         : mode == 1 ? go(route_load_kernel<T, kLanes, kEl, 1, false>, grid)
-                     : go(route_load_kernel<T, kLanes, kEl, 2, false>, grid);
+  constexpr int kTurn = kRouteWarps * (32 / kLanes);
+  int ctas = 1, most = a.S == 1 ? 6 : 8;
+  while (ctas < 8 && (int64_t)2 * ctas * a.S <= 148 * 2 &&
+         ((int64_t)most * ctas * kTurn < a.N || (int64_t)2 * ctas * kTurn * a.S < a.N))
+    ctas *= 2;
+  *direct = a.N <= (int64_t)most * ctas * kTurn;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(*direct ? (int64_t)ctas * a.S : (a.N + a.rows - 1) / a.rows));
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = *direct && ctas > 1 ? 2 : 1;
+  auto kern = *direct ? mode == 0   ? route_load_kernel<T, kLanes, kEl, 0, true>
+                        : mode == 1 ? route_load_kernel<T, kLanes, kEl, 1, true>
+                                    : route_load_kernel<T, kLanes, kEl, 2, true>
+              : mode == 0 ? route_load_kernel<T, kLanes, kEl, 0, false>
+              : mode == 1 ? route_load_kernel<T, kLanes, kEl, 1, false>
+                          : route_load_kernel<T, kLanes, kEl, 2, false>;
+  if (cudaLaunchKernelEx(&cfg, kern, a, part, o) != cudaSuccess)
+    return api_launched(0), GMM_ERR_CUDA;
+  return api_launched(1);
 }
 
 // Lanes and places per row.  Here up to 16 places, so that three CTAs are resident: 262,144 rows of
