@@ -419,6 +419,17 @@ def gmm_ivf_build(idx, resp, K, tau, ws=None, stream=None):
 _DTYPES = {torch.float32: GMM_F32, torch.bfloat16: GMM_BF16, torch.float16: GMM_F16}
 
 
+# Descriptions by their values (never changed): building one costs more than looking it up.
+@functools.lru_cache(maxsize=4096)
+def _rows_of(*fields) -> gmm_rows:
+    return gmm_rows(*fields)
+
+
+@functools.lru_cache(maxsize=4096)
+def _embed_of(*fields) -> gmm_embed_problem:
+    return gmm_embed_problem(*fields)
+
+
 def _rows(Z, scale) -> gmm_rows:
     """The rows of a logits tensor (N x K, any row stride, unit column stride)."""
     if Z.dtype not in _DTYPES:
@@ -427,7 +438,7 @@ def _rows(Z, scale) -> gmm_rows:
         raise ValueError("logits must be N x K with a unit column stride")
     N, K = Z.shape
     ld = Z.stride(0) if N > 1 else max(Z.stride(0), K)
-    return gmm_rows(N, ld, K, _DTYPES[Z.dtype], scale)
+    return _rows_of(N, ld, K, _DTYPES[Z.dtype], float(scale))
 
 
 def _same_device(X, *others):
@@ -817,7 +828,7 @@ def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=Non
         out, ldy = torch.empty(N, D, dtype=W.dtype, device=device), D
     elif out.dtype != W.dtype or out.shape != (N, D):
         raise ValueError("out must be N x D of W's type")
-    p = gmm_embed_problem(N, m, K, D, dtype, scale, ldw, _ld(out, "out") if ldy is None else ldy)
+    p = _embed_of(N, m, K, D, dtype, float(scale), ldw, _ld(out, "out") if ldy is None else ldy)
     _launch(load_library().gmm_embed, "gmm_embed", device, ctypes.byref(p), W.data_ptr(),
             idx.data_ptr(), _address(resp), out.data_ptr(), _address(dev_flags))
     return out
@@ -862,7 +873,7 @@ def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accum
             raise ValueError("out must be K x D of dY's type or float32")
         ldd = _ld(out, "out")
     dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=device)
-    p = gmm_embed_problem(N, m, K, D, dtype, scale, ldw, ldy)
+    p = _embed_of(N, m, K, D, dtype, float(scale), ldw, ldy)
     if ws is None:
         ws = torch.empty(_embed_bytes(N, m, K, D, dtype), dtype=torch.uint8, device=device)
     _launch(load_library().gmm_embed_backward, "gmm_embed_backward", device, ctypes.byref(p),
