@@ -165,14 +165,20 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
 #pragma unroll
   for (int p = 0; p < kPer; p++) {
     if (at(p) >= a.D) return;
-    float y[U::n] = {};
+    F2 sum[U::n / 2];
 #pragma unroll
     for (int j = 0; j < kM; j++) {
       float x[U::n];
       U::unpack(r[p][j], x);
 #pragma unroll
-      for (int e = 0; e < U::n; e++) y[e] = kM == 1 ? w[j] * x[e] : fmaf(w[j], x[e], y[e]);
+      for (int e = 0; e < U::n; e += 2) {
+        const F2 x2 = f2(x[e], x[e + 1]), w2 = f2(w[j], w[j]);
+        sum[e / 2] = j == 0 ? f2_mul(x2, w2) : f2_fma(x2, w2, sum[e / 2]);
+      }
     }
+    float y[U::n];
+#pragma unroll
+    for (int e = 0; e < U::n; e += 2) f2_get(sum[e / 2], y[e], y[e + 1]);
     U::template store<true>(to, at(p), lanes, a.D, y);
   }
 }
