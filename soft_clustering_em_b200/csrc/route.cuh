@@ -146,6 +146,8 @@ struct RouteRow {
     S = s0 + s1;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    // (a finite logit whose z overflows leaves finite exponentials: what comes of them is NaN too)
+    if (bad) S = __int_as_float(0x7fffffff);
   }
   __device__ __forceinline__ float lse(float scale) const { return fmaf(xm, scale, logf(S)); }
 };
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     const bool chosen = __ballot_sync(0xffffffffu, legal) >> (lane - l) & group_mask<kLanes>();
     const bool live = !q.empty && (counts || chosen);
     if (q.bad && live && l == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_NONFINITE_X);
-    // (a row with a NaN is NaN throughout: so is the sum of its exponentials)
+    // (a row with a NaN or a z of +inf is NaN throughout: so is S)
     const F2 to2 = f2(inv * a.scale, inv * a.scale), cf2 = f2(cf, cf), base2 = f2(base, base);
 #pragma unroll
     for (int e = 0; e < kEl; e += 2)

@@ -343,6 +343,57 @@ def test_nothing_to_route(G):
     assert (g == 0).all()
 
 
+@pytest.mark.parametrize("dtype,big,scale", [("f32", 1e38, 10.0), ("bf16", 1e38, 10.0),
+                                             ("f16", 6e4, 1e34)])
+@pytest.mark.parametrize("K", [8, 200, 1000])
+@pytest.mark.parametrize("N", [90, 5000])  # one launch and two
+def test_a_scaled_logit_that_overflows_is_masked_or_infinite(G, N, K, dtype, big, scale):
+    """scale times a finite logit beyond float32's range: -inf is a masked class, +inf makes what
+    the row is part of NaN, as in gmm_route's weights."""
+    import torch
+
+    spread = 0.0 if dtype == "f16" else 0.2
+    Z, x, i, _, _, idx, _, _, rng = _case(8, N, K, 2, dtype, spread=spread)
+    o = np.array([0, N // 3, 2 * N // 3, N - 10], np.int32)
+    off, flags = torch.from_numpy(o).cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    Z[N // 2 + 1, K // 2] = -big
+    d = rng.normal(size=(N, 2)).astype(np.float32)
+    dresp = torch.from_numpy(d).cuda()
+    one = torch.ones(3, device="cuda")
+    upstream = [dict(dresp=dresp), dict(dresp=dresp, renorm=True), dict(dbalance=one), dict(dz=one)]
+
+    def loss():
+        return G.gmm_route_loss(Z, idx, off, scale=scale, dev_flags=flags)
+
+    def grad(r, kw):
+        more = dict(counts=r.counts, rows=r.rows) if "dresp" not in kw else {}
+        return G.gmm_route_backward(Z, idx, **kw, **more, offsets=off, scale=scale,
+                                    dev_flags=flags)
+
+    good = loss()
+    want = [grad(good, kw) for kw in upstream]
+    assert flags.item() == 0 and all(t.isfinite().all() for t in good)
+    assert not any(t.isnan().any() for t in want)  # (1e34 times a probability: float16 has no room)
+    b = N // 2
+    Z[b, K - 1] = big
+    x = Z.float().cpu().numpy()
+    r = loss()
+    assert flags.item() == G.GMM_DEVFLAG_NONFINITE_X
+    for have, exact in zip(r[:3], A.route_loss(x, i, o, None, scale)):
+        np.testing.assert_array_equal(have.isnan().cpu().numpy(), np.isnan(exact))
+    assert r.balance.isnan().tolist() == r.z.isnan().tolist() == [False, True, False]
+    assert r.load[1].isnan().all() and torch.equal(r.load[[0, 2]], good.load[[0, 2]])
+    assert torch.equal(r.counts, good.counts) and torch.equal(r.rows, good.rows)
+    assert G.gmm_route(Z, 2, scale=scale)[1][b].isnan().all()
+    for kw, w in zip(upstream, want):
+        flags.zero_()
+        g = grad(good, kw)
+        assert flags.item() == G.GMM_DEVFLAG_NONFINITE_X
+        assert g[b].isnan().all(), kw.keys()
+        g[b] = w[b]
+        assert torch.equal(g, w)
+
+
 def test_captured_and_on_another_stream(G):
     import torch
 
