@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     bool counts = losses && in && !next_out;
     const bool legal = (unsigned)k < (unsigned)a.K;
     if (!legal && k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    const float xk = legal ? to_f32(row[k]) : -INFINITY;
+    float xk = legal ? to_f32(row[k]) : -INFINITY;
     if (n0 + kRows < r1) fetch(n0 + kRows);
     if (counts && a.offsets) {
       while (s + 1 < a.S && n >= a.offsets[s + 1]) s++;
@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     q.make(r, a.scale);
     const float c = a.scale * kLog2e, inv = 1.f / q.S;
     // the chosen: their weights and what they pull on
+    if (xk * a.scale == -INFINITY) xk = -INFINITY;  // (masked: no weight)
     const float top = a.m > 0 && g.renorm ? fmaxf(group_max<kLanes>(xk), -FLT_MAX) : q.ref;
     const float ek = legal ? ex2((xk - top) * c) : 0.f;
     const float over = g.renorm ? group_sum<kLanes>(ek) : q.S;

@@ -394,6 +394,27 @@ def test_a_scaled_logit_that_overflows_is_masked_or_infinite(G, N, K, dtype, big
         assert torch.equal(g, w)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("K", [8, 200, 1000])
+def test_a_choice_that_the_scale_masks_has_no_weight(G, K, renorm):
+    """A class is masked where its logit is -inf and where scale times its logit is."""
+    import torch
+
+    Z, x, i, _, _, _, _, _, rng = _case(10, 60, K, 3, "f32", spread=0.2)
+    i[:, 1:] = [[1, 2]]
+    i[::2, 0] = 0  # these rows name masked classes only
+    i[1::2, 0] = 4
+    Z[:, :3] = -1e38
+    same = Z.clone()
+    same[:, :3] = -np.inf
+    idx = torch.from_numpy(i.astype(np.int32)).cuda()
+    d = torch.from_numpy(rng.normal(size=(60, 3)).astype(np.float32)).cuda()
+    got, want = [G.gmm_route_backward(z, idx, d, renorm, scale=10.0) for z in (Z, same)]
+    assert torch.equal(got, want) and got.isfinite().all() and (got[::2] == 0).all()
+    got, want = [G.gmm_route_loss(z, idx, scale=10.0) for z in (Z, same)]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_captured_and_on_another_stream(G):
     import torch
 
