@@ -603,7 +603,9 @@ gmm_status gmm_embed_backward(const gmm_embed_problem* p, const void* dY, const 
  *   ended    device, B x w bytes, or NULL: != 0 is a beam that has ended (nor is its row).
  *   out_scores, parent, token   device, B x m: the m best candidates, descending, and their i and
  *            k.  Equal scores go to the lower i, then to the larger logit, then to the lower k.
- *            Where candidates run out: -inf, -1, -1.
+ *            Where candidates run out: -inf, -1, -1.  Of a beam, the m best classes are looked
+ *            at as gmm_logprobs finds them: by scale * Z in float32, equal ones by k (where the
+ *            scale makes different logits equal, the m-th may be one of them with a lower score).
  *   1 <= w <= 32, 1 <= m <= 32 (m = w for a plain step, 2 w where some may end).
  *   ws       device workspace of gmm_beam_workspace_size bytes, 256-byte aligned, any content.
  *            Calls that share it must be ordered on one stream.

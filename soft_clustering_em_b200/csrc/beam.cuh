@@ -46,11 +46,14 @@ __device__ __forceinline__ double order_double(uint64_t o) {
 // them. Scores are 64 bits wide: those of different rows lie close together, and in 32 bits a log
 // p of -15 is rounded by 5e-7.  A row's first log p is the smallest in size and so the most exact
 // one; the others stand as far behind it as their logits.  Equal scores go to the lower beam,
-// then in the order of the row.
+// then in the order of the row: of z = fl32(scale x), then of the class.  That is the order of the
+// scores too, but for logits that the scale rounds to one z.
 constexpr int kMergeThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
-  __shared__ uint64_t cand[kMostBeams * kMaxAlt];  // [beam][m]
+  __shared__ uint64_t cand[kMostBeams * kMaxAlt];    // [beam][m]
+  __shared__ uint64_t sorted[kMostBeams * kMaxAlt];  // the same by score, and where they stood
+  __shared__ uint8_t place[kMostBeams * kMaxAlt];
   const int t = threadIdx.x, lane = t & 31;
   const int64_t b = blockIdx.x;
   float score = -INFINITY;
@@ -83,6 +86,25 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     cand[c] = key;
   }
   __syncthreads();
+  // Logits that the scale rounds to one z: then each beam's candidates are ranked by score first.
+  const int total = a.w * a.m;
+  bool ranked = false;
+  if (a.scale != 1.f) {
+    for (int c = t; c < total; c += kMergeThreads) ranked |= c % a.m != 0 && cand[c] > cand[c - 1];
+    ranked = __syncthreads_or(ranked);
+  }
+  if (ranked) {
+    for (int c = t; c < total; c += kMergeThreads) {
+      const int from = c - c % a.m;
+      const uint64_t key = cand[c];
+      int rank = 0;
+      for (int q = from; q < from + a.m; q++) rank += cand[q] > key || (cand[q] == key && q < c);
+      sorted[from + rank] = key;
+      place[from + rank] = (uint8_t)(c - from);
+    }
+    __syncthreads();
+  }
+  const uint64_t* list = ranked ? sorted : cand;
   if (t >= 32) return;
   const bool dead = score == -INFINITY;
   const bool bad = !(score < INFINITY) || (!dead && !ended && !(first == first));
@@ -97,7 +119,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
   }
   int pos = 0, my_parent = -1, my_rank = 0;
   double my_score = -INFINITY;
-  uint64_t head = lane < a.w ? cand[lane * a.m] : 0;
+  uint64_t head = lane < a.w ? list[lane * a.m] : 0;
   for (int j = 0; j < a.m; j++) {
     const uint64_t best = warp_max_key(head);
     if (best == 0) break;
@@ -108,8 +130,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
       my_parent = from;
       my_rank = rank;
     }
-    if (lane == from) head = ++pos < a.m ? cand[lane * a.m + pos] : 0;
+    if (lane == from) head = ++pos < a.m ? list[lane * a.m + pos] : 0;
   }
+  if (ranked && my_parent >= 0) my_rank = place[my_parent * a.m + my_rank];
   const bool end = __shfl_sync(0xffffffffu, (int)ended, max(my_parent, 0));
   if (lane < a.m) {
     a.out[b * a.m + lane] = (float)my_score;

@@ -124,6 +124,53 @@ def test_scores_that_float32_cannot_tell_apart(G):
     assert abs(r.scores[0, 0].item() - r.scores[0, 1].item()) <= 4e-6
 
 
+def test_logits_whose_products_with_the_scale_are_equal(G):
+    """Two neighbours among the float32 numbers whose products with 0.75 round to one: in the order
+    of gmm_logprobs they are equal, but the larger one's score is 1.4e-6 higher.  Each beam offers
+    its m best classes in that order; candidates are put in the order of their scores."""
+    import torch
+
+    f = np.float32
+    small = next(x for x in np.arange(f(22), f(23), f(2) ** -19, dtype=f)
+                 if x * f(0.75) == (x + f(2) ** -19) * f(0.75))
+    large = small + f(2) ** -19
+    Z = torch.full((2, 16), -float("inf"), device="cuda")
+    Z[0, 3], Z[0, 9], Z[1, 3], Z[1, 9] = map(float, (small, large, large, small))
+    s = torch.tensor([[0.0, -7e-7]], device="cuda")
+    want = A.beam_select(Z.cpu().numpy(), s.cpu().numpy(), 4, scale=0.75)
+    assert want[1].tolist() == [[0, 1, 0, 1]] and want[2].tolist() == [[9, 3, 3, 9]]
+    for m in (2, 3, 4):
+        r = G.gmm_beam_select(Z, s, m, scale=0.75)
+        assert r.parent.tolist() == want[1][:, :m].tolist()
+        assert r.token.tolist() == want[2][:, :m].tolist()
+        assert (r.scores[0].double().cpu() - torch.from_numpy(want[0][0, :m])).abs().max() < 2e-7
+    one = G.gmm_beam_select(Z[:1], s[:, :1], 2, scale=0.75)
+    assert one.token.tolist() == [[9, 3]] and one.scores[0, 0] > one.scores[0, 1]
+    one = G.gmm_beam_select(Z[:1], s[:, :1], 1, scale=0.75)
+    assert one.token.tolist() == G.gmm_logprobs(Z[:1], m=1, scale=0.75).top_idx.tolist() == [[3]]
+
+
+@pytest.mark.parametrize("B,w,K,m", [(3, 1, 40, 8), (5, 4, 300, 32), (2, 32, 70, 32), (4, 3, 5000, 9)])
+def test_candidates_of_a_beam_follow_their_logits(G, B, w, K, m):
+    """Logits a few float32 steps apart, at a scale that makes many products equal."""
+    import torch
+
+    rng = np.random.default_rng(K + m)
+    x = (22 + rng.integers(0, 12, (B * w, K)) * 2.0 ** -19).astype(np.float32)
+    z = x * np.float32(0.75)
+    s = (rng.integers(0, 3, (B, w)) * 1e-6).astype(np.float32)
+    r = G.gmm_beam_select(torch.from_numpy(x).cuda(), torch.from_numpy(s).cuda(), m, scale=0.75)
+    scores, parent, token = (t.cpu().numpy() for t in r)
+    assert (np.diff(scores, axis=1) <= 0).all() and (parent >= 0).all()
+    for b in range(B):
+        for i in range(w):
+            row = b * w + i
+            taken = token[b, parent[b] == i]
+            best = np.lexsort((np.arange(K), -z[row]))[:m]  # what the beam offers
+            best = best[np.lexsort((np.arange(len(best)), -x[row, best].astype(np.float64)))]
+            np.testing.assert_array_equal(taken, best[:len(taken)])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("K", [100, 3000])
 def test_what_is_not_a_number(G, K, bad):
