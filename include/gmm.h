@@ -515,7 +515,8 @@ gmm_status gmm_moe(const gmm_moe_problem* p, const void* X, const int32_t* idx, 
  *   ws        device workspace of gmm_route_loss_workspace_size bytes, 256-byte aligned, any
  *             content.  Calls that share it must be ordered on one stream.
  * A NaN or a z of +inf in a row that counts makes its segment's balance, z and load NaN and
- * raises GMM_DEVFLAG_NONFINITE_X.  Results do not change from run to run.
+ * raises GMM_DEVFLAG_NONFINITE_X.  Sums over rows are formed in float32 of at most 512 rows one
+ * after another, and those in 64 bits.  Results do not change from run to run.
  * GMM_ERR_UNSUPPORTED: K > 1024, S > 2^20, N * m >= 2^31.
  */
 gmm_status gmm_route_loss_workspace_size(const gmm_rows* r, int32_t S, size_t* bytes);

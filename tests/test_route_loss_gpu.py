@@ -415,6 +415,22 @@ def test_a_choice_that_the_scale_masks_has_no_weight(G, K, renorm):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("N,K,pad", [(1 << 28, 12, 4)])
+def test_sums_over_many_like_rows(G, N, K, pad):
+    """Logits of 0, as of a router that has not learnt: p = 1 / K and lse = log K in every row, and
+    all roundings of a running sum go one way.  At most 512 of a lane's additions before 64 bits,
+    and 14 to join lanes and warps; p is off by u, and log K by 2 u, its square by 5 u."""
+    import torch
+
+    Z = torch.zeros(N, K + pad, dtype=torch.bfloat16, device="cuda")[:, :K]
+    idx = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+    r = G.gmm_route_loss(Z, idx)
+    assert r.rows.item() == N and r.counts[0].tolist() == [N] + [0] * (K - 1)
+    assert (r.load.double() * K - 1).abs().max() <= (512 + 14 + 2) * U
+    assert abs(r.balance.item() - 1) <= (512 + 14 + 2) * U
+    assert abs(r.z.item() / np.log(K) ** 2 - 1) <= (512 + 14 + 6) * U
+
+
 def test_captured_and_on_another_stream(G):
     import torch
 
