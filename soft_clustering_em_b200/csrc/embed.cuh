@@ -4,9 +4,9 @@
 //   Y_n = scale sum_j r_nj W[idx_nj]              (r = 1 without weights)
 //   dW_k = scale sum_{(n,j): idx_nj = k} r_nj dY_n
 //   dr_nj = scale <dY_n, W[idx_nj]>
-// Sums are held in float32 and rounded once.  Everything is bound by memory: the named rows
-// and the output go through once.  Measured figures are of one B200, calls back to back, beside the
-// time of the bytes alone at the rate of a large copy (6,548 GB/s).
+// Sums are held in float32 (of many chunks in 64 bits) and rounded once.  Everything is bound by
+// memory: the named rows and the output go through once.  Measured figures are of one B200, calls
+// back to back, beside the time of the bytes alone at the rate of a large copy (6,548 GB/s).
 #pragma once
 
 #include <type_traits>
@@ -790,7 +790,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
   for (int q = 0; q < kWarps; q++) {
     const uint32_t from = long_chunk[q], to = long_last[q];
     if (from == 0xffffffffu) continue;  // (the same for all threads)
-    float sum[U::n] = {};
+    float sum[U::n];
+    double total[U::n] = {};  // (a million chunks of like terms would all round one way)
     if (at < a.D) {
       for (uint32_t i0 = from + g; i0 <= to; i0 += kJoinBatch * groups) {
         float x[kJoinBatch][U::n];
@@ -800,15 +801,19 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
           if (i <= to) part(i, i == from, x[b]);
         }
 #pragma unroll
-        for (int b = 0; b < kJoinBatch; b++) {
+        for (int e = 0; e < U::n; e++) sum[e] = x[0][e];
+#pragma unroll
+        for (int b = 1; b < kJoinBatch; b++) {
           if (i0 + b * groups > to) continue;
 #pragma unroll
           for (int e = 0; e < U::n; e++) sum[e] += x[b][e];
         }
+#pragma unroll
+        for (int e = 0; e < U::n; e++) total[e] += (double)sum[e];
       }
     }
 #pragma unroll
-    for (int e = 0; e < U::n; e++) sh[threadIdx.x][e] = sum[e];
+    for (int e = 0; e < U::n; e++) sh[threadIdx.x][e] = sum[e] = (float)total[e];
     for (int o = groups / 2; o > 0; o /= 2) {
       __syncthreads();
       if (g < o) {

@@ -302,6 +302,35 @@ def test_tables_beyond_32_bits(G):
     assert dW.count_nonzero() == Y.count_nonzero()
 
 
+def test_a_class_that_millions_of_choices_name(G):
+    """Alike terms, whose roundings in a running sum all go one way: 128 of a chunk, 8 chunks' sums,
+    then 64 bits, up to 8 halves and the result."""
+    import torch
+
+    N, D = 1 << 23, 136
+    dY = torch.ones(N, D, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(N, dtype=torch.int32, device="cuda")
+    resp = torch.full((N,), 0.7, device="cuda")
+    dW = torch.empty(2, D, device="cuda")
+    G.gmm_embed_backward(dY, idx, 2, resp, out=dW)
+    want = N * float(np.float32(0.7))
+    assert (dW[1] == 0).all()
+    assert (dW[0].double() / want - 1).abs().max() <= (128 + 8 + 8 + 4) * U
+
+
+def test_an_infinite_term_among_millions(G):
+    """The sum of a class with infinities is infinite, in a long run too, or NaN for both signs."""
+    import torch
+
+    N, D = 300_000, 8
+    dY = torch.ones(N, D, device="cuda")
+    dY[100, 0], dY[200_000, 1], dY[5, 2], dY[299_999, 2] = np.inf, -np.inf, np.inf, -np.inf
+    idx = torch.zeros(N, dtype=torch.int32, device="cuda")
+    dW, _ = G.gmm_embed_backward(dY, idx, 1)
+    assert dW[0, 0] == np.inf and dW[0, 1] == -np.inf and dW[0, 2].isnan()
+    assert (dW[0, 3:] == N).all()
+
+
 def test_captured_and_on_another_stream(G):
     import torch
 
