@@ -147,7 +147,7 @@ struct RouteRow {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
     // (a finite logit whose z overflows leaves finite exponentials: what comes of them is NaN too)
-    if (bad) S = __int_as_float(0x7fffffff);
+    S = fmaf(z, 0.f, S);
   }
   __device__ __forceinline__ float lse(float scale) const { return fmaf(xm, scale, logf(S)); }
 };
@@ -460,6 +460,7 @@ struct RouteGradArgs {
   const float *dbalance, *dz;    // S each, may be null
   void* dZ;
   int64_t ldd;
+  float least;                   // the least x that scale does not take to -inf (a masked class)
 };
 
 // A warp takes `rows` consecutive rows, 32 / kLanes at a time; the counts of the segment stay in
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     bool counts = losses && in && !next_out;
     const bool legal = (unsigned)k < (unsigned)a.K;
     if (!legal && k != -1 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
-    float xk = legal ? to_f32(row[k]) : -INFINITY;
+    const float xk = legal ? to_f32(row[k]) : -INFINITY;
     if (n0 + kRows < r1) fetch(n0 + kRows);
     if (counts && a.offsets) {
       while (s + 1 < a.S && n >= a.offsets[s + 1]) s++;
@@ -544,8 +545,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     q.make(r, a.scale);
     const float c = a.scale * kLog2e, inv = 1.f / q.S;
     // the chosen: their weights and what they pull on
-    if (xk * a.scale == -INFINITY) xk = -INFINITY;  // (masked: no weight)
-    const float top = a.m > 0 && g.renorm ? fmaxf(group_max<kLanes>(xk), -FLT_MAX) : q.ref;
+    const float top = a.m > 0 && g.renorm ? fmaxf(group_max<kLanes>(xk), g.least) : q.ref;
     const float ek = legal ? ex2((xk - top) * c) : 0.f;
     const float over = g.renorm ? group_sum<kLanes>(ek) : q.S;
     const float wk = ek > 0.f || !(ek == ek) ? ek / over : 0.f;

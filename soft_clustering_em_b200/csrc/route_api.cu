@@ -1,5 +1,6 @@
 // route_api.cu -- host side of gmm_route_loss and gmm_route_backward: argument checks and
 // launches.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -107,6 +108,14 @@ gmm_status load_dispatch(const RouteArgs& a, float* part, const RouteLossOut& o,
   if (a.K <= 256) return load_launch<T, 16, 16>(a, part, o, mode, direct, st);
   if (a.K <= 512) return load_launch<T, 32, 16>(a, part, o, mode, direct, st);
   return load_launch<T, 32, 32>(a, part, o, mode, direct, st);
+}
+
+// The least float32 whose product with scale is not -inf.
+float least_logit(float scale) {
+  float x = std::max(-FLT_MAX, -FLT_MAX / scale);  // (off by a step at most)
+  if (x > -FLT_MAX) x = nextafterf(x, -INFINITY);
+  while (isinf(x * scale)) x = nextafterf(x, 0.f);
+  return x;
 }
 
 template <typename T, int kLanes, int kEl>
@@ -222,7 +231,8 @@ gmm_status gmm_route_backward(const gmm_rows* r, const void* Z, const int32_t* i
     return GMM_ERR_UNSUPPORTED;
   const RouteArgs a = {Z,    r->N,    r->ld, r->K, r->scale, idx, m,
                        mask, offsets, S,     0,    dev_flags};
-  const RouteGradArgs g = {a, dresp, renorm != 0, counts, rows, dbalance, dz, dZ, ldd};
+  const RouteGradArgs g = {a,  dresp, renorm != 0, counts, rows, dbalance,
+                           dz, dZ,    ldd,         least_logit(r->scale)};
   cudaStream_t st = (cudaStream_t)stream;
   if (r->dtype == GMM_F32) return grad_dispatch<float>(g, st);
   if (r->dtype == GMM_BF16) return grad_dispatch<__nv_bfloat16>(g, st);
