@@ -51,9 +51,8 @@ __device__ __forceinline__ double order_double(uint64_t o) {
 constexpr int kMergeThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
-  __shared__ uint64_t cand[kMostBeams * kMaxAlt];    // [beam][m]
-  __shared__ uint64_t sorted[kMostBeams * kMaxAlt];  // the same by score, and where they stood
-  __shared__ uint8_t place[kMostBeams * kMaxAlt];
+  __shared__ uint64_t cand[2 * kMostBeams * kMaxAlt];  // [beam][m], then the same by score
+  __shared__ uint8_t place[kMostBeams * kMaxAlt];      // where those stood
   const int t = threadIdx.x, lane = t & 31;
   const int64_t b = blockIdx.x;
   float score = -INFINITY;
@@ -65,6 +64,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const float first = lane < a.w ? a.top_logp[(b * a.w + lane) * a.m] : 0.f;
+  bool climbs = false;  // a candidate scores more than the one before it in its row's order
   for (int c0 = 0; c0 < a.w * a.m; c0 += kMergeThreads) {
     const int c = c0 + t, i = min(c / a.m, a.w - 1), j = c % a.m;
     const float s = __shfl_sync(0xffffffffu, score, i);
@@ -77,34 +77,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     } else if (s != -INFINITY) {
       const int64_t row = b * a.w + i;
       const int k0 = a.top_idx[row * a.m], k = a.top_idx[row * a.m + j];
+      const int before = a.scale != 1.f ? a.top_idx[row * a.m + max(j - 1, 0)] : k0;
       if (k >= 0) {
         const T* z = (const T*)a.Z + row * a.ld;
-        const double d = (double)to_f32(z[k]) - (double)to_f32(z[k0]);
+        const float x = to_f32(z[k]);
+        climbs |= x > to_f32(z[before]) && a.scale != 1.f;
+        const double d = (double)x - (double)to_f32(z[k0]);
         key = double_order((double)s + ((double)lp + d * (double)a.scale));
       }
     }
     cand[c] = key;
   }
-  __syncthreads();
   // Logits that the scale rounds to one z: then each beam's candidates are ranked by score first.
-  const int total = a.w * a.m;
-  bool ranked = false;
-  if (a.scale != 1.f) {
-    for (int c = t; c < total; c += kMergeThreads) ranked |= c % a.m != 0 && cand[c] > cand[c - 1];
-    ranked = __syncthreads_or(ranked);
-  }
+  const bool ranked = __syncthreads_or(climbs);
+  const int list = ranked ? kMostBeams * kMaxAlt : 0;
   if (ranked) {
-    for (int c = t; c < total; c += kMergeThreads) {
+    for (int c = t; c < a.w * a.m; c += kMergeThreads) {
       const int from = c - c % a.m;
       const uint64_t key = cand[c];
       int rank = 0;
       for (int q = from; q < from + a.m; q++) rank += cand[q] > key || (cand[q] == key && q < c);
-      sorted[from + rank] = key;
+      cand[list + from + rank] = key;
       place[from + rank] = (uint8_t)(c - from);
     }
     __syncthreads();
   }
-  const uint64_t* list = ranked ? sorted : cand;
   if (t >= 32) return;
   const bool dead = score == -INFINITY;
   const bool bad = !(score < INFINITY) || (!dead && !ended && !(first == first));
@@ -119,7 +116,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
   }
   int pos = 0, my_parent = -1, my_rank = 0;
   double my_score = -INFINITY;
-  uint64_t head = lane < a.w ? list[lane * a.m] : 0;
+  uint64_t head = lane < a.w ? cand[list + lane * a.m] : 0;
   for (int j = 0; j < a.m; j++) {
     const uint64_t best = warp_max_key(head);
     if (best == 0) break;
@@ -130,7 +127,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
       my_parent = from;
       my_rank = rank;
     }
-    if (lane == from) head = ++pos < a.m ? list[lane * a.m + pos] : 0;
+    if (lane == from) head = ++pos < a.m ? cand[list + lane * a.m + pos] : 0;
   }
   if (ranked && my_parent >= 0) my_rank = place[my_parent * a.m + my_rank];
   const bool end = __shfl_sync(0xffffffffu, (int)ended, max(my_parent, 0));
