@@ -790,9 +790,11 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
   for (int q = 0; q < kWarps; q++) {
     const uint32_t from = long_chunk[q], to = long_last[q];
     if (from == 0xffffffffu) continue;  // (the same for all threads)
-    float sum[U::n];
-    double total[U::n] = {};  // (a million chunks of like terms would all round one way)
+    // (alike terms all round one way: 8 batches of chunks at most in float32)
+    float sum[U::n] = {};
+    double total[U::n] = {};
     if (at < a.D) {
+      int batch = 0;
       for (uint32_t i0 = from + g; i0 <= to; i0 += kJoinBatch * groups) {
         float x[kJoinBatch][U::n];
 #pragma unroll
@@ -801,19 +803,24 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedGradArgs
           if (i <= to) part(i, i == from, x[b]);
         }
 #pragma unroll
-        for (int e = 0; e < U::n; e++) sum[e] = x[0][e];
-#pragma unroll
         for (int b = 1; b < kJoinBatch; b++) {
           if (i0 + b * groups > to) continue;
 #pragma unroll
-          for (int e = 0; e < U::n; e++) sum[e] += x[b][e];
+          for (int e = 0; e < U::n; e++) x[0][e] += x[b][e];
         }
 #pragma unroll
-        for (int e = 0; e < U::n; e++) total[e] += (double)sum[e];
+        for (int e = 0; e < U::n; e++) sum[e] += x[0][e];
+        if (++batch % 8 == 0) {
+#pragma unroll
+          for (int e = 0; e < U::n; e++) {
+            total[e] += (double)sum[e];
+            sum[e] = 0.f;
+          }
+        }
       }
     }
 #pragma unroll
-    for (int e = 0; e < U::n; e++) sh[threadIdx.x][e] = sum[e] = (float)total[e];
+    for (int e = 0; e < U::n; e++) sh[threadIdx.x][e] = sum[e] = (float)(total[e] + (double)sum[e]);
     for (int o = groups / 2; o > 0; o /= 2) {
       __syncthreads();
       if (g < o) {

@@ -304,7 +304,7 @@ def test_tables_beyond_32_bits(G):
 
 def test_a_class_that_millions_of_choices_name(G):
     """Alike terms, whose roundings in a running sum all go one way: 128 of a chunk, 8 chunks' sums,
-    then 64 bits, up to 8 halves and the result."""
+    8 of those, then 64 bits, 3 halves (32 lanes a row) and the result."""
     import torch
 
     N, D = 1 << 23, 136
