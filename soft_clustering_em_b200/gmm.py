@@ -8,6 +8,7 @@ raises -- there is no fallback implementation.
 """
 import ctypes
 import functools
+import math
 import os
 import struct
 from typing import NamedTuple, Optional
@@ -430,6 +431,10 @@ def _embed_of(*fields) -> gmm_embed_problem:
     return gmm_embed_problem(*fields)
 
 
+def _number(x) -> float:
+    return math.ldexp(x, 0)  # (float() would take text as well)
+
+
 def _rows(Z, scale) -> gmm_rows:
     """The rows of a logits tensor (N x K, any row stride, unit column stride)."""
     if Z.dtype not in _DTYPES:
@@ -438,7 +443,7 @@ def _rows(Z, scale) -> gmm_rows:
         raise ValueError("logits must be N x K with a unit column stride")
     N, K = Z.shape
     ld = Z.stride(0) if N > 1 else max(Z.stride(0), K)
-    return _rows_of(N, ld, K, _DTYPES[Z.dtype], float(scale))
+    return _rows_of(N, ld, K, _DTYPES[Z.dtype], _number(scale))
 
 
 def _same_device(X, *others):
@@ -828,7 +833,7 @@ def gmm_embed(W, idx, resp=None, scale=1.0, out=None, dev_flags=None, stream=Non
         out, ldy = torch.empty(N, D, dtype=W.dtype, device=device), D
     elif out.dtype != W.dtype or out.shape != (N, D):
         raise ValueError("out must be N x D of W's type")
-    p = _embed_of(N, m, K, D, dtype, float(scale), ldw, _ld(out, "out") if ldy is None else ldy)
+    p = _embed_of(N, m, K, D, dtype, _number(scale), ldw, _ld(out, "out") if ldy is None else ldy)
     _launch(load_library().gmm_embed, "gmm_embed", device, ctypes.byref(p), W.data_ptr(),
             idx.data_ptr(), _address(resp), out.data_ptr(), _address(dev_flags))
     return out
@@ -873,7 +878,7 @@ def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accum
             raise ValueError("out must be K x D of dY's type or float32")
         ldd = _ld(out, "out")
     dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=device)
-    p = _embed_of(N, m, K, D, dtype, float(scale), ldw, ldy)
+    p = _embed_of(N, m, K, D, dtype, _number(scale), ldw, ldy)
     if ws is None:
         ws = torch.empty(_embed_bytes(N, m, K, D, dtype), dtype=torch.uint8, device=device)
     _launch(load_library().gmm_embed_backward, "gmm_embed_backward", device, ctypes.byref(p),

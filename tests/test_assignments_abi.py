@@ -80,6 +80,21 @@ def test_router_gradient_arguments(lib):
     assert grad(lib, rows(N=0), Z=0, idx=0, dZ=0) == OK
 
 
+def test_a_scale_is_a_number():
+    import fractions
+
+    import numpy as np
+
+    Z = torch.zeros(3, 8)
+    for half in (0.5, np.float32(0.5), np.float64(0.5), np.array(0.5), fractions.Fraction(1, 2),
+                 torch.tensor(0.5)):
+        assert G._rows(Z, half).scale == 0.5
+    assert G._rows(Z, 2).scale == 2.0
+    for bad in ("0.5", b"0.5", None, [0.5], 0.5j):
+        with pytest.raises(TypeError):
+            G._rows(Z, bad)
+
+
 def problem(N=4, m=2, K=6, D=8, dtype=G.GMM_BF16, scale=1.0, ldw=8, ldy=8):
     return ctypes.byref(G.gmm_embed_problem(N, m, K, D, dtype, scale, ldw, ldy))
 

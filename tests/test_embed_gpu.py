@@ -361,6 +361,19 @@ def test_captured_and_on_another_stream(G):
         assert torch.equal(dW, G.gmm_embed_backward(dY, idx, K)[0])
 
 
+@pytest.mark.parametrize("bad", ["0.5", b"0.5", None])
+def test_a_scale_that_is_no_number_is_refused(G, bad):
+    import torch
+
+    W, idx = torch.ones(4, 8, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call in (lambda: G.gmm_embed(W, idx, scale=bad),
+                 lambda: G.gmm_embed_backward(W[:2], idx, 4, scale=bad),
+                 lambda: G.gmm_route_loss(W[:2], idx[:, None], scale=bad),
+                 lambda: G.gmm_logprobs(W, scale=bad), lambda: G.gmm_route(W, 2, scale=bad)):
+        with pytest.raises(TypeError):
+            call()
+
+
 def test_refusals(G):
     import torch
 
