@@ -457,7 +457,7 @@ gmm_status gmm_embed_backward(const gmm_embed_problem* p, const void* dY, const 
                               void* ws, size_t ws_bytes, void* stream) {
   gmm_status s = check_embed(p);
   if (s != GMM_OK) return s;
-  if (!dW && !dresp) return GMM_ERR_INVALID_ARG;
+  if (!dW && !dresp && p->N > 0) return GMM_ERR_INVALID_ARG;
   if (dresp && p->N > 0 && !W) return GMM_ERR_INVALID_ARG;
   if (p->N > 0 && (!dY || !idx)) return GMM_ERR_INVALID_ARG;
   const size_t size = elem(p->dtype);

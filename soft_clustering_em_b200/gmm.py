@@ -845,18 +845,20 @@ def gmm_embed_workspace_size(p: gmm_embed_problem) -> int:
 
 
 def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accumulate=False,
-                       ws=None, dev_flags=None, stream=None):
+                       ws=None, dev_flags=None, stream=None, table=True):
     """(dW, dresp): the gradients of gmm_embed(W, idx, resp, scale) for its upstream gradient dY
     (N x D).
 
     dW: K x D of dY's type, or in out (of dY's type or float32); with accumulate it is added to
     what out holds, and rows that idx does not name are not touched.  dresp: of resp's shape, None
     unless W is given.  ws: a uint8 device tensor of gmm_embed_workspace_size bytes (allocated here
-    when None).
+    when None).  table False: dresp alone, for a W that is not trained; dW is None and no workspace
+    is used.
     """
     if stream is not None:
         with _on(stream, dY):
-            return gmm_embed_backward(dY, idx, K, resp, W, scale, out, accumulate, ws, dev_flags)
+            return gmm_embed_backward(dY, idx, K, resp, W, scale, out, accumulate, ws, dev_flags,
+                                      table=table)
     _same_device(dY, idx, resp, W, out, ws, dev_flags)
     ldy = _ld(dY, "dY")
     N, D = dY.shape
@@ -869,22 +871,27 @@ def gmm_embed_backward(dY, idx, K, resp=None, W=None, scale=1.0, out=None, accum
         if W.dtype != dY.dtype or W.shape != (K, D):
             raise ValueError("W must be K x D of dY's type")
         ldw = _ld(W, "W")
-    if out is None:
+    ldd = D
+    if not table:
+        if W is None or out is not None or accumulate:
+            raise ValueError("without the table's gradient: W, and neither out nor accumulate")
+        ws = None
+    elif out is None:
         if accumulate:
             raise ValueError("accumulate adds to out, which is missing")
-        out, ldd = torch.empty(K, D, dtype=dY.dtype, device=device), D
+        out = torch.empty(K, D, dtype=dY.dtype, device=device)
     else:
         if out.dtype not in (dY.dtype, torch.float32) or out.shape != (K, D):
             raise ValueError("out must be K x D of dY's type or float32")
         ldd = _ld(out, "out")
     dresp = None if W is None else torch.empty(idx.shape, dtype=torch.float32, device=device)
     p = _embed_of(N, m, K, D, dtype, _number(scale), ldw, ldy)
-    if ws is None:
+    if table and ws is None:
         ws = torch.empty(_embed_bytes(N, m, K, D, dtype), dtype=torch.uint8, device=device)
     _launch(load_library().gmm_embed_backward, "gmm_embed_backward", device, ctypes.byref(p),
-            dY.data_ptr(), idx.data_ptr(), _address(resp), _address(W), out.data_ptr(),
-            _DTYPES[out.dtype], ldd, int(bool(accumulate)), _address(dresp),
-            _address(dev_flags), ws.data_ptr(), ws.numel())
+            dY.data_ptr(), idx.data_ptr(), _address(resp), _address(W), _address(out),
+            _DTYPES[out.dtype] if table else dtype, ldd, int(bool(accumulate)), _address(dresp),
+            _address(dev_flags), _address(ws), ws.numel() if table else 0)
     return out, dresp
 
 

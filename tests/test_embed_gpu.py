@@ -331,6 +331,53 @@ def test_an_infinite_term_among_millions(G):
     assert (dW[0, 3:] == N).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,m,D,pad", [(0, 1, 8, 0), (1, 1, 40, 0), (64, 2, 96, 0), (64, 3, 41, 3),
+                                       (129, 1, 2048, 0), (700, 2, 520, 0), (5000, 4, 64, 8),
+                                       (140_000, 1, 16, 0)])
+def test_the_gradient_of_the_weights_alone(G, N, m, D, pad, dtype):
+    """What the call for both gives, bit for bit; no table's gradient and no workspace."""
+    import torch
+
+    K = 300
+    rng = np.random.default_rng(N + D)
+    W, _ = _rows(rng, K, D, dtype, pad)
+    dY, _ = _rows(rng, N, D, dtype, pad)
+    idx, resp, _, _ = _assignment(rng, N, m, K, True)
+    _, want = G.gmm_embed_backward(dY, idx, K, resp, W=W, scale=0.7)
+    none, got = G.gmm_embed_backward(dY, idx, K, resp, W=W, scale=0.7, table=False)
+    assert none is None and got.shape == idx.shape and torch.equal(got, want)
+    again = torch.full_like(want, float("nan"))
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = G.embed_problem(idx, K, 0.7, W.stride(0), dY)
+    assert G.load_library().gmm_embed_backward(
+        p, dY.data_ptr(), idx.data_ptr(), resp.data_ptr(), W.data_ptr(), None, 0, 0, 0,
+        again.data_ptr(), flags.data_ptr(), None, 0,
+        torch.cuda.current_stream().cuda_stream) == G.GMM_OK
+    assert torch.equal(again, want) and flags.item() == 0
+
+
+def test_the_gradient_of_the_weights_alone_captured_and_refused(G):
+    import torch
+
+    dY, W = torch.randn(50, 24, device="cuda"), torch.randn(9, 24, device="cuda")
+    idx = torch.randint(0, 9, (50, 2), dtype=torch.int32, device="cuda")
+    resp = torch.rand(50, 2, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, got = G.gmm_embed_backward(dY, idx, 9, resp, W=W, table=False)
+    dY.normal_()
+    idx[7, 1] = 40
+    graph.replay()
+    torch.cuda.synchronize()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = G.gmm_embed_backward(dY, idx, 9, resp, W=W, dev_flags=flags, table=False)[1]
+    assert torch.equal(got, want) and got[7, 1] == 0 and flags.item() == G.GMM_DEVFLAG_BAD_INDEX
+    for kw in (dict(W=None), dict(W=W, out=torch.zeros_like(W)), dict(W=W, accumulate=True)):
+        with pytest.raises(ValueError):
+            G.gmm_embed_backward(dY, idx, 9, resp, table=False, **kw)
+
+
 def test_captured_and_on_another_stream(G):
     import torch
 
