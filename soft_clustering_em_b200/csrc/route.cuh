@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     }
     if constexpr (kDirect) {
       if (t == 0) z_here = z, rows_here = rows;
+      __syncwarp();
       if (ctas > 1) sm100::cluster_sync();
       else __syncthreads();
       if (rank == 0) {
