@@ -55,14 +55,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
   __shared__ uint8_t place[kMostBeams * kMaxAlt];      // where those stood
   const int t = threadIdx.x, lane = t & 31;
   const int64_t b = blockIdx.x;
+  grid_dependency_wait();
+  grid_dependents_launch();
   float score = -INFINITY;
   bool ended = false;
-  if (lane < a.w) {  // (from before the kernel that finds the rows' best classes)
+  if (lane < a.w) {
     score = a.scores[b * a.w + lane];
     ended = a.ended && a.ended[b * a.w + lane];
   }
-  grid_dependency_wait();
-  grid_dependents_launch();
   const float first = lane < a.w ? a.top_logp[(b * a.w + lane) * a.m] : 0.f;
   bool climbs = false;  // a candidate scores more than the one before it in its row's order
   for (int c0 = 0; c0 < a.w * a.m; c0 += kMergeThreads) {

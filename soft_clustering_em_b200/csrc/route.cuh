@@ -380,13 +380,9 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int groups = kReduceThreads / cols, g = t / cols, col = t & (cols - 1);
   // (the others of the cluster have started when its first CTA's memory is written below)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  int64_t lo = 0, hi = a.N;
-  if (a.offsets) {  // (from before the kernel that leaves the sums)
-    lo = a.offsets[s];
-    hi = a.offsets[s + 1];
-  }
   grid_dependency_wait();
   grid_dependents_launch();
+  const int64_t lo = a.offsets ? a.offsets[s] : 0, hi = a.offsets ? a.offsets[s + 1] : a.N;
   const bool legal = lo >= 0 && lo <= hi && hi <= a.N;
   if (!legal && t == 0 && a.flags) atomicOr(a.flags, GMM_DEVFLAG_BAD_INDEX);
   const int64_t size = route_slot(a.K);

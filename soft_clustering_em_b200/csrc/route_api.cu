@@ -202,8 +202,7 @@ gmm_status gmm_route_loss(const gmm_rows* r, const void* Z, const int32_t* idx, 
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cfg.attrs = attr;
-  // (it reads the offsets before it waits: they are there when the kernel above has started)
-  cfg.numAttrs = r->N > 0 ? 2 : 1;
+  cfg.numAttrs = 2;
   auto kern = threads == 256 ? route_reduce_kernel<256> : route_reduce_kernel<1024>;
   if (cudaLaunchKernelEx(&cfg, kern, a, (const float*)ws, o, cols) != cudaSuccess)
     return api_launched(0), GMM_ERR_CUDA;
