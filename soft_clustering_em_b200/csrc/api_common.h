@@ -15,7 +15,8 @@ gmm_status api_device_sms(int* sms);
 uint64_t api_wait_budget();
 
 // A launch that may start while the kernel before it in the stream ends: the kernel waits
-// (grid_dependency_wait) in every block before it touches memory.
+// (grid_dependency_wait) in every block before it touches memory, or, to go on beside the kernel
+// before it, acquires what that one has released after such a wait, and waits at its end.
 template <typename Kern, typename... Args>
 gmm_status api_launch_next(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t st,
                            Args... args) {

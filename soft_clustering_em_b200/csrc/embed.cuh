@@ -203,6 +203,24 @@ constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr uint32_t kSortCluster = 1u << 17;
 
+// What lets a kernel go on beside the sort before it in the stream.  Only a wait is sure to make
+// visible what came before, and the sort has waited: its first kernel then stores a token of the call
+// (release), and who reads it (acquire) sees all that the sort could see.  Who does not waits for the
+// sort.  The sums take the word back, so that a replayed call does not find its own token.
+struct Beside {
+  unsigned long long *word, token;  // word: in the workspace, or null: nothing goes on beside
+};
+__device__ __forceinline__ void beside_allow(const Beside& b) {
+  if (b.word && blockIdx.x == 0 && threadIdx.x == 0)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(b.word), "l"(b.token) : "memory");
+}
+__device__ __forceinline__ void beside_wait(const Beside& b) {
+  unsigned long long seen = 0;
+  if (b.word)
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(b.word) : "memory");
+  if (!b.word || seen != b.token) grid_dependency_wait();
+}
+
 // A choice on its way: its class and its place in idx.
 using Choice = uint2;
 
@@ -216,6 +234,7 @@ struct SortArgs {
   uint32_t per_warp;          // entries, a multiple of 32
   int K, shift, bits;
   uint32_t* flags;
+  Beside beside;              // with the first digit
 };
 
 // Entries i0 + 32 b + lane of a warp's part, b < kSortBatch, all on their way at once; class K
@@ -273,6 +292,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
   __syncthreads();
   grid_dependency_wait();
+  beside_allow(a.beside);
   grid_dependents_launch();
   if (a.seen)
     clear_seen(a.seen, a.K, blockIdx.x * kSortThreads + threadIdx.x, gridDim.x * kSortThreads);
@@ -389,6 +409,7 @@ struct SortAllArgs {
   uint32_t M, per_warp;
   int K, passes, bits;
   uint32_t* flags;
+  Beside beside;
 };
 
 __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAllArgs a) {
@@ -401,6 +422,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
   const uint64_t begin = min(((uint64_t)rank * kClusterWarps + w) * a.per_warp, (uint64_t)a.M);
   const uint64_t end = min(begin + a.per_warp, (uint64_t)a.M);
   grid_dependency_wait();
+  beside_allow(a.beside);
   grid_dependents_launch();
   if (a.seen) clear_seen(a.seen, a.K, rank * kClusterThreads + t, ctas * kClusterThreads);
   for (int pass = 0; pass < a.passes; pass++) {
@@ -482,10 +504,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(SortAl
 
 // ------------------------------------------------------------------ rows of zeros
 // Rows [0, rows) beside the sort, before it is known which are named; pieces of a row, one per
-// warp.
-// Does not wait for the sort before it in the stream, only ends after it: nothing that is written
-// here is read or written there, and what came before the sort is done when it lets this kernel
-// start.  (The rows behind, of classes that nothing names, get their zeros with the sums.)
+// warp.  Does not wait for the sort before it in the stream (Beside), only ends after it: nothing
+// that is written here is read or written there.  (The rows behind, of classes that nothing names,
+// get their zeros with the sums.)
 constexpr int kFillPiece = 16384;  // bytes
 // CTAs per SM of a kernel that goes on beside the sort and ends after it: all of them are resident
 // at once, also beside the sort's (one that waits keeps its place).
@@ -494,6 +515,7 @@ struct FillArgs {
   char* base;
   uint64_t rows, row_bytes, stride;  // bytes
   uint64_t parts;                    // pieces per row
+  Beside beside;
 };
 
 // n bytes of 0, by a warp.
@@ -510,6 +532,7 @@ __device__ __forceinline__ void zero_bytes(char* p, uint64_t n) {
 
 __global__ void __launch_bounds__(kEmbedThreads) embed_fill_kernel(FillArgs a) {
   grid_dependents_launch();
+  beside_wait(a.beside);
   const uint64_t pieces = a.rows * a.parts;
   for (uint64_t i = (uint64_t)blockIdx.x * (kEmbedThreads / 32) + threadIdx.x / 32; i < pieces;
        i += (uint64_t)gridDim.x * (kEmbedThreads / 32)) {
@@ -551,6 +574,7 @@ struct EmbedGradArgs {
   const uint8_t* seen;
   int fill_from, fill_rows;
   uint32_t fill_first, sum_blocks;
+  unsigned long long* beside;  // Beside's word
 };
 
 // Adds to float32 memory without waiting for what is there.  (An element is added to once in a
@@ -619,6 +643,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(EmbedGradAr
   extern __shared__ uint32_t stage[];
   grid_dependency_wait();
   grid_dependents_launch();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.beside = 0;
   uint32_t block = blockIdx.x - a.fill_first;
   if (block >= a.sum_blocks) {  // (the first ones wrap around)
     if (blockIdx.y != 0) return;
@@ -947,6 +972,7 @@ struct EmbedDotArgs {
   int m, K, D, units;
   float scale;
   uint32_t* flags;
+  Beside beside;
 };
 
 template <typename T, int kMode, int kLanes, int kMost>
@@ -957,6 +983,7 @@ __global__ void __launch_bounds__(kEmbedThreads, kBesideCtas) embed_dot_kernel(E
   constexpr int kWarps = kLanes / 32;  // of a row, where it has more than one
   __shared__ float sh[kLanes > 32 ? kWarps : 1][kMost];
   grid_dependents_launch();
+  beside_wait(a.beside);
   const int l = threadIdx.x % kLanes;
   const int64_t step = (int64_t)gridDim.x * (kEmbedThreads / kLanes);
   int64_t n = ((int64_t)blockIdx.x * kEmbedThreads + threadIdx.x) / kLanes;

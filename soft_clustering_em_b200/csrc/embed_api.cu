@@ -171,9 +171,9 @@ uint32_t grad_chunk(const gmm_embed_problem* p, uint32_t M) {
   return (uint32_t)std::min<uint64_t>(kGradChunk, std::max<uint64_t>(16, (chunk + 7) / 8 * 8));
 }
 
-// Workspace: two buffers of sorted choices, counts, named classes, cut sums.
+// Workspace: two buffers of sorted choices, counts, named classes, cut sums, Beside's word.
 struct GradLayout {
-  size_t list[2], counts, seen, part, total;
+  size_t list[2], counts, seen, part, beside, total;
   uint32_t chunk, chunks;
   int width;
 };
@@ -195,9 +195,12 @@ GradLayout grad_layout(const gmm_embed_problem* p) {
   L.chunks = M / L.chunk + (M % L.chunk != 0);
   L.width = (p->D + 7) / 8 * 8;
   L.part = take((size_t)L.chunks * 2 * L.width * 4);
+  L.beside = take(8);
   L.total = off;
   return L;
 }
+
+std::atomic<unsigned long long> grad_calls{0x9e3779b97f4a7c15ull};  // (no other content's number)
 
 struct GradCall {
   const gmm_embed_problem* p;
@@ -211,6 +214,7 @@ struct GradCall {
   uint32_t* flags;
   char* ws;
   cudaStream_t st;
+  Beside beside;  // (no word: what would go on beside the sort waits for what is before it)
 };
 
 // The choices sorted by class, in *list.
@@ -227,7 +231,7 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, uint8
     const SortAllArgs a = {g.idx,       {lists[0], lists[1]}, seen,
                            M,           part_of(M, C * kClusterWarps),
                            g.p->K,      plan.passes,          plan.bits,
-                           g.flags};
+                           g.flags,     g.beside};
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -261,6 +265,7 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, uint8
     o.bits = plan.bits;
     o.shift = i * plan.bits;
     o.flags = g.flags;
+    if (i == 0) o.beside = g.beside;
     gmm_status s;
     if ((s = api_launch_next(sort_count_kernel, dim3(plan.tiles), kSortThreads, 0, g.st, o)) !=
         GMM_OK)
@@ -272,22 +277,19 @@ gmm_status sort_launch(const GradCall& g, const GradLayout& L, uint32_t M, uint8
   return GMM_OK;
 }
 
-// `first`: nothing of this call is before it in the stream (it does not wait at its start).
 template <typename T, int kMode>
-gmm_status dot_launch(const GradCall& g, bool first) {
+gmm_status dot_launch(const GradCall& g) {
   const gmm_embed_problem* p = g.p;
   constexpr int V = Unit<T, kMode>::n;
   EmbedDotArgs a = {g.W,  g.dY, g.idx, g.dresp, p->N, p->ldw, p->ldy,
-                    p->m, p->K, p->D,  (p->D + V - 1) / V, p->scale, g.flags};
+                    p->m, p->K, p->D,  (p->D + V - 1) / V, p->scale, g.flags, g.beside};
   int sms = 0;
   gmm_status s = api_device_sms(&sms);
   if (s != GMM_OK) return s;
   auto go = [&](auto kern, int lanes) {
     const int rows = kEmbedThreads / lanes;
     const int64_t blocks = std::min<int64_t>((p->N + rows - 1) / rows, sms * kBesideCtas);
-    if (!first) return api_launch_next(kern, dim3((unsigned)blocks), kEmbedThreads, 0, g.st, a);
-    kern<<<(unsigned)blocks, kEmbedThreads, 0, g.st>>>(a);
-    return api_launched(1);
+    return api_launch_next(kern, dim3((unsigned)blocks), kEmbedThreads, 0, g.st, a);
   };
   auto lanes = [&](auto one, auto two, auto four, auto most, int n) {
     return p->m == 1 ? go(one, n) : p->m == 2 ? go(two, n) : p->m <= 4 ? go(four, n) : go(most, n);
@@ -304,14 +306,14 @@ gmm_status dot_launch(const GradCall& g, bool first) {
 }
 
 template <typename T>
-gmm_status dot_vec(const GradCall& g, bool first) {
+gmm_status dot_vec(const GradCall& g) {
   if (!g.dresp || g.p->N == 0) return GMM_OK;
   const bool aligned =
       aligned_rows(g.W, g.p->ldw, sizeof(T)) && aligned_rows(g.dY, g.p->ldy, sizeof(T));
   const int mode = unit_mode<T>(aligned, g.p->D);
-  return mode == 0   ? dot_launch<T, 0>(g, first)
-         : mode == 1 ? dot_launch<T, 1>(g, first)
-                     : dot_launch<T, 2>(g, first);
+  return mode == 0   ? dot_launch<T, 0>(g)
+         : mode == 1 ? dot_launch<T, 1>(g)
+                     : dot_launch<T, 2>(g);
 }
 
 gmm_status fill_launch(const GradCall& g, size_t size, uint64_t rows) {
@@ -321,7 +323,7 @@ gmm_status fill_launch(const GradCall& g, size_t size, uint64_t rows) {
   const uint64_t D = g.p->D;
   const bool one = g.ldd == g.p->D;  // one long row
   FillArgs a = {(char*)g.dW, one ? 1 : rows, (one ? rows * D : D) * size, (uint64_t)g.ldd * size,
-                0};
+                0, g.beside};
   a.parts = (a.row_bytes + kFillPiece - 1) / kFillPiece;
   const uint64_t blocks = (a.rows * a.parts + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32);
   return api_launch_next(embed_fill_kernel,
@@ -330,17 +332,17 @@ gmm_status fill_launch(const GradCall& g, size_t size, uint64_t rows) {
 }
 
 // Rows that get their zeros beside the sort: what goes through while it runs (6 GB in a ms, from
-// 12 us on 1 us more for every 8,192 choices).  All of them where there are no sums.
+// 12 us on 1 us more for every 8,192 choices).
 uint64_t beside_rows(const gmm_embed_problem* p, uint32_t M, size_t size) {
   const uint64_t rows = (uint64_t)(6e6 * (12.0 + M / 8192.0) / ((double)p->D * size));
-  return M == 0 ? p->K : std::min<uint64_t>(p->K, std::max<uint64_t>(rows, 1));
+  return std::min<uint64_t>(p->K, std::max<uint64_t>(rows, 1));
 }
 
 // Up to kFew choices, in one launch (and the weights' gradient in one before it).
 template <typename T, typename TO, int kMode>
 gmm_status few_launch(const GradCall& g, EmbedGradArgs a) {
   const gmm_embed_problem* p = g.p;
-  gmm_status s = dot_vec<T>(g, true);
+  gmm_status s = dot_vec<T>(g);
   if (s != GMM_OK) return s;
   const int groups = kEmbedThreads / a.lanes;
   a.sum_blocks = (a.M + groups - 1) / groups;
@@ -355,7 +357,7 @@ gmm_status few_launch(const GradCall& g, EmbedGradArgs a) {
 
 // Stream order: the sort; beside it the weights' gradient and rows of zeros; then the sums.
 template <typename T, typename TO, int kMode>
-gmm_status grad_launch(const GradCall& g) {
+gmm_status grad_launch(GradCall g) {
   const gmm_embed_problem* p = g.p;
   const GradLayout L = grad_layout(p);
   const uint32_t M = (uint32_t)(p->N * p->m);
@@ -380,13 +382,15 @@ gmm_status grad_launch(const GradCall& g) {
   a.scale = p->scale;
   a.m = p->m;
   a.add = g.add;
-  if (M > 0 && M <= kFew) return few_launch<T, TO, kMode>(g, a);
+  if (M == 0) return g.add ? GMM_OK : fill_launch(g, sizeof(TO), p->K);
+  if (M <= kFew) return few_launch<T, TO, kMode>(g, a);
+  g.beside = {(unsigned long long*)(g.ws + L.beside), ++grad_calls};
+  a.beside = g.beside.word;
   const uint64_t beside = g.add ? p->K : beside_rows(p, M, sizeof(TO));
   uint8_t* seen = beside < (uint64_t)p->K ? (uint8_t*)(g.ws + L.seen) : nullptr;
   if ((s = sort_launch(g, L, M, seen, &a.list)) != GMM_OK) return s;
-  if ((s = dot_vec<T>(g, false)) != GMM_OK) return s;
+  if ((s = dot_vec<T>(g)) != GMM_OK) return s;
   if (!g.add && (s = fill_launch(g, sizeof(TO), beside)) != GMM_OK) return s;
-  if (M == 0) return GMM_OK;
   const unsigned groups = kEmbedThreads / a.lanes;
   a.sum_blocks = (a.chunks + groups - 1) / groups;
   // the other rows' zeros: blocks of about 128 KB, one per SM ahead of the sums' so that the memory
@@ -419,7 +423,7 @@ gmm_status grad_vec(const GradCall& g) {
 
 template <typename T>
 gmm_status grad_types(const GradCall& g, bool wide) {
-  if (!g.dW) return dot_vec<T>(g, true);
+  if (!g.dW) return dot_vec<T>(g);
   return wide ? grad_vec<T, float>(g) : grad_vec<T, T>(g);
 }
 
@@ -473,7 +477,7 @@ gmm_status gmm_embed_backward(const gmm_embed_problem* p, const void* dY, const 
     return GMM_ERR_WORKSPACE;
   const GradCall g = {p,     dY,        W,         idx,       resp,
                       dW,    ldd,       accumulate != 0, dresp, dev_flags,
-                      (char*)ws, (cudaStream_t)stream};
+                      (char*)ws, (cudaStream_t)stream, {}};
   const bool wide = dW && dw_dtype == GMM_F32 && p->dtype != GMM_F32;
   if (p->dtype == GMM_F32) return grad_types<float>(g, false);
   if (p->dtype == GMM_BF16) return grad_types<__nv_bfloat16>(g, wide);

@@ -421,6 +421,44 @@ def test_a_scale_that_is_no_number_is_refused(G, bad):
             call()
 
 
+@pytest.mark.parametrize("N,m", [(500, 2), (20_000, 1), (70_000, 2)])
+def test_inputs_written_by_the_kernel_before(G, N, m):
+    """What goes on beside the sort sees what came just before it, replayed too, with a workspace of
+    any content; each replay has inputs of its own."""
+    import torch
+
+    K, D = 900, 64
+    g = torch.Generator(device="cuda").manual_seed(N)
+    dYs = torch.randn(6, N, D, device="cuda", generator=g)
+    ids = torch.randint(-1, K, (6, N, m), device="cuda", generator=g, dtype=torch.int32)
+    resp = torch.rand(N, m, device="cuda", generator=g)
+    Ws = torch.randn(6, K, D, device="cuda", generator=g)
+    dY, idx, W, dW = dYs[0].clone(), ids[0].clone(), Ws[0].clone(), torch.empty(K, D, device="cuda")
+    ws = torch.empty(G.gmm_embed_workspace_size(G.embed_problem(idx, K, 1.0, D, dY)),
+                     dtype=torch.uint8, device="cuda")
+    want = []
+    for i in range(6):
+        torch.cuda.synchronize()
+        want.append(G.gmm_embed_backward(dYs[i], ids[i], K, resp, W=Ws[i]))
+    from_dY, from_idx, from_W = dYs[0].clone(), ids[0].clone(), Ws[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        W.copy_(from_W)
+        idx.copy_(from_idx)
+        dY.copy_(from_dY)
+        _, got = G.gmm_embed_backward(dY, idx, K, resp, W=W, out=dW, ws=ws)
+    for i in (1, 2, 3, 4, 5, 1, 0):
+        if i == 3:
+            ws.fill_(255)
+        for t, v in ((from_dY, dYs[i]), (from_idx, ids[i]), (from_W, Ws[i])):
+            t.copy_(v)
+        graph.replay()
+        have = dW.clone(), got.clone()
+        graph.replay()
+        assert all(torch.equal(a, b) and torch.equal(c, b)
+                   for a, b, c in zip(have, want[i], (dW, got)))
+
+
 def test_refusals(G):
     import torch
 
