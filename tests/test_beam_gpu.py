@@ -171,6 +171,29 @@ def test_candidates_of_a_beam_follow_their_logits(G, B, w, K, m):
             np.testing.assert_array_equal(taken, best[:len(taken)])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,spread", [(50, 1.0), (1000, 0.1), (5000, 1.0), (131_072, 0.1)])
+def test_beams_of_flat_rows(G, K, spread, dtype):
+    """The best candidates of two beams 2.2 times the bound of a log p apart: in the order that 64
+    bits give them."""
+    import torch
+
+    B = 24
+    rng = np.random.default_rng(K)
+    Z = torch.from_numpy((rng.normal(size=(2 * B, K)) * spread).astype(np.float32)).to(_t(dtype))
+    x = Z.float().numpy()
+    best = A.beam_scores(x, np.zeros((B, 2), np.float32), scale=0.75).max(2)
+    big = 0.75 * np.abs(x).max()
+    bound = U * (2 * big + 387 + K / 256) + 4 * U * (2 * big + np.abs(best).max())
+    sign = np.where(rng.random(B) < 0.5, -1.0, 1.0)
+    scores = np.stack([np.zeros(B), best[:, 0] - best[:, 1] + 2.2 * sign * bound], 1)
+    scores = scores.astype(np.float32)
+    r = G.gmm_beam_select(Z.cuda(), torch.from_numpy(scores).cuda(), 2, scale=0.75)
+    np.testing.assert_array_equal(r.parent[:, 0].cpu().numpy(), sign > 0)
+    off = np.abs(r.scores[:, 0].double().cpu().numpy() - (best + scores.astype(np.float64)).max(1))
+    assert (off <= bound + U * (np.abs(best).max() + 1)).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("K", [100, 3000])
 def test_what_is_not_a_number(G, K, bad):
