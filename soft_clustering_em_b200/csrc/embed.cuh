@@ -123,9 +123,9 @@ struct Unit {
 // choices and addresses are formed once for kPer * kM units, all on their way at once.  Blocks y:
 // where a row has more units than that.  kM: at least m.
 //
-// 1e6 rows of 96 fp32, two of 4,096 entries each: 79 to 89 us (61 us of bytes), bound by
-// instruction issue (2.9 of 4 a clock) and the writes; with a thread per unit, indices and
-// addresses formed for each, 117 to 209.  16,384 of 131,072 rows of 2,048 bf16: 13 us.  8 rows of
+// 1e6 rows of 96 fp32, two of 4,096 entries each: 79 to 89 us (61 us of bytes), at no one limit
+// (2.7 of 4 instructions a clock, 65 % of the warps resident, 4.0 TB/s of mostly writes); with a
+// thread per unit, indices and addresses formed for each, 117 to 209.  16,384 of 131,072 rows of 2,048 bf16: 13 us.  8 rows of
 // those: 1.5 us.  Rows that start anywhere go element by element: 239,198 of 185 bf16 take 39 us
 // (14 us of bytes).
 template <typename T, int kMode, int kM, int kPer>
@@ -964,6 +964,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 2) embed_few_kernel(EmbedFewArg
 // ------------------------------------------------------------------ gradient of the weights
 // A group of 8, 32 or (for few rows) all 256 lanes per row n: <dY_n, W[idx_nj]> for its m choices,
 // in a fixed order.  (Like the rows of zeros it goes on beside the sort, and ends after it.)
+// The instances for more than 4 choices spill 4 to 76 bytes per thread at the 64 registers that 4
+// CTAs per SM leave, and sort_count_kernel 28 at 32.
 struct EmbedDotArgs {
   const void *W, *dY;
   const int32_t* idx;

@@ -468,6 +468,8 @@ struct RouteGradArgs {
 // 65,536 rows of 256 fp32 with 8 choices: 31 to 35 us (21 us of bytes).  262,144: 111 us (83), 94
 // without the choices' entries.  65,536 of 1,024: 97 us (83).  Of 201 bf16, rows that start
 // anywhere: 35 us (9); of 200: 22.
+// The fp32 instances from 65 classes on spill 8 to 72 bytes per thread, at 80 registers (up to 128
+// classes, three CTAs per SM) or 128 (two).
 template <typename T, int kLanes, int kEl, int kMode>
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(kEl))
     route_grad_kernel(RouteGradArgs g) {
