@@ -578,8 +578,8 @@ gmm_status gmm_embed(const gmm_embed_problem* p, const void* W, const int32_t* i
  *   dW_k = scale * sum over (n, j) with idx_nj = k of resp_nj dY_n
  *   dresp_nj = scale * <dY_n, W[idx_nj]>           (0 for a choice that is left out)
  * Choices are sorted by class and summed in that order, in float32 (a frequent class in parts of at
- * most 128 choices, 8 of those, 8 of those again, then in 64 bits), without atomics: the result does not change
- * from run to run, and is rounded once.
+ * most 128 choices, 8 of those, 8 of those again, then in 64 bits), without atomics: the result does
+ * not change from run to run, and is rounded once.
  *   dW        device, K x D of dw_dtype (GMM_F32 or dtype), rows ldd apart, or NULL.  Every row is
  *             written, zeros where nothing names it; with accumulate != 0 the gradient is added to
  *             what is there (in float32; in a GMM_F32 dW subnormal values count as 0), and rows
