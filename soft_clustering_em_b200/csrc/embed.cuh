@@ -126,8 +126,8 @@ struct Unit {
 // 1e6 rows of 96 fp32, two of 4,096 entries each: 79 to 89 us (61 us of bytes), at no one limit
 // (2.7 of 4 instructions a clock, 65 % of the warps resident, 4.0 TB/s of mostly writes); with a
 // thread per unit, indices and addresses formed for each, 117 to 209.  16,384 of 131,072 rows of
-// 2,048 bf16: 13 us.  8 rows of those: 1.5 us.  Rows that start anywhere go element by element: 239,198 of 185 bf16 take 39 us
-// (14 us of bytes).
+// 2,048 bf16: 13 us.  8 rows of those: 1.5 us.  Rows that start anywhere go element by element:
+// 239,198 of 185 bf16 take 39 us (14 us of bytes).
 template <typename T, int kMode, int kM, int kPer>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(EmbedArgs a) {
   using U = Unit<T, kMode>;
